@@ -28,6 +28,7 @@ FA_ERR_CUDA = -6
 FA_ERR_DEVICE_TIMEOUT = -7
 FA_ERR_RANGE = -8
 FA_ERR_SCRATCH = -9
+FA_ERR_INDEX = -10
 
 
 class FaError(RuntimeError):
@@ -54,6 +55,30 @@ class fa_extras_t(ctypes.Structure):
                 ("pse_stride_h", ctypes.c_int64), ("pse_stride_q", ctypes.c_int64),
                 ("pse_type", ctypes.c_int32), ("keep_prob", ctypes.c_float),
                 ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64)]
+
+
+class fa_paged_kv_t(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_stride_page", ctypes.c_int64), ("k_stride_head", ctypes.c_int64),
+                ("k_stride_slot", ctypes.c_int64), ("v_stride_page", ctypes.c_int64),
+                ("v_stride_head", ctypes.c_int64), ("v_stride_slot", ctypes.c_int64),
+                ("k_min", ctypes.c_void_p), ("k_max", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("max_pages", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
+
+
+class fa_kv_new_t(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p),
+                ("k_stride_b", ctypes.c_int64), ("k_stride_h", ctypes.c_int64),
+                ("k_stride_s", ctypes.c_int64), ("v_stride_b", ctypes.c_int64),
+                ("v_stride_h", ctypes.c_int64), ("v_stride_s", ctypes.c_int64),
+                ("q_stride_b", ctypes.c_int64), ("q_stride_h", ctypes.c_int64),
+                ("q_stride_s", ctypes.c_int64), ("qo_stride_b", ctypes.c_int64),
+                ("qo_stride_h", ctypes.c_int64), ("qo_stride_s", ctypes.c_int64),
+                ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("max_pos", ctypes.c_int32)]
 
 
 _lib = None
@@ -94,6 +119,18 @@ def library() -> ctypes.CDLL:
         lib.fa_convert_v_fp16.restype = ctypes.c_int
         lib.fa_convert_v_fp16.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
                                           ctypes.c_void_p]
+        lib.fa_kv_append.restype = ctypes.c_int
+        lib.fa_kv_append.argtypes = [ctypes.POINTER(fa_paged_kv_t), ctypes.POINTER(fa_kv_new_t)] + [
+            ctypes.c_int] * 6 + [ctypes.c_void_p] * 3
+        lib.fa_decode.restype = ctypes.c_int
+        lib.fa_decode.argtypes = [ctypes.c_void_p, ctypes.POINTER(fa_paged_kv_t), ctypes.c_void_p,
+                                  ctypes.c_void_p] + [ctypes.c_int] * 5 + [
+            ctypes.c_float, ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+            ctypes.c_int, ctypes.c_void_p]
+        lib.fa_select_pages.restype = ctypes.c_int
+        lib.fa_select_pages.argtypes = [ctypes.c_void_p, ctypes.POINTER(fa_paged_kv_t),
+                                        ctypes.c_void_p] + [ctypes.c_int] * 6 + [
+            ctypes.c_void_p] + [ctypes.c_int] * 3 + [ctypes.c_void_p]
         lib.fa_check_status.restype = ctypes.c_int
         lib.fa_check_status.argtypes = [ctypes.c_void_p]
         lib.fa_set_wait_timeout_ns.restype = None
@@ -416,3 +453,246 @@ def flash_attention_backward(q, k, v, o, lse, dout, *, o_lo=None, scale: Optiona
     _raise(fa_bwd(q, k, v, o, o_lo, lse, dout, dq, dk, dv, B, Hq, Hkv, Sq, Skv, D, Dv, scale,
                   mask_mode, seqlens, stream))
     return dq, dk, dv
+
+
+# ------------------------------------------------------------------ paged key-value cache
+def fa_kv_append(kv: fa_paged_kv_t, x: fa_kv_new_t, B: int, Hq: int, Hkv: int, Snew: int, D: int,
+                 mask_mode: int, kv_lens, new_lens=None, stream=None) -> int:
+    """Direct call of the C entry point (see include/fa_fwd.h).  Returns the FA_* code."""
+    return library().fa_kv_append(kv, x, B, Hq, Hkv, Snew, D, int(mask_mode), _ptr(kv_lens),
+                                  _ptr(new_lens), _stream(stream))
+
+
+def fa_decode(q, kv: fa_paged_kv_t, o, lse, B: int, Hq: int, Hkv: int, Sq: int, D: int,
+              scale: float, mask_mode: int, kv_lens, pre_tokens: int = -1, page_idx=None,
+              max_sel: int = 0, stream=None) -> int:
+    """Direct call of the C entry point (see include/fa_fwd.h).  Returns the FA_* code."""
+    return library().fa_decode(_ptr(q), kv, _ptr(o), _ptr(lse), B, Hq, Hkv, Sq, D, float(scale),
+                               int(mask_mode), _ptr(kv_lens), int(pre_tokens), _ptr(page_idx),
+                               int(max_sel), _stream(stream))
+
+
+def fa_select_pages(q, kv: fa_paged_kv_t, page_idx, B: int, Hq: int, Hkv: int, Sq: int, D: int,
+                    mask_mode: int, kv_lens, max_sel: int, first: int = 1, last: int = 1,
+                    stream=None) -> int:
+    """Direct call of the C entry point (see include/fa_fwd.h).  Returns the FA_* code."""
+    return library().fa_select_pages(_ptr(q), kv, _ptr(page_idx), B, Hq, Hkv, Sq, D,
+                                     int(mask_mode), _ptr(kv_lens), int(max_sel), int(first),
+                                     int(last), _stream(stream))
+
+
+def _steps(t, dims):
+    """Strides of the dims, 0 for a dim of size 1 (nothing to step over)."""
+    shape, stride = t.shape, t.stride()
+    return [0 if shape[d] == 1 else stride[d] for d in dims]
+
+
+class PagedKV:
+    """A paged key-value cache: what the paged calls need to know of it.
+
+    k_pages, v_pages: bf16 or fp16 CUDA tensors [num_pages, Hkv, page_size, D], any strides with a
+    contiguous last dimension (a [num_pages, page_size, Hkv, D] pool enters as
+    ``pool.transpose(1, 2)``); page_size 16, 32, 64, 128 or 256; D 64 or 128.
+    page_table: int32 [B, max_pages], column p the page of sequence b's tokens
+    [p * page_size, (p + 1) * page_size); entries past a sequence's last page are never read.
+    k_min, k_max: None, or contiguous [num_pages, Hkv, D] of the cache's type: the page bounds that
+    paged_kv_append keeps and select_kv_pages reads.
+
+    Holds the tensors, no copies: what is written into them between calls counts.  The object
+    itself is never changed by a call and may serve several streams."""
+
+    __slots__ = ("k_pages", "v_pages", "page_table", "k_min", "k_max", "dtype", "device", "B",
+                 "Hkv", "D", "page_size", "num_pages", "max_pages", "_flags", "_c")
+
+    def __init__(self, k_pages, v_pages, page_table, k_min=None, k_max=None):
+        import torch
+        if k_pages.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("the cache must be bf16 or fp16")
+        if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+            raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, D], of one shape")
+        if (k_min is None) != (k_max is None):
+            raise ValueError("k_min and k_max go together")
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or (
+                page_table.shape[1] > 1 and page_table.stride(1) != 1):
+            raise ValueError("page_table must be int32 [B, max_pages] with a contiguous last dimension")
+        self.num_pages, self.Hkv, self.page_size, self.D = k_pages.shape
+        self.B, self.max_pages = page_table.shape
+        bounds = () if k_min is None else (k_min, k_max)
+        for t in (k_pages, v_pages, page_table) + bounds:
+            if not t.is_cuda or t.device != k_pages.device:
+                raise ValueError("the cache's tensors must be on one CUDA device")
+        for t in (v_pages,) + bounds:
+            if t.dtype != k_pages.dtype:
+                raise ValueError("k_pages, v_pages, k_min and k_max must be of one type")
+        for t in (k_pages, v_pages):
+            if t.stride(3) != 1:
+                raise ValueError("k_pages and v_pages must have a contiguous last dimension")
+        for t in bounds:
+            if t.shape != (self.num_pages, self.Hkv, self.D) or not t.is_contiguous():
+                raise ValueError("k_min and k_max must be contiguous [num_pages, Hkv, D]")
+        if self.D not in (64, 128) or self.page_size not in (16, 32, 64, 128, 256):
+            raise ValueError("D must be 64 or 128, page_size 16, 32, 64, 128 or 256")
+        self.k_pages, self.v_pages, self.page_table = k_pages, v_pages, page_table
+        self.k_min, self.k_max = k_min, k_max
+        self.dtype, self.device = k_pages.dtype, k_pages.device
+        self._flags = FA_DTYPE_FP16 if self.dtype == torch.float16 else 0
+        ks, vs = _steps(k_pages, (0, 1, 2)), _steps(v_pages, (0, 1, 2))
+        self._c = fa_paged_kv_t(
+            k_pages.data_ptr(), v_pages.data_ptr(), *ks, *vs, _ptr(k_min), _ptr(k_max),
+            page_table.data_ptr(), _steps(page_table, (0,))[0], self.max_pages, self.num_pages,
+            self.page_size)
+
+
+def _int32_of(t, shape, device, name):
+    import torch
+    if t.dtype != torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor {tuple(shape)} on the cache's device")
+
+
+def _query_of(q, cache):
+    if q.dtype != cache.dtype or q.device != cache.device or q.dim() != 4:
+        raise ValueError("q must be [B, Hq, Sq, D] of the cache's type, on its device")
+    B, Hq, Sq, D = q.shape
+    if B != cache.B or D != cache.D or Hq % cache.Hkv:
+        raise ValueError("q does not fit the cache: B, D or Hq % Hkv")
+    return B, Hq, Sq, D
+
+
+def _on(device, stream, call):
+    """call(raw stream) with `device` current and, for a given stream, that stream current too, so
+    that what the call allocates belongs to it."""
+    import torch
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return call(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(device):
+            return call(torch.cuda.current_stream().cuda_stream)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    if stream.device != device:
+        raise ValueError("the stream is of another device than the cache")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
+
+
+def paged_kv_append(cache: PagedKV, kv_lens, k, v, *, new_lens=None, q=None, q_out=None, cos=None,
+                    sin=None, interleaved: bool = False, stream=None):
+    """New tokens into a paged cache, rotated on the way (fa_kv_append).
+
+    k, v [B, Hkv, S, D] of the cache's type, any strides with a contiguous last dimension; token i
+    of sequence b takes position kv_lens[b] + i (kv_lens int32 [B], the tokens in the cache before;
+    the caller adds the new ones).  new_lens: int32 [B], how many of the S are real (None: all).
+    q [B, Hq, S, D]: rotated by the same positions into q_out (allocated where None; may be q).
+    cos, sin: fp32 [max_pos, r / 2] of the rotated channels r <= D, r a multiple of 16; None: no
+    rotation.  interleaved: pairs (2j, 2j + 1) instead of (j, j + r / 2).
+    Updates cache.k_min / k_max where the cache has them.  Returns q_out (rows past new_lens as
+    they were: undefined in an allocated one), or None without q."""
+    import torch
+    if k.dim() != 4 or k.shape != v.shape:
+        raise ValueError("k and v must be [B, Hkv, S, D], of one shape")
+    B, Hkv, S, D = k.shape
+    if B != cache.B or Hkv != cache.Hkv or D != cache.D:
+        raise ValueError("k and v do not fit the cache: B, Hkv or D")
+    _int32_of(kv_lens, (B,), cache.device, "kv_lens")
+    if new_lens is not None:
+        _int32_of(new_lens, (B,), cache.device, "new_lens")
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        Hq = Hkv
+    else:
+        _query_of(q, cache)
+        Hq = q.shape[1]
+        if q.shape[2] != S or (q_out is not None and q_out.shape != q.shape):
+            raise ValueError("q and q_out must be [B, Hq, S, D] with k's S")
+    for t in (k, v) + (() if q is None else (q,)) + (() if q_out is None else (q_out,)):
+        if t.dtype != cache.dtype or t.device != cache.device or t.stride(3) != 1:
+            raise ValueError("k, v, q, q_out must be of the cache's type, on its device, with a contiguous last dimension")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    rot, max_pos = 0, 0
+    if cos is not None:
+        if cos.shape != sin.shape or cos.dim() != 2:
+            raise ValueError("cos and sin must be [max_pos, rotated channels / 2]")
+        for t in (cos, sin):
+            if t.dtype != torch.float32 or t.device != cache.device or not t.is_contiguous():
+                raise ValueError("cos and sin must be contiguous fp32 tensors on the cache's device")
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+
+    def call(raw):
+        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q is not None and q_out is None else q_out
+        x = fa_kv_new_t(k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(qo), *_steps(k, (0, 1, 2)),
+                        *_steps(v, (0, 1, 2)), *(_steps(q, (0, 1, 2)) if q is not None else (0, 0, 0)),
+                        *(_steps(qo, (0, 1, 2)) if q is not None else (0, 0, 0)), _ptr(cos), _ptr(sin),
+                        rot, 1 if interleaved else 0, max_pos)
+        _raise(library().fa_kv_append(cache._c, x, B, Hq, Hkv, S, D, cache._flags, kv_lens.data_ptr(),
+                                      _ptr(new_lens), raw))
+        return qo
+
+    return _on(cache.device, stream, call)
+
+
+def flash_attention_decode(q, cache: PagedKV, kv_lens, *, scale: Optional[float] = None,
+                           pre_tokens: Optional[int] = None, page_idx=None, out=None, lse=None,
+                           stream=None):
+    """Attention of each sequence's newest tokens over a paged cache (fa_decode).
+
+    q [B, Hq, Sq, D] contiguous, of the cache's type: the Sq newest tokens of each sequence, which
+    are in the cache already; kv_lens int32 [B], the tokens in the cache.  Row i is token
+    t = kv_lens[b] - Sq + i and sees keys max(0, t - pre_tokens) .. t (pre_tokens None: from 0); a
+    row that sees none gets 0 and LSE +inf.  page_idx: int32 [B, Hkv, max_sel] (select_kv_pages):
+    only these pages of each sequence are read.  Returns (o, lse fp32 [B, Hq, Sq])."""
+    import torch
+    B, Hq, Sq, D = _query_of(q, cache)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    _int32_of(kv_lens, (B,), cache.device, "kv_lens")
+    max_sel = 0
+    if page_idx is not None:
+        max_sel = page_idx.shape[-1]
+        _int32_of(page_idx, (B, cache.Hkv, max_sel), cache.device, "page_idx")
+    if pre_tokens is not None and pre_tokens < 0:
+        raise ValueError("pre_tokens must be >= 0 (None: unbounded)")
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or out.device != q.device
+                            or not out.is_contiguous()):
+        raise ValueError("out must be contiguous, of q's shape and type, on its device")
+    if lse is not None and (lse.shape != (B, Hq, Sq) or lse.dtype != torch.float32
+                            or lse.device != q.device or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 tensor [B, Hq, Sq] on q's device")
+
+    def call(raw):
+        o = torch.empty_like(q) if out is None else out
+        e = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device) if lse is None else lse
+        _raise(library().fa_decode(q.data_ptr(), cache._c, o.data_ptr(), e.data_ptr(), B, Hq, cache.Hkv,
+                                   Sq, D, 1.0 / math.sqrt(D) if scale is None else scale, cache._flags,
+                                   kv_lens.data_ptr(), -1 if pre_tokens is None else pre_tokens,
+                                   _ptr(page_idx), max_sel, raw))
+        return o, e
+
+    return _on(cache.device, stream, call)
+
+
+def select_kv_pages(q, cache: PagedKV, kv_lens, max_sel: int, *, first: int = 1, last: int = 1,
+                    out=None, stream=None):
+    """The pages of each sequence whose keys can score highest (fa_select_pages), as the page_idx
+    of flash_attention_decode: int32 [B, Hkv, max_sel], ascending, -1 behind the last.  The cache
+    needs page bounds (k_min, k_max).  first, last: so many first and last pages are always
+    chosen."""
+    import torch
+    B, Hq, Sq, D = _query_of(q, cache)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    if cache.k_min is None:
+        raise ValueError("the cache has no page bounds (k_min, k_max)")
+    _int32_of(kv_lens, (B,), cache.device, "kv_lens")
+    shape = (B, cache.Hkv, max_sel)
+    if out is not None:
+        _int32_of(out, shape, cache.device, "out")
+
+    def call(raw):
+        idx = torch.empty(shape, dtype=torch.int32, device=q.device) if out is None else out
+        _raise(library().fa_select_pages(q.data_ptr(), cache._c, idx.data_ptr(), B, Hq, cache.Hkv, Sq, D,
+                                         cache._flags, kv_lens.data_ptr(), max_sel, first, last, raw))
+        return idx
+
+    return _on(cache.device, stream, call)

@@ -10,7 +10,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfa_fwd.so")
-SOURCES = ["fa_fwd.cu"]
+SOURCES = ["fa_fwd.cu", "fa_paged.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -28,8 +28,8 @@ def up_to_date() -> bool:
     if not os.path.exists(LIB):
         return False
     t = os.path.getmtime(LIB)
-    # every source and header under csrc/ (the translation unit includes them all)
-    files = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cuh"))]
+    # every source and header under csrc/
+    files = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cuh", ".h"))]
     files.append(os.path.join(ROOT, "include", "fa_fwd.h"))
     return all(os.path.getmtime(f) <= t for f in files)
 
@@ -41,7 +41,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     # directory goes into the run path so that the library loads without it
     # on LD_LIBRARY_PATH
     cuda_lib = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path()))), "lib64")
-    cmd = [nvcc_path(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
+    cmd = [nvcc_path(), *ARCH, "-t", str(len(SOURCES)), "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
            "-shared", "-Xcompiler", "-fPIC", "-o", LIB + ".tmp",
            *[os.path.join(CSRC, s) for s in SOURCES], "-lcublas", "-Xlinker", "-rpath=" + cuda_lib]
     if verbose:

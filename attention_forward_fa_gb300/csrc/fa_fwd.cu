@@ -13,6 +13,7 @@
 #include <mutex>
 
 #include "../../include/fa_fwd.h"
+#include "fa_host.h"
 #include "fa_tiled.cuh"
 #include "fa_mla.cuh"
 #include "fa_bwd.cuh"
@@ -297,25 +298,7 @@ int sm_count() {
   return sms[dev];
 }
 
-// Launch with programmatic stream serialisation: the kernel may be scheduled
-// while the previous kernel on the stream drains; it waits for that kernel
-// (griddepcontrol.wait) before its first global memory access.
-template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kern)(Params...), unsigned grid, unsigned block, size_t smem,
-                             cudaStream_t st, Args&&... args) {
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
-}
+using fa_host::launch_dependent;
 
 template <int D, bool BF16, int NS, bool CONV, bool SPLIT, bool EXTRAS = false>
 int launch_tiled(const fa::TiledParams& prm, int units, cudaStream_t st) {
@@ -909,6 +892,15 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* o, const v
 
 }  // namespace
 
+namespace fa_host {
+int* status_ptr() { return ::status_ptr(); }
+int cuda_fail(cudaError_t e) { return ::cuda_fail(e); }
+void* scratch_alloc(size_t bytes, cudaStream_t st) { return ::scratch_alloc(bytes, st); }
+int sm_count() { return ::sm_count(); }
+long long wait_timeout_ns() { return g_timeout_ns.load(); }
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return ::get_encode(); }
+}  // namespace fa_host
+
 extern "C" {
 
 int fa_bwd(const void* q, const void* k, const void* v, const void* o, const void* o_lo,
@@ -1058,6 +1050,7 @@ int fa_check_status(void* stream) {
   }
   if (h & fa::kStatusTimeout) return FA_ERR_DEVICE_TIMEOUT;
   if (h & fa::kStatusRange) return FA_ERR_RANGE;
+  if (h & fa_host::kStatusIndex) return FA_ERR_INDEX;
   return FA_OK;
 }
 
@@ -1090,6 +1083,7 @@ const char* fa_strerror(int code) {
     case FA_ERR_DEVICE_TIMEOUT: return "bounded on-chip wait expired";
     case FA_ERR_RANGE: return "value outside the fp16 range in an fp16 product (bf16 V, top-k Q or latent; fp16 backward dS)";
     case FA_ERR_SCRATCH: return "bf16 key latent larger than the fixed scratch of fa_fwd_noalloc (32 MiB fp16)";
+    case FA_ERR_INDEX: return "page id, length or position out of range in a paged call (those keys or tokens were left out)";
     default: return "unknown error code";
   }
 }

@@ -1,0 +1,236 @@
+// fa_kv_append: new keys (rotated) and values into their pages, rotated queries
+// to q_out, page bounds brought up to date.
+//
+// Each thread owns 16 channels of a row as two 16-byte vectors A and B that
+// hold whole pairs: with pairs (j, j + r/2) A and B are the same 8 channels of
+// the two halves, with pairs (2j, 2j + 1), and past the rotated channels, they
+// are neighbours.  A row is D / 16 threads, so a block of 256 threads takes 32
+// (D 128) or 64 rows a step: `tp` tokens of one page times the heads that
+// are left.  A block stays inside one page of one sequence, so that a page's
+// bounds have one writer: no atomics, the same result every time.
+#pragma once
+#include "fa_paged.cuh"
+
+namespace fa {
+
+constexpr int kAppendThreads = 256;
+
+struct AppendParams {
+  PagedKv kv;
+  const uint16_t* k;
+  const uint16_t* v;
+  const uint16_t* q;
+  uint16_t* qo;
+  long long k_sb, k_sh, k_ss, v_sb, v_sh, v_ss, q_sb, q_sh, q_ss, o_sb, o_sh, o_ss;
+  const float* cos;
+  const float* sin;
+  int rot_dim, interleaved, max_pos;
+  const int32_t* kv_lens;
+  const int32_t* new_lens;
+  int Hq, Hkv, Snew;
+  int chunks;              // pages that one sequence's new tokens can touch
+  int tp_shift;            // tokens per step = 1 << tp_shift
+  int kv_heads, q_heads;   // heads per block of the K / V and the Q blocks
+  int k_items, q_items;    // blocks per page for K (V as many), for Q
+  int* status;
+};
+
+template <bool BF16, int D>
+__global__ void __launch_bounds__(kAppendThreads) fa_kv_append_kernel(const AppendParams p) {
+  constexpr int L = D / 16;                    // threads per row
+  constexpr int kRows = kAppendThreads / L;    // rows per step
+  __shared__ uint4 s_red[4][8][L];             // [min A, min B, max A, max B][warp][thread of the row]
+  pdl_launch_dependents();
+  pdl_wait_prior();
+  const int items = 2 * p.k_items + p.q_items;
+  const int item = blockIdx.x % items;
+  const int rest = blockIdx.x / items;
+  const int chunk = rest % p.chunks, b = rest / p.chunks;
+
+  const int ps_shift = p.kv.page_shift, ps = 1 << ps_shift;
+  const int n0 = p.new_lens ? p.new_lens[b] : p.Snew;
+  const int n_new = min(max(n0, 0), p.Snew);
+  if (n0 != n_new && threadIdx.x == 0) atomicOr(p.status, fa_host::kStatusIndex);
+  if (n_new == 0) return;
+  const int before = paged_len(p.kv, p.kv_lens[b], p.status);
+  if (before < 0) return;
+  const int page = (before >> ps_shift) + chunk;
+  // tokens [t0, t1) of the sequence, by position (64 bits: `before` may be near 2^31)
+  const long long p0 = (long long)page << ps_shift;
+  const long long end = min((long long)before + n_new, p0 + ps);
+  if (max((long long)before, p0) >= end) return;
+  if (page >= p.kv.max_pages) {
+    if (threadIdx.x == 0) atomicOr(p.status, fa_host::kStatusIndex);
+    return;
+  }
+  const int t0 = max(before, (int)p0);
+  int t1 = (int)end;
+  const int id = paged_id(p.kv, b, page, p.status);
+  if (id < 0) return;
+  if (p.rot_dim && t1 > p.max_pos) {
+    if (threadIdx.x == 0) atomicOr(p.status, fa_host::kStatusIndex);
+    t1 = p.max_pos;
+    if (t0 >= t1) return;
+  }
+
+  const int part = threadIdx.x % L;
+  const int row = threadIdx.x / L;
+  const int tp = 1 << p.tp_shift;
+  const int tl = row & (tp - 1), hl = row >> p.tp_shift, hp = kRows >> p.tp_shift;
+  const bool turns = part < p.rot_dim / 16;
+  const bool halves = turns && !p.interleaved;
+  const int offA = halves ? 8 * part : 16 * part;
+  const int offB = halves ? 8 * part + p.rot_dim / 2 : 16 * part + 8;
+  const int half = p.rot_dim / 2;
+
+  float c[8], s[8];
+  auto angles = [&](int t) {
+    if (!turns) return;
+    const float4* cp = reinterpret_cast<const float4*>(p.cos + (long long)t * half + 8 * part);
+    const float4* sp = reinterpret_cast<const float4*>(p.sin + (long long)t * half + 8 * part);
+    const float4 c0 = __ldg(cp), c1 = __ldg(cp + 1), s0 = __ldg(sp), s1 = __ldg(sp + 1);
+    c[0] = c0.x; c[1] = c0.y; c[2] = c0.z; c[3] = c0.w; c[4] = c1.x; c[5] = c1.y; c[6] = c1.z; c[7] = c1.w;
+    s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w; s[4] = s1.x; s[5] = s1.y; s[6] = s1.z; s[7] = s1.w;
+  };
+  // in fp32, each channel rounded once to the cache's type
+  auto rotate = [&](uint4& wa, uint4& wb) {
+    if (!turns) return;
+    float a[8], d[8];
+    unpack8<BF16>(wa, a);
+    unpack8<BF16>(wb, d);
+    if (p.interleaved) {
+      float x[16];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = a[j], x[8 + j] = d[j];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float e = x[2 * j], o = x[2 * j + 1];
+        x[2 * j] = e * c[j] - o * s[j];
+        x[2 * j + 1] = e * s[j] + o * c[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] = x[j], d[j] = x[8 + j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float e = a[j], o = d[j];
+        a[j] = e * c[j] - o * s[j];
+        d[j] = e * s[j] + o * c[j];
+      }
+    }
+    wa = pack8<BF16>(a);
+    wb = pack8<BF16>(d);
+  };
+  auto ld = [](const uint16_t* x) { return __ldg(reinterpret_cast<const uint4*>(x)); };
+  auto st = [](uint16_t* x, uint4 w) { *reinterpret_cast<uint4*>(x) = w; };
+
+  if (item >= 2 * p.k_items) {   // ---------------- queries: one set of angles for all heads
+    const int h0 = (item - 2 * p.k_items) * p.q_heads;
+    const int h1 = min(p.Hq, h0 + p.q_heads);
+    for (int t = t0 + tl; t < t1; t += tp) {
+      angles(t);
+      const uint16_t* src = p.q + b * p.q_sb + (long long)(t - before) * p.q_ss;
+      uint16_t* dst = p.qo + b * p.o_sb + (long long)(t - before) * p.o_ss;
+      for (int h = h0 + hl; h < h1; h += hp) {
+        // plain loads: q_out may be q
+        uint4 wa = *reinterpret_cast<const uint4*>(src + h * p.q_sh + offA);
+        uint4 wb = *reinterpret_cast<const uint4*>(src + h * p.q_sh + offB);
+        rotate(wa, wb);
+        st(dst + h * p.o_sh + offA, wa);
+        st(dst + h * p.o_sh + offB, wb);
+      }
+    }
+    return;
+  }
+  if (item >= p.k_items) {       // ---------------- values: copied
+    const int h0 = (item - p.k_items) * p.kv_heads;
+    const int h1 = min(p.Hkv, h0 + p.kv_heads);
+    for (int t = t0 + tl; t < t1; t += tp) {
+      const uint16_t* src = p.v + b * p.v_sb + (long long)(t - before) * p.v_ss;
+      uint16_t* dst = p.kv.v + (long long)id * p.kv.v_sp + (long long)(t & (ps - 1)) * p.kv.v_ss;
+      for (int h = h0 + hl; h < h1; h += hp) {
+        const uint4 wa = ld(src + h * p.v_sh + 16 * part), wb = ld(src + h * p.v_sh + 16 * part + 8);
+        st(dst + h * p.kv.v_sh + 16 * part, wa);
+        st(dst + h * p.kv.v_sh + 16 * part + 8, wb);
+      }
+    }
+    return;
+  }
+  // ---------------- keys: rotated; per page and channel the least and largest as stored
+  const uint32_t kInf = BF16 ? 0x7F807F80u : 0x7C007C00u;
+  const bool kept = (t0 & (ps - 1)) != 0;   // slot 0 holds an older key
+  const int h0 = item * p.kv_heads;
+  for (int hb = h0; hb < min(p.Hkv, h0 + p.kv_heads); hb += hp) {   // block-uniform
+    const int h = hb + hl;
+    const bool on = h < min(p.Hkv, h0 + p.kv_heads);
+    uint4 mn[2], mx[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      mn[j] = make_uint4(kInf, kInf, kInf, kInf);
+      mx[j] = make_uint4(kInf | 0x80008000u, kInf | 0x80008000u, kInf | 0x80008000u, kInf | 0x80008000u);
+    }
+    auto widen = [&](int j, uint4 lo, uint4 hi) {
+      mn[j] = make_uint4(min16x2<BF16>(mn[j].x, lo.x), min16x2<BF16>(mn[j].y, lo.y),
+                         min16x2<BF16>(mn[j].z, lo.z), min16x2<BF16>(mn[j].w, lo.w));
+      mx[j] = make_uint4(max16x2<BF16>(mx[j].x, hi.x), max16x2<BF16>(mx[j].y, hi.y),
+                         max16x2<BF16>(mx[j].z, hi.z), max16x2<BF16>(mx[j].w, hi.w));
+    };
+    if (on) {
+      for (int t = t0 + tl; t < t1; t += tp) {
+        angles(t);
+        const uint16_t* src = p.k + b * p.k_sb + (long long)(t - before) * p.k_ss + h * p.k_sh;
+        uint16_t* dst = p.kv.k + (long long)id * p.kv.k_sp + (long long)(t & (ps - 1)) * p.kv.k_ss +
+                        h * p.kv.k_sh;
+        uint4 wa = ld(src + offA), wb = ld(src + offB);
+        rotate(wa, wb);
+        st(dst + offA, wa);
+        st(dst + offB, wb);
+        widen(0, wa, wa);
+        widen(1, wb, wb);
+      }
+    }
+    if (!p.kv.k_min) continue;
+    // join the tokens of a step: first the rows of the warp, then the warps.  With 2^x tokens
+    // a step, rows that differ in the low x bits of their number hold the same head.
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto other = [&](uint4 w, int m) {
+      return make_uint4(__shfl_xor_sync(0xffffffffu, w.x, m), __shfl_xor_sync(0xffffffffu, w.y, m),
+                        __shfl_xor_sync(0xffffffffu, w.z, m), __shfl_xor_sync(0xffffffffu, w.w, m));
+    };
+    for (int m = L; m < 32 && m < (L << p.tp_shift); m <<= 1) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint4 lo = other(mn[j], m), hi = other(mx[j], m);
+        widen(j, lo, hi);
+      }
+    }
+    const int wpt = (L << p.tp_shift) >> 5;   // warps that share a head's tokens (0 or 1: none)
+    if (wpt > 1) {                            // block-uniform
+      if (lane < L) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) s_red[j][warp][lane] = mn[j], s_red[2 + j][warp][lane] = mx[j];
+      }
+      __syncthreads();
+      if (lane < L && warp % wpt == 0) {
+        for (int w = 1; w < wpt; ++w)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) widen(j, s_red[j][warp + w][lane], s_red[2 + j][warp + w][lane]);
+      }
+      __syncthreads();
+    }
+    if (on && tl == 0) {
+      const long long at = ((long long)id * p.Hkv + h) * D;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int off = j ? offB : offA;
+        uint4* lo = reinterpret_cast<uint4*>(p.kv.k_min + at + off);
+        uint4* hi = reinterpret_cast<uint4*>(p.kv.k_max + at + off);
+        if (kept) widen(j, *lo, *hi);
+        *lo = mn[j];
+        *hi = mx[j];
+      }
+    }
+  }
+}
+
+}  // namespace fa

@@ -1,0 +1,250 @@
+// Host side of the operators over a paged key-value cache (include/fa_fwd.h):
+// argument checks, variant selection and launch.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/fa_fwd.h"
+#include "fa_decode.cuh"
+#include "fa_host.h"
+#include "fa_kv_append.cuh"
+#include "fa_select.cuh"
+
+namespace {
+
+using fa_host::cuda_fail;
+using fa_host::launch_dependent;
+
+constexpr long long kMostTokens = (1LL << 31) - 65536;   // of one sequence: positions are 32-bit
+constexpr int kMostSel = 1 << 20;                        // listed pages of one KV head
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Checks of what the three entry points share; nothing is launched.
+int validate_cache(const fa_paged_kv_t* kv, int B, int Hq, int Hkv, int S, int D, int mask_mode) {
+  if (!kv || !kv->page_table) return FA_ERR_NULL;
+  if (mask_mode & ~FA_DTYPE_FP16) return FA_ERR_SHAPE;
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || S <= 0 || D <= 0 || Hq % Hkv) return FA_ERR_SHAPE;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  const int ps = kv->page_size;
+  if (ps < 16 || ps > 256 || (ps & (ps - 1))) return FA_ERR_SHAPE;
+  if (kv->num_pages <= 0 || kv->max_pages <= 0 || kv->table_stride < 0) return FA_ERR_SHAPE;
+  if ((long long)kv->max_pages * ps > kMostTokens) return FA_ERR_SHAPE;
+  if ((kv->k_min == nullptr) != (kv->k_max == nullptr)) return FA_ERR_NULL;
+  if (!aligned(kv->page_table, 4) || !aligned(kv->k_min, 16) || !aligned(kv->k_max, 16))
+    return FA_ERR_ALIGN;
+  return FA_OK;
+}
+
+// The pools: bases and strides (a stride of 0 would lay tokens over each other).
+int validate_pools(const fa_paged_kv_t* kv, int Hkv) {
+  if (!kv->k || !kv->v) return FA_ERR_NULL;
+  for (const int64_t s : {kv->k_stride_page, kv->k_stride_head, kv->k_stride_slot,
+                          kv->v_stride_page, kv->v_stride_head, kv->v_stride_slot}) {
+    if (s < 0 || s >= (1LL << 38)) return FA_ERR_SHAPE;
+    if (s % 8) return FA_ERR_ALIGN;
+  }
+  if (!kv->k_stride_slot || !kv->v_stride_slot ||
+      (Hkv > 1 && (!kv->k_stride_head || !kv->v_stride_head)) ||
+      (kv->num_pages > 1 && (!kv->k_stride_page || !kv->v_stride_page)))
+    return FA_ERR_SHAPE;
+  if (!aligned(kv->k, 16) || !aligned(kv->v, 16)) return FA_ERR_ALIGN;
+  return FA_OK;
+}
+
+fa::PagedKv device_cache(const fa_paged_kv_t* kv) {
+  fa::PagedKv c;
+  c.k = static_cast<uint16_t*>(kv->k);
+  c.v = static_cast<uint16_t*>(kv->v);
+  c.k_sp = kv->k_stride_page;
+  c.k_sh = kv->k_stride_head;
+  c.k_ss = kv->k_stride_slot;
+  c.v_sp = kv->v_stride_page;
+  c.v_sh = kv->v_stride_head;
+  c.v_ss = kv->v_stride_slot;
+  c.k_min = static_cast<uint16_t*>(kv->k_min);
+  c.k_max = static_cast<uint16_t*>(kv->k_max);
+  c.table = kv->page_table;
+  c.table_stride = kv->table_stride;
+  c.max_pages = kv->max_pages;
+  c.num_pages = kv->num_pages;
+  c.page_shift = 0;
+  while ((1 << c.page_shift) < kv->page_size) ++c.page_shift;
+  return c;
+}
+
+template <bool BF16, int D>
+cudaError_t launch_append(const fa::AppendParams& p, unsigned grid, cudaStream_t st) {
+  return launch_dependent(fa::fa_kv_append_kernel<BF16, D>, grid, fa::kAppendThreads, 0, st, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_kv_append(const fa_paged_kv_t* kv, const fa_kv_new_t* x, int B, int Hq, int Hkv, int Snew,
+                 int D, int mask_mode, const int32_t* kv_lens, const int32_t* new_lens,
+                 void* stream) {
+  if (!x) return FA_ERR_NULL;
+  int rc = validate_cache(kv, B, Hq, Hkv, Snew, D, mask_mode);
+  if (rc == FA_OK) rc = validate_pools(kv, Hkv);
+  if (rc != FA_OK) return rc;
+  if (!x->k || !x->v || !kv_lens || (x->q == nullptr) != (x->q_out == nullptr)) return FA_ERR_NULL;
+  if (x->rot_dim < 0 || x->rot_dim > D || x->rot_dim % 16 || x->interleaved < 0 || x->interleaved > 1)
+    return FA_ERR_SHAPE;
+  if (x->rot_dim && (!x->cos || !x->sin)) return FA_ERR_NULL;
+  if (x->rot_dim && x->max_pos <= 0) return FA_ERR_SHAPE;
+  for (const int64_t s : {x->k_stride_b, x->k_stride_h, x->k_stride_s, x->v_stride_b, x->v_stride_h,
+                          x->v_stride_s}) {
+    if (s < 0) return FA_ERR_SHAPE;
+    if (s % 8) return FA_ERR_ALIGN;
+  }
+  if (x->q)
+    for (const int64_t s : {x->q_stride_b, x->q_stride_h, x->q_stride_s, x->qo_stride_b,
+                            x->qo_stride_h, x->qo_stride_s}) {
+      if (s < 0) return FA_ERR_SHAPE;
+      if (s % 8) return FA_ERR_ALIGN;
+    }
+  if (x->q == x->q_out && x->q &&
+      (x->q_stride_b != x->qo_stride_b || x->q_stride_h != x->qo_stride_h || x->q_stride_s != x->qo_stride_s))
+    return FA_ERR_SHAPE;   // in place only row onto row
+  if (!aligned(x->k, 16) || !aligned(x->v, 16) || !aligned(x->q, 16) || !aligned(x->q_out, 16) ||
+      (x->rot_dim && (!aligned(x->cos, 16) || !aligned(x->sin, 16))) || !aligned(kv_lens, 4) ||
+      !aligned(new_lens, 4))
+    return FA_ERR_ALIGN;
+
+  fa::AppendParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.kv = device_cache(kv);
+  p.k = static_cast<const uint16_t*>(x->k);
+  p.v = static_cast<const uint16_t*>(x->v);
+  p.q = static_cast<const uint16_t*>(x->q);
+  p.qo = static_cast<uint16_t*>(x->q_out);
+  p.k_sb = x->k_stride_b, p.k_sh = x->k_stride_h, p.k_ss = x->k_stride_s;
+  p.v_sb = x->v_stride_b, p.v_sh = x->v_stride_h, p.v_ss = x->v_stride_s;
+  p.q_sb = x->q_stride_b, p.q_sh = x->q_stride_h, p.q_ss = x->q_stride_s;
+  p.o_sb = x->qo_stride_b, p.o_sh = x->qo_stride_h, p.o_ss = x->qo_stride_s;
+  p.cos = x->cos;
+  p.sin = x->sin;
+  p.rot_dim = x->rot_dim;
+  p.interleaved = x->interleaved;
+  p.max_pos = x->max_pos;
+  p.kv_lens = kv_lens;
+  p.new_lens = new_lens;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.Snew = Snew;
+  const int ps = kv->page_size;
+  p.chunks = (int)(((long long)Snew + ps - 2) / ps) + 1;
+  const int rows = fa::kAppendThreads / (D / 16);
+  while ((1 << p.tp_shift) < rows && (1 << p.tp_shift) < std::min(Snew, ps)) ++p.tp_shift;
+  const int hp = rows >> p.tp_shift;
+  p.kv_heads = hp;
+  p.q_heads = 4 * hp;
+  p.k_items = (Hkv + p.kv_heads - 1) / p.kv_heads;
+  p.q_items = x->q ? (Hq + p.q_heads - 1) / p.q_heads : 0;
+  const long long grid = (long long)B * p.chunks * (2 * p.k_items + p.q_items);
+  if (grid > 0x7FFFFFFFLL) return FA_ERR_SHAPE;
+  p.status = fa_host::status_ptr();
+  if (!p.status) return cuda_fail(cudaGetLastError());
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool fp16 = (mask_mode & FA_DTYPE_FP16) != 0;
+  const cudaError_t e =
+      D == 128 ? (fp16 ? launch_append<false, 128>(p, (unsigned)grid, st) : launch_append<true, 128>(p, (unsigned)grid, st))
+               : (fp16 ? launch_append<false, 64>(p, (unsigned)grid, st) : launch_append<true, 64>(p, (unsigned)grid, st));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e);
+}
+
+int fa_decode(const void* q, const fa_paged_kv_t* kv, void* o, float* lse, int B, int Hq, int Hkv,
+              int Sq, int D, float scale, int mask_mode, const int32_t* kv_lens, int pre_tokens,
+              const int32_t* page_idx, int max_sel, void* stream) {
+  int rc = validate_cache(kv, B, Hq, Hkv, Sq, D, mask_mode);
+  if (rc == FA_OK) rc = validate_pools(kv, Hkv);
+  if (rc != FA_OK) return rc;
+  if (!q || !o || !lse || !kv_lens) return FA_ERR_NULL;
+  if (!std::isfinite(scale) || pre_tokens < -1) return FA_ERR_SHAPE;
+  if (page_idx && (max_sel <= 0 || max_sel > kMostSel)) return FA_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(kv_lens, 4) || !aligned(page_idx, 4))
+    return FA_ERR_ALIGN;
+  const long long rows = (long long)B * Hq * Sq;
+  if (rows > 0x7FFFFFFFLL) return FA_ERR_SHAPE;
+  fa::DecodeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.kv = device_cache(kv);
+  p.q = static_cast<const uint16_t*>(q);
+  p.o = o;
+  p.lse = lse;
+  p.kv_lens = kv_lens;
+  p.sel = page_idx;
+  p.max_sel = max_sel;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.Sq = Sq;
+  p.pre_tokens = pre_tokens;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.status = fa_host::status_ptr();
+  if (!p.status) return cuda_fail(cudaGetLastError());
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool fp16 = (mask_mode & FA_DTYPE_FP16) != 0;
+  if (D == 128) {
+    if (fp16) fa::fa_decode_row_kernel<false, 128><<<(unsigned)rows, 128, 0, st>>>(p);
+    else fa::fa_decode_row_kernel<true, 128><<<(unsigned)rows, 128, 0, st>>>(p);
+  } else {
+    if (fp16) fa::fa_decode_row_kernel<false, 64><<<(unsigned)rows, 128, 0, st>>>(p);
+    else fa::fa_decode_row_kernel<true, 64><<<(unsigned)rows, 128, 0, st>>>(p);
+  }
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FA_OK : cuda_fail(e);
+}
+
+int fa_select_pages(const void* q, const fa_paged_kv_t* kv, int32_t* page_idx, int B, int Hq,
+                    int Hkv, int Sq, int D, int mask_mode, const int32_t* kv_lens, int max_sel,
+                    int first, int last, void* stream) {
+  const int rc = validate_cache(kv, B, Hq, Hkv, Sq, D, mask_mode);
+  if (rc != FA_OK) return rc;
+  if (!q || !page_idx || !kv_lens || !kv->k_min) return FA_ERR_NULL;
+  if (max_sel <= 0 || max_sel > kMostSel || first < 0 || last < 0 ||
+      (long long)first + last > max_sel)
+    return FA_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(page_idx, 4) || !aligned(kv_lens, 4)) return FA_ERR_ALIGN;
+  const long long units = (long long)B * Hkv;
+  if (units > 0x7FFFFFFFLL) return FA_ERR_SHAPE;
+  fa::SelectParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.kv = device_cache(kv);
+  p.q = static_cast<const uint16_t*>(q);
+  p.out = page_idx;
+  p.kv_lens = kv_lens;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.Sq = Sq;
+  p.max_sel = max_sel;
+  p.first = first;
+  p.last = last;
+  p.status = fa_host::status_ptr();
+  if (!p.status) return cuda_fail(cudaGetLastError());
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const size_t bytes = (size_t)units * kv->max_pages * 8;
+  p.score = static_cast<double*>(fa_host::scratch_alloc(bytes, st));
+  if (!p.score) return cuda_fail(cudaGetLastError());
+  const bool fp16 = (mask_mode & FA_DTYPE_FP16) != 0;
+  if (D == 128) {
+    if (fp16) fa::fa_select_kernel<false, 128><<<(unsigned)units, fa::kSelectThreads, 0, st>>>(p);
+    else fa::fa_select_kernel<true, 128><<<(unsigned)units, fa::kSelectThreads, 0, st>>>(p);
+  } else {
+    if (fp16) fa::fa_select_kernel<false, 64><<<(unsigned)units, fa::kSelectThreads, 0, st>>>(p);
+    else fa::fa_select_kernel<true, 64><<<(unsigned)units, fa::kSelectThreads, 0, st>>>(p);
+  }
+  const cudaError_t e = cudaGetLastError();
+  cudaFreeAsync(p.score, st);
+  return e == cudaSuccess ? FA_OK : cuda_fail(e);
+}
+
+}  // extern "C"

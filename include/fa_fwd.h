@@ -79,6 +79,8 @@ extern "C" {
 #define FA_ERR_SCRATCH         -9  /* fa_fwd_noalloc, top-k: the bf16 key latent     */
                                    /* needs more than its fixed scratch               */
                                    /* (B*Skv*D*2 > 32 MiB)                            */
+#define FA_ERR_INDEX          -10  /* a paged call met a page id, length or position  */
+                                   /* out of range; those keys or tokens were left out */
 
 /* ---- mask_mode flag word ----------------------------------------------- */
 /* bits 0-3: mask */
@@ -372,10 +374,146 @@ int fa_fwd_noalloc(const void* q, const void* k, const void* v, void* o, float* 
  */
 int fa_convert_v_fp16(const void* v_bf16, void* v_fp16, int64_t n_elems, void* stream);
 
+/* ---- serving over a paged key-value cache -------------------------------- */
+/*
+ * The cache is a pool of pages of page_size tokens; sequence b's tokens
+ * [p * page_size, (p + 1) * page_size) of every KV head lie in page
+ * page_table[b * table_stride + p].  Three operators read and write it:
+ *   fa_kv_append     writes new tokens' K (rotated) and V into their pages,
+ *   fa_decode        attention of a sequence's newest tokens over its pages,
+ *   fa_select_pages  the pages that fa_decode may restrict itself to.
+ * All three share the conventions above (device memory of the current device,
+ * asynchronous on `stream`, argument errors synchronous).  Their kernels read
+ * lengths and page ids on the device: an entry that they need and that is
+ * outside [0, num_pages), a length outside [0, max_pages * page_size], or a
+ * position without a row in the rotation tables leaves the keys or tokens
+ * concerned out (a sequence of such a length counts as empty and gets no
+ * tokens) and is reported as FA_ERR_INDEX by fa_check_status.  Entries
+ * of the page table past a sequence's last page are never read. */
+
+/* The cache (host struct).  Element (page, head, slot, d) of K is
+ *   k[page * k_stride_page + head * k_stride_head + slot * k_stride_slot + d],
+ * V alike; strides in elements, multiples of 8, positive where there is more
+ * than one to step over, below 2^38; bases 16-byte aligned.  Any order of page,
+ * head and slot is thus a cache (a [pages, slots, heads, D] pool, K and V halves
+ * of one pool) as long as no two tokens share memory.  page_size: 16, 32, 64, 128 or 256;
+ * max_pages entries per sequence, max_pages * page_size <= 2^31 - 65536.
+ * k_min / k_max: NULL, or [num_pages, Hkv, D] of the cache's type, contiguous,
+ * 16-byte aligned: per page and channel the least and largest stored key,
+ * written by fa_kv_append and read by fa_select_pages. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t k_stride_page, k_stride_head, k_stride_slot;
+  int64_t v_stride_page, v_stride_head, v_stride_slot;
+  void* k_min;
+  void* k_max;
+  const int32_t* page_table;
+  int64_t table_stride;
+  int32_t max_pages;
+  int32_t num_pages;
+  int32_t page_size;
+} fa_paged_kv_t;
+
+/* New tokens (host struct).  Element (b, h, i, d) of k, v (h < Hkv), q and
+ * q_out (h < Hq) at base[b * stride_b + h * stride_h + i * stride_s + d];
+ * strides in elements, >= 0, multiples of 8; bases 16-byte aligned.  q and
+ * q_out NULL: keys and values only.  q_out may be q itself (same strides).
+ * cos, sin: fp32 [max_pos, rot_dim / 2], contiguous, 16-byte aligned, row p the
+ * angles of position p; rot_dim a multiple of 16, 0 <= rot_dim <= D; 0 (tables
+ * NULL) rotates nothing.  interleaved 0: channel j < rot_dim / 2 turns with
+ * j + rot_dim / 2; 1: channel 2j with 2j + 1.  Channels >= rot_dim pass
+ * through. */
+typedef struct {
+  const void* k;
+  const void* v;
+  const void* q;
+  void* q_out;
+  int64_t k_stride_b, k_stride_h, k_stride_s;
+  int64_t v_stride_b, v_stride_h, v_stride_s;
+  int64_t q_stride_b, q_stride_h, q_stride_s;
+  int64_t qo_stride_b, qo_stride_h, qo_stride_s;
+  const float* cos;
+  const float* sin;
+  int32_t rot_dim;
+  int32_t interleaved;
+  int32_t max_pos;
+} fa_kv_new_t;
+
+/*
+ * fa_kv_append -- new tokens into the cache, rotated on the way.
+ *
+ * Token i of sequence b, i < n_b, takes position t = kv_lens[b] + i:
+ *   K page <- rotate(k, t), V page <- v, q_out <- rotate(q, t),
+ *   rotate(x, t)_a = x_a cos_t - x_b sin_t, rotate(x, t)_b = x_a sin_t + x_b cos_t
+ * for each pair of channels (a, b), in fp32, rounded once.
+ *   kv_lens   DEVICE int32[B]: tokens in the cache before the call (the caller
+ *             adds n_b afterwards);
+ *   new_lens  NULL (n_b = Snew), or DEVICE int32[B] with n_b in [0, Snew]; a
+ *             value outside is clamped and reported as FA_ERR_INDEX.  Tokens
+ *             i >= n_b are padding: nothing of them is read, and their rows of
+ *             q_out stay as they were.
+ * With k_min / k_max set, the bounds of every page that got a token are
+ * brought up to date from the keys as stored: anew for a page whose slot 0 was
+ * written, widened otherwise.
+ * No two appended tokens may share a page slot, nor two calls that overlap on
+ * the GPU a page.  D in {64, 128}; mask_mode: 0 (bf16) or FA_DTYPE_FP16, the
+ * type of the cache, k, v, q and q_out.  Allocates nothing.
+ */
+int fa_kv_append(const fa_paged_kv_t* kv, const fa_kv_new_t* x, int B, int Hq, int Hkv, int Snew,
+                 int D, int mask_mode, const int32_t* kv_lens, const int32_t* new_lens,
+                 void* stream);
+
+/*
+ * fa_decode -- attention of each sequence's Sq newest tokens over its pages.
+ *
+ *   q    [B, Hq, Sq, D], o [B, Hq, Sq, D], lse [B, Hq, Sq] fp32: contiguous, as fa_fwd
+ *   kv_lens  DEVICE int32[B]: tokens in the cache, the Sq newest included.
+ * Row i is the token t = kv_lens[b] - Sq + i and sees the keys j <= t (and, with
+ * pre_tokens >= 0, j >= t - pre_tokens; -1 is unbounded).  A row that sees no
+ * key (t < 0, an empty sequence) gets O = 0 and LSE = +inf.  Query head h reads
+ * KV head h / (Hq / Hkv).
+ *   page_idx  NULL (every page), or DEVICE int32 [B, Hkv, max_sel], contiguous:
+ *             only the listed pages (numbers p of the sequence's own pages, as
+ *             in the page table's columns) are read; an entry < 0 or past the
+ *             sequence's last page is an invalid slot; a page listed twice
+ *             counts twice.  1 <= max_sel <= 2^20.  Pages and the mask above
+ *             apply together.
+ * What lies in the cache at positions that no row of a sequence sees is never
+ * used and may be anything, NaN included; keys and values that some row sees
+ * must be finite.
+ * D in {64, 128}; mask_mode: 0 (bf16) or FA_DTYPE_FP16, the type of q, o and the
+ * cache.  P enters the value product as a hi + lo pair of that type.  The work
+ * is split over the cache's length; the pieces (fp32) go to stream-ordered
+ * scratch and are joined.  Results do not depend on what else runs.
+ */
+int fa_decode(const void* q, const fa_paged_kv_t* kv, void* o, float* lse, int B, int Hq, int Hkv,
+              int Sq, int D, float scale, int mask_mode, const int32_t* kv_lens, int pre_tokens,
+              const int32_t* page_idx, int max_sel, void* stream);
+
+/*
+ * fa_select_pages -- for every sequence and KV head, the pages whose keys can
+ * score highest: page p's score is the largest, over the group's rows r (query
+ * heads of the KV head times Sq), of
+ *   sum_d max(q_rd * k_min[p]_d, q_rd * k_max[p]_d),
+ * which no key of the page exceeds.  The `first` first and `last` last pages
+ * of a sequence are always chosen; of the others those of the largest scores,
+ * equal scores by the lower page number, until max_sel pages are listed or
+ * none is left.  page_idx [B, Hkv, max_sel] (DEVICE int32) gets the page
+ * numbers in ascending order, then -1.  The choice is that of scores in 64-bit
+ * arithmetic.  kv_lens as fa_decode; q [B, Hq, Sq, D] contiguous; q and the
+ * bounds must be finite.  first, last >= 0, first + last <= max_sel <= 2^20.
+ * Scratch: stream-ordered, 16 bytes per (sequence, KV head, page
+ * table column).
+ */
+int fa_select_pages(const void* q, const fa_paged_kv_t* kv, int32_t* page_idx, int B, int Hq,
+                    int Hkv, int Sq, int D, int mask_mode, const int32_t* kv_lens, int max_sel,
+                    int first, int last, void* stream);
+
 /* Synchronises `stream`, then returns and clears the device status word of
- * the current device: FA_OK, FA_ERR_DEVICE_TIMEOUT or FA_ERR_RANGE (the first
- * error seen since the last call), or FA_ERR_CUDA if the synchronisation
- * itself failed. */
+ * the current device: FA_OK, FA_ERR_DEVICE_TIMEOUT, FA_ERR_RANGE or
+ * FA_ERR_INDEX (in that order where several were seen since the last call), or
+ * FA_ERR_CUDA if the synchronisation itself failed. */
 int fa_check_status(void* stream);
 
 /* Sets the limit of every bounded on-chip wait (nanoseconds, default 2e9);
