@@ -1,96 +1,611 @@
 // fa_decode: attention of a sequence's newest tokens over its pages.
+//
+// Per KV head the G * Sq rows of a sequence (query heads of the group times new
+// tokens) share every key, so that a key and its value are read once and used
+// by all of them: 4 D flops per row against 4 D bytes, far below what the
+// tensor cores need to be the limit.  The kernel is a stream of K and V tiles
+// through shared memory at HBM speed with as little as possible beside it:
+//
+//   * one producer warp per SM looks up pages and copies tiles of 64 keys (K and
+//     V, 64 channels x up to 64 slots x D / 64 halves per TMA box, 128-byte
+//     swizzle) into a ring of 128 KB, more than twice what latency times
+//     bandwidth asks for;
+//   * eight consumer warps take 16 keys each (two teams of four warps take the
+//     tiles in turn), each with its own running maximum, sum and O of all
+//     rows, and meet only at the end of a unit;
+//   * products are transposed, S^T = K Q^T and O^T = V^T P^T, with the keys (then
+//     the channels) as the 16-row side of mma.m16n8k16 and the rows as its
+//     8-column side: 4 rows of a common group waste 4 of 8 columns there, but
+//     would waste 124 of the 128 lanes of a tcgen05 tile, whose accumulator
+//     also costs a round trip through TMEM before every exponential.  At
+//     8 to 32 rows the warp-level products stay hidden behind the copies;
+//   * P goes into the value product as hi + lo pairs of the cache's type (the
+//     tensor cores are idle, and a single bf16 P would add an error as large as
+//     the rounding of O).
+//
+// Work: a unit is one (sequence, KV head, group of up to 8 NT rows) with its
+// tiles.  All units' tiles in a row are cut into equal ranges, one per CTA, so
+// that ragged lengths and few long sequences fill the GPU alike; lengths are
+// read on the device.  A unit inside one range is finished there; the pieces of
+// a unit that several ranges share go to scratch (at most two per CTA, in fp32)
+// and fa_decode_join_kernel joins them in the order of the keys.
 #pragma once
 #include "fa_paged.cuh"
+#include "fa_tiled.cuh"   // bounded waits
 
 namespace fa {
 
+constexpr int kDecTile = 64;                          // keys per tile
+constexpr int kDecTeams = 2;
+constexpr int kDecWarps = 4 * kDecTeams;              // consumer warps; 16 keys of a tile each
+constexpr int kDecThreads = 32 * (kDecWarps + 1);     // and the producer
+
 struct DecodeParams {
+  CUtensorMap tm_k;   // (64 channels, slots, D / 64, heads, pages)
+  CUtensorMap tm_v;
   PagedKv kv;
   const uint16_t* q;
-  void* o;
+  uint16_t* o;
   float* lse;
   const int32_t* kv_lens;
-  const int32_t* sel;   // [B, Hkv, max_sel] or null
+  const int32_t* sel;          // [B, Hkv, max_sel] or null
   int max_sel;
-  int B, Hq, Hkv, G, Sq;
-  int pre_tokens;
+  int B, Hq, Hkv, Sq;
+  int rows;                    // G * Sq
+  int groups;                  // row groups per KV head
+  int pre_tokens;              // -1: unbounded
+  int min_tiles;               // least tiles worth a CTA
+  int ctas;
   float scale_log2;
+  float* part_o;               // [2 * ctas][8 NT][D], unnormalised
+  float2* part_ml;             // [2 * ctas][8 NT]: maximum (log2 units), sum
+  long long timeout_ns;
   int* status;
 };
 
-// One block per row: its four warps take the keys in turn, each with a running
-// maximum m, sum l and unnormalised O of its own, joined at the end.
-template <bool BF16, int D>
-__global__ void __launch_bounds__(128) fa_decode_row_kernel(const DecodeParams p) {
-  constexpr int E = D / 32;
-  __shared__ float s_o[4][D];
-  __shared__ float s_m[4], s_l[4];
-  const int i = blockIdx.x % p.Sq;
-  const int h = (blockIdx.x / p.Sq) % p.Hq;
-  const int b = blockIdx.x / p.Sq / p.Hq;
-  const int hk = h / p.G;
+template <int D, int NT>
+struct DecodeSmem {
+  static constexpr int kHalf = kDecTile * D * 2;                 // K or V of a tile
+  // A multiple of the teams: a stage then always belongs to the same team, which has seen every
+  // earlier phase of its barriers (a wait on a phase's parity also passes two phases too early).
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static_assert(kStages % kDecTeams == 0, "a stage must stay with one team");
+  static constexpr int kPitch = D + 4;                           // floats; rows 2t spread over the banks
+  static constexpr int kJoinOff = kStages * 2 * kHalf;
+  static constexpr int kQOff = kJoinOff + kDecWarps * 8 * kPitch * 4;
+  static constexpr int kQBytes = NT > 2 ? NT * (D / 16) * 32 * 8 : 0;
+  static constexpr int kMlOff = kQOff + kQBytes;                 // float2 [warps][8 NT]
+  static constexpr int kBarOff = kMlOff + kDecWarps * 8 * NT * 8;
+  static constexpr int kMetaOff = kBarOff + 2 * kStages * 8;     // int [stages][4]
+  static constexpr int kMiscOff = kMetaOff + kStages * 16;       // range, abort flag
+  static constexpr int kBytes = kMiscOff + 64;
+  static constexpr int kAlloc = kBytes + 1024;                   // slack for 1024-byte alignment
+};
+
+// Keys [lo, hi) that some row of a sequence sees, as tiles [first, first + n);
+// an empty sequence counts one tile, whose CTA writes the empty answer.
+struct DecodeSpan {
+  int lo, hi, first, n;
+};
+__device__ __forceinline__ DecodeSpan decode_span(const DecodeParams& p, int len) {
+  DecodeSpan s;
+  len = max(len, 0);
+  s.hi = len;
+  s.lo = p.pre_tokens >= 0 ? (int)max(0LL, (long long)len - p.Sq - p.pre_tokens) : 0;
+  if (p.sel) {
+    s.first = 0;
+    s.n = (int)((((long long)p.max_sel << p.kv.page_shift) + kDecTile - 1) / kDecTile);
+  } else {
+    s.first = s.lo / kDecTile;
+    s.n = max(1, (len + kDecTile - 1) / kDecTile - s.first);
+  }
+  return s;
+}
+__device__ __forceinline__ int decode_len(const DecodeParams& p, int b) {
+  const int len = p.kv_lens[b];
+  return len < 0 || len > (p.kv.max_pages << p.kv.page_shift) ? 0 : len;
+}
+
+// Tiles of all units, and of the sequences before b (whole warp).
+__device__ __forceinline__ long long decode_tiles_before(const DecodeParams& p, int b, int lane) {
+  long long sum = 0;
+  for (int i = lane; i < b; i += 32) sum += decode_span(p, decode_len(p, i)).n;
+#pragma unroll
+  for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+  return sum * p.Hkv * p.groups;
+}
+// CTAs that share `total` tiles, the first tile of CTA c's range, the CTA that has tile t.
+__device__ __forceinline__ int decode_ctas(const DecodeParams& p, long long total) {
+  return (int)min((long long)p.ctas, (total + p.min_tiles - 1) / p.min_tiles);
+}
+__device__ __forceinline__ long long decode_first(long long total, int n, int c) { return total * c / n; }
+__device__ __forceinline__ int decode_owner(long long total, int n, long long t) {
+  return (int)(((t + 1) * n - 1) / total);
+}
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, uint32_t bar, int slot,
+                                            int head, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %3, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(0), "r"(slot), "r"(head), "r"(page)
+      : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// 8x8 transpose of 16-bit values held two per lane
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// c (16 x 8, fp32) += a (16 x 16) b (16 x 8)
+template <bool BF16>
+__device__ __forceinline__ void mma_16x8(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool BF16, int D, int NT>
+__global__ void __launch_bounds__(kDecThreads, 1) fa_decode_kernel(const __grid_constant__ DecodeParams p) {
+  using SM = DecodeSmem<D, NT>;
+  constexpr int NS = SM::kStages;
+  constexpr int KS = D / 16;                   // 16-channel steps
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int len = max(0, paged_len(p.kv, p.kv_lens[b], p.status));
-  const int tok = len - p.Sq + i;
-  const int low = p.pre_tokens >= 0 ? max(0, tok - p.pre_tokens) : 0;
-  const int ps = 1 << p.kv.page_shift;
-  const int pages = (len + ps - 1) >> p.kv.page_shift;
-  const long long row = ((long long)b * p.Hq + h) * p.Sq + i;
-  float qv[E], o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const uint16_t x = p.q[row * D + lane * E + e];
-    qv[e] = lo16_f32<BF16>(x);
-    o[e] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  const int32_t* sel = p.sel ? p.sel + ((long long)b * p.Hkv + hk) * p.max_sel : nullptr;
-  const int n = sel ? p.max_sel : pages;
-  for (int s = 0; s < n; ++s) {
-    const int page = sel ? sel[s] : s;
-    if (page < 0 || page >= pages) continue;
-    const int k0 = page << p.kv.page_shift;
-    if (k0 > tok || k0 + ps <= low) continue;
-    const int id = paged_id(p.kv, b, page, p.status);
-    if (id < 0) continue;
-    for (int j = warp; j < ps; j += 4) {
-      if (k0 + j > tok || k0 + j < low) continue;
-      const uint16_t* kr = p.kv.k + (long long)id * p.kv.k_sp + hk * p.kv.k_sh + j * p.kv.k_ss + lane * E;
-      const uint16_t* vr = p.kv.v + (long long)id * p.kv.v_sp + hk * p.kv.v_sh + j * p.kv.v_ss + lane * E;
-      float x = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) x += qv[e] * lo16_f32<BF16>(kr[e]);
-#pragma unroll
-      for (int w = 16; w; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-      x *= p.scale_log2;
-      const float mn = fmaxf(m, x);
-      const float base = mn > -INFINITY ? mn : 0.f;
-      const float r = exp2f(m - base), e0 = exp2f(x - base);
-      l = l * r + e0;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * r + e0 * lo16_f32<BF16>(vr[e]);
-      m = mn;
+  auto FULL = [&](int s) { return sbase + SM::kBarOff + 8 * s; };
+  auto EMPTY = [&](int s) { return sbase + SM::kBarOff + 8 * (NS + s); };
+  int* s_meta = reinterpret_cast<int*>(smem + SM::kMetaOff);
+  long long* s_range = reinterpret_cast<long long*>(smem + SM::kMiscOff);   // start, end, tiles before s_b
+  int* s_b = reinterpret_cast<int*>(smem + SM::kMiscOff + 24);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + SM::kMiscOff + 28);
+
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(FULL(s), 1);
+      mbar_init(EMPTY(s), 4);
     }
+    fence_mbar_init();
+    *s_abort = 0;
   }
+  pdl_launch_dependents();
+  pdl_wait_prior();
+  if (warp == kDecWarps) {   // this CTA's range of tiles and the sequence it starts in
+    const long long total = decode_tiles_before(p, p.B, lane);
+    const int n = decode_ctas(p, total);
+    long long start = 0, end = 0;
+    if ((int)blockIdx.x < n) {
+      start = decode_first(total, n, blockIdx.x);
+      end = decode_first(total, n, blockIdx.x + 1);
+    }
+    // the last sequence with at most `start` tiles before it
+    long long before = 0;
+    int b = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      long long w = b0 + lane < p.B ? (long long)decode_span(p, decode_len(p, b0 + lane)).n * p.Hkv * p.groups : 0;
+      long long inc = w;
 #pragma unroll
-  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
-  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += x;
+      }
+      const unsigned in = __ballot_sync(0xffffffffu, b0 + lane < p.B && before + inc - w <= start);
+      const int last = 31 - __clz(in);               // lane 0 is in, or the search has ended
+      if (in) {
+        b = b0 + last;
+        if (lane == last) s_range[2] = before + inc - w;
+      }
+      if (in != 0xffffffffu) break;
+      before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) {
+      s_range[0] = start;
+      s_range[1] = end;
+      *s_b = b;
+    }
+    if (blockIdx.x == 0)     // lengths that the tables cannot hold are reported once
+      for (int i = lane; i < p.B; i += 32) (void)paged_len(p.kv, p.kv_lens[i], p.status);
+  }
   __syncthreads();
-  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  const float base = m > -INFINITY ? m : 0.f;
-  l = 0.f;
-  for (int w = 0; w < 4; ++w) l += s_l[w] * exp2f(s_m[w] - base);
-  if (threadIdx.x < D / 2) {
-    float a = 0.f, c = 0.f;
-    for (int w = 0; w < 4; ++w) {
-      const float f = exp2f(s_m[w] - base);
-      a += f * s_o[w][2 * threadIdx.x];
-      c += f * s_o[w][2 * threadIdx.x + 1];
+  const long long end = s_range[1];
+  const WaitCtx wc{s_abort, p.status, p.timeout_ns};
+  const int box_shift = min(p.kv.page_shift, 6);     // slots per copy
+  const int box = 1 << box_shift;
+
+  if (warp == kDecWarps) {
+    // ============================================================ producer
+    long long pos = s_range[0], before = s_range[2];
+    int b = *s_b;
+    int it = 0;
+    bool dead = false;
+    const int nsub = kDecTile >> box_shift;           // copies of K (and V) per tile
+    const uint32_t sub_bytes = (uint32_t)box * D * 2;
+    while (pos < end && !dead) {
+      const DecodeSpan s = decode_span(p, decode_len(p, b));
+      const long long mine = (long long)s.n * p.Hkv * p.groups;
+      const int unit = (int)((pos - before) / s.n), t0 = (int)((pos - before) % s.n);
+      const int hk = unit / p.groups;
+      const int nt = (int)min((long long)(s.n - t0), end - pos);
+      const int n_pages = (s.hi + (1 << p.kv.page_shift) - 1) >> p.kv.page_shift;
+      // Lane i looks up sub-block c0 + i of the unit (box keys each): page, first slot, first key.
+      auto look_up = [&](int c, int& id, int& slot, int& key) {
+        id = -1, slot = 0, key = -1;
+        if (c >= (t0 + nt) * nsub) return;
+        int page;
+        if (p.sel) {
+          const int spp = p.kv.page_shift - box_shift;    // log2 sub-blocks per page
+          const int at = c >> spp;
+          if (at >= p.max_sel) return;
+          page = p.sel[((long long)b * p.Hkv + hk) * p.max_sel + at];
+          if (page < 0 || page >= n_pages) return;
+          slot = (c & ((1 << spp) - 1)) << box_shift;
+          key = (page << p.kv.page_shift) + slot;
+        } else {
+          key = s.first * kDecTile + (c << box_shift);
+          page = key >> p.kv.page_shift;
+          slot = key & ((1 << p.kv.page_shift) - 1);
+        }
+        if (key >= s.hi || key + box <= s.lo) {           // (also any key of an empty sequence)
+          key = -1;
+          return;
+        }
+        id = paged_id(p.kv, b, page, p.status);
+        if (id < 0) key = -1;
+      };
+      int id, slot, key, id2 = -1, slot2 = 0, key2 = -1;
+      const int per = 32 / nsub;                          // tiles per look-up
+      look_up(t0 * nsub + lane, id, slot, key);
+      for (int j = 0; j < nt; ++j, ++it) {
+        const int in = j % per;
+        if (in == 0 && j) id = id2, slot = slot2, key = key2;
+        const int st = it % NS;
+        bool ok = true;
+        if (lane == 0 && it >= NS) ok = wait_bar(EMPTY(st), (it / NS - 1) & 1, wc);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) {
+          dead = true;
+          break;
+        }
+        const int sub = lane - in * nsub;
+        const bool holder = sub >= 0 && sub < nsub;
+        const unsigned live = __ballot_sync(0xffffffffu, holder && id >= 0);
+        if (holder) s_meta[st * 4 + sub] = key;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(FULL(st), 2u * sub_bytes * __popc(live));
+        __syncwarp();
+        if (holder && id >= 0) {
+          const uint32_t dst = sbase + (uint32_t)st * 2 * SM::kHalf + (uint32_t)sub * sub_bytes;
+          tma_load_5d(dst, &p.tm_k, FULL(st), slot, hk, id);
+          tma_load_5d(dst + SM::kHalf, &p.tm_v, FULL(st), slot, hk, id);
+        }
+        // the next look-up, a look-up's tiles ahead of its use
+        if (in == 0) look_up((t0 + j + per) * nsub + lane, id2, slot2, key2);
+      }
+      pos += nt;
+      if (pos >= before + mine) {
+        before += mine;
+        ++b;
+      }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    reinterpret_cast<uint32_t*>(p.o)[(row * D) / 2 + threadIdx.x] = pack16x2<BF16>(a * inv, c * inv);
+    // after an expired wait: copies in flight land before the CTA ends
+    if (dead && lane == 0)
+      for (int i = max(0, it - NS); i < it; ++i) drain_bar(FULL(i % NS), (i / NS) & 1, wc.timeout);
+    return;
   }
-  if (threadIdx.x == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : INFINITY;
+
+  // ============================================================ consumers
+  const int team = warp >> 2, quarter = warp & 3;
+  const int g = lane >> 2, t4 = lane & 3;
+  float* s_join = reinterpret_cast<float*>(smem + SM::kJoinOff);
+  uint2* s_q = reinterpret_cast<uint2*>(smem + SM::kQOff);
+  float2* s_ml = reinterpret_cast<float2*>(smem + SM::kMlOff);
+  // this lane's row of each ldmatrix: keys as stored (K), keys and channel halves (V, transposed)
+  const int sub = (16 * quarter) >> box_shift;
+  const int r0 = (16 * quarter) & (box - 1);
+  const uint32_t sub_off = (uint32_t)sub * box * D * 2;
+  const int krow = r0 + (lane & 15), kcol = lane >> 4;
+  const int vrow = r0 + (lane & 7) + ((lane >> 4) << 3), vcol = (lane >> 3) & 1;
+  auto at = [&](int row, int chunk) {   // 16-byte chunk `chunk` of a row: half, swizzled place
+    return (uint32_t)(chunk >> 3) * (uint32_t)(box * 128) + (uint32_t)row * 128 +
+           (uint32_t)(((chunk & 7) ^ (row & 7)) << 4);
+  };
+
+  long long pos = s_range[0], before = s_range[2];
+  int b = *s_b;
+  int it = 0;
+  bool dead = false;
+  for (int seg = 0; pos < end; ++seg) {
+    const int len = decode_len(p, b);
+    const DecodeSpan s = decode_span(p, len);
+    const long long mine = (long long)s.n * p.Hkv * p.groups;
+    const int unit = (int)((pos - before) / s.n), t0 = (int)((pos - before) % s.n);
+    const int hk = unit / p.groups, rg = unit % p.groups;
+    const int nt = (int)min((long long)(s.n - t0), end - pos);
+    const long long row0 = (long long)b * p.Hq * p.Sq + (long long)hk * p.rows + rg * 8 * NT;
+    const int rows = min(8 * NT, p.rows - rg * 8 * NT);
+
+    // Q as the B operand: lane (g, t4) holds row g, channels 2 t4, 2 t4 + 1 and + 8 of every step
+    uint2 qf[NT > 2 ? 1 : NT][NT > 2 ? 1 : KS];
+    if constexpr (NT > 2) {
+      named_sync(1, 32 * kDecWarps);    // the last unit's reads of s_q are done
+      for (int i = warp; i < NT * KS; i += kDecWarps) {
+        const int row = (i / KS) * 8 + g;
+        const uint32_t* x = reinterpret_cast<const uint32_t*>(p.q + (row0 + row) * D + (i % KS) * 16) + t4;
+        s_q[i * 32 + lane] = row < rows ? make_uint2(x[0], x[4]) : make_uint2(0, 0);
+      }
+      named_sync(1, 32 * kDecWarps);
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int row = n * 8 + g;
+        const uint32_t* x = reinterpret_cast<const uint32_t*>(p.q + (row0 + row) * D) + t4;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) qf[n][k] = row < rows ? make_uint2(x[8 * k], x[8 * k + 4]) : make_uint2(0, 0);
+      }
+    }
+    // this lane's rows as columns of S^T and O^T: 2 t4, 2 t4 + 1 of every 8; their tokens
+    int tok[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) tok[n][e] = len - p.Sq + (rg * 8 * NT + n * 8 + 2 * t4 + e) % p.Sq;
+    const int tok_min = len - p.Sq;
+    const int low_max = p.pre_tokens >= 0 ? len - 1 - p.pre_tokens : 0;   // lowest key that all rows see
+
+    float o[NT][KS][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][k][e] = 0.f;
+    }
+
+    for (int j = (it & 1) ^ team; j < nt; j += 2) {
+      if (dead) break;
+      const int i = it + j, st = i % NS;
+      if (!wait_bar(FULL(st), (i / NS) & 1, wc)) {
+        dead = true;
+        break;
+      }
+      const int kb = s_meta[st * 4 + sub];
+      const int key0 = kb + r0;
+      // (kb < 0: no such keys, and nothing was copied)
+      if (kb >= 0 && key0 < s.hi && key0 + 16 > s.lo) {
+        const uint32_t kbase = sbase + (uint32_t)st * 2 * SM::kHalf + sub_off;
+        float c[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          uint32_t a[4];
+          ldmatrix4(kbase + at(krow, 2 * k + kcol), a);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint2 x = NT > 2 ? s_q[(n * KS + k) * 32 + lane] : qf[NT > 2 ? 0 : n][NT > 2 ? 0 : k];
+            mma_16x8<BF16>(c[n], a, x.x, x.y);
+          }
+        }
+        // scores in log2 units; lane (g, t4): keys g (c0, c1) and g + 8 (c2, c3), rows 2 t4, 2 t4 + 1
+        const bool all = key0 + 15 <= tok_min && key0 >= low_max;
+        uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[n][e] *= p.scale_log2;
+          if (!all) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + g + 8 * (e >> 1), t = tok[n][e & 1];
+              if (key > t || (p.pre_tokens >= 0 && key < t - p.pre_tokens)) c[n][e] = -INFINITY;
+            }
+          }
+          float mx[2] = {fmaxf(c[n][0], c[n][2]), fmaxf(c[n][1], c[n][3])};
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) {
+            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], w));
+            mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], w));
+          }
+          if (__any_sync(0xffffffffu, mx[0] > m[n][0] || mx[1] > m[n][1])) {   // a larger maximum
+            float f[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float mn = fmaxf(m[n][e], mx[e]);
+              f[e] = mn > -INFINITY ? ex2_approx(m[n][e] - mn) : 1.f;
+              m[n][e] = mn;
+              l[n][e] *= f[e];
+            }
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              o[n][k][0] *= f[0];
+              o[n][k][1] *= f[1];
+              o[n][k][2] *= f[0];
+              o[n][k][3] *= f[1];
+            }
+          }
+          const float b0 = m[n][0] > -INFINITY ? m[n][0] : 0.f, b1 = m[n][1] > -INFINITY ? m[n][1] : 0.f;
+          const float p0 = ex2_approx(c[n][0] - b0), p1 = ex2_approx(c[n][1] - b1);
+          const float p2 = ex2_approx(c[n][2] - b0), p3 = ex2_approx(c[n][3] - b1);
+          l[n][0] += p0 + p2;
+          l[n][1] += p1 + p3;
+          const uint32_t h0 = pack16x2<BF16>(p0, p1), h1 = pack16x2<BF16>(p2, p3);
+          ph[n][0] = transpose8(h0);
+          ph[n][1] = transpose8(h1);
+          pl[n][0] = transpose8(pack_residual_x2(p0, p1, h0, BF16));
+          pl[n][1] = transpose8(pack_residual_x2(p2, p3, h1, BF16));
+        }
+        // keys that no row sees have P = 0, and their V may hold anything: it becomes 0 too
+        const bool whole = key0 >= s.lo && key0 + 16 <= s.hi;
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;   // keys 2 t4, 2 t4 + 1 and + 8
+        if (!whole) {
+          auto seen = [&](int k) { return key0 + k >= s.lo && key0 + k < s.hi; };
+          keep0 = (seen(2 * t4) ? 0xffffu : 0u) | (seen(2 * t4 + 1) ? 0xffff0000u : 0u);
+          keep1 = (seen(2 * t4 + 8) ? 0xffffu : 0u) | (seen(2 * t4 + 9) ? 0xffff0000u : 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          uint32_t a[4];
+          ldmatrix4_trans(kbase + SM::kHalf + at(vrow, 2 * k + vcol), a);
+          if (!whole) {
+            a[0] &= keep0;
+            a[1] &= keep0;
+            a[2] &= keep1;
+            a[3] &= keep1;
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_16x8<BF16>(o[n][k], a, ph[n][0], ph[n][1]);
+            mma_16x8<BF16>(o[n][k], a, pl[n][0], pl[n][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(EMPTY(st));
+    }
+    it += nt;
+
+    // ---- join the eight warps' pieces of the unit
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], w);
+        if (g == 0) s_ml[warp * 8 * NT + n * 8 + 2 * t4 + e] = make_float2(m[n][e], l[n][e]);
+      }
+    }
+    named_sync(1, 32 * kDecWarps);
+    const bool direct = t0 == 0 && nt == s.n;
+    const long long slot = 2LL * blockIdx.x + (seg ? 1 : 0);
+    const int tid = threadIdx.x;                 // < 256
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, s_ml[w * 8 * NT + n * 8 + 2 * t4 + e].x);
+        const float f = m[n][e] > -INFINITY ? ex2_approx(m[n][e] - top) : 0.f;
+        float* dst = s_join + (warp * 8 + 2 * t4 + e) * SM::kPitch + g;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          dst[16 * k] = o[n][k][e] * f;
+          dst[16 * k + 8] = o[n][k][e + 2] * f;
+        }
+      }
+      named_sync(1, 32 * kDecWarps);
+      const int r = tid / (D / 4), d = 4 * (tid % (D / 4));
+      if (r < 8 && n * 8 + r < rows) {
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, s_ml[w * 8 * NT + n * 8 + r].x);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) {
+          const float2 ml = s_ml[w * 8 * NT + n * 8 + r];
+          sum += ml.x > -INFINITY ? ml.y * ex2_approx(ml.x - top) : 0.f;
+          const float4 y = *reinterpret_cast<const float4*>(s_join + (w * 8 + r) * SM::kPitch + d);
+          x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        }
+        if (direct) {
+          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          *reinterpret_cast<uint2*>(p.o + (row0 + n * 8 + r) * D + d) =
+              make_uint2(pack16x2<BF16>(x.x * inv, x.y * inv), pack16x2<BF16>(x.z * inv, x.w * inv));
+          if (d == 0) p.lse[row0 + n * 8 + r] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : INFINITY;
+        } else {
+          const long long at_row = slot * (8 * NT) + n * 8 + r;
+          *reinterpret_cast<float4*>(p.part_o + at_row * D + d) = x;
+          if (d == 0) p.part_ml[at_row] = make_float2(top, sum);
+        }
+      }
+      named_sync(1, 32 * kDecWarps);
+    }
+    pos += nt;
+    if (pos >= before + mine) {
+      before += mine;
+      ++b;
+    }
+  }
+}
+
+// Joins the pieces of the units that several CTAs shared, one warp per row: the
+// schedule is computed anew from the lengths, the pieces summed in the order of
+// the keys (the same bits every time).
+template <bool BF16, int D>
+__global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_constant__ DecodeParams p, int rows8) {
+  pdl_launch_dependents();
+  pdl_wait_prior();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * 8 + warp;
+  const long long per_b = (long long)p.Hq * p.Sq;
+  if (row >= per_b * p.B) return;
+  const int b = (int)(row / per_b);
+  const int in_b = (int)(row % per_b);
+  const int hk = in_b / p.rows, r = in_b % p.rows;
+  const int rg = r / rows8, rr = r % rows8;
+  const long long total = decode_tiles_before(p, p.B, lane);
+  const int ctas = decode_ctas(p, total);
+  const int n = decode_span(p, decode_len(p, b)).n;
+  const long long t0 = decode_tiles_before(p, b, lane) + (long long)(hk * p.groups + rg) * n;
+  const int c0 = decode_owner(total, ctas, t0), c1 = decode_owner(total, ctas, t0 + n - 1);
+  if (c0 == c1) return;          // finished by its CTA
+  // CTA c0's piece is its last one unless its range starts with the unit; the others start inside it
+  const long long first = 2LL * c0 + (decode_first(total, ctas, c0) == t0 ? 0 : 1);
+  auto at = [&](int c) { return (c == c0 ? first : 2LL * c) * rows8 + rr; };
+  float m = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[at(c)].x);
+#pragma unroll
+  for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+  const float top = m > -INFINITY ? m : 0.f;
+  constexpr int E = D / 32;
+  float o[E], l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const long long a = at(c);
+    const float2 ml = p.part_ml[a];
+    const float f = ml.x > -INFINITY ? ex2_approx(ml.x - top) : 0.f;
+    l += ml.y * f;
+    float x[E];
+    if constexpr (E == 4) {
+      const float4 y = *reinterpret_cast<const float4*>(p.part_o + a * D + 4 * lane);
+      x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+    } else {
+      const float2 y = *reinterpret_cast<const float2*>(p.part_o + a * D + 2 * lane);
+      x[0] = y.x, x[1] = y.y;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fmaf(f, x[e], o[e]);
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D) + (E / 2) * lane;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) dst[e / 2] = pack16x2<BF16>(o[e] * inv, o[e + 1] * inv);
+  if (lane == 0) p.lse[row] = l > 0.f ? (top + log2f(l)) * 0.6931471805599453f : INFINITY;
 }
 
 }  // namespace fa

@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <mutex>
 
 #include "../../include/fa_fwd.h"
 #include "fa_decode.cuh"
@@ -80,6 +81,67 @@ fa::PagedKv device_cache(const fa_paged_kv_t* kv) {
 template <bool BF16, int D>
 cudaError_t launch_append(const fa::AppendParams& p, unsigned grid, cudaStream_t st) {
   return launch_dependent(fa::fa_kv_append_kernel<BF16, D>, grid, fa::kAppendThreads, 0, st, p);
+}
+
+// 5-D view (64 channels, slots, D / 64, heads, pages) of a pool, in boxes of
+// one page's and head's `box` slots with all channels, 128-byte swizzle: in
+// shared memory [D / 64][box][64].
+bool encode_pool(CUtensorMap* tm, const void* base, bool fp16, int D, int Hkv, const fa_paged_kv_t* kv,
+                 int64_t s_page, int64_t s_head, int64_t s_slot, int box) {
+  auto enc = fa_host::tensor_map_encoder();
+  if (!enc) return false;
+  // a stride over a single head or page is never stepped; it only has to be valid
+  if (Hkv == 1) s_head = 64;
+  if (kv->num_pages == 1) s_page = 64;
+  cuuint64_t dims[5] = {64, (cuuint64_t)kv->page_size, (cuuint64_t)(D / 64), (cuuint64_t)Hkv,
+                        (cuuint64_t)kv->num_pages};
+  cuuint64_t strides[4] = {(cuuint64_t)s_slot * 2, 128, (cuuint64_t)s_head * 2, (cuuint64_t)s_page * 2};
+  cuuint32_t boxes[5] = {64, (cuuint32_t)box, (cuuint32_t)(D / 64), 1, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return enc(tm, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+             const_cast<void*>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool BF16, int D, int NT>
+int launch_decode(fa::DecodeParams& p, long long most_tiles, cudaStream_t st) {
+  auto kern = fa::fa_decode_kernel<BF16, D, NT>;
+  constexpr int smem = fa::DecodeSmem<D, NT>::kAlloc;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  static std::once_flag once[64];
+  static cudaError_t attr_err[64];
+  std::call_once(once[dev & 63], [&] {
+    attr_err[dev & 63] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
+  if (attr_err[dev & 63] != cudaSuccess) return cuda_fail(attr_err[dev & 63]);
+  const int sms = fa_host::sm_count();
+  if (sms <= 0) return cuda_fail(cudaErrorInvalidDevice);
+  p.ctas = (int)std::min<long long>(sms, most_tiles);
+  const size_t o_bytes = (size_t)2 * p.ctas * 8 * NT * D * 4;
+  void* scratch = fa_host::scratch_alloc(o_bytes + (size_t)2 * p.ctas * 8 * NT * 8, st);
+  if (!scratch) return cuda_fail(cudaGetLastError());
+  p.part_o = static_cast<float*>(scratch);
+  p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(scratch) + o_bytes);
+  cudaError_t e = launch_dependent(kern, (unsigned)p.ctas, fa::kDecThreads, smem, st, p);
+  if (e == cudaSuccess) {
+    const long long rows = (long long)p.B * p.Hq * p.Sq;
+    e = launch_dependent(fa::fa_decode_join_kernel<BF16, D>, (unsigned)((rows + 7) / 8), 256, 0, st, p, 8 * NT);
+  }
+  cudaFreeAsync(scratch, st);
+  return e == cudaSuccess ? FA_OK : cuda_fail(e);
+}
+
+template <bool BF16, int D>
+int launch_decode_rows(fa::DecodeParams& p, long long tiles_per_unit, cudaStream_t st) {
+  // as few columns as hold the rows; more than 32 rows go in groups that read the keys again
+  const int nt = p.rows <= 8 ? 1 : p.rows <= 16 ? 2 : 4;
+  p.groups = (p.rows + 8 * nt - 1) / (8 * nt);
+  const long long most = tiles_per_unit * p.B * p.Hkv * p.groups;
+  return nt == 1 ? launch_decode<BF16, D, 1>(p, most, st)
+         : nt == 2 ? launch_decode<BF16, D, 2>(p, most, st)
+                   : launch_decode<BF16, D, 4>(p, most, st);
 }
 
 }  // namespace
@@ -174,9 +236,14 @@ int fa_decode(const void* q, const fa_paged_kv_t* kv, void* o, float* lse, int B
   if (rows > 0x7FFFFFFFLL) return FA_ERR_SHAPE;
   fa::DecodeParams p;
   std::memset(&p, 0, sizeof(p));
+  const bool fp16 = (mask_mode & FA_DTYPE_FP16) != 0;
+  const int box = std::min(kv->page_size, fa::kDecTile);
+  if (!encode_pool(&p.tm_k, kv->k, fp16, D, Hkv, kv, kv->k_stride_page, kv->k_stride_head, kv->k_stride_slot, box) ||
+      !encode_pool(&p.tm_v, kv->v, fp16, D, Hkv, kv, kv->v_stride_page, kv->v_stride_head, kv->v_stride_slot, box))
+    return cuda_fail(cudaErrorInvalidValue);
   p.kv = device_cache(kv);
   p.q = static_cast<const uint16_t*>(q);
-  p.o = o;
+  p.o = static_cast<uint16_t*>(o);
   p.lse = lse;
   p.kv_lens = kv_lens;
   p.sel = page_idx;
@@ -184,23 +251,21 @@ int fa_decode(const void* q, const fa_paged_kv_t* kv, void* o, float* lse, int B
   p.B = B;
   p.Hq = Hq;
   p.Hkv = Hkv;
-  p.G = Hq / Hkv;
   p.Sq = Sq;
+  p.rows = Hq / Hkv * Sq;
   p.pre_tokens = pre_tokens;
+  p.min_tiles = 1;
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.timeout_ns = fa_host::wait_timeout_ns();
   p.status = fa_host::status_ptr();
   if (!p.status) return cuda_fail(cudaGetLastError());
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool fp16 = (mask_mode & FA_DTYPE_FP16) != 0;
-  if (D == 128) {
-    if (fp16) fa::fa_decode_row_kernel<false, 128><<<(unsigned)rows, 128, 0, st>>>(p);
-    else fa::fa_decode_row_kernel<true, 128><<<(unsigned)rows, 128, 0, st>>>(p);
-  } else {
-    if (fp16) fa::fa_decode_row_kernel<false, 64><<<(unsigned)rows, 128, 0, st>>>(p);
-    else fa::fa_decode_row_kernel<true, 64><<<(unsigned)rows, 128, 0, st>>>(p);
-  }
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? FA_OK : cuda_fail(e);
+  // the most tiles that a unit can have: the lengths are known on the device only
+  const long long keys = (long long)(page_idx ? max_sel : kv->max_pages) * kv->page_size;
+  const long long tiles = (keys + fa::kDecTile - 1) / fa::kDecTile;
+  if (D == 128)
+    return fp16 ? launch_decode_rows<false, 128>(p, tiles, st) : launch_decode_rows<true, 128>(p, tiles, st);
+  return fp16 ? launch_decode_rows<false, 64>(p, tiles, st) : launch_decode_rows<true, 64>(p, tiles, st);
 }
 
 int fa_select_pages(const void* q, const fa_paged_kv_t* kv, int32_t* page_idx, int B, int Hq,

@@ -262,8 +262,8 @@ def _check(got_o, got_l, ref, dtype, where=""):
     lim = (2 * es + 2.0 ** -20 * X + 2.0 ** -15)[..., None] * A + (u + 2.0 ** -20) * np.abs(O) + SUB[dtype]
     err = np.abs(o - O)
     assert (err <= lim).all(), f"{where}: O off by {(err / np.maximum(lim, 1e-30)).max():.3g} of its bound"
-    le = np.abs(l - L)[~empty]
-    ll = (es + 2.0 ** -21 * X + 2.0 ** -20 * (1 + np.abs(np.where(empty, 0, L))))[~empty]
+    le = np.abs(l[~empty] - L[~empty])
+    ll = (es + 2.0 ** -21 * X)[~empty] + 2.0 ** -20 * (1 + np.abs(L[~empty]))
     assert (le <= ll).all(), f"{where}: LSE off by {(le / ll).max():.3g} of its bound"
 
 
@@ -334,6 +334,29 @@ def test_decode_listed_pages(dtype, B, Hq, Hkv, D, page, Sq, lens, sel):
     o, l = fa.flash_attention_decode(_dev(q, dtype), c.obj, c.ints(lens), page_idx=_dev(idx))
     assert _status() == 0
     _check(o, l, P.decode(q, c.k, c.v, c.table, lens, 1 / math.sqrt(D), None, idx), dtype)
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,page,Sq,pre,sel", [
+    ("bf16", 8, 4, 128, 64, 1, None, 0), ("fp16", 6, 6, 64, 16, 1, None, 0), ("bf16", 12, 1, 128, 32, 1, None, 0),
+    ("bf16", 20, 2, 128, 16, 2, None, 0), ("fp16", 8, 4, 128, 256, 5, 300, 0), ("bf16", 8, 4, 64, 64, 1, None, 7),
+    ("fp16", 32, 2, 64, 128, 3, None, 0),
+])
+def test_decode_many_units_per_block(dtype, Hq, Hkv, D, page, Sq, pre, sel):
+    """70 sequences of mixed lengths: every block of the grid takes several
+    units, whole ones and pieces of shared ones, many tiles each."""
+    import attention_forward_fa_gb300 as fa
+    rng = np.random.default_rng(20)
+    lens = [int(x) for x in rng.integers(0, 1500, 70)]
+    lens[3], lens[40], lens[69] = 0, 1, 2900
+    c = Cache(21, dtype, 70, Hkv, D, page, lens)
+    q = _round(c.rng.standard_normal((70, Hq, Sq, D)), dtype)
+    idx = None
+    if sel:
+        idx = np.sort(c.rng.integers(-3, c.table.shape[1], (70, Hkv, sel)).astype(np.int32), -1)
+    o, l = fa.flash_attention_decode(_dev(q, dtype), c.obj, c.ints(lens), pre_tokens=pre,
+                                     page_idx=None if idx is None else _dev(idx))
+    assert _status() == 0
+    _check(o, l, P.decode(q, c.k, c.v, c.table, lens, D ** -0.5, pre, idx), dtype)
 
 
 def test_decode_leaves_out_bad_pages():
