@@ -144,6 +144,22 @@ int launch_decode_rows(fa::DecodeParams& p, long long tiles_per_unit, cudaStream
                    : launch_decode<BF16, D, 4>(p, most, st);
 }
 
+template <bool BF16, int D>
+int launch_select(fa::SelectParams& p, long long units, cudaStream_t st) {
+  const size_t pages = (size_t)units * p.kv.max_pages;
+  uint8_t* scratch = static_cast<uint8_t*>(fa_host::scratch_alloc(pages * 16, st));
+  if (!scratch) return cuda_fail(cudaGetLastError());
+  p.score = reinterpret_cast<float2*>(scratch);
+  p.near = reinterpret_cast<int32_t*>(scratch + pages * 8);
+  p.mark = reinterpret_cast<int32_t*>(scratch + pages * 12);
+  cudaError_t e = launch_dependent(fa::fa_page_score_kernel<BF16, D>, (unsigned)(units * p.chunks),
+                                   32 * fa::kScoreWarps, 0, st, p);
+  if (e == cudaSuccess)
+    e = launch_dependent(fa::fa_select_kernel<BF16, D>, (unsigned)units, fa::kSelectThreads, 0, st, p);
+  cudaFreeAsync(scratch, st);
+  return e == cudaSuccess ? FA_OK : cuda_fail(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -288,28 +304,18 @@ int fa_select_pages(const void* q, const fa_paged_kv_t* kv, int32_t* page_idx, i
   p.kv_lens = kv_lens;
   p.Hq = Hq;
   p.Hkv = Hkv;
-  p.G = Hq / Hkv;
-  p.Sq = Sq;
+  p.rows = Hq / Hkv * Sq;
   p.max_sel = max_sel;
   p.first = first;
   p.last = last;
+  p.chunks = (kv->max_pages + fa::kScorePages - 1) / fa::kScorePages;
+  if (units * p.chunks > 0x7FFFFFFFLL) return FA_ERR_SHAPE;
   p.status = fa_host::status_ptr();
   if (!p.status) return cuda_fail(cudaGetLastError());
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const size_t bytes = (size_t)units * kv->max_pages * 8;
-  p.score = static_cast<double*>(fa_host::scratch_alloc(bytes, st));
-  if (!p.score) return cuda_fail(cudaGetLastError());
   const bool fp16 = (mask_mode & FA_DTYPE_FP16) != 0;
-  if (D == 128) {
-    if (fp16) fa::fa_select_kernel<false, 128><<<(unsigned)units, fa::kSelectThreads, 0, st>>>(p);
-    else fa::fa_select_kernel<true, 128><<<(unsigned)units, fa::kSelectThreads, 0, st>>>(p);
-  } else {
-    if (fp16) fa::fa_select_kernel<false, 64><<<(unsigned)units, fa::kSelectThreads, 0, st>>>(p);
-    else fa::fa_select_kernel<true, 64><<<(unsigned)units, fa::kSelectThreads, 0, st>>>(p);
-  }
-  const cudaError_t e = cudaGetLastError();
-  cudaFreeAsync(p.score, st);
-  return e == cudaSuccess ? FA_OK : cuda_fail(e);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return D == 128 ? (fp16 ? launch_select<false, 128>(p, units, st) : launch_select<true, 128>(p, units, st))
+                  : (fp16 ? launch_select<false, 64>(p, units, st) : launch_select<true, 64>(p, units, st));
 }
 
 }  // extern "C"

@@ -502,7 +502,7 @@ int fa_decode(const void* q, const fa_paged_kv_t* kv, void* o, float* lse, int B
  * none is left.  page_idx [B, Hkv, max_sel] (DEVICE int32) gets the page
  * numbers in ascending order, then -1.  The choice is that of scores in 64-bit
  * arithmetic.  kv_lens as fa_decode; q [B, Hq, Sq, D] contiguous; q and the
- * bounds must be finite.  first, last >= 0, first + last <= max_sel <= 2^20.
+ * bounds of a sequence's pages must be finite, k_min <= k_max.  first, last >= 0, first + last <= max_sel <= 2^20.
  * Scratch: stream-ordered, 16 bytes per (sequence, KV head, page
  * table column).
  */
