@@ -6,13 +6,13 @@
 // tensor cores need to be the limit.  The kernel is a stream of K and V tiles
 // through shared memory at HBM speed with as little as possible beside it:
 //
-//   * one producer warp per SM looks up pages and copies tiles of 64 keys (K and
-//     V, 64 channels x up to 64 slots x D / 64 halves per TMA box, 128-byte
-//     swizzle) into a ring of 128 KB, more than twice what latency times
-//     bandwidth asks for;
-//   * eight consumer warps take 16 keys each (two teams of four warps take the
-//     tiles in turn), each with its own running maximum, sum and O of all
-//     rows, and meet only at the end of a unit;
+//   * a CTA is one producer warp and four consumer warps, two CTAs per SM: while
+//     one joins its warps' results and starts the next unit the other streams;
+//   * the producer looks up pages and copies tiles of 64 keys (K and V, 64
+//     channels x up to 64 slots x D / 64 halves per TMA box, 128-byte swizzle)
+//     into a ring of 96 KB, 192 KB per SM: four times latency times bandwidth;
+//   * each consumer takes 16 keys of every tile with a running maximum, sum and
+//     O of all rows of its own; they meet only at the end of a unit;
 //   * products are transposed, S^T = K Q^T and O^T = V^T P^T, with the keys (then
 //     the channels) as the 16-row side of mma.m16n8k16 and the rows as its
 //     8-column side: 4 rows of a common group waste 4 of 8 columns there, but
@@ -24,11 +24,12 @@
 //     the rounding of O).
 //
 // Work: a unit is one (sequence, KV head, group of up to 8 NT rows) with its
-// tiles.  All units' tiles in a row are cut into equal ranges, one per CTA, so
-// that ragged lengths and few long sequences fill the GPU alike; lengths are
-// read on the device.  A unit inside one range is finished there; the pieces of
-// a unit that several ranges share go to scratch (at most two per CTA, in fp32)
-// and fa_decode_join_kernel joins them in the order of the keys.
+// tiles and a charge of kUnitTiles for what it costs by itself.  All units in a
+// row are cut into equal ranges, one per CTA, so that ragged lengths and few
+// long sequences fill the GPU alike; lengths are read on the device.  A unit
+// inside one range is finished there; the pieces of a unit that several ranges
+// share go to scratch (at most two per CTA, in fp32) and fa_decode_join_kernel
+// joins them in the order of the keys.
 #pragma once
 #include "fa_paged.cuh"
 #include "fa_tiled.cuh"   // bounded waits
@@ -36,9 +37,10 @@
 namespace fa {
 
 constexpr int kDecTile = 64;                          // keys per tile
-constexpr int kDecTeams = 2;
-constexpr int kDecWarps = 4 * kDecTeams;              // consumer warps; 16 keys of a tile each
+constexpr int kDecWarps = 4;                          // consumer warps, 16 keys of a tile each
+constexpr int kDecCtasPerSm = 2;
 constexpr int kDecThreads = 32 * (kDecWarps + 1);     // and the producer
+constexpr int kUnitTiles = 1;                         // a unit's own cost, in tiles
 
 struct DecodeParams {
   CUtensorMap tm_k;   // (64 channels, slots, D / 64, heads, pages)
@@ -54,10 +56,9 @@ struct DecodeParams {
   int rows;                    // G * Sq
   int groups;                  // row groups per KV head
   int pre_tokens;              // -1: unbounded
-  int min_tiles;               // least tiles worth a CTA
   int ctas;
   float scale_log2;
-  float* part_o;               // [2 * ctas][8 NT][D], unnormalised
+  float* part_o;               // [2 * ctas][8 NT][D], unnormalised: slot 2 c + 1 begins its unit
   float2* part_ml;             // [2 * ctas][8 NT]: maximum (log2 units), sum
   long long timeout_ns;
   int* status;
@@ -66,12 +67,12 @@ struct DecodeParams {
 template <int D, int NT>
 struct DecodeSmem {
   static constexpr int kHalf = kDecTile * D * 2;                 // K or V of a tile
-  // A multiple of the teams: a stage then always belongs to the same team, which has seen every
-  // earlier phase of its barriers (a wait on a phase's parity also passes two phases too early).
-  static constexpr int kStages = D == 128 ? 4 : 8;
-  static_assert(kStages % kDecTeams == 0, "a stage must stay with one team");
-  static constexpr int kPitch = D + 4;                           // floats; rows 2t spread over the banks
-  static constexpr int kJoinOff = kStages * 2 * kHalf;
+  // One team takes every tile, so that it has seen every earlier phase of a stage's barriers (a
+  // wait on a phase's parity also passes two phases too early: teams that take turns would need a
+  // stage count that leaves each stage with one of them).
+  static constexpr int kStages = (NT > 3 ? 2 : 3) * (128 / D);
+  static constexpr int kPitch = 64 + 4;                          // floats; rows 2t spread over the banks
+  static constexpr int kJoinOff = kStages * 2 * kHalf;           // 64 channels of 8 rows of every warp
   static constexpr int kQOff = kJoinOff + kDecWarps * 8 * kPitch * 4;
   static constexpr int kQBytes = NT > 2 ? NT * (D / 16) * 32 * 8 : 0;
   static constexpr int kMlOff = kQOff + kQBytes;                 // float2 [warps][8 NT]
@@ -79,7 +80,7 @@ struct DecodeSmem {
   static constexpr int kMetaOff = kBarOff + 2 * kStages * 8;     // int [stages][4]
   static constexpr int kMiscOff = kMetaOff + kStages * 16;       // range, abort flag
   static constexpr int kBytes = kMiscOff + 64;
-  static constexpr int kAlloc = kBytes + 1024;                   // slack for 1024-byte alignment
+  static_assert(kBytes <= 115712, "two CTAs must fit an SM's 228 KB, 1 KB of it reserved for each");
 };
 
 // Keys [lo, hi) that some row of a sequence sees, as tiles [first, first + n);
@@ -102,25 +103,45 @@ __device__ __forceinline__ DecodeSpan decode_span(const DecodeParams& p, int len
   return s;
 }
 __device__ __forceinline__ int decode_len(const DecodeParams& p, int b) {
-  const int len = p.kv_lens[b];
+  // from L2: the join kernel may read lengths that this SM's L1 holds from an earlier call
+  const int len = __ldcg(p.kv_lens + b);
   return len < 0 || len > (p.kv.max_pages << p.kv.page_shift) ? 0 : len;
 }
 
-// Tiles of all units, and of the sequences before b (whole warp).
-__device__ __forceinline__ long long decode_tiles_before(const DecodeParams& p, int b, int lane) {
-  long long sum = 0;
-  for (int i = lane; i < b; i += 32) sum += decode_span(p, decode_len(p, i)).n;
+// Charged tiles of one unit of sequence b, and of all units of the sequences before b (whole warp).
+__device__ __forceinline__ int decode_charge(const DecodeParams& p, int b) {
+  return decode_span(p, decode_len(p, b)).n + kUnitTiles;
+}
+__device__ __forceinline__ long long decode_charge_before(const DecodeParams& p, int b, int lane, int mine) {
+  long long sum = lane < b ? mine : 0;      // `mine`: sequence `lane`'s
+  for (int i = lane + 32; i < b; i += 32) sum += decode_charge(p, i);
 #pragma unroll
   for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
   return sum * p.Hkv * p.groups;
 }
-// CTAs that share `total` tiles, the first tile of CTA c's range, the CTA that has tile t.
+// CTAs that share `total` charged tiles, the start of CTA c's range, the CTA that has tile t.
 __device__ __forceinline__ int decode_ctas(const DecodeParams& p, long long total) {
-  return (int)min((long long)p.ctas, (total + p.min_tiles - 1) / p.min_tiles);
+  return (int)min((long long)p.ctas, total);
 }
 __device__ __forceinline__ long long decode_first(long long total, int n, int c) { return total * c / n; }
 __device__ __forceinline__ int decode_owner(long long total, int n, long long t) {
   return (int)(((t + 1) * n - 1) / total);
+}
+// The part of a unit that a range [pos, end) of charged tiles holds: tiles [t0, t0 + nt) of n.
+struct DecodePiece {
+  int unit, t0, nt, n;
+  long long next;   // the range's position behind it
+};
+__device__ __forceinline__ DecodePiece decode_piece(int n, long long before, long long pos, long long end) {
+  DecodePiece d;
+  const int charge = n + kUnitTiles;
+  const int off = (int)((pos - before) % charge);
+  d.unit = (int)((pos - before) / charge);
+  d.next = min(end, pos + charge - off);
+  d.t0 = max(0, off - kUnitTiles);
+  d.nt = max(0, off + (int)(d.next - pos) - kUnitTiles) - d.t0;
+  d.n = n;
+  return d;
 }
 
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, uint32_t bar, int slot,
@@ -165,12 +186,11 @@ __device__ __forceinline__ void mma_16x8(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 template <bool BF16, int D, int NT>
-__global__ void __launch_bounds__(kDecThreads, 1) fa_decode_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(const __grid_constant__ DecodeParams p) {
   using SM = DecodeSmem<D, NT>;
   constexpr int NS = SM::kStages;
   constexpr int KS = D / 16;                   // 16-channel steps
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto FULL = [&](int s) { return sbase + SM::kBarOff + 8 * s; };
@@ -185,15 +205,17 @@ __global__ void __launch_bounds__(kDecThreads, 1) fa_decode_kernel(const __grid_
     tma_prefetch_desc(&p.tm_v);
     for (int s = 0; s < NS; ++s) {
       mbar_init(FULL(s), 1);
-      mbar_init(EMPTY(s), 4);
+      mbar_init(EMPTY(s), kDecWarps);
     }
     fence_mbar_init();
     *s_abort = 0;
   }
-  pdl_launch_dependents();
+  // In this order: the join kernel may then read the lengths as soon as it runs.
   pdl_wait_prior();
+  pdl_launch_dependents();
   if (warp == kDecWarps) {   // this CTA's range of tiles and the sequence it starts in
-    const long long total = decode_tiles_before(p, p.B, lane);
+    const int first32 = lane < p.B ? decode_charge(p, lane) : 0;
+    const long long total = decode_charge_before(p, p.B, lane, first32);
     const int n = decode_ctas(p, total);
     long long start = 0, end = 0;
     if ((int)blockIdx.x < n) {
@@ -204,7 +226,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) fa_decode_kernel(const __grid_
     long long before = 0;
     int b = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-      long long w = b0 + lane < p.B ? (long long)decode_span(p, decode_len(p, b0 + lane)).n * p.Hkv * p.groups : 0;
+      const long long w = (long long)(b0 == 0 ? first32 : b0 + lane < p.B ? decode_charge(p, b0 + lane) : 0) * p.Hkv * p.groups;
       long long inc = w;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -244,10 +266,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) fa_decode_kernel(const __grid_
     const uint32_t sub_bytes = (uint32_t)box * D * 2;
     while (pos < end && !dead) {
       const DecodeSpan s = decode_span(p, decode_len(p, b));
-      const long long mine = (long long)s.n * p.Hkv * p.groups;
-      const int unit = (int)((pos - before) / s.n), t0 = (int)((pos - before) % s.n);
-      const int hk = unit / p.groups;
-      const int nt = (int)min((long long)(s.n - t0), end - pos);
+      const long long mine = (long long)(s.n + kUnitTiles) * p.Hkv * p.groups;
+      const DecodePiece d = decode_piece(s.n, before, pos, end);
+      const int hk = d.unit / p.groups, t0 = d.t0, nt = d.nt;
       const int n_pages = (s.hi + (1 << p.kv.page_shift) - 1) >> p.kv.page_shift;
       // Lane i looks up sub-block c0 + i of the unit (box keys each): page, first slot, first key.
       auto look_up = [&](int c, int& id, int& slot, int& key) {
@@ -302,7 +323,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) fa_decode_kernel(const __grid_
         // the next look-up, a look-up's tiles ahead of its use
         if (in == 0) look_up((t0 + j + per) * nsub + lane, id2, slot2, key2);
       }
-      pos += nt;
+      pos = d.next;
       if (pos >= before + mine) {
         before += mine;
         ++b;
@@ -315,14 +336,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) fa_decode_kernel(const __grid_
   }
 
   // ============================================================ consumers
-  const int team = warp >> 2, quarter = warp & 3;
   const int g = lane >> 2, t4 = lane & 3;
   float* s_join = reinterpret_cast<float*>(smem + SM::kJoinOff);
   uint2* s_q = reinterpret_cast<uint2*>(smem + SM::kQOff);
   float2* s_ml = reinterpret_cast<float2*>(smem + SM::kMlOff);
   // this lane's row of each ldmatrix: keys as stored (K), keys and channel halves (V, transposed)
-  const int sub = (16 * quarter) >> box_shift;
-  const int r0 = (16 * quarter) & (box - 1);
+  const int sub = (16 * warp) >> box_shift;
+  const int r0 = (16 * warp) & (box - 1);
   const uint32_t sub_off = (uint32_t)sub * box * D * 2;
   const int krow = r0 + (lane & 15), kcol = lane >> 4;
   const int vrow = r0 + (lane & 7) + ((lane >> 4) << 3), vcol = (lane >> 3) & 1;
@@ -335,14 +355,21 @@ __global__ void __launch_bounds__(kDecThreads, 1) fa_decode_kernel(const __grid_
   int b = *s_b;
   int it = 0;
   bool dead = false;
-  for (int seg = 0; pos < end; ++seg) {
+  while (pos < end) {
     const int len = decode_len(p, b);
     const DecodeSpan s = decode_span(p, len);
-    const long long mine = (long long)s.n * p.Hkv * p.groups;
-    const int unit = (int)((pos - before) / s.n), t0 = (int)((pos - before) % s.n);
-    const int hk = unit / p.groups, rg = unit % p.groups;
-    const int nt = (int)min((long long)(s.n - t0), end - pos);
-    const long long row0 = (long long)b * p.Hq * p.Sq + (long long)hk * p.rows + rg * 8 * NT;
+    const long long mine = (long long)(s.n + kUnitTiles) * p.Hkv * p.groups;
+    const DecodePiece d = decode_piece(s.n, before, pos, end);
+    const int hk = d.unit / p.groups, rg = d.unit % p.groups;
+    const int seq = b;
+    pos = d.next;
+    if (pos >= before + mine) {
+      before += mine;
+      ++b;
+    }
+    if (d.nt == 0) continue;       // nothing but the charge
+    const int nt = d.nt;
+    const long long row0 = (long long)seq * p.Hq * p.Sq + (long long)hk * p.rows + rg * 8 * NT;
     const int rows = min(8 * NT, p.rows - rg * 8 * NT);
 
     // Q as the B operand: lane (g, t4) holds row g, channels 2 t4, 2 t4 + 1 and + 8 of every step
@@ -384,7 +411,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) fa_decode_kernel(const __grid_
         for (int e = 0; e < 4; ++e) o[n][k][e] = 0.f;
     }
 
-    for (int j = (it & 1) ^ team; j < nt; j += 2) {
+    for (int j = 0; j < nt; ++j) {
       if (dead) break;
       const int i = it + j, st = i % NS;
       if (!wait_bar(FULL(st), (i / NS) & 1, wc)) {
@@ -487,7 +514,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) fa_decode_kernel(const __grid_
     }
     it += nt;
 
-    // ---- join the eight warps' pieces of the unit
+    // ---- join the warps' pieces of the unit
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -498,55 +525,60 @@ __global__ void __launch_bounds__(kDecThreads, 1) fa_decode_kernel(const __grid_
       }
     }
     named_sync(1, 32 * kDecWarps);
-    const bool direct = t0 == 0 && nt == s.n;
-    const long long slot = 2LL * blockIdx.x + (seg ? 1 : 0);
-    const int tid = threadIdx.x;                 // < 256
+    const bool direct = d.t0 == 0 && nt == d.n;
+    const long long slot = 2LL * blockIdx.x + (d.t0 == 0 ? 1 : 0);
+    const int r = threadIdx.x / 16, c4 = 4 * (threadIdx.x % 16);   // 128 threads: 8 rows x 64 channels
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      float f[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float top = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, s_ml[w * 8 * NT + n * 8 + 2 * t4 + e].x);
-        const float f = m[n][e] > -INFINITY ? ex2_approx(m[n][e] - top) : 0.f;
-        float* dst = s_join + (warp * 8 + 2 * t4 + e) * SM::kPitch + g;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          dst[16 * k] = o[n][k][e] * f;
-          dst[16 * k + 8] = o[n][k][e + 2] * f;
-        }
+        f[e] = m[n][e] > -INFINITY ? ex2_approx(m[n][e] - top) : 0.f;
       }
-      named_sync(1, 32 * kDecWarps);
-      const int r = tid / (D / 4), d = 4 * (tid % (D / 4));
-      if (r < 8 && n * 8 + r < rows) {
-        float top = -INFINITY, sum = 0.f;
+      float top = -INFINITY, sum = 0.f;      // of row r
 #pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, s_ml[w * 8 * NT + n * 8 + r].x);
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, s_ml[w * 8 * NT + n * 8 + r].x);
 #pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) {
-          const float2 ml = s_ml[w * 8 * NT + n * 8 + r];
-          sum += ml.x > -INFINITY ? ml.y * ex2_approx(ml.x - top) : 0.f;
-          const float4 y = *reinterpret_cast<const float4*>(s_join + (w * 8 + r) * SM::kPitch + d);
-          x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-        }
-        if (direct) {
-          const float inv = sum > 0.f ? 1.f / sum : 0.f;
-          *reinterpret_cast<uint2*>(p.o + (row0 + n * 8 + r) * D + d) =
-              make_uint2(pack16x2<BF16>(x.x * inv, x.y * inv), pack16x2<BF16>(x.z * inv, x.w * inv));
-          if (d == 0) p.lse[row0 + n * 8 + r] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : INFINITY;
-        } else {
-          const long long at_row = slot * (8 * NT) + n * 8 + r;
-          *reinterpret_cast<float4*>(p.part_o + at_row * D + d) = x;
-          if (d == 0) p.part_ml[at_row] = make_float2(top, sum);
-        }
+      for (int w = 0; w < kDecWarps; ++w) {
+        const float2 ml = s_ml[w * 8 * NT + n * 8 + r];
+        sum += ml.x > -INFINITY ? ml.y * ex2_approx(ml.x - top) : 0.f;
       }
-      named_sync(1, 32 * kDecWarps);
-    }
-    pos += nt;
-    if (pos >= before + mine) {
-      before += mine;
-      ++b;
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float* dst = s_join + (warp * 8 + 2 * t4 + e) * SM::kPitch + g;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            dst[16 * k] = o[n][4 * h + k][e] * f[e];
+            dst[16 * k + 8] = o[n][4 * h + k][e + 2] * f[e];
+          }
+        }
+        named_sync(1, 32 * kDecWarps);
+        if (n * 8 + r < rows) {
+          const int ch = 64 * h + c4;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < kDecWarps; ++w) {
+            const float4 y = *reinterpret_cast<const float4*>(s_join + (w * 8 + r) * SM::kPitch + c4);
+            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+          }
+          if (direct) {
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            *reinterpret_cast<uint2*>(p.o + (row0 + n * 8 + r) * D + ch) =
+                make_uint2(pack16x2<BF16>(x.x * inv, x.y * inv), pack16x2<BF16>(x.z * inv, x.w * inv));
+            if (ch == 0) p.lse[row0 + n * 8 + r] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : INFINITY;
+          } else {
+            const long long at_row = slot * (8 * NT) + n * 8 + r;
+            *reinterpret_cast<float4*>(p.part_o + at_row * D + ch) = x;
+            if (ch == 0) p.part_ml[at_row] = make_float2(top, sum);
+          }
+        }
+        named_sync(1, 32 * kDecWarps);
+      }
     }
   }
 }
@@ -556,8 +588,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) fa_decode_kernel(const __grid_
 // the keys (the same bits every time).
 template <bool BF16, int D>
 __global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_constant__ DecodeParams p, int rows8) {
+  // The schedule before the wait: by the time this kernel runs every CTA of the decode kernel has
+  // seen the kernels before it finish, so that the lengths are final.
   pdl_launch_dependents();
-  pdl_wait_prior();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 8 + warp;
   const long long per_b = (long long)p.Hq * p.Sq;
@@ -566,15 +599,15 @@ __global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_consta
   const int in_b = (int)(row % per_b);
   const int hk = in_b / p.rows, r = in_b % p.rows;
   const int rg = r / rows8, rr = r % rows8;
-  const long long total = decode_tiles_before(p, p.B, lane);
+  const int first32 = lane < p.B ? decode_charge(p, lane) : 0;
+  const int n = decode_charge(p, b) - kUnitTiles;
+  const long long total = decode_charge_before(p, p.B, lane, first32);
   const int ctas = decode_ctas(p, total);
-  const int n = decode_span(p, decode_len(p, b)).n;
-  const long long t0 = decode_tiles_before(p, b, lane) + (long long)(hk * p.groups + rg) * n;
+  const long long t0 = decode_charge_before(p, b, lane, first32) + (long long)(hk * p.groups + rg) * (n + kUnitTiles) + kUnitTiles;
   const int c0 = decode_owner(total, ctas, t0), c1 = decode_owner(total, ctas, t0 + n - 1);
+  pdl_wait_prior();
   if (c0 == c1) return;          // finished by its CTA
-  // CTA c0's piece is its last one unless its range starts with the unit; the others start inside it
-  const long long first = 2LL * c0 + (decode_first(total, ctas, c0) == t0 ? 0 : 1);
-  auto at = [&](int c) { return (c == c0 ? first : 2LL * c) * rows8 + rr; };
+  auto at = [&](int c) { return (2LL * c + (c == c0 ? 1 : 0)) * rows8 + rr; };
   float m = -INFINITY;
   for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[at(c)].x);
 #pragma unroll
@@ -584,7 +617,7 @@ __global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_consta
   float o[E], l = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int c = c0; c <= c1; ++c) {
     const long long a = at(c);
     const float2 ml = p.part_ml[a];

@@ -107,7 +107,7 @@ bool encode_pool(CUtensorMap* tm, const void* base, bool fp16, int D, int Hkv, c
 template <bool BF16, int D, int NT>
 int launch_decode(fa::DecodeParams& p, long long most_tiles, cudaStream_t st) {
   auto kern = fa::fa_decode_kernel<BF16, D, NT>;
-  constexpr int smem = fa::DecodeSmem<D, NT>::kAlloc;
+  constexpr int smem = fa::DecodeSmem<D, NT>::kBytes;
   int dev = 0;
   cudaGetDevice(&dev);
   static std::once_flag once[64];
@@ -118,7 +118,7 @@ int launch_decode(fa::DecodeParams& p, long long most_tiles, cudaStream_t st) {
   if (attr_err[dev & 63] != cudaSuccess) return cuda_fail(attr_err[dev & 63]);
   const int sms = fa_host::sm_count();
   if (sms <= 0) return cuda_fail(cudaErrorInvalidDevice);
-  p.ctas = (int)std::min<long long>(sms, most_tiles);
+  p.ctas = (int)std::min<long long>(fa::kDecCtasPerSm * sms, most_tiles);
   const size_t o_bytes = (size_t)2 * p.ctas * 8 * NT * D * 4;
   void* scratch = fa_host::scratch_alloc(o_bytes + (size_t)2 * p.ctas * 8 * NT * 8, st);
   if (!scratch) return cuda_fail(cudaGetLastError());
@@ -136,11 +136,12 @@ int launch_decode(fa::DecodeParams& p, long long most_tiles, cudaStream_t st) {
 template <bool BF16, int D>
 int launch_decode_rows(fa::DecodeParams& p, long long tiles_per_unit, cudaStream_t st) {
   // as few columns as hold the rows; more than 32 rows go in groups that read the keys again
-  const int nt = p.rows <= 8 ? 1 : p.rows <= 16 ? 2 : 4;
+  const int nt = p.rows <= 32 ? (p.rows + 7) / 8 : 4;
   p.groups = (p.rows + 8 * nt - 1) / (8 * nt);
-  const long long most = tiles_per_unit * p.B * p.Hkv * p.groups;
+  const long long most = (tiles_per_unit + fa::kUnitTiles) * p.B * p.Hkv * p.groups;
   return nt == 1 ? launch_decode<BF16, D, 1>(p, most, st)
          : nt == 2 ? launch_decode<BF16, D, 2>(p, most, st)
+         : nt == 3 ? launch_decode<BF16, D, 3>(p, most, st)
                    : launch_decode<BF16, D, 4>(p, most, st);
 }
 
@@ -270,7 +271,6 @@ int fa_decode(const void* q, const fa_paged_kv_t* kv, void* o, float* lse, int B
   p.Sq = Sq;
   p.rows = Hq / Hkv * Sq;
   p.pre_tokens = pre_tokens;
-  p.min_tiles = 1;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.timeout_ns = fa_host::wait_timeout_ns();
   p.status = fa_host::status_ptr();

@@ -1,9 +1,10 @@
-"""CPU model of the decode kernel's tile ring: one producer, two consumer teams
-that take the tiles in turn, full / empty barriers that are waited on by the
-parity of a phase, copies that may land in any order.  Every interleaving is
-visited.  A wait on parity P passes whenever the barrier's current phase has
-the other parity, so a waiter that is two phases ahead passes too early: with a
-stage count that is not a multiple of the teams that happens, otherwise never."""
+"""CPU model of the decode kernel's tile ring: one producer, consumer teams that
+take the tiles in turn, full / empty barriers that are waited on by the parity
+of a phase, copies that may land in any order.  Every interleaving is visited.
+A wait on parity P passes whenever the barrier's current phase has the other
+parity, so a waiter that is two phases ahead passes too early.  The kernel has
+one team, which is sound with any number of stages; with two that happens
+unless each stage stays with one of them."""
 import pytest
 
 
@@ -47,6 +48,12 @@ def faults(stages, tiles, teams=2):
                 todo.append(s)
     assert done == 1 or bad
     return bad
+
+
+@pytest.mark.parametrize("stages", [2, 3, 4, 6])
+def test_one_team_is_sound(stages):
+    for tiles in (1, stages, 2 * stages + 1, 3 * stages + 1):
+        assert faults(stages, tiles, teams=1) == set()
 
 
 @pytest.mark.parametrize("stages", [2, 4, 6])
