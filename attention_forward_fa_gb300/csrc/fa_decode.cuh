@@ -7,18 +7,22 @@
 // through shared memory at HBM speed with as little as possible beside it:
 //
 //   * a CTA is one producer warp and four consumer warps, two CTAs per SM: while
-//     one joins its warps' results and starts the next unit the other streams;
+//     one waits at a barrier or ends a unit the other streams;
 //   * the producer looks up pages and copies tiles of 64 keys (K and V, 64
 //     channels x up to 64 slots x D / 64 halves per TMA box, 128-byte swizzle)
 //     into a ring of 96 KB, 192 KB per SM: four times latency times bandwidth;
-//   * each consumer takes 16 keys of every tile with a running maximum, sum and
-//     O of all rows of its own; they meet only at the end of a unit;
+//   * of every tile each consumer scores 16 keys against all rows, puts their P
+//     into shared memory and then adds all 64 keys' values to its quarter of the
+//     channels: O of 8 NT rows costs a thread 8 NT registers instead of 32 NT
+//     with a whole O per warp, and nothing has to be joined at a unit's end but
+//     the sums.  (The warps-by-keys form spilled at 24 rows, spent 2.4 us per
+//     unit, and took 66 us against XX us for five draft tokens in a window.)
 //   * products are transposed, S^T = K Q^T and O^T = V^T P^T, with the keys (then
 //     the channels) as the 16-row side of mma.m16n8k16 and the rows as its
 //     8-column side: 4 rows of a common group waste 4 of 8 columns there, but
 //     would waste 124 of the 128 lanes of a tcgen05 tile, whose accumulator
-//     also costs a round trip through TMEM before every exponential.  At
-//     8 to 32 rows the warp-level products stay hidden behind the copies;
+//     also costs a round trip through TMEM before every exponential.  Up to 64
+//     rows the warp-level products stay behind the copies;
 //   * P goes into the value product as hi + lo pairs of the cache's type (the
 //     tensor cores are idle, and a single bf16 P would add an error as large as
 //     the rounding of O).
@@ -41,6 +45,11 @@ constexpr int kDecWarps = 4;                          // consumer warps, 16 keys
 constexpr int kDecCtasPerSm = 2;
 constexpr int kDecThreads = 32 * (kDecWarps + 1);     // and the producer
 constexpr int kUnitTiles = 1;                         // a unit's own cost, in tiles
+// A row's reference (the subtrahend of its exponents) follows its maximum lazily: it stays while no
+// score exceeds it by more than this many powers of two, so that the usual tile needs one vote and
+// no shuffles.  P <= 2^8 fits both 16-bit types; every sum is relative to the reference.
+constexpr float kMaxOver = 8.f;
+constexpr float kNoScore = -3.402823466e38f;          // the reference before a row's first key
 
 struct DecodeParams {
   CUtensorMap tm_k;   // (64 channels, slots, D / 64, heads, pages)
@@ -67,18 +76,18 @@ struct DecodeParams {
 template <int D, int NT>
 struct DecodeSmem {
   static constexpr int kHalf = kDecTile * D * 2;                 // K or V of a tile
-  // One team takes every tile, so that it has seen every earlier phase of a stage's barriers (a
-  // wait on a phase's parity also passes two phases too early: teams that take turns would need a
-  // stage count that leaves each stage with one of them).
-  static constexpr int kStages = (NT > 3 ? 2 : 3) * (128 / D);
-  static constexpr int kPitch = 64 + 4;                          // floats; rows 2t spread over the banks
-  static constexpr int kJoinOff = kStages * 2 * kHalf;           // 64 channels of 8 rows of every warp
-  static constexpr int kQOff = kJoinOff + kDecWarps * 8 * kPitch * 4;
-  static constexpr int kQBytes = NT > 2 ? NT * (D / 16) * 32 * 8 : 0;
-  static constexpr int kMlOff = kQOff + kQBytes;                 // float2 [warps][8 NT]
-  static constexpr int kBarOff = kMlOff + kDecWarps * 8 * NT * 8;
-  static constexpr int kMetaOff = kBarOff + 2 * kStages * 8;     // int [stages][4]
-  static constexpr int kMiscOff = kMetaOff + kStages * 16;       // range, abort flag
+  // The consumers take every tile, so that each has seen every earlier phase of a stage's barriers
+  // (a wait on a phase's parity also passes two phases too early: teams that take turns would need
+  // a stage count that leaves each stage with one of them).
+  static constexpr int kStages = (NT > 4 ? 2 : 3) * (128 / D);
+  static constexpr bool kQShared = NT > 4;                       // Q in shared memory or in registers
+  static constexpr int kPOff = kStages * 2 * kHalf;              // uint4 [4 x 16 keys][NT][lane]: P hi, lo
+  static constexpr int kQOff = kPOff + kDecWarps * NT * 512;
+  static constexpr int kMaxOff = kQOff + (kQShared ? NT * (D / 32) * 512 : 0);   // float [warps][8 NT]
+  static constexpr int kSumOff = kMaxOff + kDecWarps * 8 * NT * 4;               // float [warps][8 NT]
+  static constexpr int kMetaOff = kSumOff + kDecWarps * 8 * NT * 4;              // int4 [stages]
+  static constexpr int kBarOff = kMetaOff + kStages * 16;
+  static constexpr int kMiscOff = kBarOff + 2 * kStages * 8;     // range, abort flag
   static constexpr int kBytes = kMiscOff + 64;
   static_assert(kBytes <= 115712, "two CTAs must fit an SM's 228 KB, 1 KB of it reserved for each");
 };
@@ -195,7 +204,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto FULL = [&](int s) { return sbase + SM::kBarOff + 8 * s; };
   auto EMPTY = [&](int s) { return sbase + SM::kBarOff + 8 * (NS + s); };
-  int* s_meta = reinterpret_cast<int*>(smem + SM::kMetaOff);
+  int* s_meta = reinterpret_cast<int*>(smem + SM::kMetaOff);   // per stage: first key of each 16, or -1
   long long* s_range = reinterpret_cast<long long*>(smem + SM::kMiscOff);   // start, end, tiles before s_b
   int* s_b = reinterpret_cast<int*>(smem + SM::kMiscOff + 24);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + SM::kMiscOff + 28);
@@ -311,7 +320,8 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
         const int sub = lane - in * nsub;
         const bool holder = sub >= 0 && sub < nsub;
         const unsigned live = __ballot_sync(0xffffffffu, holder && id >= 0);
-        if (holder) s_meta[st * 4 + sub] = key;
+        if (holder)
+          for (int k = 0; k < box; k += 16) s_meta[st * 4 + (sub * box + k) / 16] = key < 0 ? -1 : key + k;
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(FULL(st), 2u * sub_bytes * __popc(live));
         __syncwarp();
@@ -336,20 +346,28 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
   }
 
   // ============================================================ consumers
+  constexpr int DT = D / 64;                         // 16-channel steps of this warp's quarter of O
   const int g = lane >> 2, t4 = lane & 3;
-  float* s_join = reinterpret_cast<float*>(smem + SM::kJoinOff);
-  uint2* s_q = reinterpret_cast<uint2*>(smem + SM::kQOff);
-  float2* s_ml = reinterpret_cast<float2*>(smem + SM::kMlOff);
-  // this lane's row of each ldmatrix: keys as stored (K), keys and channel halves (V, transposed)
-  const int sub = (16 * warp) >> box_shift;
-  const int r0 = (16 * warp) & (box - 1);
-  const uint32_t sub_off = (uint32_t)sub * box * D * 2;
-  const int krow = r0 + (lane & 15), kcol = lane >> 4;
-  const int vrow = r0 + (lane & 7) + ((lane >> 4) << 3), vcol = (lane >> 3) & 1;
-  auto at = [&](int row, int chunk) {   // 16-byte chunk `chunk` of a row: half, swizzled place
-    return (uint32_t)(chunk >> 3) * (uint32_t)(box * 128) + (uint32_t)row * 128 +
-           (uint32_t)(((chunk & 7) ^ (row & 7)) << 4);
+  uint4* s_p = reinterpret_cast<uint4*>(smem + SM::kPOff);
+  uint4* s_q = reinterpret_cast<uint4*>(smem + SM::kQOff);
+  float* s_max = reinterpret_cast<float*>(smem + SM::kMaxOff);
+  float* s_sum = reinterpret_cast<float*>(smem + SM::kSumOff);
+  auto sync = [&]() { named_sync(1, 32 * kDecWarps); };
+  // In a stage, 16 keys start at place(q) for q = 0 .. 3 (a copy is [D / 64][box][64]); a row of 64
+  // channels is 128 bytes, its 16-byte chunk c at place c ^ (row & 7).
+  const uint32_t half = (uint32_t)box * 128;
+  auto place = [&](int q) {
+    return (uint32_t)((16 * q) >> box_shift) * (uint32_t)box * D * 2 + (uint32_t)((16 * q) & (box - 1)) * 128;
   };
+  // this lane's row of each ldmatrix: keys as stored for K; for V transposed, keys by 8, channels by 8
+  const uint32_t klane = place(warp) + (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
+  uint32_t vlane[DT];
+#pragma unroll
+  for (int i = 0; i < DT; ++i) {
+    const int ch = 16 * (warp * DT + i);
+    vlane[i] = SM::kHalf + (uint32_t)(ch >> 6) * half + ((lane & 7) + ((lane >> 4) << 3)) * 128 +
+               ((((ch & 63) / 8 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
+  }
 
   long long pos = s_range[0], before = s_range[2];
   int b = *s_b;
@@ -361,223 +379,229 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
     const long long mine = (long long)(s.n + kUnitTiles) * p.Hkv * p.groups;
     const DecodePiece d = decode_piece(s.n, before, pos, end);
     const int hk = d.unit / p.groups, rg = d.unit % p.groups;
-    const int seq = b;
+    const long long row0 = (long long)b * p.Hq * p.Sq + (long long)hk * p.rows + rg * 8 * NT;
     pos = d.next;
     if (pos >= before + mine) {
       before += mine;
       ++b;
     }
     if (d.nt == 0) continue;       // nothing but the charge
-    const int nt = d.nt;
-    const long long row0 = (long long)seq * p.Hq * p.Sq + (long long)hk * p.rows + rg * 8 * NT;
     const int rows = min(8 * NT, p.rows - rg * 8 * NT);
 
-    // Q as the B operand: lane (g, t4) holds row g, channels 2 t4, 2 t4 + 1 and + 8 of every step
-    uint2 qf[NT > 2 ? 1 : NT][NT > 2 ? 1 : KS];
-    if constexpr (NT > 2) {
-      named_sync(1, 32 * kDecWarps);    // the last unit's reads of s_q are done
-      for (int i = warp; i < NT * KS; i += kDecWarps) {
-        const int row = (i / KS) * 8 + g;
-        const uint32_t* x = reinterpret_cast<const uint32_t*>(p.q + (row0 + row) * D + (i % KS) * 16) + t4;
-        s_q[i * 32 + lane] = row < rows ? make_uint2(x[0], x[4]) : make_uint2(0, 0);
-      }
-      named_sync(1, 32 * kDecWarps);
+    // Q as the B operand: lane (g, t4) holds row g, channels 2 t4, 2 t4 + 1 and + 8 of every step;
+    // two steps per word
+    uint4 qf[SM::kQShared ? 1 : NT][SM::kQShared ? 1 : KS / 2];
+    auto load_q = [&](int n, int k2) {
+      const int row = n * 8 + g;
+      const uint32_t* x = reinterpret_cast<const uint32_t*>(p.q + (row0 + row) * D + k2 * 32) + t4;
+      return row < rows ? make_uint4(x[0], x[4], x[8], x[12]) : make_uint4(0, 0, 0, 0);
+    };
+    if constexpr (SM::kQShared) {   // (the last unit's reads of it lie before its last barrier)
+      for (int i = warp; i < NT * KS / 2; i += kDecWarps) s_q[i * 32 + lane] = load_q(i / (KS / 2), i % (KS / 2));
+      sync();
     } else {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int row = n * 8 + g;
-        const uint32_t* x = reinterpret_cast<const uint32_t*>(p.q + (row0 + row) * D) + t4;
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int k = 0; k < KS; ++k) qf[n][k] = row < rows ? make_uint2(x[8 * k], x[8 * k + 4]) : make_uint2(0, 0);
-      }
+        for (int k2 = 0; k2 < KS / 2; ++k2) qf[n][k2] = load_q(n, k2);
     }
-    // this lane's rows as columns of S^T and O^T: 2 t4, 2 t4 + 1 of every 8; their tokens
-    int tok[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) tok[n][e] = len - p.Sq + (rg * 8 * NT + n * 8 + 2 * t4 + e) % p.Sq;
-    const int tok_min = len - p.Sq;
+    const int tok_min = len - p.Sq;                                       // the first row's token
     const int low_max = p.pre_tokens >= 0 ? len - 1 - p.pre_tokens : 0;   // lowest key that all rows see
 
-    float o[NT][KS][4], m[NT][2], l[NT][2];
+    float o[NT][DT][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      m[n][0] = m[n][1] = -INFINITY;
+      m[n][0] = m[n][1] = kNoScore;
       l[n][0] = l[n][1] = 0.f;
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][k][e] = 0.f;
+      for (int i = 0; i < DT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
     }
 
-    for (int j = 0; j < nt; ++j) {
-      if (dead) break;
-      const int i = it + j, st = i % NS;
-      if (!wait_bar(FULL(st), (i / NS) & 1, wc)) {
-        dead = true;
-        break;
-      }
-      const int kb = s_meta[st * 4 + sub];
-      const int key0 = kb + r0;
-      // (kb < 0: no such keys, and nothing was copied)
-      if (kb >= 0 && key0 < s.hi && key0 + 16 > s.lo) {
-        const uint32_t kbase = sbase + (uint32_t)st * 2 * SM::kHalf + sub_off;
-        float c[NT][4];
+    for (int j = 0; j < d.nt; ++j, ++it) {
+      const int st = it % NS;
+      // (after an expired wait: the barriers below still see every warp, the answer is void)
+      if (!dead && !wait_bar(FULL(st), (it / NS) & 1, wc)) dead = true;
+      const int4 keys = *reinterpret_cast<const int4*>(s_meta + 4 * st);
+      const uint32_t base = sbase + (uint32_t)st * 2 * SM::kHalf;
+      const int kq = warp == 0 ? keys.x : warp == 1 ? keys.y : warp == 2 ? keys.z : keys.w;
+      // 16 keys that were not copied (their K is stale) lie past every row's token
+      const int key0 = kq < 0 ? 0x7FFFFF00 : kq;
+      float c[NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+      for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t a[4];
-          ldmatrix4(kbase + at(krow, 2 * k + kcol), a);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint2 x = NT > 2 ? s_q[(n * KS + k) * 32 + lane] : qf[NT > 2 ? 0 : n][NT > 2 ? 0 : k];
-            mma_16x8<BF16>(c[n], a, x.x, x.y);
-          }
-        }
-        // scores in log2 units; lane (g, t4): keys g (c0, c1) and g + 8 (c2, c3), rows 2 t4, 2 t4 + 1
-        const bool all = key0 + 15 <= tok_min && key0 >= low_max;
-        uint32_t ph[NT][2], pl[NT][2];
+      for (int k2 = 0; k2 < KS / 2; ++k2) {
+        uint32_t a0[4], a1[4];
+        const uint32_t at = base + (klane ^ (uint32_t)((k2 & 1) << 6)) + (k2 >> 1) * half;
+        ldmatrix4(at, a0);
+        ldmatrix4(at ^ 32u, a1);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+          const uint4 x = SM::kQShared ? s_q[(n * (KS / 2) + k2) * 32 + lane] : qf[SM::kQShared ? 0 : n][SM::kQShared ? 0 : k2];
+          mma_16x8<BF16>(c[n], a0, x.x, x.y);
+          mma_16x8<BF16>(c[n], a1, x.z, x.w);
+        }
+      }
+      // scores in log2 units; lane (g, t4): keys g (c0, c1) and g + 8 (c2, c3), rows 2 t4, 2 t4 + 1
+      float over = -INFINITY;        // the most that a score exceeds its row's reference by
+      const bool all = key0 + 15 <= tok_min && key0 >= low_max;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) c[n][e] *= p.scale_log2;
-          if (!all) {
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = key0 + g + 8 * (e >> 1), t = tok[n][e & 1];
-              if (key > t || (p.pre_tokens >= 0 && key < t - p.pre_tokens)) c[n][e] = -INFINITY;
-            }
+        for (int e = 0; e < 4; ++e) c[n][e] *= p.scale_log2;
+      if (!all) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = key0 + g + 8 * (e >> 1);
+            const int t = tok_min + (p.Sq == 1 ? 0 : (rg * 8 * NT + n * 8 + 2 * t4 + (e & 1)) % p.Sq);
+            if (key > t || (p.pre_tokens >= 0 && key < t - p.pre_tokens)) c[n][e] = -INFINITY;
           }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) over = fmaxf(over, c[n][e] - m[n][e & 1]);   // (NaN is dropped)
+      if (named_or(2, 32 * kDecWarps, over > kMaxOver)) {   // the references move up to the maxima
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
           float mx[2] = {fmaxf(c[n][0], c[n][2]), fmaxf(c[n][1], c[n][3])};
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) {
             mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], w));
             mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], w));
           }
-          if (__any_sync(0xffffffffu, mx[0] > m[n][0] || mx[1] > m[n][1])) {   // a larger maximum
-            float f[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float mn = fmaxf(m[n][e], mx[e]);
-              f[e] = mn > -INFINITY ? ex2_approx(m[n][e] - mn) : 1.f;
-              m[n][e] = mn;
-              l[n][e] *= f[e];
-            }
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-              o[n][k][0] *= f[0];
-              o[n][k][1] *= f[1];
-              o[n][k][2] *= f[0];
-              o[n][k][3] *= f[1];
-            }
-          }
-          const float b0 = m[n][0] > -INFINITY ? m[n][0] : 0.f, b1 = m[n][1] > -INFINITY ? m[n][1] : 0.f;
-          const float p0 = ex2_approx(c[n][0] - b0), p1 = ex2_approx(c[n][1] - b1);
-          const float p2 = ex2_approx(c[n][2] - b0), p3 = ex2_approx(c[n][3] - b1);
-          l[n][0] += p0 + p2;
-          l[n][1] += p1 + p3;
-          const uint32_t h0 = pack16x2<BF16>(p0, p1), h1 = pack16x2<BF16>(p2, p3);
-          ph[n][0] = transpose8(h0);
-          ph[n][1] = transpose8(h1);
-          pl[n][0] = transpose8(pack_residual_x2(p0, p1, h0, BF16));
-          pl[n][1] = transpose8(pack_residual_x2(p2, p3, h1, BF16));
+          if (g == 0) *reinterpret_cast<float2*>(s_max + (warp * NT + n) * 8 + 2 * t4) = make_float2(mx[0], mx[1]);
         }
-        // keys that no row sees have P = 0, and their V may hold anything: it becomes 0 too
-        const bool whole = key0 >= s.lo && key0 + 16 <= s.hi;
+        sync();
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float top[2] = {m[n][0], m[n][1]}, f[2];
+#pragma unroll
+          for (int w = 0; w < kDecWarps; ++w) {
+            const float2 x = *reinterpret_cast<const float2*>(s_max + (w * NT + n) * 8 + 2 * t4);
+            top[0] = fmaxf(top[0], x.x);
+            top[1] = fmaxf(top[1], x.y);
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            f[e] = ex2_approx(m[n][e] - top[e]);
+            m[n][e] = top[e];
+            l[n][e] *= f[e];
+          }
+#pragma unroll
+          for (int i = 0; i < DT; ++i) {
+            o[n][i][0] *= f[0];
+            o[n][i][1] *= f[1];
+            o[n][i][2] *= f[0];
+            o[n][i][3] *= f[1];
+          }
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float p0 = ex2_approx(c[n][0] - m[n][0]), p1 = ex2_approx(c[n][1] - m[n][1]);
+        const float p2 = ex2_approx(c[n][2] - m[n][0]), p3 = ex2_approx(c[n][3] - m[n][1]);
+        l[n][0] += p0 + p2;
+        l[n][1] += p1 + p3;
+        const uint32_t h0 = pack16x2<BF16>(p0, p1), h1 = pack16x2<BF16>(p2, p3);
+        s_p[(warp * NT + n) * 32 + lane] =
+            make_uint4(transpose8(h0), transpose8(h1), transpose8(pack_residual_x2(p0, p1, h0, BF16)),
+                       transpose8(pack_residual_x2(p2, p3, h1, BF16)));
+      }
+      sync();
+      // Keys that no row sees have P = 0, and their V may hold anything (or be stale): it becomes 0.
+      const int4 hi4 = make_int4(keys.x + 16, keys.y + 16, keys.z + 16, keys.w + 16);
+      const bool whole = min(min(keys.x, keys.y), min(keys.z, keys.w)) >= s.lo &&
+                         max(max(hi4.x, hi4.y), max(hi4.z, hi4.w)) <= s.hi;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
         uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;   // keys 2 t4, 2 t4 + 1 and + 8
         if (!whole) {
-          auto seen = [&](int k) { return key0 + k >= s.lo && key0 + k < s.hi; };
+          const int k0 = q == 0 ? keys.x : q == 1 ? keys.y : q == 2 ? keys.z : keys.w;
+          auto seen = [&](int k) { return k0 >= 0 && k0 + k >= s.lo && k0 + k < s.hi; };
           keep0 = (seen(2 * t4) ? 0xffffu : 0u) | (seen(2 * t4 + 1) ? 0xffff0000u : 0u);
           keep1 = (seen(2 * t4 + 8) ? 0xffffu : 0u) | (seen(2 * t4 + 9) ? 0xffff0000u : 0u);
         }
+        uint32_t a[DT][4];
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t a[4];
-          ldmatrix4_trans(kbase + SM::kHalf + at(vrow, 2 * k + vcol), a);
+        for (int i = 0; i < DT; ++i) {
+          ldmatrix4_trans(base + place(q) + vlane[i], a[i]);
           if (!whole) {
-            a[0] &= keep0;
-            a[1] &= keep0;
-            a[2] &= keep1;
-            a[3] &= keep1;
+            a[i][0] &= keep0;
+            a[i][1] &= keep0;
+            a[i][2] &= keep1;
+            a[i][3] &= keep1;
           }
+        }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma_16x8<BF16>(o[n][k], a, ph[n][0], ph[n][1]);
-            mma_16x8<BF16>(o[n][k], a, pl[n][0], pl[n][1]);
-          }
+        for (int n = 0; n < NT; ++n) {
+          const uint4 pp = s_p[(q * NT + n) * 32 + lane];
+#pragma unroll
+          for (int i = 0; i < DT; ++i) mma_16x8<BF16>(o[n][i], a[i], pp.x, pp.y);
+#pragma unroll
+          for (int i = 0; i < DT; ++i) mma_16x8<BF16>(o[n][i], a[i], pp.z, pp.w);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(EMPTY(st));
     }
-    it += nt;
 
-    // ---- join the warps' pieces of the unit
+    // ---- the unit's sums; each warp writes its channels
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], w);
-        if (g == 0) s_ml[warp * 8 * NT + n * 8 + 2 * t4 + e] = make_float2(m[n][e], l[n][e]);
-      }
+      if (g == 0) *reinterpret_cast<float2*>(s_sum + (warp * NT + n) * 8 + 2 * t4) = make_float2(l[n][0], l[n][1]);
     }
-    named_sync(1, 32 * kDecWarps);
-    const bool direct = d.t0 == 0 && nt == d.n;
-    const long long slot = 2LL * blockIdx.x + (d.t0 == 0 ? 1 : 0);
-    const int r = threadIdx.x / 16, c4 = 4 * (threadIdx.x % 16);   // 128 threads: 8 rows x 64 channels
+    sync();
+    const bool direct = d.t0 == 0 && d.nt == d.n;
+    const long long part0 = (2LL * blockIdx.x + (d.t0 == 0 ? 1 : 0)) * (8 * NT);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float f[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, s_ml[w * 8 * NT + n * 8 + 2 * t4 + e].x);
-        f[e] = m[n][e] > -INFINITY ? ex2_approx(m[n][e] - top) : 0.f;
-      }
-      float top = -INFINITY, sum = 0.f;      // of row r
-#pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, s_ml[w * 8 * NT + n * 8 + r].x);
+      float sum[2] = {0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < kDecWarps; ++w) {
-        const float2 ml = s_ml[w * 8 * NT + n * 8 + r];
-        sum += ml.x > -INFINITY ? ml.y * ex2_approx(ml.x - top) : 0.f;
+        const float2 x = *reinterpret_cast<const float2*>(s_sum + (w * NT + n) * 8 + 2 * t4);
+        sum[0] += x.x;
+        sum[1] += x.y;
       }
+      if (direct) {
+        const float i0 = sum[0] > 0.f ? 1.f / sum[0] : 0.f, i1 = sum[1] > 0.f ? 1.f / sum[1] : 0.f;
+        const int row = n * 8 + g;
 #pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
+        for (int i = 0; i < DT; ++i) {
+          // transposed back: lane (g, t4) gets row g, channels 2 t4 and 2 t4 + 1 (and + 8)
+          const uint32_t x = transpose8(pack16x2<BF16>(o[n][i][0] * i0, o[n][i][1] * i1));
+          const uint32_t y = transpose8(pack16x2<BF16>(o[n][i][2] * i0, o[n][i][3] * i1));
+          if (row < rows) {
+            uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (row0 + row) * D + 16 * (warp * DT + i)) + t4;
+            dst[0] = x;
+            dst[4] = y;
+          }
+        }
+      } else {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float* dst = s_join + (warp * 8 + 2 * t4 + e) * SM::kPitch + g;
+          float* dst = p.part_o + (part0 + n * 8 + 2 * t4 + e) * D + 16 * warp * DT + g;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            dst[16 * k] = o[n][4 * h + k][e] * f[e];
-            dst[16 * k + 8] = o[n][4 * h + k][e + 2] * f[e];
+          for (int i = 0; i < DT; ++i) {
+            dst[16 * i] = o[n][i][e];
+            dst[16 * i + 8] = o[n][i][e + 2];
           }
         }
-        named_sync(1, 32 * kDecWarps);
-        if (n * 8 + r < rows) {
-          const int ch = 64 * h + c4;
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      if (warp == 0 && g == 0) {
 #pragma unroll
-          for (int w = 0; w < kDecWarps; ++w) {
-            const float4 y = *reinterpret_cast<const float4*>(s_join + (w * 8 + r) * SM::kPitch + c4);
-            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-          }
-          if (direct) {
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
-            *reinterpret_cast<uint2*>(p.o + (row0 + n * 8 + r) * D + ch) =
-                make_uint2(pack16x2<BF16>(x.x * inv, x.y * inv), pack16x2<BF16>(x.z * inv, x.w * inv));
-            if (ch == 0) p.lse[row0 + n * 8 + r] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : INFINITY;
-          } else {
-            const long long at_row = slot * (8 * NT) + n * 8 + r;
-            *reinterpret_cast<float4*>(p.part_o + at_row * D + ch) = x;
-            if (ch == 0) p.part_ml[at_row] = make_float2(top, sum);
-          }
+        for (int e = 0; e < 2; ++e) {
+          const int row = n * 8 + 2 * t4 + e;
+          if (!direct) p.part_ml[part0 + row] = make_float2(m[n][e], sum[e]);
+          else if (row < rows)
+            p.lse[row0 + row] = sum[e] > 0.f ? (m[n][e] + log2f(sum[e])) * 0.6931471805599453f : INFINITY;
         }
-        named_sync(1, 32 * kDecWarps);
       }
     }
   }
@@ -612,7 +636,7 @@ __global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_consta
   for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[at(c)].x);
 #pragma unroll
   for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-  const float top = m > -INFINITY ? m : 0.f;
+  const float top = m;
   constexpr int E = D / 32;
   float o[E], l = 0.f;
 #pragma unroll
@@ -621,7 +645,7 @@ __global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_consta
   for (int c = c0; c <= c1; ++c) {
     const long long a = at(c);
     const float2 ml = p.part_ml[a];
-    const float f = ml.x > -INFINITY ? ex2_approx(ml.x - top) : 0.f;
+    const float f = ex2_approx(ml.x - top);
     l += ml.y * f;
     float x[E];
     if constexpr (E == 4) {

@@ -135,14 +135,17 @@ int launch_decode(fa::DecodeParams& p, long long most_tiles, cudaStream_t st) {
 
 template <bool BF16, int D>
 int launch_decode_rows(fa::DecodeParams& p, long long tiles_per_unit, cudaStream_t st) {
-  // as few columns as hold the rows; more than 32 rows go in groups that read the keys again
-  const int nt = p.rows <= 32 ? (p.rows + 7) / 8 : 4;
+  // as few columns as hold the rows; more than 64 rows go in groups that read the keys again
+  const int nt = p.rows <= 32 ? (p.rows + 7) / 8 : 8;
   p.groups = (p.rows + 8 * nt - 1) / (8 * nt);
   const long long most = (tiles_per_unit + fa::kUnitTiles) * p.B * p.Hkv * p.groups;
-  return nt == 1 ? launch_decode<BF16, D, 1>(p, most, st)
-         : nt == 2 ? launch_decode<BF16, D, 2>(p, most, st)
-         : nt == 3 ? launch_decode<BF16, D, 3>(p, most, st)
-                   : launch_decode<BF16, D, 4>(p, most, st);
+  switch (nt) {
+    case 1: return launch_decode<BF16, D, 1>(p, most, st);
+    case 2: return launch_decode<BF16, D, 2>(p, most, st);
+    case 3: return launch_decode<BF16, D, 3>(p, most, st);
+    case 4: return launch_decode<BF16, D, 4>(p, most, st);
+    default: return launch_decode<BF16, D, 8>(p, most, st);
+  }
 }
 
 template <bool BF16, int D>
