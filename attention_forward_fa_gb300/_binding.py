@@ -481,12 +481,6 @@ def fa_select_pages(q, kv: fa_paged_kv_t, page_idx, B: int, Hq: int, Hkv: int, S
                                      int(last), _stream(stream))
 
 
-def _steps(t, dims):
-    """Strides of the dims, 0 for a dim of size 1 (nothing to step over)."""
-    shape, stride = t.shape, t.stride()
-    return [0 if shape[d] == 1 else stride[d] for d in dims]
-
-
 class PagedKV:
     """A paged key-value cache: what the paged calls need to know of it.
 
@@ -536,11 +530,10 @@ class PagedKV:
         self.k_min, self.k_max = k_min, k_max
         self.dtype, self.device = k_pages.dtype, k_pages.device
         self._flags = FA_DTYPE_FP16 if self.dtype == torch.float16 else 0
-        ks, vs = _steps(k_pages, (0, 1, 2)), _steps(v_pages, (0, 1, 2))
         self._c = fa_paged_kv_t(
-            k_pages.data_ptr(), v_pages.data_ptr(), *ks, *vs, _ptr(k_min), _ptr(k_max),
-            page_table.data_ptr(), _steps(page_table, (0,))[0], self.max_pages, self.num_pages,
-            self.page_size)
+            k_pages.data_ptr(), v_pages.data_ptr(), *k_pages.stride()[:3], *v_pages.stride()[:3],
+            _ptr(k_min), _ptr(k_max), page_table.data_ptr(), page_table.stride(0), self.max_pages,
+            self.num_pages, self.page_size)
 
 
 def _int32_of(t, shape, device, name):
@@ -558,13 +551,20 @@ def _query_of(q, cache):
     return B, Hq, Sq, D
 
 
-def _on(device, stream, call):
+def _raw_here(device) -> Optional[int]:
+    """The raw current stream where `device` is the current device, else None."""
+    import torch
+    if torch.cuda.current_device() != device.index:
+        return None
+    fast = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # a tenth of current_stream()'s time
+    return torch.cuda.current_stream().cuda_stream if fast is None else fast(device.index)
+
+
+def _elsewhere(device, stream, call):
     """call(raw stream) with `device` current and, for a given stream, that stream current too, so
     that what the call allocates belongs to it."""
     import torch
     if stream is None:
-        if torch.cuda.current_device() == device.index:
-            return call(torch.cuda.current_stream().cuda_stream)
         with torch.cuda.device(device):
             return call(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
@@ -621,15 +621,16 @@ def paged_kv_append(cache: PagedKV, kv_lens, k, v, *, new_lens=None, q=None, q_o
 
     def call(raw):
         qo = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q is not None and q_out is None else q_out
-        x = fa_kv_new_t(k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(qo), *_steps(k, (0, 1, 2)),
-                        *_steps(v, (0, 1, 2)), *(_steps(q, (0, 1, 2)) if q is not None else (0, 0, 0)),
-                        *(_steps(qo, (0, 1, 2)) if q is not None else (0, 0, 0)), _ptr(cos), _ptr(sin),
-                        rot, 1 if interleaved else 0, max_pos)
+        none = (0, 0, 0)
+        x = fa_kv_new_t(k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(qo), *k.stride()[:3], *v.stride()[:3],
+                        *(none if q is None else q.stride()[:3]), *(none if q is None else qo.stride()[:3]),
+                        _ptr(cos), _ptr(sin), rot, 1 if interleaved else 0, max_pos)
         _raise(library().fa_kv_append(cache._c, x, B, Hq, Hkv, S, D, cache._flags, kv_lens.data_ptr(),
                                       _ptr(new_lens), raw))
         return qo
 
-    return _on(cache.device, stream, call)
+    raw = _raw_here(cache.device) if stream is None else None
+    return _elsewhere(cache.device, stream, call) if raw is None else call(raw)
 
 
 def flash_attention_decode(q, cache: PagedKV, kv_lens, *, scale: Optional[float] = None,
@@ -669,7 +670,8 @@ def flash_attention_decode(q, cache: PagedKV, kv_lens, *, scale: Optional[float]
                                    _ptr(page_idx), max_sel, raw))
         return o, e
 
-    return _on(cache.device, stream, call)
+    raw = _raw_here(cache.device) if stream is None else None
+    return _elsewhere(cache.device, stream, call) if raw is None else call(raw)
 
 
 def select_kv_pages(q, cache: PagedKV, kv_lens, max_sel: int, *, first: int = 1, last: int = 1,
@@ -695,4 +697,5 @@ def select_kv_pages(q, cache: PagedKV, kv_lens, max_sel: int, *, first: int = 1,
                                          cache._flags, kv_lens.data_ptr(), max_sel, first, last, raw))
         return idx
 
-    return _on(cache.device, stream, call)
+    raw = _raw_here(cache.device) if stream is None else None
+    return _elsewhere(cache.device, stream, call) if raw is None else call(raw)

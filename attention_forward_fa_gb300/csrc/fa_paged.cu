@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include "../../include/fa_fwd.h"
 #include "fa_decode.cuh"
@@ -41,18 +42,23 @@ int validate_cache(const fa_paged_kv_t* kv, int B, int Hq, int Hkv, int S, int D
   return FA_OK;
 }
 
-// The pools: bases and strides (a stride of 0 would lay tokens over each other).
+// A stride that steps over `n` things: refused where negative, 0 (things would share memory) or not
+// a multiple of 8; of no meaning, and any, where there is one thing only.
+int validate_stride(int64_t s, int64_t n, bool may_share) {
+  if (n <= 1) return FA_OK;
+  if (s < 0 || s >= (1LL << 38) || (s == 0 && !may_share)) return FA_ERR_SHAPE;
+  return s % 8 ? FA_ERR_ALIGN : FA_OK;
+}
+
+// The pools: bases and strides.
 int validate_pools(const fa_paged_kv_t* kv, int Hkv) {
   if (!kv->k || !kv->v) return FA_ERR_NULL;
-  for (const int64_t s : {kv->k_stride_page, kv->k_stride_head, kv->k_stride_slot,
-                          kv->v_stride_page, kv->v_stride_head, kv->v_stride_slot}) {
-    if (s < 0 || s >= (1LL << 38)) return FA_ERR_SHAPE;
-    if (s % 8) return FA_ERR_ALIGN;
-  }
-  if (!kv->k_stride_slot || !kv->v_stride_slot ||
-      (Hkv > 1 && (!kv->k_stride_head || !kv->v_stride_head)) ||
-      (kv->num_pages > 1 && (!kv->k_stride_page || !kv->v_stride_page)))
-    return FA_ERR_SHAPE;
+  int rc = FA_OK;
+  for (const auto& [s, n] : {std::pair<int64_t, int64_t>{kv->k_stride_page, kv->num_pages}, {kv->v_stride_page, kv->num_pages},
+                             {kv->k_stride_head, Hkv}, {kv->v_stride_head, Hkv},
+                             {kv->k_stride_slot, kv->page_size}, {kv->v_stride_slot, kv->page_size}})
+    if (rc == FA_OK) rc = validate_stride(s, n, false);
+  if (rc != FA_OK) return rc;
   if (!aligned(kv->k, 16) || !aligned(kv->v, 16)) return FA_ERR_ALIGN;
   return FA_OK;
 }
@@ -90,7 +96,7 @@ bool encode_pool(CUtensorMap* tm, const void* base, bool fp16, int D, int Hkv, c
                  int64_t s_page, int64_t s_head, int64_t s_slot, int box) {
   auto enc = fa_host::tensor_map_encoder();
   if (!enc) return false;
-  // a stride over a single head or page is never stepped; it only has to be valid
+  // a stride over a single head or page is never stepped; for the map it has to be valid
   if (Hkv == 1) s_head = 64;
   if (kv->num_pages == 1) s_page = 64;
   cuuint64_t dims[5] = {64, (cuuint64_t)kv->page_size, (cuuint64_t)(D / 64), (cuuint64_t)Hkv,
@@ -151,13 +157,13 @@ int launch_decode_rows(fa::DecodeParams& p, long long tiles_per_unit, cudaStream
 template <bool BF16, int D>
 int launch_select(fa::SelectParams& p, long long units, cudaStream_t st) {
   const size_t pages = (size_t)units * p.kv.max_pages;
-  uint8_t* scratch = static_cast<uint8_t*>(fa_host::scratch_alloc(pages * 16, st));
+  uint8_t* scratch = static_cast<uint8_t*>(fa_host::scratch_alloc(pages * 24, st));
   if (!scratch) return cuda_fail(cudaGetLastError());
   p.score = reinterpret_cast<float2*>(scratch);
-  p.near = reinterpret_cast<int32_t*>(scratch + pages * 8);
-  p.mark = reinterpret_cast<int32_t*>(scratch + pages * 12);
-  cudaError_t e = launch_dependent(fa::fa_page_score_kernel<BF16, D>, (unsigned)(units * p.chunks),
-                                   32 * fa::kScoreWarps, 0, st, p);
+  p.exact = reinterpret_cast<unsigned long long*>(scratch + pages * 8);
+  p.near = reinterpret_cast<int32_t*>(scratch + pages * 16);
+  p.mark = reinterpret_cast<uint32_t*>(scratch + pages * 20);
+  cudaError_t e = launch_dependent(fa::fa_page_score_kernel<BF16, D>, (unsigned)(units * p.chunks), 32, 0, st, p);
   if (e == cudaSuccess)
     e = launch_dependent(fa::fa_select_kernel<BF16, D>, (unsigned)units, fa::kSelectThreads, 0, st, p);
   cudaFreeAsync(scratch, st);
@@ -180,20 +186,22 @@ int fa_kv_append(const fa_paged_kv_t* kv, const fa_kv_new_t* x, int B, int Hq, i
     return FA_ERR_SHAPE;
   if (x->rot_dim && (!x->cos || !x->sin)) return FA_ERR_NULL;
   if (x->rot_dim && x->max_pos <= 0) return FA_ERR_SHAPE;
-  for (const int64_t s : {x->k_stride_b, x->k_stride_h, x->k_stride_s, x->v_stride_b, x->v_stride_h,
-                          x->v_stride_s}) {
-    if (s < 0) return FA_ERR_SHAPE;
-    if (s % 8) return FA_ERR_ALIGN;
+  rc = FA_OK;
+  auto strides = [&](int64_t sb, int64_t sh, int64_t ss, int heads, bool may_share) {
+    for (const auto& [s, n] : {std::pair<int64_t, int64_t>{sb, B}, {sh, heads}, {ss, Snew}})
+      if (rc == FA_OK) rc = validate_stride(s, n, may_share);
+  };
+  strides(x->k_stride_b, x->k_stride_h, x->k_stride_s, Hkv, true);
+  strides(x->v_stride_b, x->v_stride_h, x->v_stride_s, Hkv, true);
+  if (x->q) {
+    strides(x->q_stride_b, x->q_stride_h, x->q_stride_s, Hq, true);
+    strides(x->qo_stride_b, x->qo_stride_h, x->qo_stride_s, Hq, false);
   }
-  if (x->q)
-    for (const int64_t s : {x->q_stride_b, x->q_stride_h, x->q_stride_s, x->qo_stride_b,
-                            x->qo_stride_h, x->qo_stride_s}) {
-      if (s < 0) return FA_ERR_SHAPE;
-      if (s % 8) return FA_ERR_ALIGN;
-    }
-  if (x->q == x->q_out && x->q &&
-      (x->q_stride_b != x->qo_stride_b || x->q_stride_h != x->qo_stride_h || x->q_stride_s != x->qo_stride_s))
-    return FA_ERR_SHAPE;   // in place only row onto row
+  if (rc != FA_OK) return rc;
+  if (x->q && x->q == x->q_out &&   // in place only row onto row
+      ((B > 1 && x->q_stride_b != x->qo_stride_b) || (Hq > 1 && x->q_stride_h != x->qo_stride_h) ||
+       (Snew > 1 && x->q_stride_s != x->qo_stride_s)))
+    return FA_ERR_SHAPE;
   if (!aligned(x->k, 16) || !aligned(x->v, 16) || !aligned(x->q, 16) || !aligned(x->q_out, 16) ||
       (x->rot_dim && (!aligned(x->cos, 16) || !aligned(x->sin, 16))) || !aligned(kv_lens, 4) ||
       !aligned(new_lens, 4))
@@ -305,7 +313,7 @@ int fa_select_pages(const void* q, const fa_paged_kv_t* kv, int32_t* page_idx, i
   p.q = static_cast<const uint16_t*>(q);
   p.out = page_idx;
   p.kv_lens = kv_lens;
-  p.Hq = Hq;
+  p.B = B;
   p.Hkv = Hkv;
   p.rows = Hq / Hkv * Sq;
   p.max_sel = max_sel;

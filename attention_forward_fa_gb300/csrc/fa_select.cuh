@@ -10,11 +10,14 @@
 //
 // The answer is a list of whole numbers, the one that 64-bit arithmetic gives,
 // while these scores carry fp32 error.  So each page also gets
-// a = |q| . (|max| + |min|), which bounds that error by e = 2^-14 a (at most 32
-// steps of 17 addends, each truncated to 2^-23 of the largest, for 256
-// products), and the second kernel takes what lies more than 2 e above the
-// threshold, drops what lies more than 2 e below, and scores the few in between
-// (two of 2048 on normal data) again in 64 bits.  Why that is right: let T be
+// a = |q| . (|max| + |min|), which bounds that error by e = 2^-17 a: two matrix
+// instructions at a time start from zero and truncate their addends, exact
+// products and the sum so far, to 2^-23 of the largest (33 2^-23 of the sum of
+// magnitudes at most), and up to 8 such pairs are added with 2^-24 each;
+// (66 + 8) 2^-24 < 2^-17.  (One accumulator through all of them would need 2^-14,
+// and leave four pages of 2048 in doubt instead of one half.)  The
+// second kernel takes what lies more than 2 e above the threshold, drops what
+// lies more than 2 e below, and scores what is in between again in 64 bits.  Why that is right: let T be
 // the k-th largest approximate score and E the k-th largest exact one.  Moving
 // each value by at most e moves the k-th largest by at most e, so |E - T| <= e;
 // a score above T + 2 e is exactly above T + e >= E, one below T - 2 e below E.
@@ -28,98 +31,139 @@ struct SelectParams {
   const uint16_t* q;
   int32_t* out;
   const int32_t* kv_lens;
-  float2* score;          // [B * Hkv, max_pages]: score, error scale; later 64-bit scores of the near ones
-  int32_t* near;          // [B * Hkv, max_pages]: pages near the threshold
-  int32_t* mark;          // [B * Hkv, max_pages]: of those, which are taken
-  int Hq, Hkv, rows, max_sel, first, last;   // rows = G * Sq
-  int chunks;             // blocks of pages per (sequence, KV head)
+  float2* score;          // [B * Hkv, max_pages]: score, error scale
+  unsigned long long* exact;   // [B * Hkv, max_pages] each: what does not fit shared memory of the pages
+  int32_t* near;          //   near the threshold: their 64-bit scores, their numbers and (a bit each)
+  uint32_t* mark;         //   which of them are taken
+  int B, Hkv, rows, max_sel, first, last;   // rows = G * Sq
+  int chunks;             // blocks per (sequence, KV head)
   int* status;
 };
 
-constexpr int kScoreWarps = 4;
-constexpr int kScorePages = 16 * kScoreWarps;   // pages per block
+constexpr int kScoreGroups = 3;                 // groups of 16 pages per block of one warp
+constexpr int kScorePages = 16 * kScoreGroups;
 constexpr int kSelectThreads = 512;
 constexpr int kSelectCached = 8192;             // scores kept in shared memory
-constexpr float kScoreEps = 1.f / 16384.f;
+constexpr int kNearCached = 256;                // and pages near the threshold
+constexpr float kScoreEps = 1.f / 131072.f;
 
 __device__ __forceinline__ int select_pages_of(const PagedKv& c, int len) {
   if (len < 0 || len > (c.max_pages << c.page_shift)) return 0;
   return (len + (1 << c.page_shift) - 1) >> c.page_shift;
 }
 
+// One warp per block of 48 pages.  Each lane copies to shared memory, all at once, the very 16-byte
+// pieces that it will feed to the matrix instructions, so that nothing has to be exchanged and no
+// register waits for memory: 24 KB in flight per warp (D 128), nine warps per SM, and three
+// independent chains of matrix instructions per warp.  (Measured with the second kernel, 2048 pages
+// of 64 (sequence, KV head) pairs, D 128: bounds loaded to registers, 12 warps of 8 KB per SM, 38.6
+// us; one long run of groups per warp through a ring of three, one chain at a time, 31.1 us; this
+// 28.1 us.)
 template <bool BF16, int D>
-__global__ void __launch_bounds__(32 * kScoreWarps) fa_page_score_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(32) fa_page_score_kernel(const SelectParams p) {
   constexpr int C = D / 32;
-  pdl_launch_dependents();
+  __shared__ __align__(16) uint4 s_in[kScoreGroups][2][2][C][32];   // [group][bound][page half][step][lane]
   pdl_wait_prior();
+  pdl_launch_dependents();   // (after the wait: the next kernel may read the lengths as it starts)
   const int unit = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
   const int b = unit / p.Hkv, hk = unit % p.Hkv;
   const int n = select_pages_of(p.kv, p.kv_lens[b]);
-  if (chunk == 0 && hk == 0 && threadIdx.x == 0) (void)paged_len(p.kv, p.kv_lens[b], p.status);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-  const int s0 = chunk * kScorePages + warp * 16;
-  if (s0 >= n) return;
-  // pages s0 + g and s0 + g + 8: 8 channels at 32 c + 8 t4 of either bound
-  uint4 mn[2][C], mx[2][C];
-  bool good[2];
+  const int lane = threadIdx.x, g = lane >> 2, t4 = lane & 3;
+  if (chunk == 0 && hk == 0 && lane == 0) (void)paged_len(p.kv, p.kv_lens[b], p.status);
+  const int first = chunk * kScorePages;
+  if (first >= n) return;
+  const int last = min(n, first + kScorePages);
+  int ids[(kScorePages + 31) / 32];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int s = s0 + g + 8 * j;
-    const int id = s < n ? paged_id(p.kv, b, s, p.status) : -1;
-    good[j] = id >= 0;
-    const long long at = ((long long)max(id, 0) * p.Hkv + hk) * D + 8 * t4;
+  for (int i = 0; i < (kScorePages + 31) / 32; ++i)
+    ids[i] = first + 32 * i + lane < last ? paged_id(p.kv, b, first + 32 * i + lane, p.status) : -1;
+  // of pages 16 group + g and + 8: 8 channels at 32 c + 8 t4 of either bound
+  bool good[kScoreGroups][2];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      mn[j][c] = good[j] ? __ldg(reinterpret_cast<const uint4*>(p.kv.k_min + at + 32 * c)) : make_uint4(0, 0, 0, 0);
-      mx[j][c] = good[j] ? __ldg(reinterpret_cast<const uint4*>(p.kv.k_max + at + 32 * c)) : make_uint4(0, 0, 0, 0);
-    }
-  }
-  const uint16_t* q = p.q + ((long long)b * p.Hq * (p.rows / (p.Hq / p.Hkv)) + (long long)hk * p.rows) * D + 8 * t4;
-  float best[2] = {-INFINITY, -INFINITY}, scale[2] = {0.f, 0.f};
-  bool odd[2] = {false, false};       // a score that is not finite: only 64 bits can tell
-  auto magnitude = [](uint32_t x) { return x & 0x7FFF7FFFu; };
-  for (int r0 = 0; r0 < p.rows; r0 += 8) {
-    float acc[4] = {0.f, 0.f, 0.f, 0.f}, err[4] = {0.f, 0.f, 0.f, 0.f};
-    const bool on = r0 + g < p.rows;
+  for (int gr = 0; gr < kScoreGroups; ++gr) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const uint4 w = on ? __ldg(reinterpret_cast<const uint4*>(q + (long long)(r0 + g) * D + 32 * c)) : make_uint4(0, 0, 0, 0);
-      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-      const uint32_t lo[2][4] = {{mn[0][c].x, mn[0][c].y, mn[0][c].z, mn[0][c].w}, {mn[1][c].x, mn[1][c].y, mn[1][c].z, mn[1][c].w}};
-      const uint32_t hi[2][4] = {{mx[0][c].x, mx[0][c].y, mx[0][c].z, mx[0][c].w}, {mx[1][c].x, mx[1][c].y, mx[1][c].z, mx[1][c].w}};
+    for (int j = 0; j < 2; ++j) {
+      const int id = __shfl_sync(0xffffffffu, ids[gr / 2], 16 * (gr & 1) + g + 8 * j);
+      good[gr][j] = id >= 0;
+      if (id < 0) continue;        // (its stale bounds reach no other page's products)
+      const long long at = ((long long)id * p.Hkv + hk) * D + 8 * t4;
 #pragma unroll
-      for (int h = 0; h < 4; h += 2) {
-        const uint32_t ah[4] = {hi[0][h], hi[1][h], hi[0][h + 1], hi[1][h + 1]};
-        const uint32_t al[4] = {lo[0][h], lo[1][h], lo[0][h + 1], lo[1][h + 1]};
-        mma_16x8<BF16>(acc, ah, max16x2<BF16>(x[h], 0u), max16x2<BF16>(x[h + 1], 0u));
-        mma_16x8<BF16>(acc, al, min16x2<BF16>(x[h], 0u), min16x2<BF16>(x[h + 1], 0u));
-        const uint32_t bh[4] = {magnitude(ah[0]), magnitude(ah[1]), magnitude(ah[2]), magnitude(ah[3])};
-        const uint32_t bl[4] = {magnitude(al[0]), magnitude(al[1]), magnitude(al[2]), magnitude(al[3])};
-        mma_16x8<BF16>(err, bh, magnitude(x[h]), magnitude(x[h + 1]));
-        mma_16x8<BF16>(err, bl, magnitude(x[h]), magnitude(x[h + 1]));
+      for (int c = 0; c < C; ++c) {
+        cp_async16(smem_u32(&s_in[gr][0][j][c][lane]), p.kv.k_min + at + 32 * c);
+        cp_async16(smem_u32(&s_in[gr][1][j][c][lane]), p.kv.k_max + at + 32 * c);
       }
     }
-    // lane (g, t4): pages g (0, 1) and g + 8 (2, 3), rows 2 t4 and 2 t4 + 1
+    cp_async_commit();
+  }
+  const uint16_t* q = p.q + (long long)unit * p.rows * D + 8 * t4;   // [B, Hkv, rows, D]
+  auto magnitude = [](uint32_t x) { return x & 0x7FFF7FFFu; };
+  float best[kScoreGroups][2], scale[kScoreGroups][2];
+  bool odd[kScoreGroups][2];       // a score that is not finite: only 64 bits can tell
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (r0 + 2 * t4 + (e & 1) >= p.rows) continue;
-      best[e >> 1] = fmaxf(best[e >> 1], acc[e]);
-      scale[e >> 1] = fmaxf(scale[e >> 1], err[e]);
-      odd[e >> 1] |= !(fabsf(acc[e]) < INFINITY) || !(err[e] < INFINITY);
+  for (int gr = 0; gr < kScoreGroups; ++gr)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) best[gr][j] = -INFINITY, scale[gr][j] = 0.f, odd[gr][j] = false;
+  for (int r0 = 0; r0 < p.rows; r0 += 8) {
+    uint4 w[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      w[c] = r0 + g < p.rows ? __ldg(reinterpret_cast<const uint4*>(q + (long long)(r0 + g) * D + 32 * c)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int gr = 0; gr < kScoreGroups; ++gr) {
+      if (r0 == 0) {               // (every lane waits for its own copies only)
+        if (gr == 0) asm volatile("cp.async.wait_group %0;" ::"n"(kScoreGroups - 1) : "memory");
+        else if (gr == 1) asm volatile("cp.async.wait_group %0;" ::"n"(kScoreGroups - 2) : "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+      }
+      float acc[4] = {0.f, 0.f, 0.f, 0.f}, err[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const uint4 l0 = s_in[gr][0][0][c][lane], l1 = s_in[gr][0][1][c][lane];
+        const uint4 h0 = s_in[gr][1][0][c][lane], h1 = s_in[gr][1][1][c][lane];
+        const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+        const uint32_t lo[2][4] = {{l0.x, l0.y, l0.z, l0.w}, {l1.x, l1.y, l1.z, l1.w}};
+        const uint32_t hi[2][4] = {{h0.x, h0.y, h0.z, h0.w}, {h1.x, h1.y, h1.z, h1.w}};
+#pragma unroll
+        for (int h = 0; h < 4; h += 2) {
+          const uint32_t ah[4] = {hi[0][h], hi[1][h], hi[0][h + 1], hi[1][h + 1]};
+          const uint32_t al[4] = {lo[0][h], lo[1][h], lo[0][h + 1], lo[1][h + 1]};
+          float u[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};   // from zero: see the bound above
+          mma_16x8<BF16>(u, ah, max16x2<BF16>(x[h], 0u), max16x2<BF16>(x[h + 1], 0u));
+          mma_16x8<BF16>(u, al, min16x2<BF16>(x[h], 0u), min16x2<BF16>(x[h + 1], 0u));
+          const uint32_t bh[4] = {magnitude(ah[0]), magnitude(ah[1]), magnitude(ah[2]), magnitude(ah[3])};
+          const uint32_t bl[4] = {magnitude(al[0]), magnitude(al[1]), magnitude(al[2]), magnitude(al[3])};
+          mma_16x8<BF16>(v, bh, magnitude(x[h]), magnitude(x[h + 1]));
+          mma_16x8<BF16>(v, bl, magnitude(x[h]), magnitude(x[h + 1]));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] += u[e], err[e] += v[e];
+        }
+      }
+      // lane (g, t4): pages g (0, 1) and g + 8 (2, 3), rows 2 t4 and 2 t4 + 1
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (r0 + 2 * t4 + (e & 1) >= p.rows) continue;
+        best[gr][e >> 1] = fmaxf(best[gr][e >> 1], acc[e]);
+        scale[gr][e >> 1] = fmaxf(scale[gr][e >> 1], err[e]);
+        odd[gr][e >> 1] |= !(fabsf(acc[e]) < INFINITY) || !(err[e] < INFINITY);
+      }
     }
   }
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int gr = 0; gr < kScoreGroups; ++gr) {
 #pragma unroll
-    for (int w = 1; w < 4; w <<= 1) {
-      best[j] = fmaxf(best[j], __shfl_xor_sync(0xffffffffu, best[j], w));
-      scale[j] = fmaxf(scale[j], __shfl_xor_sync(0xffffffffu, scale[j], w));
-      odd[j] |= __shfl_xor_sync(0xffffffffu, (int)odd[j], w) != 0;
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int x = 1; x < 4; x <<= 1) {
+        best[gr][j] = fmaxf(best[gr][j], __shfl_xor_sync(0xffffffffu, best[gr][j], x));
+        scale[gr][j] = fmaxf(scale[gr][j], __shfl_xor_sync(0xffffffffu, scale[gr][j], x));
+        odd[gr][j] |= __shfl_xor_sync(0xffffffffu, (int)odd[gr][j], x) != 0;
+      }
+      const int s = first + 16 * gr + g + 8 * j;
+      if (t4 == 0 && s < last)      // a page that is none scores below all others
+        p.score[(long long)unit * p.kv.max_pages + s] =
+            good[gr][j] ? make_float2(odd[gr][j] ? 0.f : best[gr][j], odd[gr][j] ? INFINITY : scale[gr][j])
+                        : make_float2(-INFINITY, 0.f);
     }
-    const int s = s0 + g + 8 * j;
-    if (t4 == 0 && s < n)      // a page that is none scores below all others
-      p.score[(long long)unit * p.kv.max_pages + s] =
-          good[j] ? make_float2(odd[j] ? 0.f : best[j], odd[j] ? INFINITY : scale[j]) : make_float2(-INFINITY, 0.f);
   }
 }
 
@@ -137,19 +181,23 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kSelectThreads) fa_select_kernel(const SelectParams p) {
   constexpr int kWarps = kSelectThreads / 32;
-  constexpr int E = D / 32;
+  constexpr int E = D / 32;   // channels per lane
   __shared__ uint32_t s_key[kSelectCached];
   __shared__ int s_hist[256];
-  __shared__ int s_warp[kWarps];
+  __shared__ int2 s_warp[kWarps];
+  __shared__ unsigned long long s_exact[kNearCached];
+  __shared__ int32_t s_list[kNearCached];
+  __shared__ uint32_t s_mark[kNearCached / 32 + 1];
   __shared__ float s_top[kWarps];
+  __shared__ uint32_t s_lo[kWarps], s_hi[kWarps];
   __shared__ uint32_t s_prefix;
-  __shared__ int s_left, s_near;
-  pdl_launch_dependents();
-  pdl_wait_prior();
+  __shared__ int s_left;
   const int unit = blockIdx.x;
   const int b = unit / p.Hkv, hk = unit % p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n = select_pages_of(p.kv, p.kv_lens[b]);
+  const int n = select_pages_of(p.kv, __ldcg(p.kv_lens + b));
+  pdl_launch_dependents();
+  pdl_wait_prior();
   int32_t* out = p.out + (long long)unit * p.max_sel;
   if (n <= p.max_sel) {
     for (int s = tid; s < p.max_sel; s += kSelectThreads) out[s] = s < n ? s : -1;
@@ -160,26 +208,42 @@ __global__ void __launch_bounds__(kSelectThreads) fa_select_kernel(const SelectP
   const int lo_s = p.first, hi_s = n - p.last;     // the pages that compete: more than `want`
   const int want = p.max_sel - p.first - p.last;
   float eps = 0.f;
+  uint32_t kmin = 0xffffffffu, kmax = 0;
   for (int s = lo_s + tid; s < hi_s; s += kSelectThreads) {
     const float2 x = score[s];
+    const uint32_t k = ordered(x.x);
     eps = fmaxf(eps, x.y);
-    if (s - lo_s < kSelectCached) s_key[s - lo_s] = ordered(x.x);
+    kmin = min(kmin, k);
+    kmax = max(kmax, k);
+    if (s - lo_s < kSelectCached) s_key[s - lo_s] = k;
   }
 #pragma unroll
   for (int w = 16; w; w >>= 1) eps = fmaxf(eps, __shfl_xor_sync(0xffffffffu, eps, w));
-  if (lane == 0) s_top[warp] = eps;
-  if (tid == 0) s_prefix = 0, s_left = want, s_near = 0;
+  kmin = __reduce_min_sync(0xffffffffu, kmin);
+  kmax = __reduce_max_sync(0xffffffffu, kmax);
+  if (lane == 0) s_top[warp] = eps, s_lo[warp] = kmin, s_hi[warp] = kmax;
+  if (tid < 256) s_hist[tid] = 0;
+  if (tid == 0) s_left = want;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    eps = fmaxf(eps, s_top[w]);
+    kmin = min(kmin, s_lo[w]);
+    kmax = max(kmax, s_hi[w]);
+  }
   auto key = [&](int s) { return s - lo_s < kSelectCached ? s_key[s - lo_s] : ordered(score[s].x); };
 
-  // the want-th largest key, eight bits at a time
-  if (want > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) s_hist[tid] = 0;
-      __syncthreads();
-      const uint32_t prefix = s_prefix;
+  // the want-th largest key, up to eight bits at a time below the bits that all keys share
+  // (scores have few exponents: without that the first passes would count into one place)
+  uint32_t prefix = kmin;
+  if (want > 0 && kmin != kmax) {
+    int bits = 32 - __clz(kmin ^ kmax);              // undecided
+    prefix = bits < 32 ? kmin >> bits : 0;
+    while (bits > 0) {
+      const int w = min(bits, 8), shift = bits - w;
       for (int s = lo_s + tid; s < hi_s; s += kSelectThreads) {
         const uint32_t k = key(s);
-        if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&s_hist[(k >> shift) & 255], 1);
+        if (bits == 32 || (k >> bits) == prefix) atomicAdd(&s_hist[(k >> shift) & ((1u << w) - 1)], 1);
       }
       __syncthreads();
       if (warp == 0) {   // lane i has digits 255 - 8 i down to 248 - 8 i
@@ -199,34 +263,34 @@ __global__ void __launch_bounds__(kSelectThreads) fa_select_kernel(const SelectP
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             if (above < left && left <= above + c[e]) {
-              s_prefix = (prefix << 8) | (uint32_t)(255 - 8 * lane - e);
+              s_prefix = (prefix << w) | (uint32_t)(255 - 8 * lane - e);
               s_left = left - above;
               break;
             }
             above += c[e];
           }
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_hist[255 - 8 * lane - e] = 0;
       }
       __syncthreads();
+      prefix = s_prefix;
+      bits = shift;
     }
-  } else {
-    __syncthreads();
   }
-  eps = 0.f;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) eps = fmaxf(eps, s_top[w]);
-  // in 64 bits, so that the rounding of the limits adds nothing
-  const double mid = want > 0 ? (double)unordered(s_prefix) : INFINITY;
-  const double two = 2.0 * (kScoreEps * (double)eps + 0x1p-100);   // (products may underflow)
+  // the limits, rounded outwards, as keys (a zero limit takes the sign that keeps zeros near)
+  const float mid = unordered(prefix);
+  const float two = __fmul_ru(2.f * kScoreEps, eps) + 0x1p-100f;   // (products may underflow)
   const bool blind = !(two < INFINITY);           // a bound that is not finite: all of them in 64 bits
-  const double above = mid + two, below = mid - two;
+  const float up = __fadd_ru(mid, two), down = __fadd_rd(mid, -two);
+  const uint32_t above = ordered(up == 0.f ? 0.f : up), below = ordered(down == 0.f ? -0.f : down);
   // 0: out, 1: taken, 2: near.  A page that is none (-inf) is never near a finite threshold.
   auto kind = [&](int s) {
     if (s < lo_s || s >= hi_s) return 1;
     if (want == 0) return 0;
     if (blind) return 2;
-    const double x = (double)unordered(key(s));
-    return x > above ? 1 : x >= below ? 2 : 0;
+    const uint32_t k = key(s);
+    return k > above ? 1 : k >= below ? 2 : 0;
   };
   // each thread has a run of pages, so that counts in thread order are counts in page order
   const int run = (n + kSelectThreads - 1) / kSelectThreads;
@@ -237,79 +301,80 @@ __global__ void __launch_bounds__(kSelectThreads) fa_select_kernel(const SelectP
     sure += k == 1;
     near += k == 2;
   }
-  int packed = __reduce_add_sync(0xffffffffu, sure);
-  if (lane == 0) s_warp[warp] = packed;
-  if (near) atomicAdd(&s_near, near);
-  __syncthreads();
-  int n_sure = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) n_sure += s_warp[w];
-  const int n_near = s_near;
-  const int take = p.max_sel - n_sure;            // of the near ones
-  __syncthreads();
-  if (n_near > take) {                            // (block-uniform) some of them have to go
-    if (tid == 0) s_near = 0;
-    __syncthreads();
-    for (int s = a0; s < a1; ++s)
-      if (kind(s) == 2) p.near[base + atomicAdd(&s_near, 1)] = s;
-    __syncthreads();
-    double* exact = reinterpret_cast<double*>(p.score + base);   // by place in the list, over scores that ...
-    const uint16_t* q = p.q + ((long long)b * p.Hq * (p.rows / (p.Hq / p.Hkv)) + (long long)hk * p.rows) * D + E * lane;
-    // ... pages past the cached ones still need: their kinds are kept in `mark` first
-    for (int s = a0; s < a1; ++s) p.mark[base + s] = kind(s) == 1;
-    __syncthreads();
-    for (int i = warp; i < n_near; i += kWarps) {
-      const int s = p.near[base + i];
-      const int id = p.kv.table[(long long)b * p.kv.table_stride + s];
-      double best = -INFINITY;
-      if (id >= 0 && id < p.kv.num_pages) {
-        const long long at = ((long long)id * p.Hkv + hk) * D + E * lane;
-        double mn[E], mx[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          mn[e] = lo16_f32<BF16>(p.kv.k_min[at + e]);
-          mx[e] = lo16_f32<BF16>(p.kv.k_max[at + e]);
-        }
-        for (int r = 0; r < p.rows; ++r) {
-          double x = 0.;
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const double w = lo16_f32<BF16>(q[(long long)r * D + e]);
-            x += w > 0. ? w * mx[e] : w * mn[e];
-          }
-#pragma unroll
-          for (int w = 16; w; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-          best = fmax(best, x);
-        }
-      }
-      if (lane == 0) exact[i] = best;
-    }
-    __syncthreads();
-    for (int i = tid; i < n_near; i += kSelectThreads) {
-      const double x = exact[i];
-      const int s = p.near[base + i];
-      int before = 0;
-      for (int j = 0; j < n_near; ++j) before += exact[j] > x || (exact[j] == x && p.near[base + j] < s);
-      if (before < take) p.mark[base + s] = 1;
-    }
-    __syncthreads();
-  }
-  const bool marked = n_near > take;
-  auto taken = [&](int s) { return marked ? p.mark[base + s] != 0 : kind(s) != 0; };
-  int mine = 0;
-  for (int s = a0; s < a1; ++s) mine += taken(s);
-  int inc = mine;
+  int2 inc = make_int2(sure, near);
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, inc, d);
-    if (lane >= d) inc += x;
+    const int x = __shfl_up_sync(0xffffffffu, inc.x, d), y = __shfl_up_sync(0xffffffffu, inc.y, d);
+    if (lane >= d) inc.x += x, inc.y += y;
   }
   if (lane == 31) s_warp[warp] = inc;
+  if (tid <= kNearCached / 32) s_mark[tid] = 0;
   __syncthreads();
-  int place = inc - mine;
-  for (int w = 0; w < warp; ++w) place += s_warp[w];
-  for (int s = a0; s < a1; ++s)
-    if (taken(s) && place < p.max_sel) out[place++] = s;
+  int n_sure = 0, n_near = 0, place = inc.x - sure, near0 = inc.y - near;   // of all, and before this run
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int2 x = s_warp[w];
+    n_sure += x.x;
+    n_near += x.y;
+    if (w < warp) place += x.x, near0 += x.y;
+  }
+  const int take = p.max_sel - n_sure;                 // of the near ones
+  const bool choose = n_near > take;                   // (block-uniform) some of them have to go
+  const bool small = n_near <= kNearCached;
+  unsigned long long* exact = small ? s_exact : p.exact + base;
+  int32_t* list = small ? s_list : p.near + base;
+  uint32_t* mark = small ? s_mark : p.mark + base;
+  if (choose) {
+    for (int s = a0, i = near0; s < a1; ++s)
+      if (kind(s) == 2) exact[i] = 0, list[i++] = s;
+    if (!small)
+      for (int i = tid; i < (n_near + 31) / 32; i += kSelectThreads) mark[i] = 0;
+    __syncthreads();
+    // a warp per page and row; the rows' maximum as an ordered number
+    const uint16_t* q = p.q + (long long)unit * p.rows * D + E * lane;
+    for (long long i = warp; i < (long long)n_near * p.rows; i += kWarps) {
+      const int at_list = (int)(i / p.rows), r = (int)(i % p.rows);
+      const int id = p.kv.table[(long long)b * p.kv.table_stride + list[at_list]];
+      if (id < 0 || id >= p.kv.num_pages) continue;      // below all others
+      const long long at = ((long long)id * p.Hkv + hk) * D + E * lane;
+      double x = 0.;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const uint32_t wq = *reinterpret_cast<const uint32_t*>(q + (long long)r * D + e);
+        const uint32_t lo = *reinterpret_cast<const uint32_t*>(p.kv.k_min + at + e);
+        const uint32_t hi = *reinterpret_cast<const uint32_t*>(p.kv.k_max + at + e);
+        const float q0 = lo16_f32<BF16>(wq), q1 = hi16_f32<BF16>(wq);
+        x = fma((double)q0, (double)(q0 > 0.f ? lo16_f32<BF16>(hi) : lo16_f32<BF16>(lo)), x);
+        x = fma((double)q1, (double)(q1 > 0.f ? hi16_f32<BF16>(hi) : hi16_f32<BF16>(lo)), x);
+      }
+#pragma unroll
+      for (int w = 16; w; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
+      if (lane == 0) {
+        const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.);   // (-0 as 0)
+        atomicMax(exact + at_list, u >> 63 ? ~u : u | 0x8000000000000000ull);
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < n_near; i += kSelectThreads) {   // the list is in page order
+      const unsigned long long x = exact[i];
+      int ahead = 0;
+      for (int j = 0; j < n_near; ++j) ahead += exact[j] > x || (exact[j] == x && j < i);
+      if (ahead < take) atomicOr(&mark[i >> 5], 1u << (i & 31));
+    }
+    __syncthreads();
+  }
+  if (choose) {
+    for (int w = 0; w < near0 >> 5; ++w) place += __popc(mark[w]);
+    place += __popc(mark[near0 >> 5] & ((1u << (near0 & 31)) - 1));
+  } else {
+    place += near0;
+  }
+  for (int s = a0, i = near0; s < a1; ++s) {
+    const int k = kind(s);
+    const bool in = k == 1 || (k == 2 && (!choose || (mark[i >> 5] >> (i & 31) & 1)));
+    i += k == 2;
+    if (in && place < p.max_sel) out[place++] = s;
+  }
 }
 
 }  // namespace fa

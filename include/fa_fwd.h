@@ -393,8 +393,8 @@ int fa_convert_v_fp16(const void* v_bf16, void* v_fp16, int64_t n_elems, void* s
 
 /* The cache (host struct).  Element (page, head, slot, d) of K is
  *   k[page * k_stride_page + head * k_stride_head + slot * k_stride_slot + d],
- * V alike; strides in elements, multiples of 8, positive where there is more
- * than one to step over, below 2^38; bases 16-byte aligned.  Any order of page,
+ * V alike; strides in elements, multiples of 8, positive, below 2^38 (a stride
+ * over one page or head is not looked at); bases 16-byte aligned.  Any order of page,
  * head and slot is thus a cache (a [pages, slots, heads, D] pool, K and V halves
  * of one pool) as long as no two tokens share memory.  page_size: 16, 32, 64, 128 or 256;
  * max_pages entries per sequence, max_pages * page_size <= 2^31 - 65536.
@@ -417,8 +417,9 @@ typedef struct {
 
 /* New tokens (host struct).  Element (b, h, i, d) of k, v (h < Hkv), q and
  * q_out (h < Hq) at base[b * stride_b + h * stride_h + i * stride_s + d];
- * strides in elements, >= 0, multiples of 8; bases 16-byte aligned.  q and
- * q_out NULL: keys and values only.  q_out may be q itself (same strides).
+ * strides in elements, >= 0 (q_out: positive), multiples of 8, below 2^38 (one
+ * over a size of 1 is not looked at); bases 16-byte aligned.  q and q_out NULL:
+ * keys and values only.  q_out may be q itself (same strides).
  * cos, sin: fp32 [max_pos, rot_dim / 2], contiguous, 16-byte aligned, row p the
  * angles of position p; rot_dim a multiple of 16, 0 <= rot_dim <= D; 0 (tables
  * NULL) rotates nothing.  interleaved 0: channel j < rot_dim / 2 turns with
@@ -503,7 +504,7 @@ int fa_decode(const void* q, const fa_paged_kv_t* kv, void* o, float* lse, int B
  * numbers in ascending order, then -1.  The choice is that of scores in 64-bit
  * arithmetic.  kv_lens as fa_decode; q [B, Hq, Sq, D] contiguous; q and the
  * bounds of a sequence's pages must be finite, k_min <= k_max.  first, last >= 0, first + last <= max_sel <= 2^20.
- * Scratch: stream-ordered, 16 bytes per (sequence, KV head, page
+ * Scratch: stream-ordered, 24 bytes per (sequence, KV head, page
  * table column).
  */
 int fa_select_pages(const void* q, const fa_paged_kv_t* kv, int32_t* page_idx, int B, int Hq,

@@ -72,7 +72,7 @@ def select(kv=None, **kw):
 
 
 def append(kv=None, new=None, **kw):
-    a = dict(B=1, Hq=8, Hkv=2, S=1, D=128, mask_mode=0, kv_lens=P, new_lens=None)
+    a = dict(B=2, Hq=8, Hkv=2, S=3, D=128, mask_mode=0, kv_lens=P, new_lens=None)
     a.update(kw)
     n = dict(k=P, v=P, q=P, q_out=P, cos=P, sin=P, rot_dim=64, interleaved=0, max_pos=100)
     n.update({f"{t}_stride_{d}": 1024 for t in ("k", "v", "q", "qo") for d in "bhs"})
@@ -131,6 +131,7 @@ def test_select_needs_bounds():
     (dict(interleaved=2), {}, -2), (dict(max_pos=0), {}, -2), (dict(k_stride_b=-8), {}, -2),
     (dict(q_stride_s=-8), {}, -2), (dict(qo_stride_s=2048), {}, -2),
     (dict(k_stride_s=1020), {}, -4), (dict(v_stride_h=4), {}, -4), (dict(q_stride_b=4, qo_stride_b=4), {}, -4),
+    (dict(q_out=P + 16, qo_stride_s=0), {}, -2), (dict(v_stride_b=1 << 38), {}, -2),
     (dict(k=P + 8), {}, -4), (dict(q=P + 8), {}, -4), (dict(cos=P + 4), {}, -4),
     ({}, dict(new_lens=P + 1), -4), ({}, dict(B=1 << 30, S=1 << 10), -2),
 ])
