@@ -14,6 +14,7 @@
 namespace fa {
 
 constexpr int kAppendThreads = 256;
+constexpr int kBatch = 2;      // rows per thread in flight (queries: heads, values: tokens)
 
 struct AppendParams {
   PagedKv kv;
@@ -30,13 +31,13 @@ struct AppendParams {
   int Hq, Hkv, Snew;
   int chunks;              // pages that one sequence's new tokens can touch
   int tp_shift;            // tokens per step = 1 << tp_shift
-  int kv_heads, q_heads;   // heads per block of the K / V and the Q blocks
+  int q_heads;             // heads per block of the Q blocks (the K and V blocks: those of one step)
   int k_items, q_items;    // blocks per page for K (V as many), for Q
   int* status;
 };
 
 template <bool BF16, int D>
-__global__ void __launch_bounds__(kAppendThreads) fa_kv_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const AppendParams p) {
   constexpr int L = D / 16;                    // threads per row
   constexpr int kRows = kAppendThreads / L;    // rows per step
   __shared__ uint4 s_red[4][8][L];             // [min A, min B, max A, max B][warp][thread of the row]
@@ -48,11 +49,11 @@ __global__ void __launch_bounds__(kAppendThreads) fa_kv_append_kernel(const Appe
   const int chunk = rest % p.chunks, b = rest / p.chunks;
 
   const int ps_shift = p.kv.page_shift, ps = 1 << ps_shift;
-  const int n0 = p.new_lens ? p.new_lens[b] : p.Snew;
+  const int n0 = p.new_lens ? p.new_lens[b] : p.Snew, len0 = p.kv_lens[b];
   const int n_new = min(max(n0, 0), p.Snew);
   if (n0 != n_new && threadIdx.x == 0) atomicOr(p.status, fa_host::kStatusIndex);
   if (n_new == 0) return;
-  const int before = paged_len(p.kv, p.kv_lens[b], p.status);
+  const int before = paged_len(p.kv, len0, p.status);
   if (before < 0) return;
   const int page = (before >> ps_shift) + chunk;
   // tokens [t0, t1) of the sequence, by position (64 bits: `before` may be near 2^31)
@@ -65,8 +66,13 @@ __global__ void __launch_bounds__(kAppendThreads) fa_kv_append_kernel(const Appe
   }
   const int t0 = max(before, (int)p0);
   int t1 = (int)end;
-  const int id = paged_id(p.kv, b, page, p.status);
-  if (id < 0) return;
+  // (looked at only before the first store: the loads of the tokens do not wait for it)
+  const int id = p.kv.table[(long long)b * p.kv.table_stride + page];
+  auto no_page = [&]() {
+    if (id >= 0 && id < p.kv.num_pages) return false;
+    atomicOr(p.status, fa_host::kStatusIndex);
+    return true;
+  };
   if (p.rot_dim && t1 > p.max_pos) {
     if (threadIdx.x == 0) atomicOr(p.status, fa_host::kStatusIndex);
     t1 = p.max_pos;
@@ -128,30 +134,51 @@ __global__ void __launch_bounds__(kAppendThreads) fa_kv_append_kernel(const Appe
     const int h0 = (item - 2 * p.k_items) * p.q_heads;
     const int h1 = min(p.Hq, h0 + p.q_heads);
     for (int t = t0 + tl; t < t1; t += tp) {
-      angles(t);
       const uint16_t* src = p.q + b * p.q_sb + (long long)(t - before) * p.q_ss;
       uint16_t* dst = p.qo + b * p.o_sb + (long long)(t - before) * p.o_ss;
-      for (int h = h0 + hl; h < h1; h += hp) {
-        // plain loads: q_out may be q
-        uint4 wa = *reinterpret_cast<const uint4*>(src + h * p.q_sh + offA);
-        uint4 wb = *reinterpret_cast<const uint4*>(src + h * p.q_sh + offB);
-        rotate(wa, wb);
-        st(dst + h * p.o_sh + offA, wa);
-        st(dst + h * p.o_sh + offB, wb);
+      angles(t);
+      for (int h = h0 + hl; h < h1; h += kBatch * hp) {
+        uint4 wa[kBatch], wb[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          if (h + i * hp >= h1) break;
+          // plain loads: q_out may be q
+          wa[i] = *reinterpret_cast<const uint4*>(src + (h + i * hp) * p.q_sh + offA);
+          wb[i] = *reinterpret_cast<const uint4*>(src + (h + i * hp) * p.q_sh + offB);
+        }
+        if (no_page()) return;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          if (h + i * hp >= h1) break;
+          rotate(wa[i], wb[i]);
+          st(dst + (h + i * hp) * p.o_sh + offA, wa[i]);
+          st(dst + (h + i * hp) * p.o_sh + offB, wb[i]);
+        }
       }
     }
     return;
   }
   if (item >= p.k_items) {       // ---------------- values: copied
-    const int h0 = (item - p.k_items) * p.kv_heads;
-    const int h1 = min(p.Hkv, h0 + p.kv_heads);
-    for (int t = t0 + tl; t < t1; t += tp) {
-      const uint16_t* src = p.v + b * p.v_sb + (long long)(t - before) * p.v_ss;
-      uint16_t* dst = p.kv.v + (long long)id * p.kv.v_sp + (long long)(t & (ps - 1)) * p.kv.v_ss;
-      for (int h = h0 + hl; h < h1; h += hp) {
-        const uint4 wa = ld(src + h * p.v_sh + 16 * part), wb = ld(src + h * p.v_sh + 16 * part + 8);
-        st(dst + h * p.kv.v_sh + 16 * part, wa);
-        st(dst + h * p.kv.v_sh + 16 * part + 8, wb);
+    const int h = (item - p.k_items) * hp + hl;
+    if (h >= p.Hkv) return;
+    const uint16_t* src = p.v + b * p.v_sb + h * p.v_sh + 16 * part;
+    for (int t = t0 + tl; t < t1; t += kBatch * tp) {
+      uint4 wa[kBatch], wb[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (t + i * tp >= t1) break;
+        const uint16_t* x = src + (long long)(t + i * tp - before) * p.v_ss;
+        wa[i] = ld(x);
+        wb[i] = ld(x + 8);
+      }
+      if (no_page()) return;
+      uint16_t* dst = p.kv.v + (long long)id * p.kv.v_sp + h * p.kv.v_sh + 16 * part;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (t + i * tp >= t1) break;
+        uint16_t* y = dst + (long long)((t + i * tp) & (ps - 1)) * p.kv.v_ss;
+        st(y, wa[i]);
+        st(y + 8, wb[i]);
       }
     }
     return;
@@ -159,76 +186,74 @@ __global__ void __launch_bounds__(kAppendThreads) fa_kv_append_kernel(const Appe
   // ---------------- keys: rotated; per page and channel the least and largest as stored
   const uint32_t kInf = BF16 ? 0x7F807F80u : 0x7C007C00u;
   const bool kept = (t0 & (ps - 1)) != 0;   // slot 0 holds an older key
-  const int h0 = item * p.kv_heads;
-  for (int hb = h0; hb < min(p.Hkv, h0 + p.kv_heads); hb += hp) {   // block-uniform
-    const int h = hb + hl;
-    const bool on = h < min(p.Hkv, h0 + p.kv_heads);
-    uint4 mn[2], mx[2];
+  const int h = item * hp + hl;
+  const bool on = h < p.Hkv;
+  uint4 mn[2], mx[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    mn[j] = make_uint4(kInf, kInf, kInf, kInf);
+    mx[j] = make_uint4(kInf | 0x80008000u, kInf | 0x80008000u, kInf | 0x80008000u, kInf | 0x80008000u);
+  }
+  auto widen = [&](int j, uint4 lo, uint4 hi) {
+    mn[j] = make_uint4(min16x2<BF16>(mn[j].x, lo.x), min16x2<BF16>(mn[j].y, lo.y),
+                       min16x2<BF16>(mn[j].z, lo.z), min16x2<BF16>(mn[j].w, lo.w));
+    mx[j] = make_uint4(max16x2<BF16>(mx[j].x, hi.x), max16x2<BF16>(mx[j].y, hi.y),
+                       max16x2<BF16>(mx[j].z, hi.z), max16x2<BF16>(mx[j].w, hi.w));
+  };
+  if (on) {
+    const uint16_t* src = p.k + b * p.k_sb + h * p.k_sh;
+    for (int t = t0 + tl; t < t1; t += tp) {
+      const uint16_t* x = src + (long long)(t - before) * p.k_ss;
+      uint4 wa = ld(x + offA), wb = ld(x + offB);
+      angles(t);
+      rotate(wa, wb);
+      if (no_page()) break;
+      uint16_t* y = p.kv.k + (long long)id * p.kv.k_sp + h * p.kv.k_sh + (long long)(t & (ps - 1)) * p.kv.k_ss;
+      st(y + offA, wa);
+      st(y + offB, wb);
+      widen(0, wa, wa);
+      widen(1, wb, wb);
+    }
+  }
+  if (no_page()) return;   // (block-uniform)
+  if (!p.kv.k_min) return;
+  // join the tokens of a step: first the rows of the warp, then the warps.  With 2^x tokens
+  // a step, rows that differ in the low x bits of their number hold the same head.
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto other = [&](uint4 w, int m) {
+    return make_uint4(__shfl_xor_sync(0xffffffffu, w.x, m), __shfl_xor_sync(0xffffffffu, w.y, m),
+                      __shfl_xor_sync(0xffffffffu, w.z, m), __shfl_xor_sync(0xffffffffu, w.w, m));
+  };
+  for (int m = L; m < 32 && m < (L << p.tp_shift); m <<= 1) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      mn[j] = make_uint4(kInf, kInf, kInf, kInf);
-      mx[j] = make_uint4(kInf | 0x80008000u, kInf | 0x80008000u, kInf | 0x80008000u, kInf | 0x80008000u);
+      const uint4 lo = other(mn[j], m), hi = other(mx[j], m);
+      widen(j, lo, hi);
     }
-    auto widen = [&](int j, uint4 lo, uint4 hi) {
-      mn[j] = make_uint4(min16x2<BF16>(mn[j].x, lo.x), min16x2<BF16>(mn[j].y, lo.y),
-                         min16x2<BF16>(mn[j].z, lo.z), min16x2<BF16>(mn[j].w, lo.w));
-      mx[j] = make_uint4(max16x2<BF16>(mx[j].x, hi.x), max16x2<BF16>(mx[j].y, hi.y),
-                         max16x2<BF16>(mx[j].z, hi.z), max16x2<BF16>(mx[j].w, hi.w));
-    };
-    if (on) {
-      for (int t = t0 + tl; t < t1; t += tp) {
-        angles(t);
-        const uint16_t* src = p.k + b * p.k_sb + (long long)(t - before) * p.k_ss + h * p.k_sh;
-        uint16_t* dst = p.kv.k + (long long)id * p.kv.k_sp + (long long)(t & (ps - 1)) * p.kv.k_ss +
-                        h * p.kv.k_sh;
-        uint4 wa = ld(src + offA), wb = ld(src + offB);
-        rotate(wa, wb);
-        st(dst + offA, wa);
-        st(dst + offB, wb);
-        widen(0, wa, wa);
-        widen(1, wb, wb);
-      }
+  }
+  const int wpt = (L << p.tp_shift) >> 5;   // warps that share a head's tokens (0 or 1: none)
+  if (wpt > 1) {                            // block-uniform
+    if (lane < L) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) s_red[j][warp][lane] = mn[j], s_red[2 + j][warp][lane] = mx[j];
     }
-    if (!p.kv.k_min) continue;
-    // join the tokens of a step: first the rows of the warp, then the warps.  With 2^x tokens
-    // a step, rows that differ in the low x bits of their number hold the same head.
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    auto other = [&](uint4 w, int m) {
-      return make_uint4(__shfl_xor_sync(0xffffffffu, w.x, m), __shfl_xor_sync(0xffffffffu, w.y, m),
-                        __shfl_xor_sync(0xffffffffu, w.z, m), __shfl_xor_sync(0xffffffffu, w.w, m));
-    };
-    for (int m = L; m < 32 && m < (L << p.tp_shift); m <<= 1) {
+    __syncthreads();
+    if (lane < L && warp % wpt == 0) {
+      for (int w = 1; w < wpt; ++w)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint4 lo = other(mn[j], m), hi = other(mx[j], m);
-        widen(j, lo, hi);
-      }
+        for (int j = 0; j < 2; ++j) widen(j, s_red[j][warp + w][lane], s_red[2 + j][warp + w][lane]);
     }
-    const int wpt = (L << p.tp_shift) >> 5;   // warps that share a head's tokens (0 or 1: none)
-    if (wpt > 1) {                            // block-uniform
-      if (lane < L) {
+  }
+  if (on && tl == 0) {
+    const long long at = ((long long)id * p.Hkv + h) * D;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) s_red[j][warp][lane] = mn[j], s_red[2 + j][warp][lane] = mx[j];
-      }
-      __syncthreads();
-      if (lane < L && warp % wpt == 0) {
-        for (int w = 1; w < wpt; ++w)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) widen(j, s_red[j][warp + w][lane], s_red[2 + j][warp + w][lane]);
-      }
-      __syncthreads();
-    }
-    if (on && tl == 0) {
-      const long long at = ((long long)id * p.Hkv + h) * D;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int off = j ? offB : offA;
-        uint4* lo = reinterpret_cast<uint4*>(p.kv.k_min + at + off);
-        uint4* hi = reinterpret_cast<uint4*>(p.kv.k_max + at + off);
-        if (kept) widen(j, *lo, *hi);
-        *lo = mn[j];
-        *hi = mx[j];
-      }
+    for (int j = 0; j < 2; ++j) {
+      const int off = j ? offB : offA;
+      uint4* lo = reinterpret_cast<uint4*>(p.kv.k_min + at + off);
+      uint4* hi = reinterpret_cast<uint4*>(p.kv.k_max + at + off);
+      if (kept) widen(j, *lo, *hi);
+      *lo = mn[j];
+      *hi = mx[j];
     }
   }
 }

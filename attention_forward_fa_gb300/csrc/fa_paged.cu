@@ -233,9 +233,8 @@ int fa_kv_append(const fa_paged_kv_t* kv, const fa_kv_new_t* x, int B, int Hq, i
   const int rows = fa::kAppendThreads / (D / 16);
   while ((1 << p.tp_shift) < rows && (1 << p.tp_shift) < std::min(Snew, ps)) ++p.tp_shift;
   const int hp = rows >> p.tp_shift;
-  p.kv_heads = hp;
-  p.q_heads = 4 * hp;
-  p.k_items = (Hkv + p.kv_heads - 1) / p.kv_heads;
+  p.q_heads = 2 * fa::kBatch * hp;
+  p.k_items = (Hkv + hp - 1) / hp;
   p.q_items = x->q ? (Hq + p.q_heads - 1) / p.q_heads : 0;
   const long long grid = (long long)B * p.chunks * (2 * p.k_items + p.q_items);
   if (grid > 0x7FFFFFFFLL) return FA_ERR_SHAPE;
