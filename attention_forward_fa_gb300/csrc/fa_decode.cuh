@@ -10,13 +10,14 @@
 //     one waits at a barrier or ends a unit the other streams;
 //   * the producer looks up pages and copies tiles of 64 keys (K and V, 64
 //     channels x up to 64 slots x D / 64 halves per TMA box, 128-byte swizzle)
-//     into a ring of 96 KB, 192 KB per SM: four times latency times bandwidth;
+//     into a ring of 64 KB, 128 KB per SM, more than twice latency times
+//     bandwidth (rings of 96 KB, or three CTAs: no faster);
 //   * of every tile each consumer scores 16 keys against all rows, puts their P
 //     into shared memory and then adds all 64 keys' values to its quarter of the
 //     channels: O of 8 NT rows costs a thread 8 NT registers instead of 32 NT
 //     with a whole O per warp, and nothing has to be joined at a unit's end but
 //     the sums.  (The warps-by-keys form spilled at 24 rows, spent 2.4 us per
-//     unit, and took 66 us against XX us for five draft tokens in a window.)
+//     unit, and took 66 us against 52 us for five draft tokens in a window.)
 //   * products are transposed, S^T = K Q^T and O^T = V^T P^T, with the keys (then
 //     the channels) as the 16-row side of mma.m16n8k16 and the rows as its
 //     8-column side: 4 rows of a common group waste 4 of 8 columns there, but
@@ -44,7 +45,7 @@ constexpr int kDecTile = 64;                          // keys per tile
 constexpr int kDecWarps = 4;                          // consumer warps, 16 keys of a tile each
 constexpr int kDecCtasPerSm = 2;
 constexpr int kDecThreads = 32 * (kDecWarps + 1);     // and the producer
-constexpr int kUnitTiles = 1;                         // a unit's own cost, in tiles
+constexpr int kUnitTiles = 2;                         // a unit's own cost, in tiles (0: ragged lengths 30 % slower)
 // A row's reference (the subtrahend of its exponents) follows its maximum lazily: it stays while no
 // score exceeds it by more than this many powers of two, so that the usual tile needs one vote and
 // no shuffles.  P <= 2^8 fits both 16-bit types; every sum is relative to the reference.
@@ -79,7 +80,7 @@ struct DecodeSmem {
   // The consumers take every tile, so that each has seen every earlier phase of a stage's barriers
   // (a wait on a phase's parity also passes two phases too early: teams that take turns would need
   // a stage count that leaves each stage with one of them).
-  static constexpr int kStages = (NT > 4 ? 2 : 3) * (128 / D);
+  static constexpr int kStages = 2 * (128 / D);
   static constexpr bool kQShared = NT > 4;                       // Q in shared memory or in registers
   static constexpr int kPOff = kStages * 2 * kHalf;              // uint4 [4 x 16 keys][NT][lane]: P hi, lo
   static constexpr int kQOff = kPOff + kDecWarps * NT * 512;
@@ -206,8 +207,9 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
   auto EMPTY = [&](int s) { return sbase + SM::kBarOff + 8 * (NS + s); };
   int* s_meta = reinterpret_cast<int*>(smem + SM::kMetaOff);   // per stage: first key of each 16, or -1
   long long* s_range = reinterpret_cast<long long*>(smem + SM::kMiscOff);   // start, end, tiles before s_b
-  int* s_b = reinterpret_cast<int*>(smem + SM::kMiscOff + 24);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + SM::kMiscOff + 28);
+  int* s_b = reinterpret_cast<int*>(smem + SM::kMiscOff + 24);              // and its length
+  int* s_len = s_b + 1;
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + SM::kMiscOff + 32);
 
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&p.tm_k);
@@ -223,7 +225,8 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
   pdl_wait_prior();
   pdl_launch_dependents();
   if (warp == kDecWarps) {   // this CTA's range of tiles and the sequence it starts in
-    const int first32 = lane < p.B ? decode_charge(p, lane) : 0;
+    const int len32 = lane < p.B ? decode_len(p, lane) : 0;
+    const int first32 = lane < p.B ? decode_span(p, len32).n + kUnitTiles : 0;
     const long long total = decode_charge_before(p, p.B, lane, first32);
     const int n = decode_ctas(p, total);
     long long start = 0, end = 0;
@@ -246,7 +249,10 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
       const int last = 31 - __clz(in);               // lane 0 is in, or the search has ended
       if (in) {
         b = b0 + last;
-        if (lane == last) s_range[2] = before + inc - w;
+        if (lane == last) {
+          s_range[2] = before + inc - w;
+          *s_len = b0 == 0 ? len32 : decode_len(p, b);
+        }
       }
       if (in != 0xffffffffu) break;
       before += __shfl_sync(0xffffffffu, inc, 31);
@@ -268,13 +274,13 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
   if (warp == kDecWarps) {
     // ============================================================ producer
     long long pos = s_range[0], before = s_range[2];
-    int b = *s_b;
+    int b = *s_b, len = *s_len;
     int it = 0;
     bool dead = false;
     const int nsub = kDecTile >> box_shift;           // copies of K (and V) per tile
     const uint32_t sub_bytes = (uint32_t)box * D * 2;
     while (pos < end && !dead) {
-      const DecodeSpan s = decode_span(p, decode_len(p, b));
+      const DecodeSpan s = decode_span(p, len);
       const long long mine = (long long)(s.n + kUnitTiles) * p.Hkv * p.groups;
       const DecodePiece d = decode_piece(s.n, before, pos, end);
       const int hk = d.unit / p.groups, t0 = d.t0, nt = d.nt;
@@ -336,7 +342,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
       pos = d.next;
       if (pos >= before + mine) {
         before += mine;
-        ++b;
+        if (++b < p.B) len = decode_len(p, b);
       }
     }
     // after an expired wait: copies in flight land before the CTA ends
@@ -370,11 +376,11 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
   }
 
   long long pos = s_range[0], before = s_range[2];
-  int b = *s_b;
+  int b = *s_b, next_len = *s_len;
   int it = 0;
   bool dead = false;
   while (pos < end) {
-    const int len = decode_len(p, b);
+    const int len = next_len;
     const DecodeSpan s = decode_span(p, len);
     const long long mine = (long long)(s.n + kUnitTiles) * p.Hkv * p.groups;
     const DecodePiece d = decode_piece(s.n, before, pos, end);
@@ -383,7 +389,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
     pos = d.next;
     if (pos >= before + mine) {
       before += mine;
-      ++b;
+      if (++b < p.B) next_len = decode_len(p, b);   // (used a unit later)
     }
     if (d.nt == 0) continue;       // nothing but the charge
     const int rows = min(8 * NT, p.rows - rg * 8 * NT);
@@ -632,37 +638,51 @@ __global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_consta
   pdl_wait_prior();
   if (c0 == c1) return;          // finished by its CTA
   auto at = [&](int c) { return (2LL * c + (c == c0 ? 1 : 0)) * rows8 + rr; };
-  float m = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[at(c)].x);
-#pragma unroll
-  for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-  const float top = m;
-  constexpr int E = D / 32;
-  float o[E], l = 0.f;
+  // Eight pieces at a time: their loads wait for nothing but each other.
+  constexpr int E = D / 32, kPieces = 8;
+  float m = kNoScore, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll 8
-  for (int c = c0; c <= c1; ++c) {
-    const long long a = at(c);
-    const float2 ml = p.part_ml[a];
-    const float f = ex2_approx(ml.x - top);
-    l += ml.y * f;
-    float x[E];
-    if constexpr (E == 4) {
-      const float4 y = *reinterpret_cast<const float4*>(p.part_o + a * D + 4 * lane);
-      x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
-    } else {
-      const float2 y = *reinterpret_cast<const float2*>(p.part_o + a * D + 2 * lane);
-      x[0] = y.x, x[1] = y.y;
-    }
+  for (int cb = c0; cb <= c1; cb += kPieces) {
+    float2 ml[kPieces];
+    float x[kPieces][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(f, x[e], o[e]);
+    for (int i = 0; i < kPieces; ++i) {
+      const bool in = cb + i <= c1;
+      const long long a = at(in ? cb + i : cb);
+      ml[i] = p.part_ml[a];
+      if (!in) ml[i] = make_float2(kNoScore, 0.f);
+      const float* src = p.part_o + a * D + E * lane;
+      if constexpr (E == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(src);
+        x[i][0] = y.x, x[i][1] = y.y, x[i][2] = y.z, x[i][3] = y.w;
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(src);
+        x[i][0] = y.x, x[i][1] = y.y;
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) top = fmaxf(top, ml[i].x);
+    const float keep = ex2_approx(m - top);
+    m = top;
+    l *= keep;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= keep;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const bool in = cb + i <= c1;
+      const float f = in ? ex2_approx(ml[i].x - top) : 0.f;
+      l = fmaf(f, ml[i].y, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = in ? fmaf(f, x[i][e], o[e]) : o[e];
+    }
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D) + (E / 2) * lane;
 #pragma unroll
   for (int e = 0; e < E; e += 2) dst[e / 2] = pack16x2<BF16>(o[e] * inv, o[e + 1] * inv);
-  if (lane == 0) p.lse[row] = l > 0.f ? (top + log2f(l)) * 0.6931471805599453f : INFINITY;
+  if (lane == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : INFINITY;
 }
 
 }  // namespace fa
