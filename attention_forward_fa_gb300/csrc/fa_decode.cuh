@@ -81,7 +81,7 @@ struct DecodeSmem {
   // (a wait on a phase's parity also passes two phases too early: teams that take turns would need
   // a stage count that leaves each stage with one of them).
   static constexpr int kStages = 2 * (128 / D);
-  static constexpr bool kQShared = NT > 4;                       // Q in shared memory or in registers
+  static constexpr bool kQShared = NT > 2;                       // Q in shared memory or in registers
   static constexpr int kPOff = kStages * 2 * kHalf;              // uint4 [4 x 16 keys][NT][lane]: P hi, lo
   static constexpr int kQOff = kPOff + kDecWarps * NT * 512;
   static constexpr int kMaxOff = kQOff + (kQShared ? NT * (D / 32) * 512 : 0);   // float [warps][8 NT]
@@ -432,9 +432,11 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
       const int kq = warp == 0 ? keys.x : warp == 1 ? keys.y : warp == 2 ? keys.z : keys.w;
       // 16 keys that were not copied (their K is stale) lie past every row's token
       const int key0 = kq < 0 ? 0x7FFFFF00 : kq;
-      float c[NT][4];
+      float c[NT][4], c2[NT][4];       // (two chains of products: with few rows their latency shows)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[n][e] = c2[n][e] = 0.f;
 #pragma unroll
       for (int k2 = 0; k2 < KS / 2; ++k2) {
         uint32_t a0[4], a1[4];
@@ -445,9 +447,13 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
         for (int n = 0; n < NT; ++n) {
           const uint4 x = SM::kQShared ? s_q[(n * (KS / 2) + k2) * 32 + lane] : qf[SM::kQShared ? 0 : n][SM::kQShared ? 0 : k2];
           mma_16x8<BF16>(c[n], a0, x.x, x.y);
-          mma_16x8<BF16>(c[n], a1, x.z, x.w);
+          mma_16x8<BF16>(NT > 2 ? c[n] : c2[n], a1, x.z, x.w);
         }
       }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[n][e] += c2[n][e];
       // scores in log2 units; lane (g, t4): keys g (c0, c1) and g + 8 (c2, c3), rows 2 t4, 2 t4 + 1
       float over = -INFINITY;        // the most that a score exceeds its row's reference by
       const bool all = key0 + 15 <= tok_min && key0 >= low_max;
@@ -505,6 +511,17 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
           }
         }
       }
+      // this warp's channels of V: their way from shared memory is hidden by the exponentials (up to
+      // 32 rows; with more O leaves no registers for it)
+      uint32_t v[4][DT][4];
+      auto load_v = [&](int q) {
+#pragma unroll
+        for (int i = 0; i < DT; ++i) ldmatrix4_trans(base + place(q) + vlane[i], v[q][i]);
+      };
+      if constexpr (NT <= 4) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) load_v(q);
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const float p0 = ex2_approx(c[n][0] - m[n][0]), p1 = ex2_approx(c[n][1] - m[n][1]);
@@ -521,33 +538,37 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
       const int4 hi4 = make_int4(keys.x + 16, keys.y + 16, keys.z + 16, keys.w + 16);
       const bool whole = min(min(keys.x, keys.y), min(keys.z, keys.w)) >= s.lo &&
                          max(max(hi4.x, hi4.y), max(hi4.z, hi4.w)) <= s.hi;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;   // keys 2 t4, 2 t4 + 1 and + 8
-        if (!whole) {
-          const int k0 = q == 0 ? keys.x : q == 1 ? keys.y : q == 2 ? keys.z : keys.w;
-          auto seen = [&](int k) { return k0 >= 0 && k0 + k >= s.lo && k0 + k < s.hi; };
-          keep0 = (seen(2 * t4) ? 0xffffu : 0u) | (seen(2 * t4 + 1) ? 0xffff0000u : 0u);
-          keep1 = (seen(2 * t4 + 8) ? 0xffffu : 0u) | (seen(2 * t4 + 9) ? 0xffff0000u : 0u);
-        }
-        uint32_t a[DT][4];
+      auto keep_seen = [&](int q) {
+        const int k0 = q == 0 ? keys.x : q == 1 ? keys.y : q == 2 ? keys.z : keys.w;
+        auto seen = [&](int k) { return k0 >= 0 && k0 + k >= s.lo && k0 + k < s.hi; };
+        // keys 2 t4, 2 t4 + 1 and + 8
+        const uint32_t keep0 = (seen(2 * t4) ? 0xffffu : 0u) | (seen(2 * t4 + 1) ? 0xffff0000u : 0u);
+        const uint32_t keep1 = (seen(2 * t4 + 8) ? 0xffffu : 0u) | (seen(2 * t4 + 9) ? 0xffff0000u : 0u);
 #pragma unroll
         for (int i = 0; i < DT; ++i) {
-          ldmatrix4_trans(base + place(q) + vlane[i], a[i]);
-          if (!whole) {
-            a[i][0] &= keep0;
-            a[i][1] &= keep0;
-            a[i][2] &= keep1;
-            a[i][3] &= keep1;
-          }
+          v[q][i][0] &= keep0;
+          v[q][i][1] &= keep0;
+          v[q][i][2] &= keep1;
+          v[q][i][3] &= keep1;
+        }
+      };
+      if (NT <= 4 && !whole) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) keep_seen(q);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if constexpr (NT > 4) {
+          load_v(q);
+          if (!whole) keep_seen(q);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const uint4 pp = s_p[(q * NT + n) * 32 + lane];
 #pragma unroll
-          for (int i = 0; i < DT; ++i) mma_16x8<BF16>(o[n][i], a[i], pp.x, pp.y);
+          for (int i = 0; i < DT; ++i) mma_16x8<BF16>(o[n][i], v[q][i], pp.x, pp.y);
 #pragma unroll
-          for (int i = 0; i < DT; ++i) mma_16x8<BF16>(o[n][i], a[i], pp.z, pp.w);
+          for (int i = 0; i < DT; ++i) mma_16x8<BF16>(o[n][i], v[q][i], pp.z, pp.w);
         }
       }
       __syncwarp();
@@ -613,16 +634,20 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
   }
 }
 
-// Joins the pieces of the units that several CTAs shared, one warp per row: the
-// schedule is computed anew from the lengths, the pieces summed in the order of
-// the keys (the same bits every time).
-template <bool BF16, int D>
+// Joins the pieces of the units that several CTAs shared: the schedule is
+// computed anew from the lengths, the pieces summed in an order that depends on
+// it alone (the same bits every time).  WPR warps per row: 8 where there are few
+// rows, whose units may then have as many pieces as the grid has CTAs; 1 else.
+template <bool BF16, int D, int WPR>
 __global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_constant__ DecodeParams p, int rows8) {
+  __shared__ __align__(16) float s_o[WPR > 1 ? 8 : 1][D];
+  __shared__ float2 s_ml[8];
   // The schedule before the wait: by the time this kernel runs every CTA of the decode kernel has
   // seen the kernels before it finish, so that the lengths are final.
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 8 + warp;
+  const long long row = (long long)blockIdx.x * (8 / WPR) + warp / WPR;
+  const int part = warp % WPR;
   const long long per_b = (long long)p.Hq * p.Sq;
   if (row >= per_b * p.B) return;
   const int b = (int)(row / per_b);
@@ -643,7 +668,7 @@ __global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_consta
   float m = kNoScore, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int cb = c0; cb <= c1; cb += kPieces) {
+  for (int cb = c0 + part * kPieces; cb <= c1; cb += WPR * kPieces) {
     float2 ml[kPieces];
     float x[kPieces][E];
 #pragma unroll
@@ -676,6 +701,25 @@ __global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_consta
       l = fmaf(f, ml[i].y, l);
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = in ? fmaf(f, x[i][e], o[e]) : o[e];
+    }
+  }
+  if constexpr (WPR > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[part][E * lane + e] = o[e];
+    if (lane == 0) s_ml[part] = make_float2(m, l);
+    __syncthreads();
+    if (part) return;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) m = fmaxf(m, s_ml[w].x);
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) {
+      const float f = ex2_approx(s_ml[w].x - m);
+      l = fmaf(f, s_ml[w].y, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(f, s_o[w][E * lane + e], o[e]);
     }
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;

@@ -133,7 +133,9 @@ int launch_decode(fa::DecodeParams& p, long long most_tiles, cudaStream_t st) {
   cudaError_t e = launch_dependent(kern, (unsigned)p.ctas, fa::kDecThreads, smem, st, p);
   if (e == cudaSuccess) {
     const long long rows = (long long)p.B * p.Hq * p.Sq;
-    e = launch_dependent(fa::fa_decode_join_kernel<BF16, D>, (unsigned)((rows + 7) / 8), 256, 0, st, p, 8 * NT);
+    e = rows <= 8LL * sms   // one wave of blocks
+            ? launch_dependent(fa::fa_decode_join_kernel<BF16, D, 8>, (unsigned)rows, 256, 0, st, p, 8 * NT)
+            : launch_dependent(fa::fa_decode_join_kernel<BF16, D, 1>, (unsigned)((rows + 7) / 8), 256, 0, st, p, 8 * NT);
   }
   cudaFreeAsync(scratch, st);
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
