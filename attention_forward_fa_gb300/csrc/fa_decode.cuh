@@ -118,16 +118,26 @@ __device__ __forceinline__ int decode_len(const DecodeParams& p, int b) {
   return len < 0 || len > (p.kv.max_pages << p.kv.page_shift) ? 0 : len;
 }
 
-// Charged tiles of one unit of sequence b, and of all units of the sequences before b (whole warp).
-__device__ __forceinline__ int decode_charge(const DecodeParams& p, int b) {
-  return decode_span(p, decode_len(p, b)).n + kUnitTiles;
-}
-__device__ __forceinline__ long long decode_charge_before(const DecodeParams& p, int b, int lane, int mine) {
-  long long sum = lane < b ? mine : 0;      // `mine`: sequence `lane`'s
-  for (int i = lane + 32; i < b; i += 32) sum += decode_charge(p, i);
+// The lengths and charges of sequences base + 32 i + lane: eight independent loads.
+constexpr int kChunks = 8;
+__device__ __forceinline__ void decode_charges(const DecodeParams& p, int base, int lane, int (&len)[kChunks],
+                                               int (&c)[kChunks]) {
 #pragma unroll
-  for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-  return sum * p.Hkv * p.groups;
+  for (int i = 0; i < kChunks; ++i) {
+    len[i] = c[i] = 0;
+    if (base + 32 * i < p.B) {         // (the same for the whole warp: a small batch pays for one chunk)
+      const int b = base + 32 * i + lane;
+      if (b < p.B) len[i] = decode_len(p, b);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i)
+    if (base + 32 * i + lane < p.B) c[i] = decode_span(p, len[i]).n + kUnitTiles;
+}
+__device__ __forceinline__ long long warp_sum(long long x) {
+#pragma unroll
+  for (int w = 16; w; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
+  return x;
 }
 // CTAs that share `total` charged tiles, the start of CTA c's range, the CTA that has tile t.
 __device__ __forceinline__ int decode_ctas(const DecodeParams& p, long long total) {
@@ -137,20 +147,25 @@ __device__ __forceinline__ long long decode_first(long long total, int n, int c)
 __device__ __forceinline__ int decode_owner(long long total, int n, long long t) {
   return (int)(((t + 1) * n - 1) / total);
 }
-// The part of a unit that a range [pos, end) of charged tiles holds: tiles [t0, t0 + nt) of n.
-struct DecodePiece {
-  int unit, t0, nt, n;
-  long long next;   // the range's position behind it
+// A walk over the units of a CTA's range: unit `unit` (KV head, row group) of sequence b, from its
+// charged tile `off`; `left` charged tiles to go.
+struct DecodeWalk {
+  int b, unit, off;
+  long long left;
 };
-__device__ __forceinline__ DecodePiece decode_piece(int n, long long before, long long pos, long long end) {
+// The tiles [t0, t0 + nt) of a unit of n that the walk's next step holds.
+struct DecodePiece {
+  int t0, nt;
+};
+__device__ __forceinline__ DecodePiece decode_step(DecodeWalk& w, int n, int units) {
   DecodePiece d;
   const int charge = n + kUnitTiles;
-  const int off = (int)((pos - before) % charge);
-  d.unit = (int)((pos - before) / charge);
-  d.next = min(end, pos + charge - off);
-  d.t0 = max(0, off - kUnitTiles);
-  d.nt = max(0, off + (int)(d.next - pos) - kUnitTiles) - d.t0;
-  d.n = n;
+  const int take = (int)min((long long)(charge - w.off), w.left);
+  d.t0 = max(0, w.off - kUnitTiles);
+  d.nt = max(0, w.off + take - kUnitTiles) - d.t0;
+  w.left -= take;
+  w.off = 0;                    // (whatever is left starts with a unit)
+  if (++w.unit == units) w.unit = 0, ++w.b;
   return d;
 }
 
@@ -206,10 +221,10 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
   auto FULL = [&](int s) { return sbase + SM::kBarOff + 8 * s; };
   auto EMPTY = [&](int s) { return sbase + SM::kBarOff + 8 * (NS + s); };
   int* s_meta = reinterpret_cast<int*>(smem + SM::kMetaOff);   // per stage: first key of each 16, or -1
-  long long* s_range = reinterpret_cast<long long*>(smem + SM::kMiscOff);   // start, end, tiles before s_b
-  int* s_b = reinterpret_cast<int*>(smem + SM::kMiscOff + 24);              // and its length
-  int* s_len = s_b + 1;
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + SM::kMiscOff + 32);
+  DecodeWalk* s_walk = reinterpret_cast<DecodeWalk*>(smem + SM::kMiscOff);   // where this CTA starts,
+  int* s_len = reinterpret_cast<int*>(smem + SM::kMiscOff + 24);             // the length there
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + SM::kMiscOff + 28);
+  const int units = p.Hkv * p.groups;                // per sequence
 
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&p.tm_k);
@@ -224,66 +239,71 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
   // In this order: the join kernel may then read the lengths as soon as it runs.
   pdl_wait_prior();
   pdl_launch_dependents();
-  if (warp == kDecWarps) {   // this CTA's range of tiles and the sequence it starts in
-    const int len32 = lane < p.B ? decode_len(p, lane) : 0;
-    const int first32 = lane < p.B ? decode_span(p, len32).n + kUnitTiles : 0;
-    const long long total = decode_charge_before(p, p.B, lane, first32);
+  if (warp == kDecWarps) {   // this CTA's range of charged tiles, and the sequence it starts in
+    int len[kChunks], c[kChunks];
+    long long sum = 0;
+    for (int base = 32 * kChunks; base < p.B; base += 32 * kChunks) {
+      decode_charges(p, base, lane, len, c);
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) sum += c[i];
+    }
+    decode_charges(p, 0, lane, len, c);         // (kept for the search)
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) sum += c[i];
+    const long long total = warp_sum(sum) * units;
     const int n = decode_ctas(p, total);
     long long start = 0, end = 0;
     if ((int)blockIdx.x < n) {
       start = decode_first(total, n, blockIdx.x);
       end = decode_first(total, n, blockIdx.x + 1);
     }
-    // the last sequence with at most `start` tiles before it
-    long long before = 0;
-    int b = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const long long w = (long long)(b0 == 0 ? first32 : b0 + lane < p.B ? decode_charge(p, b0 + lane) : 0) * p.Hkv * p.groups;
-      long long inc = w;
+    const long long first = start / units;   // in charges of one unit per sequence: the sequence is
+    long long before = 0;                    // the last with at most so many before it
+    int mine = 0, my_len = 0, at = -1;       // of its chunk of 32, and where that begins
+    for (int base = 0; at < 0; base += 32 * kChunks) {
+      if (base) decode_charges(p, base, lane, len, c);
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += x;
+      for (int i = 0; i < kChunks; ++i) {
+        if (at >= 0) break;
+        const int in = __reduce_add_sync(0xffffffffu, (unsigned)c[i]);   // (32 of at most 2^25 + 2)
+        if (before + in > first || base + 32 * (i + 1) >= p.B) at = base + 32 * i, mine = c[i], my_len = len[i];
+        else before += in;
       }
-      const unsigned in = __ballot_sync(0xffffffffu, b0 + lane < p.B && before + inc - w <= start);
-      const int last = 31 - __clz(in);               // lane 0 is in, or the search has ended
-      if (in) {
-        b = b0 + last;
-        if (lane == last) {
-          s_range[2] = before + inc - w;
-          *s_len = b0 == 0 ? len32 : decode_len(p, b);
-        }
-      }
-      if (in != 0xffffffffu) break;
-      before += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (lane == 0) {
-      s_range[0] = start;
-      s_range[1] = end;
-      *s_b = b;
+    int inc = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += x;
     }
-    if (blockIdx.x == 0)     // lengths that the tables cannot hold are reported once
-      for (int i = lane; i < p.B; i += 32) (void)paged_len(p.kv, p.kv_lens[i], p.status);
+    const unsigned here = __ballot_sync(0xffffffffu, mine > 0 && before + inc - mine <= first);
+    if (lane == 31 - __clz(here)) {
+      const long long off = start - (before + inc - mine) * units;
+      *s_walk = DecodeWalk{at + lane, (int)(off / mine), (int)(off % mine), end - start};
+      *s_len = my_len;
+    }
+  } else if (blockIdx.x == 0) {   // lengths that the tables cannot hold are reported once
+    for (int i = threadIdx.x; i < p.B; i += 32 * kDecWarps) (void)paged_len(p.kv, p.kv_lens[i], p.status);
   }
   __syncthreads();
-  const long long end = s_range[1];
+  DecodeWalk walk = *s_walk;
   const WaitCtx wc{s_abort, p.status, p.timeout_ns};
   const int box_shift = min(p.kv.page_shift, 6);     // slots per copy
   const int box = 1 << box_shift;
 
   if (warp == kDecWarps) {
     // ============================================================ producer
-    long long pos = s_range[0], before = s_range[2];
-    int b = *s_b, len = *s_len;
+    int len = *s_len;
     int it = 0;
     bool dead = false;
     const int nsub = kDecTile >> box_shift;           // copies of K (and V) per tile
     const uint32_t sub_bytes = (uint32_t)box * D * 2;
-    while (pos < end && !dead) {
+    while (walk.left > 0 && !dead) {
       const DecodeSpan s = decode_span(p, len);
-      const long long mine = (long long)(s.n + kUnitTiles) * p.Hkv * p.groups;
-      const DecodePiece d = decode_piece(s.n, before, pos, end);
-      const int hk = d.unit / p.groups, t0 = d.t0, nt = d.nt;
+      const int b = walk.b, hk = walk.unit / p.groups;
+      const DecodePiece d = decode_step(walk, s.n, units);
+      if (walk.b != b && walk.left > 0) len = decode_len(p, walk.b);
+      const int t0 = d.t0, nt = d.nt;
       const int n_pages = (s.hi + (1 << p.kv.page_shift) - 1) >> p.kv.page_shift;
       // Lane i looks up sub-block c0 + i of the unit (box keys each): page, first slot, first key.
       auto look_up = [&](int c, int& id, int& slot, int& key) {
@@ -339,11 +359,6 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
         // the next look-up, a look-up's tiles ahead of its use
         if (in == 0) look_up((t0 + j + per) * nsub + lane, id2, slot2, key2);
       }
-      pos = d.next;
-      if (pos >= before + mine) {
-        before += mine;
-        if (++b < p.B) len = decode_len(p, b);
-      }
     }
     // after an expired wait: copies in flight land before the CTA ends
     if (dead && lane == 0)
@@ -375,21 +390,25 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
                ((((ch & 63) / 8 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
   }
 
-  long long pos = s_range[0], before = s_range[2];
-  int b = *s_b, next_len = *s_len;
+  int next_len = *s_len;
   int it = 0;
   bool dead = false;
-  while (pos < end) {
-    const int len = next_len;
+  auto first_row = [&](const DecodeWalk& w) {
+    return (long long)w.b * p.Hq * p.Sq + (long long)(w.unit / p.groups) * p.rows + (w.unit % p.groups) * 8 * NT;
+  };
+  while (walk.left > 0) {
+    const int len = next_len, rg = walk.unit % p.groups, b = walk.b;
+    const long long row0 = first_row(walk);
     const DecodeSpan s = decode_span(p, len);
-    const long long mine = (long long)(s.n + kUnitTiles) * p.Hkv * p.groups;
-    const DecodePiece d = decode_piece(s.n, before, pos, end);
-    const int hk = d.unit / p.groups, rg = d.unit % p.groups;
-    const long long row0 = (long long)b * p.Hq * p.Sq + (long long)hk * p.rows + rg * 8 * NT;
-    pos = d.next;
-    if (pos >= before + mine) {
-      before += mine;
-      if (++b < p.B) next_len = decode_len(p, b);   // (used a unit later)
+    const DecodePiece d = decode_step(walk, s.n, units);
+    if (walk.left > 0) {           // what the next unit will want: its length, and Q on its way to L1
+      if (walk.b != b) next_len = decode_len(p, walk.b);
+      if (warp == 0) {
+        const uint8_t* x = reinterpret_cast<const uint8_t*>(p.q + first_row(walk) * D);
+        const int bytes = min(8 * NT, p.rows - (walk.unit % p.groups) * 8 * NT) * D * 2;
+        for (int i = 128 * lane; i < bytes; i += 128 * 32)
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(x + i));
+      }
     }
     if (d.nt == 0) continue;       // nothing but the charge
     const int rows = min(8 * NT, p.rows - rg * 8 * NT);
@@ -585,7 +604,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
       if (g == 0) *reinterpret_cast<float2*>(s_sum + (warp * NT + n) * 8 + 2 * t4) = make_float2(l[n][0], l[n][1]);
     }
     sync();
-    const bool direct = d.t0 == 0 && d.nt == d.n;
+    const bool direct = d.t0 == 0 && d.nt == s.n;
     const long long part0 = (2LL * blockIdx.x + (d.t0 == 0 ? 1 : 0)) * (8 * NT);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -654,11 +673,21 @@ __global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_consta
   const int in_b = (int)(row % per_b);
   const int hk = in_b / p.rows, r = in_b % p.rows;
   const int rg = r / rows8, rr = r % rows8;
-  const int first32 = lane < p.B ? decode_charge(p, lane) : 0;
-  const int n = decode_charge(p, b) - kUnitTiles;
-  const long long total = decode_charge_before(p, p.B, lane, first32);
+  long long total = 0, before = 0;
+  for (int base = 0; base < p.B; base += 32 * kChunks) {
+    int len[kChunks], c[kChunks];
+    decode_charges(p, base, lane, len, c);
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      total += c[i];
+      if (base + 32 * i + lane < b) before += c[i];
+    }
+  }
+  const int units = p.Hkv * p.groups;
+  total = warp_sum(total) * units;
   const int ctas = decode_ctas(p, total);
-  const long long t0 = decode_charge_before(p, b, lane, first32) + (long long)(hk * p.groups + rg) * (n + kUnitTiles) + kUnitTiles;
+  const int n = decode_span(p, decode_len(p, b)).n;
+  const long long t0 = warp_sum(before) * units + (long long)(hk * p.groups + rg) * (n + kUnitTiles) + kUnitTiles;
   const int c0 = decode_owner(total, ctas, t0), c1 = decode_owner(total, ctas, t0 + n - 1);
   pdl_wait_prior();
   if (c0 == c1) return;          // finished by its CTA
