@@ -143,8 +143,13 @@ int launch_decode(fa::DecodeParams& p, long long most_tiles, cudaStream_t st) {
 
 template <bool BF16, int D>
 int launch_decode_rows(fa::DecodeParams& p, long long tiles_per_unit, cudaStream_t st) {
-  // as few columns as hold the rows; more than 64 rows go in groups that read the keys again
-  const int nt = p.rows <= 32 ? (p.rows + 7) / 8 : 8;
+  // As few passes over the keys as 64 rows each allow, and as few columns of 8 as then hold a pass's
+  // rows: up to 32 rows the time is that of the keys (16 sequences of 4096 tokens, 8 KV heads of 128:
+  // 48 us at 4 rows, 57 us at 32), past that the matrix instructions' (71 us at 40 rows, 84 at 48,
+  // 113 at 64; 40 rows as 64 took 112 us).
+  const int passes = (p.rows + 63) / 64;
+  const int need = ((p.rows + passes - 1) / passes + 7) / 8;
+  const int nt = need == 7 ? 8 : need;
   p.groups = (p.rows + 8 * nt - 1) / (8 * nt);
   const long long most = (tiles_per_unit + fa::kUnitTiles) * p.B * p.Hkv * p.groups;
   switch (nt) {
@@ -152,6 +157,8 @@ int launch_decode_rows(fa::DecodeParams& p, long long tiles_per_unit, cudaStream
     case 2: return launch_decode<BF16, D, 2>(p, most, st);
     case 3: return launch_decode<BF16, D, 3>(p, most, st);
     case 4: return launch_decode<BF16, D, 4>(p, most, st);
+    case 5: return launch_decode<BF16, D, 5>(p, most, st);
+    case 6: return launch_decode<BF16, D, 6>(p, most, st);
     default: return launch_decode<BF16, D, 8>(p, most, st);
   }
 }
