@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
     for (int j = 0; j < d.nt; ++j, ++it) {
       const int st = it % NS;
       // (after an expired wait: the barriers below still see every warp, the answer is void)
-      if (!dead && !wait_bar(FULL(st), (it / NS) & 1, wc)) dead = true;
+      if (!dead) dead = !__all_sync(0xffffffffu, wait_bar(FULL(st), (it / NS) & 1, wc));
       const int4 keys = *reinterpret_cast<const int4*>(s_meta + 4 * st);
       const uint32_t base = sbase + (uint32_t)st * 2 * SM::kHalf;
       const int kq = warp == 0 ? keys.x : warp == 1 ? keys.y : warp == 2 ? keys.z : keys.w;

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const A
     if (!turns) return;
     const float4* cp = reinterpret_cast<const float4*>(p.cos + (long long)t * half + 8 * part);
     const float4* sp = reinterpret_cast<const float4*>(p.sin + (long long)t * half + 8 * part);
-    const float4 c0 = __ldg(cp), c1 = __ldg(cp + 1), s0 = __ldg(sp), s1 = __ldg(sp + 1);
+    const float4 c0 = cp[0], c1 = cp[1], s0 = sp[0], s1 = sp[1];
     c[0] = c0.x; c[1] = c0.y; c[2] = c0.z; c[3] = c0.w; c[4] = c1.x; c[5] = c1.y; c[6] = c1.z; c[7] = c1.w;
     s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w; s[4] = s1.x; s[5] = s1.y; s[6] = s1.z; s[7] = s1.w;
   };
@@ -127,7 +127,9 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const A
     wa = pack8<BF16>(a);
     wb = pack8<BF16>(d);
   };
-  auto ld = [](const uint16_t* x) { return __ldg(reinterpret_cast<const uint4*>(x)); };
+  // (no loads by the read-only path: the kernel may have started before the one that wrote its
+  // inputs ended, and only ordinary loads are promised to see those writes after the wait)
+  auto ld = [](const uint16_t* x) { return *reinterpret_cast<const uint4*>(x); };
   auto st = [](uint16_t* x, uint4 w) { *reinterpret_cast<uint4*>(x) = w; };
 
   if (item >= 2 * p.k_items) {   // ---------------- queries: one set of angles for all heads
@@ -142,9 +144,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const A
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
           if (h + i * hp >= h1) break;
-          // plain loads: q_out may be q
-          wa[i] = *reinterpret_cast<const uint4*>(src + (h + i * hp) * p.q_sh + offA);
-          wb[i] = *reinterpret_cast<const uint4*>(src + (h + i * hp) * p.q_sh + offB);
+          wa[i] = ld(src + (h + i * hp) * p.q_sh + offA);
+          wb[i] = ld(src + (h + i * hp) * p.q_sh + offB);
         }
         if (no_page()) return;
 #pragma unroll

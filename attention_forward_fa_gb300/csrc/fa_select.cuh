@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(32) fa_page_score_kernel(const SelectParams p)
     uint4 w[C];
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      w[c] = r0 + g < p.rows ? __ldg(reinterpret_cast<const uint4*>(q + (long long)(r0 + g) * D + 32 * c)) : make_uint4(0, 0, 0, 0);
+      w[c] = r0 + g < p.rows ? *reinterpret_cast<const uint4*>(q + (long long)(r0 + g) * D + 32 * c) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int gr = 0; gr < kScoreGroups; ++gr) {
       if (r0 == 0) {               // (every lane waits for its own copies only)

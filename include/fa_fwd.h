@@ -419,7 +419,8 @@ typedef struct {
  * q_out (h < Hq) at base[b * stride_b + h * stride_h + i * stride_s + d];
  * strides in elements, >= 0 (q_out: positive), multiples of 8, below 2^38 (one
  * over a size of 1 is not looked at); bases 16-byte aligned.  q and q_out NULL:
- * keys and values only.  q_out may be q itself (same strides).
+ * keys and values only.  q_out may be q itself (same strides) and
+ * must not overlap the inputs otherwise.
  * cos, sin: fp32 [max_pos, rot_dim / 2], contiguous, 16-byte aligned, row p the
  * angles of position p; rot_dim a multiple of 16, 0 <= rot_dim <= D; 0 (tables
  * NULL) rotates nothing.  interleaved 0: channel j < rot_dim / 2 turns with

@@ -247,6 +247,12 @@ DECODE = [
     ("bf16", 3, 8, 2, 64, 16, 5, [700, 64, 3], 100, "hnd"),
     ("fp16", 2, 4, 1, 128, 128, 3, [1000, 130], 0, "nhd"),
     ("bf16", 1, 4, 1, 128, 64, 1, [20000], None, "hnd"),
+    ("bf16", 2, 64, 1, 128, 64, 1, [300, 33], None, "hnd"),
+    ("fp16", 1, 16, 2, 128, 32, 8, [260], None, "nhd"),
+    ("fp16", 2, 56, 1, 64, 16, 1, [300, 17], None, "hnd"),
+    ("bf16", 1, 8, 1, 64, 128, 17, [150], 40, "halves"),
+    ("bf16", 1, 20, 1, 128, 16, 2, [99], None, "hnd"),
+    ("bf16", 1, 128, 1, 128, 256, 1, [500], None, "hnd"),
     ("fp16", 2, 16, 16, 64, 16, 1, [5000, 4999], 4097, "hnd"),
 ]
 
@@ -359,6 +365,53 @@ def test_decode_many_units_per_block(dtype, Hq, Hkv, D, page, Sq, pre, sel):
     _check(o, l, P.decode(q, c.k, c.v, c.table, lens, D ** -0.5, pre, idx), dtype)
 
 
+@pytest.mark.parametrize("pre", [0, 50, 400])
+def test_decode_listed_pages_in_a_window(pre):
+    import attention_forward_fa_gb300 as fa
+    lens, page = [700, 64, 3], 32
+    c = Cache(22, "bf16", 3, 2, 128, page, lens)
+    idx = c.rng.integers(-1, c.table.shape[1], (3, 2, 12)).astype(np.int32)
+    idx[0, 0, :3] = [21, 20, 21]           # the newest page twice
+    q = _round(c.rng.standard_normal((3, 8, 3, 128)), "bf16")
+    o, l = fa.flash_attention_decode(_dev(q, "bf16"), c.obj, c.ints(lens), page_idx=_dev(idx), pre_tokens=pre)
+    assert _status() == 0
+    _check(o, l, P.decode(q, c.k, c.v, c.table, lens, 128 ** -0.5, pre, idx), "bf16")
+
+
+def test_decode_more_sequences_than_one_look_up():
+    """700 sequences, empty ones among them: the lengths come in several rounds."""
+    import attention_forward_fa_gb300 as fa
+    rng = np.random.default_rng(23)
+    lens = [int(x) for x in rng.integers(0, 90, 700)]
+    lens[300] = 2000
+    c = Cache(24, "fp16", 700, 1, 64, 16, lens)
+    q = _round(c.rng.standard_normal((700, 2, 1, 64)), "fp16")
+    o, l = fa.flash_attention_decode(_dev(q, "fp16"), c.obj, c.ints(lens))
+    assert _status() == 0
+    _check(o, l, P.decode(q, c.k, c.v, c.table, lens, 0.125), "fp16")
+
+
+def test_two_streams_at_once():
+    """Eager calls of all three operators on two streams, each with scratch of its own."""
+    import torch
+    import attention_forward_fa_gb300 as fa
+    cs = [Cache(25 + i, "bf16", 2, 4, 128, 64, [4000, 900], bounds=True) for i in range(2)]
+    qs = [_dev(_round(c.rng.standard_normal((2, 16, 1, 128)), "bf16"), "bf16") for c in cs]
+    n = cs[0].ints([3999, 899])
+    want = [(fa.flash_attention_decode(q, c.obj, n), fa.select_kv_pages(q, c.obj, n, 20)) for q, c in zip(qs, cs)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for _ in range(30):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append((fa.flash_attention_decode(qs[i], cs[i].obj, n), fa.select_kv_pages(qs[i], cs[i].obj, n, 20)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for (o, l), idx in got[i]:
+            assert torch.equal(o, want[i][0][0]) and torch.equal(l, want[i][0][1]) and torch.equal(idx, want[i][1])
+    assert _status() == 0
+
+
 def test_decode_leaves_out_bad_pages():
     """A page id outside the pool: its keys are masked, the status says so; the
     other sequences are as they would be."""
@@ -433,6 +486,7 @@ SELECT = [
     ("bf16", 1, 2, 2, 64, 256, 1, [1000], 64, 2, 3),
     ("bf16", 2, 2, 1, 64, 16, 1, [40000, 20001], 33, 1, 1),
     ("fp16", 1, 8, 8, 128, 16, 1, [1600], 99, 1, 1),
+    ("bf16", 1, 2, 1, 128, 16, 1, [150000], 200, 1, 1),
 ]
 
 
@@ -467,6 +521,24 @@ def test_select_ties_and_near_ties():
         got = fa.select_kv_pages(_dev(q, "bf16"), c.obj, c.ints([n * 16]), M)
         assert _status() == 0
         assert np.array_equal(got.cpu().numpy(), P.select(q, lo, hi, c.table, [n * 16], 16, M)), case
+
+
+def test_select_many_near_the_threshold():
+    """Pages that differ past fp32 only, more of them than are kept on chip, and
+    more pages than scores are kept: all told apart in 64 bits."""
+    import attention_forward_fa_gb300 as fa
+    n, M = 9000, 700
+    c = Cache(28, "bf16", 1, 1, 64, 16, [n * 16], bounds=True)
+    q = np.ones((1, 1, 1, 64))
+    lo, hi = np.zeros_like(c.lo), np.zeros_like(c.hi)
+    hi[:, 0, 0] = 2.0 ** 20
+    hi[:, 0, 1] = 2.0 ** -20 * c.rng.integers(0, 256, hi.shape[0])    # many ties as well
+    hi[:, 0, 2] = 2.0 ** -28 * c.rng.integers(0, 256, hi.shape[0])
+    c.tlo.copy_(_dev(lo, "bf16"))
+    c.thi.copy_(_dev(hi, "bf16"))
+    got = fa.select_kv_pages(_dev(q, "bf16"), c.obj, c.ints([n * 16]), M)
+    assert _status() == 0
+    assert np.array_equal(got.cpu().numpy(), P.select(q, lo, hi, c.table, [n * 16], 16, M))
 
 
 def test_select_extreme_bounds_and_bad_pages():
