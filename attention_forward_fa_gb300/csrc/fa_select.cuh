@@ -21,6 +21,7 @@
 // the k-th largest approximate score and E the k-th largest exact one.  Moving
 // each value by at most e moves the k-th largest by at most e, so |E - T| <= e;
 // a score above T + 2 e is exactly above T + e >= E, one below T - 2 e below E.
+// (T itself is only followed down to an interval shorter than 2 e.)
 #pragma once
 #include "fa_decode.cuh"   // mma_16x8
 
@@ -43,8 +44,8 @@ struct SelectParams {
 constexpr int kScoreGroups = 3;                 // groups of 16 pages per block of one warp
 constexpr int kScorePages = 16 * kScoreGroups;
 constexpr int kSelectThreads = 512;
-constexpr int kSelectCached = 8192;             // scores kept in shared memory
-constexpr int kNearCached = 256;                // and pages near the threshold
+constexpr int kKeys = 8;                        // scores per thread held in registers (4096 pages)
+constexpr int kNearCached = 256;                // pages near the threshold kept in shared memory
 constexpr float kScoreEps = 1.f / 131072.f;
 
 __device__ __forceinline__ int select_pages_of(const PagedKv& c, int len) {
@@ -182,7 +183,6 @@ template <bool BF16, int D>
 __global__ void __launch_bounds__(kSelectThreads) fa_select_kernel(const SelectParams p) {
   constexpr int kWarps = kSelectThreads / 32;
   constexpr int E = D / 32;   // channels per lane
-  __shared__ uint32_t s_key[kSelectCached];
   __shared__ int s_hist[256];
   __shared__ int2 s_warp[kWarps];
   __shared__ unsigned long long s_exact[kNearCached];
@@ -207,49 +207,74 @@ __global__ void __launch_bounds__(kSelectThreads) fa_select_kernel(const SelectP
   const float2* score = p.score + base;
   const int lo_s = p.first, hi_s = n - p.last;     // the pages that compete: more than `want`
   const int want = p.max_sel - p.first - p.last;
+  // Each thread has a run of pages, so that counts in thread order are counts in page order.  Their
+  // keys stay in registers where a run is at most kKeys, and are read again (from L2) in every pass
+  // over longer runs, kKeys at a time.
+  const int run = (n + kSelectThreads - 1) / kSelectThreads;
+  const int a0 = min(n, tid * run), a1 = min(n, a0 + run);
+  uint32_t keys[kKeys];
+  auto competes = [&](int s) { return s >= lo_s && s < min(hi_s, a1); };
   float eps = 0.f;
   uint32_t kmin = 0xffffffffu, kmax = 0;
-  for (int s = lo_s + tid; s < hi_s; s += kSelectThreads) {
-    const float2 x = score[s];
-    const uint32_t k = ordered(x.x);
-    eps = fmaxf(eps, x.y);
-    kmin = min(kmin, k);
-    kmax = max(kmax, k);
-    if (s - lo_s < kSelectCached) s_key[s - lo_s] = k;
+  for (int s0 = a0; s0 < a1; s0 += kKeys) {
+#pragma unroll
+    for (int j = 0; j < kKeys; ++j) {
+      if (!competes(s0 + j)) continue;
+      const float2 x = score[s0 + j];
+      keys[j] = ordered(x.x);
+      eps = fmaxf(eps, x.y);
+      kmin = min(kmin, keys[j]);
+      kmax = max(kmax, keys[j]);
+    }
   }
+  auto fetch = [&](int s0) {
+    if (run <= kKeys) return;
+#pragma unroll
+    for (int j = 0; j < kKeys; ++j)
+      if (competes(s0 + j)) keys[j] = ordered(score[s0 + j].x);
+  };
 #pragma unroll
   for (int w = 16; w; w >>= 1) eps = fmaxf(eps, __shfl_xor_sync(0xffffffffu, eps, w));
   kmin = __reduce_min_sync(0xffffffffu, kmin);
   kmax = __reduce_max_sync(0xffffffffu, kmax);
   if (lane == 0) s_top[warp] = eps, s_lo[warp] = kmin, s_hi[warp] = kmax;
   if (tid < 256) s_hist[tid] = 0;
+  if (tid <= kNearCached / 32) s_mark[tid] = 0;
   if (tid == 0) s_left = want;
   __syncthreads();
+  // (every warp by itself over the 16 partial results)
+  eps = s_top[lane % kWarps];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    eps = fmaxf(eps, s_top[w]);
-    kmin = min(kmin, s_lo[w]);
-    kmax = max(kmax, s_hi[w]);
-  }
-  auto key = [&](int s) { return s - lo_s < kSelectCached ? s_key[s - lo_s] : ordered(score[s].x); };
+  for (int w = kWarps / 2; w; w >>= 1) eps = fmaxf(eps, __shfl_xor_sync(0xffffffffu, eps, w));
+  kmin = __reduce_min_sync(0xffffffffu, s_lo[lane % kWarps]);
+  kmax = __reduce_max_sync(0xffffffffu, s_hi[lane % kWarps]);
+  const float two = __fmul_ru(2.f * kScoreEps, eps) + 0x1p-100f;   // 2 e (products may underflow)
 
   // the want-th largest key, up to eight bits at a time below the bits that all keys share
-  // (scores have few exponents: without that the first passes would count into one place)
+  // (scores have few exponents: without that the first passes would count into one place), until
+  // what is left undecided is less than the scores' errors: T is then that interval
   uint32_t prefix = kmin;
+  int bits = 0;                                      // undecided
   if (want > 0 && kmin != kmax) {
-    int bits = 32 - __clz(kmin ^ kmax);              // undecided
+    bits = 32 - __clz(kmin ^ kmax);
     prefix = bits < 32 ? kmin >> bits : 0;
     while (bits > 0) {
       const int w = min(bits, 8), shift = bits - w;
-      for (int s = lo_s + tid; s < hi_s; s += kSelectThreads) {
-        const uint32_t k = key(s);
-        if (bits == 32 || (k >> bits) == prefix) atomicAdd(&s_hist[(k >> shift) & ((1u << w) - 1)], 1);
+#pragma unroll 1
+      for (int s0 = a0; s0 < a1; s0 += kKeys) {
+        fetch(s0);
+#pragma unroll
+        for (int j = 0; j < kKeys; ++j)
+          if (competes(s0 + j) && (bits == 32 || (keys[j] >> bits) == prefix))
+            atomicAdd(&s_hist[(keys[j] >> shift) & ((1u << w) - 1)], 1);
       }
       __syncthreads();
       if (warp == 0) {   // lane i has digits 255 - 8 i down to 248 - 8 i
         int c[8], sum = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum += c[e] = s_hist[255 - 8 * lane - e];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_hist[255 - 8 * lane - e] = 0;
         int inc = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -260,46 +285,46 @@ __global__ void __launch_bounds__(kSelectThreads) fa_select_kernel(const SelectP
         __syncwarp();
         int above = inc - sum;
         if (above < left && left <= inc) {
+          int e = 0;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (above < left && left <= above + c[e]) {
-              s_prefix = (prefix << w) | (uint32_t)(255 - 8 * lane - e);
-              s_left = left - above;
-              break;
-            }
-            above += c[e];
-          }
+          for (int i = 0; i < 7; ++i)
+            if (e == i && above + c[i] < left) above += c[i], e = i + 1;
+          s_prefix = (prefix << w) | (uint32_t)(255 - 8 * lane - e);
+          s_left = left - above;
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s_hist[255 - 8 * lane - e] = 0;
       }
       __syncthreads();
       prefix = s_prefix;
       bits = shift;
+      if (unordered(prefix << bits | ((1u << bits) - 1)) - unordered(prefix << bits) <= two) break;
     }
   }
   // the limits, rounded outwards, as keys (a zero limit takes the sign that keeps zeros near)
-  const float mid = unordered(prefix);
-  const float two = __fmul_ru(2.f * kScoreEps, eps) + 0x1p-100f;   // (products may underflow)
   const bool blind = !(two < INFINITY);           // a bound that is not finite: all of them in 64 bits
-  const float up = __fadd_ru(mid, two), down = __fadd_rd(mid, -two);
+  const float up = __fadd_ru(unordered(prefix << bits | ((1u << bits) - 1)), two);
+  const float down = __fadd_rd(unordered(prefix << bits), -two);
   const uint32_t above = ordered(up == 0.f ? 0.f : up), below = ordered(down == 0.f ? -0.f : down);
-  // 0: out, 1: taken, 2: near.  A page that is none (-inf) is never near a finite threshold.
-  auto kind = [&](int s) {
-    if (s < lo_s || s >= hi_s) return 1;
-    if (want == 0) return 0;
-    if (blind) return 2;
-    const uint32_t k = key(s);
-    return k > above ? 1 : k >= below ? 2 : 0;
+  // Which pages of [s0, s0 + kKeys) are taken and which near, as bits.  (A page that is none, -inf,
+  // is never near a finite threshold.)
+  auto sort_out = [&](int s0, unsigned& sure, unsigned& near) {
+    fetch(s0);
+    sure = near = 0;
+#pragma unroll
+    for (int j = 0; j < kKeys; ++j) {
+      const int s = s0 + j;
+      if (s >= a1) continue;
+      if (!competes(s)) sure |= 1u << j;                  // first or last: always
+      else if (want > 0 && !blind && keys[j] > above) sure |= 1u << j;
+      else if (want > 0 && (blind || keys[j] >= below)) near |= 1u << j;
+    }
   };
-  // each thread has a run of pages, so that counts in thread order are counts in page order
-  const int run = (n + kSelectThreads - 1) / kSelectThreads;
-  const int a0 = min(n, tid * run), a1 = min(n, a0 + run);
+  unsigned sure_bits = 0, near_bits = 0;                  // of the run's last kKeys (its only ones, mostly)
   int sure = 0, near = 0;
-  for (int s = a0; s < a1; ++s) {
-    const int k = kind(s);
-    sure += k == 1;
-    near += k == 2;
+#pragma unroll 1
+  for (int s0 = a0; s0 < a1; s0 += kKeys) {
+    sort_out(s0, sure_bits, near_bits);
+    sure += __popc(sure_bits);
+    near += __popc(near_bits);
   }
   int2 inc = make_int2(sure, near);
 #pragma unroll
@@ -308,16 +333,12 @@ __global__ void __launch_bounds__(kSelectThreads) fa_select_kernel(const SelectP
     if (lane >= d) inc.x += x, inc.y += y;
   }
   if (lane == 31) s_warp[warp] = inc;
-  if (tid <= kNearCached / 32) s_mark[tid] = 0;
   __syncthreads();
-  int n_sure = 0, n_near = 0, place = inc.x - sure, near0 = inc.y - near;   // of all, and before this run
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int2 x = s_warp[w];
-    n_sure += x.x;
-    n_near += x.y;
-    if (w < warp) place += x.x, near0 += x.y;
-  }
+  // of all, and before this run: every warp adds up the 16 by itself
+  const int2 part = lane < kWarps ? s_warp[lane] : make_int2(0, 0);
+  const int n_sure = __reduce_add_sync(0xffffffffu, part.x), n_near = __reduce_add_sync(0xffffffffu, part.y);
+  int place = __reduce_add_sync(0xffffffffu, lane < warp ? part.x : 0) + inc.x - sure;
+  const int near0 = __reduce_add_sync(0xffffffffu, lane < warp ? part.y : 0) + inc.y - near;
   const int take = p.max_sel - n_sure;                 // of the near ones
   const bool choose = n_near > take;                   // (block-uniform) some of them have to go
   const bool small = n_near <= kNearCached;
@@ -325,17 +346,30 @@ __global__ void __launch_bounds__(kSelectThreads) fa_select_kernel(const SelectP
   int32_t* list = small ? s_list : p.near + base;
   uint32_t* mark = small ? s_mark : p.mark + base;
   if (choose) {
-    for (int s = a0, i = near0; s < a1; ++s)
-      if (kind(s) == 2) exact[i] = 0, list[i++] = s;
+#pragma unroll 1
+    for (int s0 = a0, i = near0; s0 < a1; s0 += kKeys) {
+      if (run > kKeys) sort_out(s0, sure_bits, near_bits);
+      for (unsigned x = near_bits; x; x &= x - 1, ++i) {
+        exact[i] = 0;
+        list[i] = s0 + __ffs(x) - 1;
+      }
+    }
     if (!small)
       for (int i = tid; i < (n_near + 31) / 32; i += kSelectThreads) mark[i] = 0;
     __syncthreads();
     // a warp per page and row; the rows' maximum as an ordered number
     const uint16_t* q = p.q + (long long)unit * p.rows * D + E * lane;
-    for (long long i = warp; i < (long long)n_near * p.rows; i += kWarps) {
-      const int at_list = (int)(i / p.rows), r = (int)(i % p.rows);
+#pragma unroll 1
+    for (int at_list = 0, r = warp; at_list < n_near;) {
+      if (r >= p.rows) {
+        r -= p.rows, ++at_list;
+        continue;
+      }
       const int id = p.kv.table[(long long)b * p.kv.table_stride + list[at_list]];
-      if (id < 0 || id >= p.kv.num_pages) continue;      // below all others
+      if (id < 0 || id >= p.kv.num_pages) {              // below all others
+        r += kWarps;
+        continue;
+      }
       const long long at = ((long long)id * p.Hkv + hk) * D + E * lane;
       double x = 0.;
 #pragma unroll
@@ -353,11 +387,14 @@ __global__ void __launch_bounds__(kSelectThreads) fa_select_kernel(const SelectP
         const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.);   // (-0 as 0)
         atomicMax(exact + at_list, u >> 63 ? ~u : u | 0x8000000000000000ull);
       }
+      r += kWarps;
     }
     __syncthreads();
+#pragma unroll 1
     for (int i = tid; i < n_near; i += kSelectThreads) {   // the list is in page order
       const unsigned long long x = exact[i];
       int ahead = 0;
+#pragma unroll 1
       for (int j = 0; j < n_near; ++j) ahead += exact[j] > x || (exact[j] == x && j < i);
       if (ahead < take) atomicOr(&mark[i >> 5], 1u << (i & 31));
     }
@@ -369,11 +406,19 @@ __global__ void __launch_bounds__(kSelectThreads) fa_select_kernel(const SelectP
   } else {
     place += near0;
   }
-  for (int s = a0, i = near0; s < a1; ++s) {
-    const int k = kind(s);
-    const bool in = k == 1 || (k == 2 && (!choose || (mark[i >> 5] >> (i & 31) & 1)));
-    i += k == 2;
-    if (in && place < p.max_sel) out[place++] = s;
+#pragma unroll 1
+  for (int s0 = a0, i = near0; s0 < a1; s0 += kKeys) {
+    if (run > kKeys) sort_out(s0, sure_bits, near_bits);
+#pragma unroll 1
+    for (unsigned x = sure_bits | near_bits; x; x &= x - 1) {
+      const int j = __ffs(x) - 1;
+      bool in = true;
+      if (near_bits >> j & 1) {
+        in = !choose || (mark[i >> 5] >> (i & 31) & 1);
+        ++i;
+      }
+      if (in && place < p.max_sel) out[place++] = s0 + j;
+    }
   }
 }
 
