@@ -22,8 +22,9 @@
 //     the channels) as the 16-row side of mma.m16n8k16 and the rows as its
 //     8-column side: 4 rows of a common group waste 4 of 8 columns there, but
 //     would waste 124 of the 128 lanes of a tcgen05 tile, whose accumulator
-//     also costs a round trip through TMEM before every exponential.  Up to 64
-//     rows the warp-level products stay behind the copies;
+//     also costs a round trip through TMEM before every exponential.  Up to 32
+//     rows the warp-level products stay behind the copies (launch_decode_rows
+//     has the figures past that);
 //   * P goes into the value product as hi + lo pairs of the cache's type (the
 //     tensor cores are idle, and a single bf16 P would add an error as large as
 //     the rounding of O).

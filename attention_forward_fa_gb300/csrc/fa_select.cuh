@@ -57,9 +57,10 @@ __device__ __forceinline__ int select_pages_of(const PagedKv& c, int len) {
 // pieces that it will feed to the matrix instructions, so that nothing has to be exchanged and no
 // register waits for memory: 24 KB in flight per warp (D 128), nine warps per SM, and three
 // independent chains of matrix instructions per warp.  (Measured with the second kernel, 2048 pages
-// of 64 (sequence, KV head) pairs, D 128: bounds loaded to registers, 12 warps of 8 KB per SM, 38.6
-// us; one long run of groups per warp through a ring of three, one chain at a time, 31.1 us; this
-// 28.1 us.)
+// of 64 (sequence, KV head) pairs, D 128, 67 MB of bounds: this 25.9 us, of which 18 are this
+// kernel's, in two rounds of blocks and the end of a third; bounds loaded to registers, 12 warps of
+// 8 KB per SM, 38.6 us; one long run of groups per warp through a ring of three 35 us: one group at
+// a time leaves the latency of its matrix instructions bare.)
 template <bool BF16, int D>
 __global__ void __launch_bounds__(32) fa_page_score_kernel(const SelectParams p) {
   constexpr int C = D / 32;
