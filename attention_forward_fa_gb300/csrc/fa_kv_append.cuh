@@ -25,7 +25,7 @@ struct AppendParams {
   long long k_sb, k_sh, k_ss, v_sb, v_sh, v_ss, q_sb, q_sh, q_ss, o_sb, o_sh, o_ss;
   const float* cos;
   const float* sin;
-  int rot_dim, interleaved, max_pos;
+  int rot_dim, max_pos;
   const int32_t* kv_lens;
   const int32_t* new_lens;
   int Hq, Hkv, Snew;
@@ -36,7 +36,7 @@ struct AppendParams {
   int* status;
 };
 
-template <bool BF16, int D>
+template <bool BF16, int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const AppendParams p) {
   constexpr int L = D / 16;                    // threads per row
   constexpr int kRows = kAppendThreads / L;    // rows per step
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const A
   const int tp = 1 << p.tp_shift;
   const int tl = row & (tp - 1), hl = row >> p.tp_shift, hp = kRows >> p.tp_shift;
   const bool turns = part < p.rot_dim / 16;
-  const bool halves = turns && !p.interleaved;
+  const bool halves = turns && !INTERLEAVED;
   const int offA = halves ? 8 * part : 16 * part;
   const int offB = halves ? 8 * part + p.rot_dim / 2 : 16 * part + 8;
   const int half = p.rot_dim / 2;
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const A
     float a[8], d[8];
     unpack8<BF16>(wa, a);
     unpack8<BF16>(wb, d);
-    if (p.interleaved) {
+    if constexpr (INTERLEAVED) {
       float x[16];
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = a[j], x[8 + j] = d[j];

@@ -85,8 +85,9 @@ fa::PagedKv device_cache(const fa_paged_kv_t* kv) {
 }
 
 template <bool BF16, int D>
-cudaError_t launch_append(const fa::AppendParams& p, unsigned grid, cudaStream_t st) {
-  return launch_dependent(fa::fa_kv_append_kernel<BF16, D>, grid, fa::kAppendThreads, 0, st, p);
+cudaError_t launch_append(const fa::AppendParams& p, bool interleaved, unsigned grid, cudaStream_t st) {
+  return interleaved ? launch_dependent(fa::fa_kv_append_kernel<BF16, D, true>, grid, fa::kAppendThreads, 0, st, p)
+                     : launch_dependent(fa::fa_kv_append_kernel<BF16, D, false>, grid, fa::kAppendThreads, 0, st, p);
 }
 
 // 5-D view (64 channels, slots, D / 64, heads, pages) of a pool, in boxes of
@@ -230,7 +231,6 @@ int fa_kv_append(const fa_paged_kv_t* kv, const fa_kv_new_t* x, int B, int Hq, i
   p.cos = x->cos;
   p.sin = x->sin;
   p.rot_dim = x->rot_dim;
-  p.interleaved = x->interleaved;
   p.max_pos = x->max_pos;
   p.kv_lens = kv_lens;
   p.new_lens = new_lens;
@@ -251,9 +251,11 @@ int fa_kv_append(const fa_paged_kv_t* kv, const fa_kv_new_t* x, int B, int Hq, i
   if (!p.status) return cuda_fail(cudaGetLastError());
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool fp16 = (mask_mode & FA_DTYPE_FP16) != 0;
+  const bool il = x->interleaved != 0;
+  const unsigned blocks = (unsigned)grid;
   const cudaError_t e =
-      D == 128 ? (fp16 ? launch_append<false, 128>(p, (unsigned)grid, st) : launch_append<true, 128>(p, (unsigned)grid, st))
-               : (fp16 ? launch_append<false, 64>(p, (unsigned)grid, st) : launch_append<true, 64>(p, (unsigned)grid, st));
+      D == 128 ? (fp16 ? launch_append<false, 128>(p, il, blocks, st) : launch_append<true, 128>(p, il, blocks, st))
+               : (fp16 ? launch_append<false, 64>(p, il, blocks, st) : launch_append<true, 64>(p, il, blocks, st));
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
