@@ -41,8 +41,7 @@ struct SelectParams {
   int* status;
 };
 
-constexpr int kScoreGroups = 3;                 // groups of 16 pages per block of one warp
-constexpr int kScorePages = 16 * kScoreGroups;
+constexpr int kScorePages = 16;                 // pages per block of one warp
 constexpr int kSelectThreads = 512;
 constexpr int kKeys = 8;                        // scores per thread held in registers (4096 pages)
 constexpr int kNearCached = 256;                // pages near the threshold kept in shared memory
@@ -53,18 +52,17 @@ __device__ __forceinline__ int select_pages_of(const PagedKv& c, int len) {
   return (len + (1 << c.page_shift) - 1) >> c.page_shift;
 }
 
-// One warp per block of 48 pages.  Each lane copies to shared memory, all at once, the very 16-byte
-// pieces that it will feed to the matrix instructions, so that nothing has to be exchanged and no
-// register waits for memory: 24 KB in flight per warp (D 128), nine warps per SM, and three
-// independent chains of matrix instructions per warp.  (Measured with the second kernel, 2048 pages
-// of 64 (sequence, KV head) pairs, D 128, 67 MB of bounds: this 25.9 us, of which 18 are this
-// kernel's, in two rounds of blocks and the end of a third; bounds loaded to registers, 12 warps of
-// 8 KB per SM, 38.6 us; one long run of groups per warp through a ring of three 35 us: one group at
-// a time leaves the latency of its matrix instructions bare.)
+// One warp per block of 16 pages.  Each lane copies to shared memory, all at once, the very 16-byte pieces that
+// it will feed to the matrix instructions, so that nothing has to be exchanged and no register waits
+// for memory: 8 KB in flight per warp (D 128), 24 warps per SM.  (Measured with the second kernel,
+// 2048 pages of 64 (sequence, KV head) pairs, D 128, 67 MB of bounds: this 23.3 us, of which 15.6 are
+// this kernel's; 32 pages per warp 24.4 us, 48 25.9 us, 64 25.5 us: fewer, longer blocks end
+// unevenly; bounds loaded to registers, 12 warps per SM, 38.6 us; one long run of pages per warp
+// through a ring of three groups 35 us: it leaves the latency of the matrix instructions bare.)
 template <bool BF16, int D>
 __global__ void __launch_bounds__(32) fa_page_score_kernel(const SelectParams p) {
   constexpr int C = D / 32;
-  __shared__ __align__(16) uint4 s_in[kScoreGroups][2][2][C][32];   // [group][bound][page half][step][lane]
+  __shared__ __align__(16) uint4 s_in[2][2][C][32];   // [bound][page half][step][lane]
   pdl_wait_prior();
   pdl_launch_dependents();   // (after the wait: the next kernel may read the lengths as it starts)
   const int unit = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
@@ -74,98 +72,76 @@ __global__ void __launch_bounds__(32) fa_page_score_kernel(const SelectParams p)
   if (chunk == 0 && hk == 0 && lane == 0) (void)paged_len(p.kv, p.kv_lens[b], p.status);
   const int first = chunk * kScorePages;
   if (first >= n) return;
-  const int last = min(n, first + kScorePages);
-  int ids[(kScorePages + 31) / 32];
+  const int ids = lane < 16 && first + lane < n ? paged_id(p.kv, b, first + lane, p.status) : -1;
+  // of pages first + g and first + g + 8: 8 channels at 32 c + 8 t4 of either bound
+  bool good[2];
 #pragma unroll
-  for (int i = 0; i < (kScorePages + 31) / 32; ++i)
-    ids[i] = first + 32 * i + lane < last ? paged_id(p.kv, b, first + 32 * i + lane, p.status) : -1;
-  // of pages 16 group + g and + 8: 8 channels at 32 c + 8 t4 of either bound
-  bool good[kScoreGroups][2];
+  for (int j = 0; j < 2; ++j) {
+    const int id = __shfl_sync(0xffffffffu, ids, g + 8 * j);
+    good[j] = id >= 0;
+    if (id < 0) continue;          // (its stale bounds reach no other page's products)
+    const long long at = ((long long)id * p.Hkv + hk) * D + 8 * t4;
 #pragma unroll
-  for (int gr = 0; gr < kScoreGroups; ++gr) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int id = __shfl_sync(0xffffffffu, ids[gr / 2], 16 * (gr & 1) + g + 8 * j);
-      good[gr][j] = id >= 0;
-      if (id < 0) continue;        // (its stale bounds reach no other page's products)
-      const long long at = ((long long)id * p.Hkv + hk) * D + 8 * t4;
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        cp_async16(smem_u32(&s_in[gr][0][j][c][lane]), p.kv.k_min + at + 32 * c);
-        cp_async16(smem_u32(&s_in[gr][1][j][c][lane]), p.kv.k_max + at + 32 * c);
-      }
+    for (int c = 0; c < C; ++c) {
+      cp_async16(smem_u32(&s_in[0][j][c][lane]), p.kv.k_min + at + 32 * c);
+      cp_async16(smem_u32(&s_in[1][j][c][lane]), p.kv.k_max + at + 32 * c);
     }
-    cp_async_commit();
   }
+  cp_async_commit();
   const uint16_t* q = p.q + (long long)unit * p.rows * D + 8 * t4;   // [B, Hkv, rows, D]
   auto magnitude = [](uint32_t x) { return x & 0x7FFF7FFFu; };
-  float best[kScoreGroups][2], scale[kScoreGroups][2];
-  bool odd[kScoreGroups][2];       // a score that is not finite: only 64 bits can tell
-#pragma unroll
-  for (int gr = 0; gr < kScoreGroups; ++gr)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) best[gr][j] = -INFINITY, scale[gr][j] = 0.f, odd[gr][j] = false;
+  float best[2] = {-INFINITY, -INFINITY}, scale[2] = {0.f, 0.f};
+  bool odd[2] = {false, false};    // a score that is not finite: only 64 bits can tell
   for (int r0 = 0; r0 < p.rows; r0 += 8) {
     uint4 w[C];
 #pragma unroll
     for (int c = 0; c < C; ++c)
       w[c] = r0 + g < p.rows ? *reinterpret_cast<const uint4*>(q + (long long)(r0 + g) * D + 32 * c) : make_uint4(0, 0, 0, 0);
+    if (r0 == 0) cp_async_wait_all();          // (every lane its own copies)
+    float acc[4] = {0.f, 0.f, 0.f, 0.f}, err[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int gr = 0; gr < kScoreGroups; ++gr) {
-      if (r0 == 0) {               // (every lane waits for its own copies only)
-        if (gr == 0) asm volatile("cp.async.wait_group %0;" ::"n"(kScoreGroups - 1) : "memory");
-        else if (gr == 1) asm volatile("cp.async.wait_group %0;" ::"n"(kScoreGroups - 2) : "memory");
-        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+    for (int c = 0; c < C; ++c) {
+      const uint4 l0 = s_in[0][0][c][lane], l1 = s_in[0][1][c][lane];
+      const uint4 h0 = s_in[1][0][c][lane], h1 = s_in[1][1][c][lane];
+      const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+      const uint32_t lo[2][4] = {{l0.x, l0.y, l0.z, l0.w}, {l1.x, l1.y, l1.z, l1.w}};
+      const uint32_t hi[2][4] = {{h0.x, h0.y, h0.z, h0.w}, {h1.x, h1.y, h1.z, h1.w}};
+#pragma unroll
+      for (int h = 0; h < 4; h += 2) {
+        const uint32_t ah[4] = {hi[0][h], hi[1][h], hi[0][h + 1], hi[1][h + 1]};
+        const uint32_t al[4] = {lo[0][h], lo[1][h], lo[0][h + 1], lo[1][h + 1]};
+        float u[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};   // from zero: see the bound above
+        mma_16x8<BF16>(u, ah, max16x2<BF16>(x[h], 0u), max16x2<BF16>(x[h + 1], 0u));
+        mma_16x8<BF16>(u, al, min16x2<BF16>(x[h], 0u), min16x2<BF16>(x[h + 1], 0u));
+        const uint32_t bh[4] = {magnitude(ah[0]), magnitude(ah[1]), magnitude(ah[2]), magnitude(ah[3])};
+        const uint32_t bl[4] = {magnitude(al[0]), magnitude(al[1]), magnitude(al[2]), magnitude(al[3])};
+        mma_16x8<BF16>(v, bh, magnitude(x[h]), magnitude(x[h + 1]));
+        mma_16x8<BF16>(v, bl, magnitude(x[h]), magnitude(x[h + 1]));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] += u[e], err[e] += v[e];
       }
-      float acc[4] = {0.f, 0.f, 0.f, 0.f}, err[4] = {0.f, 0.f, 0.f, 0.f};
+    }
+    // lane (g, t4): pages g (0, 1) and g + 8 (2, 3), rows 2 t4 and 2 t4 + 1
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const uint4 l0 = s_in[gr][0][0][c][lane], l1 = s_in[gr][0][1][c][lane];
-        const uint4 h0 = s_in[gr][1][0][c][lane], h1 = s_in[gr][1][1][c][lane];
-        const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-        const uint32_t lo[2][4] = {{l0.x, l0.y, l0.z, l0.w}, {l1.x, l1.y, l1.z, l1.w}};
-        const uint32_t hi[2][4] = {{h0.x, h0.y, h0.z, h0.w}, {h1.x, h1.y, h1.z, h1.w}};
-#pragma unroll
-        for (int h = 0; h < 4; h += 2) {
-          const uint32_t ah[4] = {hi[0][h], hi[1][h], hi[0][h + 1], hi[1][h + 1]};
-          const uint32_t al[4] = {lo[0][h], lo[1][h], lo[0][h + 1], lo[1][h + 1]};
-          float u[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};   // from zero: see the bound above
-          mma_16x8<BF16>(u, ah, max16x2<BF16>(x[h], 0u), max16x2<BF16>(x[h + 1], 0u));
-          mma_16x8<BF16>(u, al, min16x2<BF16>(x[h], 0u), min16x2<BF16>(x[h + 1], 0u));
-          const uint32_t bh[4] = {magnitude(ah[0]), magnitude(ah[1]), magnitude(ah[2]), magnitude(ah[3])};
-          const uint32_t bl[4] = {magnitude(al[0]), magnitude(al[1]), magnitude(al[2]), magnitude(al[3])};
-          mma_16x8<BF16>(v, bh, magnitude(x[h]), magnitude(x[h + 1]));
-          mma_16x8<BF16>(v, bl, magnitude(x[h]), magnitude(x[h + 1]));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[e] += u[e], err[e] += v[e];
-        }
-      }
-      // lane (g, t4): pages g (0, 1) and g + 8 (2, 3), rows 2 t4 and 2 t4 + 1
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (r0 + 2 * t4 + (e & 1) >= p.rows) continue;
-        best[gr][e >> 1] = fmaxf(best[gr][e >> 1], acc[e]);
-        scale[gr][e >> 1] = fmaxf(scale[gr][e >> 1], err[e]);
-        odd[gr][e >> 1] |= !(fabsf(acc[e]) < INFINITY) || !(err[e] < INFINITY);
-      }
+    for (int e = 0; e < 4; ++e) {
+      if (r0 + 2 * t4 + (e & 1) >= p.rows) continue;
+      best[e >> 1] = fmaxf(best[e >> 1], acc[e]);
+      scale[e >> 1] = fmaxf(scale[e >> 1], err[e]);
+      odd[e >> 1] |= !(fabsf(acc[e]) < INFINITY) || !(err[e] < INFINITY);
     }
   }
 #pragma unroll
-  for (int gr = 0; gr < kScoreGroups; ++gr) {
+  for (int j = 0; j < 2; ++j) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int x = 1; x < 4; x <<= 1) {
-        best[gr][j] = fmaxf(best[gr][j], __shfl_xor_sync(0xffffffffu, best[gr][j], x));
-        scale[gr][j] = fmaxf(scale[gr][j], __shfl_xor_sync(0xffffffffu, scale[gr][j], x));
-        odd[gr][j] |= __shfl_xor_sync(0xffffffffu, (int)odd[gr][j], x) != 0;
-      }
-      const int s = first + 16 * gr + g + 8 * j;
-      if (t4 == 0 && s < last)      // a page that is none scores below all others
-        p.score[(long long)unit * p.kv.max_pages + s] =
-            good[gr][j] ? make_float2(odd[gr][j] ? 0.f : best[gr][j], odd[gr][j] ? INFINITY : scale[gr][j])
-                        : make_float2(-INFINITY, 0.f);
+    for (int x = 1; x < 4; x <<= 1) {
+      best[j] = fmaxf(best[j], __shfl_xor_sync(0xffffffffu, best[j], x));
+      scale[j] = fmaxf(scale[j], __shfl_xor_sync(0xffffffffu, scale[j], x));
+      odd[j] |= __shfl_xor_sync(0xffffffffu, (int)odd[j], x) != 0;
     }
+    const int s = first + g + 8 * j;
+    if (t4 == 0 && s < n)            // a page that is none scores below all others
+      p.score[(long long)unit * p.kv.max_pages + s] =
+          good[j] ? make_float2(odd[j] ? 0.f : best[j], odd[j] ? INFINITY : scale[j]) : make_float2(-INFINITY, 0.f);
   }
 }
 
