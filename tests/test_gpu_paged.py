@@ -685,3 +685,23 @@ def test_wrappers_refuse_what_does_not_fit():
     with pytest.raises(ValueError):
         fa.paged_kv_append(c.obj, n, x, x, cos=torch.zeros(50, 8, device="cuda"))
     assert _status() == 0
+
+
+def test_front_page_serving_example_runs():
+    """The front page's generation step, as written there; over all pages and over
+    the chosen ones it answers what the reference does."""
+    import re
+    from pathlib import Path
+    import torch
+    import attention_forward_fa_gb300 as fa
+    text = (Path(__file__).resolve().parents[1] / "README.md").read_text()
+    block = [b for b in re.findall(r"```python\n(.*?)```", text, re.S) if "paged_kv_append" in b][0]
+    env = {"torch": torch, "fa": fa}
+    torch.manual_seed(30)
+    exec(compile(block, "serving-example", "exec"), env)
+    k, v, t = _host(env["k_pages"]), _host(env["v_pages"]), env["table"].cpu().numpy()
+    q, pages = _host(env["q"]), env["pages"].cpu().numpy()
+    _check(env["o"], env["lse"], P.decode(q, k, v, t, [1001, 38], 128 ** -0.5), "bf16")
+    lo, hi = (_host(b) for b in env["bounds"])
+    assert np.array_equal(pages, P.select(q, lo, hi, t, [1001, 38], 64, 8))
+    _check(env["o8"], env["lse8"], P.decode(q, k, v, t, [1001, 38], 128 ** -0.5, None, pages), "bf16")
