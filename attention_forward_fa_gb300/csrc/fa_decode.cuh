@@ -54,9 +54,14 @@ constexpr int kDecCtasPerSm = 2;
 constexpr int kDecThreads = 32 * (kDecWarps + 1);     // and the producer
 constexpr int kUnitTiles = 2;                         // a unit's own cost, in tiles (0: ragged lengths 30 % slower)
 // A row's reference (the subtrahend of its exponents) follows its maximum lazily: it stays while no
-// score exceeds it by more than this many powers of two, so that the usual tile needs one vote and
-// no shuffles.  P <= 2^8 fits both 16-bit types; every sum is relative to the reference.
+// score exceeds it by more than kMaxOver powers of two (beyond the lift below), so that the usual
+// tile needs one vote and no shuffles; every sum is relative to the reference.  With fp16 the
+// reference is set kLift below the maximum, so that the largest P lie between 2^7 and 2^15 and small
+// ones keep an absolute error of 2^-25 / 2^7 of the largest instead of 2^-25 (fp16's subnormals);
+// bf16 has fp32's range and needs none.
 constexpr float kMaxOver = 8.f;
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.f : 7.f;
 constexpr float kNoScore = -3.402823466e38f;          // the reference before a row's first key
 
 struct DecodeParams {
@@ -76,7 +81,7 @@ struct DecodeParams {
   int ctas;
   float scale_log2;
   float* part_o;               // [2 * ctas][8 NT][D], unnormalised: slot 2 c + 1 begins its unit
-  float2* part_ml;             // [2 * ctas][8 NT]: maximum (log2 units), sum
+  float2* part_ml;             // [2 * ctas][8 NT]: reference (log2 units), sum
   long long timeout_ns;
   int* status;
 };
@@ -501,7 +506,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) over = fmaxf(over, c[n][e] - m[n][e & 1]);   // (NaN is dropped)
-      if (named_or(2, 32 * kDecWarps, over > kMaxOver)) {   // the references move up to the maxima
+      if (named_or(2, 32 * kDecWarps, over > kMaxOver + kLift<BF16>)) {   // the references move up
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float mx[2] = {fmaxf(c[n][0], c[n][2]), fmaxf(c[n][1], c[n][3])};
@@ -519,8 +524,8 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
 #pragma unroll
           for (int w = 0; w < kDecWarps; ++w) {
             const float2 x = *reinterpret_cast<const float2*>(s_max + (w * NT + n) * 8 + 2 * t4);
-            top[0] = fmaxf(top[0], x.x);
-            top[1] = fmaxf(top[1], x.y);
+            top[0] = fmaxf(top[0], x.x - kLift<BF16>);
+            top[1] = fmaxf(top[1], x.y - kLift<BF16>);
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {

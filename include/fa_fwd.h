@@ -389,7 +389,10 @@ int fa_convert_v_fp16(const void* v_bf16, void* v_fp16, int64_t n_elems, void* s
  * position without a row in the rotation tables leaves the keys or tokens
  * concerned out (a sequence of such a length counts as empty and gets no
  * tokens) and is reported as FA_ERR_INDEX by fa_check_status.  Entries
- * of the page table past a sequence's last page are never read. */
+ * of the page table past a sequence's last page are never read.  Make one call
+ * of each kind before a stream capture (kernels and scratch pool are set up on
+ * first use); captured calls read lengths, tables and lists anew at every
+ * replay, and scratch that a call takes in a capture belongs to that graph. */
 
 /* The cache (host struct).  Element (page, head, slot, d) of K is
  *   k[page * k_stride_page + head * k_stride_head + slot * k_stride_slot + d],

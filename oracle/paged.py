@@ -53,15 +53,16 @@ def append(k_pages, v_pages, table, lens, k, v, new_lens, cos=None, sin=None,
 
 
 def decode(q, k_pages, v_pages, table, lens, scale, pre_tokens=None, page_idx=None):
-    """(O, LSE, A, X): the attention of q [B, Hq, Sq, D] over the pages, its
+    """(O, LSE, A, X, V): the attention of q [B, Hq, Sq, D] over the pages, its
     log-sum-exp (+inf for a row that sees no key, O = 0 there), and for error
-    bounds A = sum_j p_j |v_j| per output and X = max over the row's keys of
-    scale * sum_d |q_d k_jd|."""
+    bounds A = sum_j p_j |v_j| and V = sum_j |v_j| per output and X = max over
+    the row's keys of scale * sum_d |q_d k_jd|."""
     B, Hq, Sq, D = q.shape
     Hkv, page = k_pages.shape[1], k_pages.shape[2]
     G = Hq // Hkv
     O = np.zeros((B, Hq, Sq, D))
     A = np.zeros((B, Hq, Sq, D))
+    V = np.zeros((B, Hq, Sq, D))
     L = np.full((B, Hq, Sq), np.inf)
     X = np.zeros((B, Hq, Sq))
     for b in range(B):
@@ -92,9 +93,10 @@ def decode(q, k_pages, v_pages, table, lens, scale, pre_tokens=None, page_idx=No
                     l = e.sum()
                     O[b, h * G + g, i] = (e / l) @ vs
                     A[b, h * G + g, i] = (e / l) @ np.abs(vs)
+                    V[b, h * G + g, i] = np.abs(vs).sum(0)
                     L[b, h * G + g, i] = m + np.log(l)
                     X[b, h * G + g, i] = abs(scale) * (np.abs(ks) @ np.abs(x)).max()
-    return O, L, A, X
+    return O, L, A, X, V
 
 
 def select(q, k_min, k_max, table, lens, page, max_sel, first=1, last=1):

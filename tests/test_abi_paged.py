@@ -161,3 +161,14 @@ def test_cache_object_refuses_what_is_no_cache():
 
 def test_error_string_of_paged_calls():
     assert "page" in B.fa_strerror(B.FA_ERR_INDEX)
+
+
+def test_wrappers_refuse_a_stream_of_another_device():
+    import torch
+
+    class Other:
+        device = torch.device("cuda", 1)
+        cuda_stream = 0
+
+    with pytest.raises(ValueError):
+        B._elsewhere(torch.device("cuda", 0), Other(), lambda raw: pytest.fail("called"))

@@ -13,7 +13,9 @@ value at most):
     subtraction (2^-22 of the largest |score|, itself <= X) and of the
     exponential and the hi + lo split of P (2^-16 together), so that
     |O - ref| <= (2 e_s + 2^-20 X + 2^-15) A + (u + 2^-20) |ref| with
-    A = sum_j p_j |v_j| (numerator and denominator: twice);
+    A = sum_j p_j |v_j| (numerator and denominator: twice).  An fp16 P has an
+    absolute error of up to 2^-25 besides (its subnormals), where the largest P
+    of the row is at least 2^7: 2^-32 sum_j |v_j| more;
   * |LSE - ref| <= e_s + 2^-21 X + 2^-20 (1 + |ref|).
 Whole numbers and untouched memory are equal bit for bit."""
 import math
@@ -258,7 +260,7 @@ DECODE = [
 
 
 def _check(got_o, got_l, ref, dtype, where=""):
-    O, L, A, X = ref
+    O, L, A, X, V = ref
     o, l = _host(got_o), _host(got_l)
     u = U[dtype]
     empty = np.isposinf(L)
@@ -266,6 +268,7 @@ def _check(got_o, got_l, ref, dtype, where=""):
     assert (o[empty] == 0).all()
     es = 2.0 ** -16 * X
     lim = (2 * es + 2.0 ** -20 * X + 2.0 ** -15)[..., None] * A + (u + 2.0 ** -20) * np.abs(O) + SUB[dtype]
+    lim += (2.0 ** -32 if dtype == "fp16" else 0.0) * V
     err = np.abs(o - O)
     assert (err <= lim).all(), f"{where}: O off by {(err / np.maximum(lim, 1e-30)).max():.3g} of its bound"
     le = np.abs(l[~empty] - L[~empty])
@@ -285,15 +288,40 @@ def test_decode(case):
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.2, 1.0, 5.0])
-def test_decode_scales_and_peaks(scale):
-    """Scores from flat to one-hot, and a negative scale."""
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_decode_scales_and_peaks(dtype, scale):
+    """Scores from flat to one-hot, and a negative scale; a channel whose values
+    are 0 at the keys that matter shows the small probabilities."""
     import attention_forward_fa_gb300 as fa
     lens = [300, 33]
-    c = Cache(6, "bf16", 2, 2, 128, 32, lens)
-    q = _round(c.rng.standard_normal((2, 8, 1, 128)), "bf16")
-    o, l = fa.flash_attention_decode(_dev(q, "bf16"), c.obj, c.ints(lens), scale=scale)
+    c = Cache(6, dtype, 2, 2, 128, 32, lens)
+    q = _round(c.rng.standard_normal((2, 8, 1, 128)), dtype)
+    s = np.einsum("hd,kd->hk", q[0, :4, 0], c.k[c.table[0], 0].reshape(-1, 128)[:300])
+    v = c.v[c.table[0], 0].reshape(-1, 128)
+    v[np.unique(np.argsort(-abs(scale) * s, axis=1)[:, :2]), 5] = 0
+    c.v[c.table[0], 0] = v.reshape(-1, 32, 128)
+    c.tv.copy_(_dev(c.v, dtype))
+    o, l = fa.flash_attention_decode(_dev(q, dtype), c.obj, c.ints(lens), scale=scale)
     assert _status() == 0
-    _check(o, l, P.decode(q, c.k, c.v, c.table, lens, scale), "bf16", f"scale {scale}")
+    _check(o, l, P.decode(q, c.k, c.v, c.table, lens, scale), dtype, f"scale {scale}")
+
+
+def test_decode_growing_scores():
+    """Keys of ever larger scores: the reference of every row moves many times,
+    in the middle of the pieces and between them, and never by too little."""
+    import attention_forward_fa_gb300 as fa
+    for dtype, step in (("bf16", 0.02), ("fp16", 0.02), ("fp16", 0.3), ("bf16", -0.05)):
+        lens = [1500]
+        c = Cache(29, dtype, 1, 1, 64, 64, lens)
+        k = c.k[c.table[0], 0].reshape(-1, 64)
+        k[:, 0] = _round(np.arange(k.shape[0]) * step, dtype)
+        c.k[c.table[0], 0] = k.reshape(-1, 64, 64)
+        c.tk.copy_(_dev(c.k, dtype))
+        q = _round(0.1 * c.rng.standard_normal((1, 4, 1, 64)), dtype)
+        q[..., 0] = np.array([1.0, 0.5, -1.0, 0.0])[None, :, None]
+        o, l = fa.flash_attention_decode(_dev(q, dtype), c.obj, c.ints(lens), scale=1.0)
+        assert _status() == 0
+        _check(o, l, P.decode(q, c.k, c.v, c.table, lens, 1.0), dtype, f"{dtype} {step}")
 
 
 @pytest.mark.parametrize("dtype,Sq,pre", [("bf16", 1, None), ("fp16", 1, 20), ("bf16", 4, 37), ("fp16", 3, None)])
@@ -611,6 +639,7 @@ def test_other_streams_and_graphs():
     o, l = fa.flash_attention_decode(q[0], c.obj, n, stream=s)
     i = fa.select_kv_pages(q[0], c.obj, n, 8, stream=s.cuda_stream)
     s.synchronize()
+    assert torch.equal(fa.select_kv_pages(q[0], c.obj, n, 8, stream=0), picks[0])     # the default stream by its handle
     assert torch.equal(o, want[0][0]) and torch.equal(l, want[0][1]) and torch.equal(i, picks[0])
     graphs, outs = [], []
     for x in q[:2]:

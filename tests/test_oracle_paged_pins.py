@@ -46,7 +46,7 @@ def test_decode_over_all_pages_is_the_dense_reference():
     k, v = rng.standard_normal((2, B, Hkv, S, D))
     q = rng.standard_normal((B, Hq, S, D))
     kp, vp, table = _scatter(k, v, 16, 9, rng)
-    O, L, _, _ = P.decode(q[:, :, S - Sq:], kp, vp, table, [S, S], 0.3)
+    O, L, _, _, _ = P.decode(q[:, :, S - Sq:], kp, vp, table, [S, S], 0.3)
     for b in range(B):
         for h in range(Hq):
             Od, Ld = A.attention_fwd(q[b:b + 1, h:h + 1], k[b:b + 1, h // 2:h // 2 + 1],
@@ -60,14 +60,14 @@ def test_decode_limits():
     k, v = rng.standard_normal((2, 1, 1, 40, 8))
     q = rng.standard_normal((1, 1, 2, 8))
     kp, vp, table = _scatter(k, v, 16, 5, rng)
-    O, L, _, _ = P.decode(q, kp, vp, table, [1], 1.0)         # row 0 lies before the first token
+    O, L, _, _, _ = P.decode(q, kp, vp, table, [1], 1.0)         # row 0 lies before the first token
     assert np.all(O[0, 0, 0] == 0) and np.isposinf(L[0, 0, 0])
     assert np.allclose(O[0, 0, 1], v[0, 0, 0])                # a single key
-    O, L, _, _ = P.decode(q, kp, vp, table, [0], 1.0)
+    O, L, _, _, _ = P.decode(q, kp, vp, table, [0], 1.0)
     assert np.all(O == 0) and np.isposinf(L).all()
-    O, _, _, _ = P.decode(q, kp, vp, table, [40], 1.0, pre_tokens=0)
+    O, _, _, _, _ = P.decode(q, kp, vp, table, [40], 1.0, pre_tokens=0)
     assert np.allclose(O[0, 0], v[0, 0, 38:40])               # each row sees itself alone
-    O, _, _, _ = P.decode(0 * q, kp, vp, table, [40], 1.0, page_idx=np.array([[[1, -1, 1, 9]]]))
+    O, _, _, _, _ = P.decode(0 * q, kp, vp, table, [40], 1.0, page_idx=np.array([[[1, -1, 1, 9]]]))
     assert np.allclose(O[0, 0, 0], v[0, 0, 16:32].mean(0))    # listed twice, invalid slots
 
 
