@@ -64,26 +64,38 @@ template <bool BF16>
 constexpr float kLift = BF16 ? 0.f : 7.f;
 constexpr float kNoScore = -3.402823466e38f;          // the reference before a row's first key
 
-struct DecodeParams {
-  CUtensorMap tm_k;   // (64 channels, slots, D / 64, heads, pages)
-  CUtensorMap tm_v;
-  PagedKv kv;
+// What every warp needs, in as few lines of the parameter bank as it takes: the first touch of each
+// is a miss, and the way to a CTA's first copy would pay them one after the other.
+struct DecodeCore {
+  const int32_t* kv_lens;
+  const int32_t* table;
+  long long table_stride;
+  const int32_t* sel;          // [B, Hkv, max_sel] or null
+  int max_len;                 // what a table row holds
+  int num_pages, page_shift;   // page size = 1 << page_shift
+  int max_sel, sel_tiles;      // listed pages, and as tiles
+  int B, Hkv;
+  int rows;                    // G * Sq
+  int groups;                  // row groups per KV head
+  int units;                   // Hkv * groups
+  int ctas;
+  unsigned long long units_inv, ctas_inv;   // ceil(2^64 / x): quotients by a product's upper half
+  int Sq;
+  int pre_tokens;              // -1: unbounded
+  int reach;                   // Sq + pre_tokens: the keys that some row sees are the last `reach`; -1: all
+  float scale_log2;
+  int* status;
   const uint16_t* q;
   uint16_t* o;
   float* lse;
-  const int32_t* kv_lens;
-  const int32_t* sel;          // [B, Hkv, max_sel] or null
-  int max_sel;
-  int B, Hq, Hkv, Sq;
-  int rows;                    // G * Sq
-  int groups;                  // row groups per KV head
-  int pre_tokens;              // -1: unbounded
-  int ctas;
-  float scale_log2;
   float* part_o;               // [2 * ctas][8 NT][D], unnormalised: slot 2 c + 1 begins its unit
   float2* part_ml;             // [2 * ctas][8 NT]: reference (log2 units), sum
   long long timeout_ns;
-  int* status;
+};
+struct DecodeParams {
+  DecodeCore c;
+  CUtensorMap tm_k;   // (64 channels, slots, D / 64, heads, pages)
+  CUtensorMap tm_v;
 };
 
 template <int D, int NT>
@@ -110,29 +122,23 @@ struct DecodeSmem {
 struct DecodeSpan {
   int lo, hi, first, n;
 };
-__device__ __forceinline__ DecodeSpan decode_span(const DecodeParams& p, int len) {
+__device__ __forceinline__ DecodeSpan decode_span(const DecodeCore& p, int len) {
   DecodeSpan s;
-  len = max(len, 0);
   s.hi = len;
-  s.lo = p.pre_tokens >= 0 ? (int)max(0LL, (long long)len - p.Sq - p.pre_tokens) : 0;
-  if (p.sel) {
-    s.first = 0;
-    s.n = (int)((((long long)p.max_sel << p.kv.page_shift) + kDecTile - 1) / kDecTile);
-  } else {
-    s.first = s.lo / kDecTile;
-    s.n = max(1, (len + kDecTile - 1) / kDecTile - s.first);
-  }
+  s.lo = p.reach >= 0 ? max(0, len - p.reach) : 0;
+  s.first = p.sel ? 0 : s.lo / kDecTile;
+  s.n = p.sel ? p.sel_tiles : max(1, (len + kDecTile - 1) / kDecTile - s.first);
   return s;
 }
-__device__ __forceinline__ int decode_len(const DecodeParams& p, int b) {
+__device__ __forceinline__ int decode_len(const DecodeCore& p, int b) {
   // from L2: the join kernel may read lengths that this SM's L1 holds from an earlier call
   const int len = __ldcg(p.kv_lens + b);
-  return len < 0 || len > (p.kv.max_pages << p.kv.page_shift) ? 0 : len;
+  return len < 0 || len > p.max_len ? 0 : len;
 }
 
 // The lengths and charges of sequences base + 32 i + lane: eight independent loads.
 constexpr int kChunks = 8;
-__device__ __forceinline__ void decode_charges(const DecodeParams& p, int base, int lane, int (&len)[kChunks],
+__device__ __forceinline__ void decode_charges(const DecodeCore& p, int base, int lane, int (&len)[kChunks],
                                                int (&c)[kChunks]) {
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
@@ -146,18 +152,31 @@ __device__ __forceinline__ void decode_charges(const DecodeParams& p, int base, 
   for (int i = 0; i < kChunks; ++i)
     if (base + 32 * i + lane < p.B) c[i] = decode_span(p, len[i]).n + kUnitTiles;
 }
+// Sum over the warp of numbers below 2^59, in three pieces by the warp's reduction.
 __device__ __forceinline__ long long warp_sum(long long x) {
-#pragma unroll
-  for (int w = 16; w; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-  return x;
+  const unsigned m = 0xffffffu;
+  const long long lo = __reduce_add_sync(0xffffffffu, (unsigned)x & m);
+  const long long mid = __reduce_add_sync(0xffffffffu, (unsigned)(x >> 24) & m);
+  const long long hi = __reduce_add_sync(0xffffffffu, (unsigned)(x >> 48));
+  return lo + (mid << 24) + (hi << 48);
+}
+// Quotient of numbers >= 0; the schedule's fit 32 bits but for the longest, and it waits for them.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+// a / d by inv = ceil(2^64 / d) (0 stands for d = 1): exact while a * d < 2^64.
+__device__ __forceinline__ long long times_inverse(long long a, unsigned long long inv) {
+  return inv ? (long long)__umul64hi((unsigned long long)a, inv) : a;
 }
 // CTAs that share `total` charged tiles, the start of CTA c's range, the CTA that has tile t.
-__device__ __forceinline__ int decode_ctas(const DecodeParams& p, long long total) {
+__device__ __forceinline__ int decode_ctas(const DecodeCore& p, long long total) {
   return (int)min((long long)p.ctas, total);
 }
-__device__ __forceinline__ long long decode_first(long long total, int n, int c) { return total * c / n; }
+__device__ __forceinline__ long long decode_first(const DecodeCore& p, long long total, int c) {
+  return total <= p.ctas ? c : times_inverse(total * c, p.ctas_inv);
+}
 __device__ __forceinline__ int decode_owner(long long total, int n, long long t) {
-  return (int)(((t + 1) * n - 1) / total);
+  return (int)quotient((t + 1) * n - 1, total);
 }
 // A walk over the units of a CTA's range: unit `unit` (KV head, row group) of sequence b, from its
 // charged tile `off`; `left` charged tiles to go.
@@ -223,7 +242,8 @@ __device__ __forceinline__ void mma_16x8(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 template <bool BF16, int D, int NT>
-__global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(const __grid_constant__ DecodeParams params) {
+  const DecodeCore& p = params.c;
   using SM = DecodeSmem<D, NT>;
   constexpr int NS = SM::kStages;
   constexpr int KS = D / 16;                   // 16-channel steps
@@ -236,11 +256,10 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
   DecodeWalk* s_walk = reinterpret_cast<DecodeWalk*>(smem + SM::kMiscOff);   // where this CTA starts,
   int* s_len = reinterpret_cast<int*>(smem + SM::kMiscOff + 24);             // the length there
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + SM::kMiscOff + 28);
-  const int units = p.Hkv * p.groups;                // per sequence
 
   if (threadIdx.x == 0) {
-    tma_prefetch_desc(&p.tm_k);
-    tma_prefetch_desc(&p.tm_v);
+    tma_prefetch_desc(&params.tm_k);
+    tma_prefetch_desc(&params.tm_v);
     for (int s = 0; s < NS; ++s) {
       mbar_init(FULL(s), 1);
       mbar_init(EMPTY(s), kDecWarps);
@@ -253,54 +272,72 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
   pdl_launch_dependents();
   if (warp == kDecWarps) {   // this CTA's range of charged tiles, and the sequence it starts in
     int len[kChunks], c[kChunks];
-    long long sum = 0;
-    for (int base = 32 * kChunks; base < p.B; base += 32 * kChunks) {
-      decode_charges(p, base, lane, len, c);
+    int mine = 0, my_len = 0, inc;           // of the sequence `at + lane`, its chunk of 32 summed up
+    auto scan = [&](int x) {
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+      }
+      return x;
+    };
+    long long total, start = 0, end = 0, first, before = 0;
+    int at = 0;
+    auto range = [&]() {
+      if ((int)blockIdx.x < decode_ctas(p, total)) {
+        start = decode_first(p, total, blockIdx.x);
+        end = decode_first(p, total, blockIdx.x + 1);
+      }
+      // in charges of one unit per sequence: the sequence is the last with at most so many before it
+      first = times_inverse(start, p.units_inv);
+    };
+    if (p.B <= 32) {
+      if (lane < p.B) {
+        my_len = decode_len(p, lane);
+        mine = decode_span(p, my_len).n + kUnitTiles;
+      }
+      inc = scan(mine);
+      total = (long long)__shfl_sync(0xffffffffu, inc, 31) * p.units;
+      range();
+    } else {
+      long long sum = 0;
+      for (int base = 32 * kChunks; base < p.B; base += 32 * kChunks) {
+        decode_charges(p, base, lane, len, c);
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) sum += c[i];
+      }
+      decode_charges(p, 0, lane, len, c);         // (kept for the search)
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) sum += c[i];
-    }
-    decode_charges(p, 0, lane, len, c);         // (kept for the search)
+      total = warp_sum(sum) * p.units;
+      range();
+      at = -1;
+      for (int base = 0; at < 0; base += 32 * kChunks) {
+        if (base) decode_charges(p, base, lane, len, c);
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) sum += c[i];
-    const long long total = warp_sum(sum) * units;
-    const int n = decode_ctas(p, total);
-    long long start = 0, end = 0;
-    if ((int)blockIdx.x < n) {
-      start = decode_first(total, n, blockIdx.x);
-      end = decode_first(total, n, blockIdx.x + 1);
-    }
-    const long long first = start / units;   // in charges of one unit per sequence: the sequence is
-    long long before = 0;                    // the last with at most so many before it
-    int mine = 0, my_len = 0, at = -1;       // of its chunk of 32, and where that begins
-    for (int base = 0; at < 0; base += 32 * kChunks) {
-      if (base) decode_charges(p, base, lane, len, c);
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        if (at >= 0) break;
-        const int in = __reduce_add_sync(0xffffffffu, (unsigned)c[i]);   // (32 of at most 2^25 + 2)
-        if (before + in > first || base + 32 * (i + 1) >= p.B) at = base + 32 * i, mine = c[i], my_len = len[i];
-        else before += in;
+        for (int i = 0; i < kChunks; ++i) {
+          if (at >= 0) break;
+          const int in = __reduce_add_sync(0xffffffffu, (unsigned)c[i]);   // (32 of at most 2^25 + 2)
+          if (before + in > first || base + 32 * (i + 1) >= p.B) at = base + 32 * i, mine = c[i], my_len = len[i];
+          else before += in;
+        }
       }
-    }
-    int inc = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += x;
+      inc = scan(mine);
     }
     const unsigned here = __ballot_sync(0xffffffffu, mine > 0 && before + inc - mine <= first);
     if (lane == 31 - __clz(here)) {
-      const long long off = start - (before + inc - mine) * units;
-      *s_walk = DecodeWalk{at + lane, (int)(off / mine), (int)(off % mine), end - start};
+      const long long off = start - (before + inc - mine) * p.units;
+      const int unit = (int)quotient(off, mine);
+      *s_walk = DecodeWalk{at + lane, unit, (int)(off - (long long)unit * mine), end - start};
       *s_len = my_len;
     }
   } else if (blockIdx.x == 0) {   // lengths that the tables cannot hold are reported once
-    for (int i = threadIdx.x; i < p.B; i += 32 * kDecWarps) (void)paged_len(p.kv, p.kv_lens[i], p.status);
+    for (int i = threadIdx.x; i < p.B; i += 32 * kDecWarps) if (const int len = p.kv_lens[i]; len < 0 || len > p.max_len) atomicOr(p.status, fa_host::kStatusIndex);
   }
   __syncthreads();
   DecodeWalk walk = *s_walk;
   const WaitCtx wc{s_abort, p.status, p.timeout_ns};
-  const int box_shift = min(p.kv.page_shift, 6);     // slots per copy
+  const int box_shift = min(p.page_shift, 6);     // slots per copy
   const int box = 1 << box_shift;
 
   if (warp == kDecWarps) {
@@ -313,40 +350,43 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
     while (walk.left > 0 && !dead) {
       const DecodeSpan s = decode_span(p, len);
       const int b = walk.b, hk = walk.unit / p.groups;
-      const DecodePiece d = decode_step(walk, s.n, units);
+      const DecodePiece d = decode_step(walk, s.n, p.units);
       if (walk.b != b && walk.left > 0) len = decode_len(p, walk.b);
       const int t0 = d.t0, nt = d.nt;
-      const int n_pages = (s.hi + (1 << p.kv.page_shift) - 1) >> p.kv.page_shift;
+      const int n_pages = (s.hi + (1 << p.page_shift) - 1) >> p.page_shift;
       // Lane i looks up sub-block c0 + i of the unit (box keys each): page, first slot, first key.
       auto look_up = [&](int c, int& id, int& slot, int& key) {
         id = -1, slot = 0, key = -1;
         if (c >= (t0 + nt) * nsub) return;
         int page;
         if (p.sel) {
-          const int spp = p.kv.page_shift - box_shift;    // log2 sub-blocks per page
+          const int spp = p.page_shift - box_shift;    // log2 sub-blocks per page
           const int at = c >> spp;
           if (at >= p.max_sel) return;
           page = p.sel[((long long)b * p.Hkv + hk) * p.max_sel + at];
           if (page < 0 || page >= n_pages) return;
           slot = (c & ((1 << spp) - 1)) << box_shift;
-          key = (page << p.kv.page_shift) + slot;
+          key = (page << p.page_shift) + slot;
         } else {
           key = s.first * kDecTile + (c << box_shift);
-          page = key >> p.kv.page_shift;
-          slot = key & ((1 << p.kv.page_shift) - 1);
+          page = key >> p.page_shift;
+          slot = key & ((1 << p.page_shift) - 1);
         }
         if (key >= s.hi || key + box <= s.lo) {           // (also any key of an empty sequence)
           key = -1;
           return;
         }
-        id = paged_id(p.kv, b, page, p.status);
-        if (id < 0) key = -1;
+        id = p.table[(long long)b * p.table_stride + page];
+        if (id < 0 || id >= p.num_pages) {
+          atomicOr(p.status, fa_host::kStatusIndex);
+          id = key = -1;
+        }
       };
       int id, slot, key, id2 = -1, slot2 = 0, key2 = -1;
       const int per = 32 / nsub;                          // tiles per look-up
       look_up(t0 * nsub + lane, id, slot, key);
       for (int j = 0; j < nt; ++j, ++it) {
-        const int in = j % per;
+        const int in = j & (per - 1);
         if (in == 0 && j) id = id2, slot = slot2, key = key2;
         const int st = it % NS;
         bool ok = true;
@@ -365,8 +405,8 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
         __syncwarp();
         if (holder && id >= 0) {
           const uint32_t dst = sbase + (uint32_t)st * 2 * SM::kHalf + (uint32_t)sub * sub_bytes;
-          tma_load_5d(dst, &p.tm_k, FULL(st), slot, hk, id);
-          tma_load_5d(dst + SM::kHalf, &p.tm_v, FULL(st), slot, hk, id);
+          tma_load_5d(dst, &params.tm_k, FULL(st), slot, hk, id);
+          tma_load_5d(dst + SM::kHalf, &params.tm_v, FULL(st), slot, hk, id);
         }
         // the next look-up, a look-up's tiles ahead of its use
         if (in == 0) look_up((t0 + j + per) * nsub + lane, id2, slot2, key2);
@@ -406,13 +446,13 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
   int it = 0;
   bool dead = false;
   auto first_row = [&](const DecodeWalk& w) {
-    return (long long)w.b * p.Hq * p.Sq + (long long)(w.unit / p.groups) * p.rows + (w.unit % p.groups) * 8 * NT;
+    return ((long long)w.b * p.Hkv + w.unit / p.groups) * p.rows + (w.unit % p.groups) * 8 * NT;
   };
   while (walk.left > 0) {
     const int len = next_len, rg = walk.unit % p.groups, b = walk.b;
     const long long row0 = first_row(walk);
     const DecodeSpan s = decode_span(p, len);
-    const DecodePiece d = decode_step(walk, s.n, units);
+    const DecodePiece d = decode_step(walk, s.n, p.units);
     if (walk.left > 0) {           // what the next unit will want: its length, and Q on its way to L1
       if (walk.b != b) next_len = decode_len(p, walk.b);
       if (warp == 0) {
@@ -670,7 +710,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
 // it alone (the same bits every time).  WPR warps per row: 8 where there are few
 // rows, whose units may then have as many pieces as the grid has CTAs; 1 else.
 template <bool BF16, int D, int WPR>
-__global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_constant__ DecodeParams p, int rows8) {
+__global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_constant__ DecodeCore p, int rows8) {
   __shared__ __align__(16) float s_o[WPR > 1 ? 8 : 1][D];
   __shared__ float2 s_ml[8];
   // The schedule before the wait: by the time this kernel runs every CTA of the decode kernel has
@@ -679,7 +719,7 @@ __global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_consta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * (8 / WPR) + warp / WPR;
   const int part = warp % WPR;
-  const long long per_b = (long long)p.Hq * p.Sq;
+  const long long per_b = (long long)p.Hkv * p.rows;
   if (row >= per_b * p.B) return;
   const int b = (int)(row / per_b);
   const int in_b = (int)(row % per_b);
@@ -695,11 +735,10 @@ __global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_consta
       if (base + 32 * i + lane < b) before += c[i];
     }
   }
-  const int units = p.Hkv * p.groups;
-  total = warp_sum(total) * units;
+  total = warp_sum(total) * p.units;
   const int ctas = decode_ctas(p, total);
   const int n = decode_span(p, decode_len(p, b)).n;
-  const long long t0 = warp_sum(before) * units + (long long)(hk * p.groups + rg) * (n + kUnitTiles) + kUnitTiles;
+  const long long t0 = warp_sum(before) * p.units + (long long)(hk * p.groups + rg) * (n + kUnitTiles) + kUnitTiles;
   const int c0 = decode_owner(total, ctas, t0), c1 = decode_owner(total, ctas, t0 + n - 1);
   pdl_wait_prior();
   if (c0 == c1) return;          // finished by its CTA

@@ -125,18 +125,21 @@ int launch_decode(fa::DecodeParams& p, long long most_tiles, cudaStream_t st) {
   if (attr_err[dev & 63] != cudaSuccess) return cuda_fail(attr_err[dev & 63]);
   const int sms = fa_host::sm_count();
   if (sms <= 0) return cuda_fail(cudaErrorInvalidDevice);
-  p.ctas = (int)std::min<long long>(fa::kDecCtasPerSm * sms, most_tiles);
-  const size_t o_bytes = (size_t)2 * p.ctas * 8 * NT * D * 4;
-  void* scratch = fa_host::scratch_alloc(o_bytes + (size_t)2 * p.ctas * 8 * NT * 8, st);
+  p.c.ctas = (int)std::min<long long>(fa::kDecCtasPerSm * sms, most_tiles);
+  auto inverse = [](unsigned long long d) { return d == 1 ? 0ull : ~0ull / d + 1; };   // ceil(2^64 / d)
+  p.c.ctas_inv = inverse(p.c.ctas);
+  p.c.units_inv = inverse(p.c.units);
+  const size_t o_bytes = (size_t)2 * p.c.ctas * 8 * NT * D * 4;
+  void* scratch = fa_host::scratch_alloc(o_bytes + (size_t)2 * p.c.ctas * 8 * NT * 8, st);
   if (!scratch) return cuda_fail(cudaGetLastError());
-  p.part_o = static_cast<float*>(scratch);
-  p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(scratch) + o_bytes);
-  cudaError_t e = launch_dependent(kern, (unsigned)p.ctas, fa::kDecThreads, smem, st, p);
+  p.c.part_o = static_cast<float*>(scratch);
+  p.c.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(scratch) + o_bytes);
+  cudaError_t e = launch_dependent(kern, (unsigned)p.c.ctas, fa::kDecThreads, smem, st, p);
   if (e == cudaSuccess) {
-    const long long rows = (long long)p.B * p.Hq * p.Sq;
+    const long long rows = (long long)p.c.B * p.c.Hkv * p.c.rows;
     e = rows <= 8LL * sms   // one wave of blocks
-            ? launch_dependent(fa::fa_decode_join_kernel<BF16, D, 8>, (unsigned)rows, 256, 0, st, p, 8 * NT)
-            : launch_dependent(fa::fa_decode_join_kernel<BF16, D, 1>, (unsigned)((rows + 7) / 8), 256, 0, st, p, 8 * NT);
+            ? launch_dependent(fa::fa_decode_join_kernel<BF16, D, 8>, (unsigned)rows, 256, 0, st, p.c, 8 * NT)
+            : launch_dependent(fa::fa_decode_join_kernel<BF16, D, 1>, (unsigned)((rows + 7) / 8), 256, 0, st, p.c, 8 * NT);
   }
   cudaFreeAsync(scratch, st);
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
@@ -148,11 +151,14 @@ int launch_decode_rows(fa::DecodeParams& p, long long tiles_per_unit, cudaStream
   // rows: up to 32 rows the time is that of the keys (16 sequences of 4096 tokens, 8 KV heads of 128:
   // 48 us at 4 rows, 57 us at 32), past that the matrix instructions' (71 us at 40 rows, 84 at 48,
   // 113 at 64; 40 rows as 64 took 112 us).
-  const int passes = (p.rows + 63) / 64;
-  const int need = ((p.rows + passes - 1) / passes + 7) / 8;
+  fa::DecodeCore& c = p.c;
+  const int passes = (c.rows + 63) / 64;
+  const int need = ((c.rows + passes - 1) / passes + 7) / 8;
   const int nt = need == 7 ? 8 : need;
-  p.groups = (p.rows + 8 * nt - 1) / (8 * nt);
-  const long long most = (tiles_per_unit + fa::kUnitTiles) * p.B * p.Hkv * p.groups;
+  c.groups = (c.rows + 8 * nt - 1) / (8 * nt);
+  if ((long long)c.Hkv * c.groups > 0x7FFFFFFFLL) return FA_ERR_SHAPE;
+  c.units = c.Hkv * c.groups;
+  const long long most = (tiles_per_unit + fa::kUnitTiles) * c.B * c.units;
   switch (nt) {
     case 1: return launch_decode<BF16, D, 1>(p, most, st);
     case 2: return launch_decode<BF16, D, 2>(p, most, st);
@@ -279,27 +285,33 @@ int fa_decode(const void* q, const fa_paged_kv_t* kv, void* o, float* lse, int B
   if (!encode_pool(&p.tm_k, kv->k, fp16, D, Hkv, kv, kv->k_stride_page, kv->k_stride_head, kv->k_stride_slot, box) ||
       !encode_pool(&p.tm_v, kv->v, fp16, D, Hkv, kv, kv->v_stride_page, kv->v_stride_head, kv->v_stride_slot, box))
     return cuda_fail(cudaErrorInvalidValue);
-  p.kv = device_cache(kv);
-  p.q = static_cast<const uint16_t*>(q);
-  p.o = static_cast<uint16_t*>(o);
-  p.lse = lse;
-  p.kv_lens = kv_lens;
-  p.sel = page_idx;
-  p.max_sel = max_sel;
-  p.B = B;
-  p.Hq = Hq;
-  p.Hkv = Hkv;
-  p.Sq = Sq;
-  p.rows = Hq / Hkv * Sq;
-  p.pre_tokens = pre_tokens;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.timeout_ns = fa_host::wait_timeout_ns();
-  p.status = fa_host::status_ptr();
-  if (!p.status) return cuda_fail(cudaGetLastError());
+  fa::DecodeCore& c = p.c;
+  c.kv_lens = kv_lens;
+  c.table = kv->page_table;
+  c.table_stride = kv->table_stride;
+  c.sel = page_idx;
+  c.max_len = kv->max_pages * kv->page_size;
+  c.num_pages = kv->num_pages;
+  c.page_shift = device_cache(kv).page_shift;
+  c.max_sel = max_sel;
+  c.B = B;
+  c.Hkv = Hkv;
+  c.rows = Hq / Hkv * Sq;
+  c.Sq = Sq;
+  c.pre_tokens = pre_tokens;
+  c.reach = pre_tokens < 0 ? -1 : (int)std::min<long long>((long long)Sq + pre_tokens, 0x7FFFFFFF);
+  c.scale_log2 = scale * 1.4426950408889634f;
+  c.q = static_cast<const uint16_t*>(q);
+  c.o = static_cast<uint16_t*>(o);
+  c.lse = lse;
+  c.timeout_ns = fa_host::wait_timeout_ns();
+  c.status = fa_host::status_ptr();
+  if (!c.status) return cuda_fail(cudaGetLastError());
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // the most tiles that a unit can have: the lengths are known on the device only
   const long long keys = (long long)(page_idx ? max_sel : kv->max_pages) * kv->page_size;
   const long long tiles = (keys + fa::kDecTile - 1) / fa::kDecTile;
+  c.sel_tiles = (int)tiles;
   if (D == 128)
     return fp16 ? launch_decode_rows<false, 128>(p, tiles, st) : launch_decode_rows<true, 128>(p, tiles, st);
   return fp16 ? launch_decode_rows<false, 64>(p, tiles, st) : launch_decode_rows<true, 64>(p, tiles, st);
