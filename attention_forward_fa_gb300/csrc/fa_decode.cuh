@@ -396,14 +396,16 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
           break;
         }
         const int sub = lane - in * nsub;
-        const bool holder = sub >= 0 && sub < nsub;
-        const unsigned live = __ballot_sync(0xffffffffu, holder && id >= 0);
-        if (holder)
-          for (int k = 0; k < box; k += 16) s_meta[st * 4 + (sub * box + k) / 16] = key < 0 ? -1 : key + k;
+        const bool mine = sub >= 0 && sub < nsub && id >= 0;
+        const unsigned live = __ballot_sync(0xffffffffu, mine);
+        // lanes 0 to 3: the first key of each 16
+        const int off = 16 * lane;
+        const int first = __shfl_sync(0xffffffffu, key, in * nsub + ((off & (kDecTile - 1)) >> box_shift));
+        if (lane < 4) s_meta[st * 4 + lane] = first < 0 ? -1 : first + (off & (box - 1));
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(FULL(st), 2u * sub_bytes * __popc(live));
         __syncwarp();
-        if (holder && id >= 0) {
+        if (mine) {
           const uint32_t dst = sbase + (uint32_t)st * 2 * SM::kHalf + (uint32_t)sub * sub_bytes;
           tma_load_5d(dst, &params.tm_k, FULL(st), slot, hk, id);
           tma_load_5d(dst + SM::kHalf, &params.tm_v, FULL(st), slot, hk, id);
@@ -707,17 +709,19 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
 
 // Joins the pieces of the units that several CTAs shared: the schedule is
 // computed anew from the lengths, the pieces summed in an order that depends on
-// it alone (the same bits every time).  WPR warps per row: 8 where there are few
-// rows, whose units may then have as many pieces as the grid has CTAs; 1 else.
+// it alone (the same bits every time).  WPR warps per row: 1 where there are many
+// rows, 8 where there are few, 32 where a unit may have so many pieces (one KV
+// head over 131072 tokens has one per CTA, 304).
 template <bool BF16, int D, int WPR>
-__global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_constant__ DecodeCore p, int rows8) {
-  __shared__ __align__(16) float s_o[WPR > 1 ? 8 : 1][D];
-  __shared__ float2 s_ml[8];
+__global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) fa_decode_join_kernel(const __grid_constant__ DecodeCore p, int rows8) {
+  constexpr int kWarps = WPR > 8 ? WPR : 8;
+  __shared__ __align__(16) float s_o[WPR][D];
+  __shared__ float2 s_ml[WPR];
   // The schedule before the wait: by the time this kernel runs every CTA of the decode kernel has
   // seen the kernels before it finish, so that the lengths are final.
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * (8 / WPR) + warp / WPR;
+  const long long row = (long long)blockIdx.x * (kWarps / WPR) + warp / WPR;
   const int part = warp % WPR;
   const long long per_b = (long long)p.Hkv * p.rows;
   if (row >= per_b * p.B) return;
@@ -743,27 +747,31 @@ __global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_consta
   pdl_wait_prior();
   if (c0 == c1) return;          // finished by its CTA
   auto at = [&](int c) { return (2LL * c + (c == c0 ? 1 : 0)) * rows8 + rr; };
-  // Eight pieces at a time: their loads wait for nothing but each other.
-  constexpr int E = D / 32, kPieces = 8;
+  // Some pieces at a time: their loads wait for nothing but each other.
+  constexpr int E = D / 32, kPieces = WPR > 1 ? 4 : 8;
   float m = kNoScore, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int cb = c0 + part * kPieces; cb <= c1; cb += WPR * kPieces) {
+  for (int cb = c0 + part; cb <= c1; cb += WPR * kPieces) {
     float2 ml[kPieces];
     float x[kPieces][E];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const bool in = cb + i <= c1;
-      const long long a = at(in ? cb + i : cb);
-      ml[i] = p.part_ml[a];
-      if (!in) ml[i] = make_float2(kNoScore, 0.f);
-      const float* src = p.part_o + a * D + E * lane;
-      if constexpr (E == 4) {
-        const float4 y = *reinterpret_cast<const float4*>(src);
-        x[i][0] = y.x, x[i][1] = y.y, x[i][2] = y.z, x[i][3] = y.w;
-      } else {
-        const float2 y = *reinterpret_cast<const float2*>(src);
-        x[i][0] = y.x, x[i][1] = y.y;
+      const int c = cb + i * WPR;
+      ml[i] = make_float2(kNoScore, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[i][e] = 0.f;
+      if (c <= c1) {
+        const long long a = at(c);
+        ml[i] = p.part_ml[a];
+        const float* src = p.part_o + a * D + E * lane;
+        if constexpr (E == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(src);
+          x[i][0] = y.x, x[i][1] = y.y, x[i][2] = y.z, x[i][3] = y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(src);
+          x[i][0] = y.x, x[i][1] = y.y;
+        }
       }
     }
     float top = m;
@@ -776,11 +784,10 @@ __global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_consta
     for (int e = 0; e < E; ++e) o[e] *= keep;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const bool in = cb + i <= c1;
-      const float f = in ? ex2_approx(ml[i].x - top) : 0.f;
+      const float f = ex2_approx(ml[i].x - top);     // (a piece that is none is all 0)
       l = fmaf(f, ml[i].y, l);
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = in ? fmaf(f, x[i][e], o[e]) : o[e];
+      for (int e = 0; e < E; ++e) o[e] = fmaf(f, x[i][e], o[e]);
     }
   }
   if constexpr (WPR > 1) {
@@ -789,12 +796,15 @@ __global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_consta
     if (lane == 0) s_ml[part] = make_float2(m, l);
     __syncthreads();
     if (part) return;
+    const float2 ml = lane < WPR ? s_ml[lane] : make_float2(kNoScore, 0.f);
+    m = ml.x;
 #pragma unroll
-    for (int w = 0; w < WPR; ++w) m = fmaxf(m, s_ml[w].x);
+    for (int w = WPR / 2; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+    m = __shfl_sync(0xffffffffu, m, 0);
     l = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll
+#pragma unroll 8
     for (int w = 0; w < WPR; ++w) {
       const float f = ex2_approx(s_ml[w].x - m);
       l = fmaf(f, s_ml[w].y, l);

@@ -137,9 +137,12 @@ int launch_decode(fa::DecodeParams& p, long long most_tiles, cudaStream_t st) {
   cudaError_t e = launch_dependent(kern, (unsigned)p.c.ctas, fa::kDecThreads, smem, st, p);
   if (e == cudaSuccess) {
     const long long rows = (long long)p.c.B * p.c.Hkv * p.c.rows;
-    e = rows <= 8LL * sms   // one wave of blocks
-            ? launch_dependent(fa::fa_decode_join_kernel<BF16, D, 8>, (unsigned)rows, 256, 0, st, p.c, 8 * NT)
-            : launch_dependent(fa::fa_decode_join_kernel<BF16, D, 1>, (unsigned)((rows + 7) / 8), 256, 0, st, p.c, 8 * NT);
+    if (rows > 8LL * sms)   // more than one wave of blocks of a row each
+      e = launch_dependent(fa::fa_decode_join_kernel<BF16, D, 1>, (unsigned)((rows + 7) / 8), 256, 0, st, p.c, 8 * NT);
+    else if (p.c.ctas / ((long long)p.c.B * p.c.units) < 32)   // pieces of a unit, nearly
+      e = launch_dependent(fa::fa_decode_join_kernel<BF16, D, 8>, (unsigned)rows, 256, 0, st, p.c, 8 * NT);
+    else
+      e = launch_dependent(fa::fa_decode_join_kernel<BF16, D, 32>, (unsigned)rows, 1024, 0, st, p.c, 8 * NT);
   }
   cudaFreeAsync(scratch, st);
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
@@ -147,14 +150,13 @@ int launch_decode(fa::DecodeParams& p, long long most_tiles, cudaStream_t st) {
 
 template <bool BF16, int D>
 int launch_decode_rows(fa::DecodeParams& p, long long tiles_per_unit, cudaStream_t st) {
-  // As few passes over the keys as 64 rows each allow, and as few columns of 8 as then hold a pass's
-  // rows: up to 32 rows the time is that of the keys (16 sequences of 4096 tokens, 8 KV heads of 128:
-  // 48 us at 4 rows, 57 us at 32), past that the matrix instructions' (71 us at 40 rows, 84 at 48,
-  // 113 at 64; 40 rows as 64 took 112 us).
+  // As few passes over the keys as 48 rows each allow, and as few columns of 8 as then hold a pass's
+  // rows.  Up to 32 rows the time is that of the keys, past that the matrix instructions', about 1.5
+  // us a row whatever the split (16 sequences of 4096 tokens, 8 KV heads of 128, bf16: 47 us at 4
+  // rows, 58 at 32, 69 at 40, 83 at 48, 101 at 64, 148 at 96; one pass of 64 rows spilled and took 127).
   fa::DecodeCore& c = p.c;
-  const int passes = (c.rows + 63) / 64;
-  const int need = ((c.rows + passes - 1) / passes + 7) / 8;
-  const int nt = need == 7 ? 8 : need;
+  const int passes = (c.rows + 47) / 48;
+  const int nt = ((c.rows + passes - 1) / passes + 7) / 8;
   c.groups = (c.rows + 8 * nt - 1) / (8 * nt);
   if ((long long)c.Hkv * c.groups > 0x7FFFFFFFLL) return FA_ERR_SHAPE;
   c.units = c.Hkv * c.groups;
@@ -165,8 +167,7 @@ int launch_decode_rows(fa::DecodeParams& p, long long tiles_per_unit, cudaStream
     case 3: return launch_decode<BF16, D, 3>(p, most, st);
     case 4: return launch_decode<BF16, D, 4>(p, most, st);
     case 5: return launch_decode<BF16, D, 5>(p, most, st);
-    case 6: return launch_decode<BF16, D, 6>(p, most, st);
-    default: return launch_decode<BF16, D, 8>(p, most, st);
+    default: return launch_decode<BF16, D, 6>(p, most, st);
   }
 }
 
