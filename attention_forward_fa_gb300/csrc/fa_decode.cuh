@@ -39,9 +39,9 @@
 //
 // Measured (32 query heads on 8 KV heads of 128, bf16, both kernels): 8 sequences
 // of 131072 tokens 599 us, 7.17 TB/s; 64 of mixed lengths up to 8192 167 us, 6.63
-// TB/s; one of 517 tokens 6.9 us, of which 2.5 pass before the first tile is
-// there (lengths, page ids, copies: three dependent trips to memory) and 2 are
-// the join.  What a call adds to its bytes' time is thus 5 to 10 us.
+// TB/s; one of 517 tokens 5.6 us, of which 1.9 pass before the first tile is
+// there (lengths, page ids, copies: three dependent trips to memory) and 1.4 are
+// the join.  What a call adds to its bytes' time is thus 4 to 9 us.
 #pragma once
 #include "fa_paged.cuh"
 #include "fa_tiled.cuh"   // bounded waits
