@@ -22,6 +22,7 @@ using fa_host::cuda_fail;
 using fa_host::launch_dependent;
 
 constexpr long long kMostTokens = (1LL << 31) - 65536;   // of one sequence: positions are 32-bit
+constexpr long long kMostRows = (1LL << 31) - 65536;     // of a call (B * heads * tokens), counted in 32 bits
 constexpr int kMostSel = 1 << 20;                        // listed pages of one KV head
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -198,6 +199,7 @@ int fa_kv_append(const fa_paged_kv_t* kv, const fa_kv_new_t* x, int B, int Hq, i
   int rc = validate_cache(kv, B, Hq, Hkv, Snew, D, mask_mode);
   if (rc == FA_OK) rc = validate_pools(kv, Hkv);
   if (rc != FA_OK) return rc;
+  if ((long long)B * (x->q ? Hq : Hkv) > kMostRows / Snew) return FA_ERR_SHAPE;
   if (!x->k || !x->v || !kv_lens || (x->q == nullptr) != (x->q_out == nullptr)) return FA_ERR_NULL;
   if (x->rot_dim < 0 || x->rot_dim > D || x->rot_dim % 16 || x->interleaved < 0 || x->interleaved > 1)
     return FA_ERR_SHAPE;
@@ -277,8 +279,7 @@ int fa_decode(const void* q, const fa_paged_kv_t* kv, void* o, float* lse, int B
   if (page_idx && (max_sel <= 0 || max_sel > kMostSel)) return FA_ERR_SHAPE;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(kv_lens, 4) || !aligned(page_idx, 4))
     return FA_ERR_ALIGN;
-  const long long rows = (long long)B * Hq * Sq;
-  if (rows > 0x7FFFFFFFLL) return FA_ERR_SHAPE;
+  if ((long long)B * Hq > kMostRows / Sq) return FA_ERR_SHAPE;
   fa::DecodeParams p;
   std::memset(&p, 0, sizeof(p));
   const bool fp16 = (mask_mode & FA_DTYPE_FP16) != 0;
@@ -328,8 +329,8 @@ int fa_select_pages(const void* q, const fa_paged_kv_t* kv, int32_t* page_idx, i
       (long long)first + last > max_sel)
     return FA_ERR_SHAPE;
   if (!aligned(q, 16) || !aligned(page_idx, 4) || !aligned(kv_lens, 4)) return FA_ERR_ALIGN;
+  if ((long long)B * Hq > kMostRows / Sq) return FA_ERR_SHAPE;
   const long long units = (long long)B * Hkv;
-  if (units > 0x7FFFFFFFLL) return FA_ERR_SHAPE;
   fa::SelectParams p;
   std::memset(&p, 0, sizeof(p));
   p.kv = device_cache(kv);

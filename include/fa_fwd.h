@@ -400,7 +400,8 @@ int fa_convert_v_fp16(const void* v_bf16, void* v_fp16, int64_t n_elems, void* s
  * over one page or head is not looked at); bases 16-byte aligned.  Any order of page,
  * head and slot is thus a cache (a [pages, slots, heads, D] pool, K and V halves
  * of one pool) as long as no two tokens share memory.  page_size: 16, 32, 64, 128 or 256;
- * max_pages entries per sequence, max_pages * page_size <= 2^31 - 65536.
+ * max_pages entries per sequence, max_pages * page_size <= 2^31 - 65536; the same
+ * limit holds for the rows of a call's queries (B * Hq * Sq) or new keys.
  * k_min / k_max: NULL, or [num_pages, Hkv, D] of the cache's type, contiguous,
  * 16-byte aligned: per page and channel the least and largest stored key,
  * written by fa_kv_append and read by fa_select_pages. */

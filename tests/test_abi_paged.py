@@ -99,6 +99,15 @@ def test_shapes(call, kw, code):
     assert call(**kw) == code
 
 
+@pytest.mark.parametrize("kw", [
+    dict(B=(1 << 31) - 1, Hq=(1 << 31) - 2, S=(1 << 31) - 1),        # past 64 bits as a product
+    dict(B=1 << 30, Hq=1 << 30, S=16), dict(B=1 << 16, S=1 << 12), dict(S=(1 << 28) - 8192 + 1),
+])
+@pytest.mark.parametrize("call", [decode, select, append])
+def test_more_rows_than_32_bits_count(call, kw):
+    assert call(**kw) == -2
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(q=None), -1), (dict(o=None), -1), (dict(lse=None), -1), (dict(kv_lens=None), -1),
     (dict(scale=float("nan")), -2), (dict(scale=float("inf")), -2), (dict(pre_tokens=-2), -2),
