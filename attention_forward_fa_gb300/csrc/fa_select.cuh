@@ -55,7 +55,7 @@ __device__ __forceinline__ int select_pages_of(const PagedKv& c, int len) {
 // One warp per block of 16 pages.  Each lane copies to shared memory, all at once, the very 16-byte pieces that
 // it will feed to the matrix instructions, so that nothing has to be exchanged and no register waits
 // for memory: 8 KB in flight per warp (D 128), 24 warps per SM.  (Measured with the second kernel,
-// 2048 pages of 64 (sequence, KV head) pairs, D 128, 67 MB of bounds: this 23.3 us, of which 15.6 are
+// 2048 pages of 64 (sequence, KV head) pairs, D 128, 67 MB of bounds: this 22.5 us, of which 15.6 are
 // this kernel's; 32 pages per warp 24.4 us, 48 25.9 us, 64 25.5 us: fewer, longer blocks end
 // unevenly; bounds loaded to registers, 12 warps per SM, 38.6 us; one long run of pages per warp
 // through a ring of three groups 35 us: it leaves the latency of the matrix instructions bare.)
@@ -159,7 +159,6 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kSelectThreads) fa_select_kernel(const SelectParams p) {
   constexpr int kWarps = kSelectThreads / 32;
-  constexpr int E = D / 32;   // channels per lane
   __shared__ int s_hist[256];
   __shared__ int2 s_warp[kWarps];
   __shared__ unsigned long long s_exact[kNearCached];
@@ -167,7 +166,7 @@ __global__ void __launch_bounds__(kSelectThreads) fa_select_kernel(const SelectP
   __shared__ uint32_t s_mark[kNearCached / 32 + 1];
   __shared__ float s_top[kWarps];
   __shared__ uint32_t s_lo[kWarps], s_hi[kWarps];
-  __shared__ uint32_t s_prefix;
+  __shared__ int s_digit;
   __shared__ int s_left;
   const int unit = blockIdx.x;
   const int b = unit / p.Hkv, hk = unit % p.Hkv;
@@ -227,6 +226,37 @@ __global__ void __launch_bounds__(kSelectThreads) fa_select_kernel(const SelectP
   kmax = __reduce_max_sync(0xffffffffu, s_hi[lane % kWarps]);
   const float two = __fmul_ru(2.f * kScoreEps, eps) + 0x1p-100f;   // 2 e (products may underflow)
 
+  // The digit that the s_left-th largest of the counted has, and how many of that digit are still to be
+  // taken; clears the counts.
+  auto pick = [&]() {
+    __syncthreads();
+    if (warp == 0) {   // lane i has digits 255 - 8 i down to 248 - 8 i
+      int c[8], sum = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += c[e] = s_hist[255 - 8 * lane - e];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s_hist[255 - 8 * lane - e] = 0;
+      int inc = sum;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += x;
+      }
+      const int left = s_left;
+      __syncwarp();
+      int above = inc - sum;
+      if (above < left && left <= inc) {
+        int e = 0;
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+          if (e == i && above + c[i] < left) above += c[i], e = i + 1;
+        s_digit = 255 - 8 * lane - e;
+        s_left = left - above;
+      }
+    }
+    __syncthreads();
+  };
+
   // the want-th largest key, up to eight bits at a time below the bits that all keys share
   // (scores have few exponents: without that the first passes would count into one place), until
   // what is left undecided is less than the scores' errors: T is then that interval
@@ -245,33 +275,8 @@ __global__ void __launch_bounds__(kSelectThreads) fa_select_kernel(const SelectP
           if (competes(s0 + j) && (bits == 32 || (keys[j] >> bits) == prefix))
             atomicAdd(&s_hist[(keys[j] >> shift) & ((1u << w) - 1)], 1);
       }
-      __syncthreads();
-      if (warp == 0) {   // lane i has digits 255 - 8 i down to 248 - 8 i
-        int c[8], sum = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += c[e] = s_hist[255 - 8 * lane - e];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s_hist[255 - 8 * lane - e] = 0;
-        int inc = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int x = __shfl_up_sync(0xffffffffu, inc, d);
-          if (lane >= d) inc += x;
-        }
-        const int left = s_left;
-        __syncwarp();
-        int above = inc - sum;
-        if (above < left && left <= inc) {
-          int e = 0;
-#pragma unroll
-          for (int i = 0; i < 7; ++i)
-            if (e == i && above + c[i] < left) above += c[i], e = i + 1;
-          s_prefix = (prefix << w) | (uint32_t)(255 - 8 * lane - e);
-          s_left = left - above;
-        }
-      }
-      __syncthreads();
-      prefix = s_prefix;
+      pick();
+      prefix = prefix << w | (uint32_t)s_digit;
       bits = shift;
       if (unordered(prefix << bits | ((1u << bits) - 1)) - unordered(prefix << bits) <= two) break;
     }
@@ -331,49 +336,88 @@ __global__ void __launch_bounds__(kSelectThreads) fa_select_kernel(const SelectP
         list[i] = s0 + __ffs(x) - 1;
       }
     }
-    if (!small)
-      for (int i = tid; i < (n_near + 31) / 32; i += kSelectThreads) mark[i] = 0;
+    if (tid == 0) s_left = take;
     __syncthreads();
-    // a warp per page and row; the rows' maximum as an ordered number
-    const uint16_t* q = p.q + (long long)unit * p.rows * D + E * lane;
+    // Eight lanes per page and row, D / 8 channels each; the rows' maximum as an ordered number.  (64-bit
+    // sums are slow here, two a cycle and SM: a whole warp per page and row spends more of them on
+    // adding up its lanes than on the products.  2048 pages all alike, 4 rows of 64 channels: that
+    // took 995 us, this 540.)
+    constexpr int kItems = kSelectThreads / 8;
+    const int sub = lane & 7;
+    const uint16_t* q = p.q + (long long)unit * p.rows * D + D / 8 * sub;
+    const int step_page = kItems / p.rows, step_row = kItems % p.rows;
+    int mine = (tid >> 3) / p.rows, row = (tid >> 3) % p.rows;
 #pragma unroll 1
-    for (int at_list = 0, r = warp; at_list < n_near;) {
-      if (r >= p.rows) {
-        r -= p.rows, ++at_list;
-        continue;
-      }
-      const int id = p.kv.table[(long long)b * p.kv.table_stride + list[at_list]];
-      if (id < 0 || id >= p.kv.num_pages) {              // below all others
-        r += kWarps;
-        continue;
-      }
-      const long long at = ((long long)id * p.Hkv + hk) * D + E * lane;
+    while (__any_sync(0xffffffffu, mine < n_near)) {
+      const int id = mine < n_near ? p.kv.table[(long long)b * p.kv.table_stride + list[mine]] : -1;
+      const bool good = id >= 0 && id < p.kv.num_pages;  // else below all others
       double x = 0.;
+      if (good) {
+        const long long at = ((long long)id * p.Hkv + hk) * D + D / 8 * sub;
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const uint32_t wq = *reinterpret_cast<const uint32_t*>(q + (long long)r * D + e);
-        const uint32_t lo = *reinterpret_cast<const uint32_t*>(p.kv.k_min + at + e);
-        const uint32_t hi = *reinterpret_cast<const uint32_t*>(p.kv.k_max + at + e);
-        const float q0 = lo16_f32<BF16>(wq), q1 = hi16_f32<BF16>(wq);
-        x = fma((double)q0, (double)(q0 > 0.f ? lo16_f32<BF16>(hi) : lo16_f32<BF16>(lo)), x);
-        x = fma((double)q1, (double)(q1 > 0.f ? hi16_f32<BF16>(hi) : hi16_f32<BF16>(lo)), x);
+        for (int e = 0; e < D / 8; e += 8) {
+          const uint4 wq = *reinterpret_cast<const uint4*>(q + (long long)row * D + e);
+          const uint4 lo = *reinterpret_cast<const uint4*>(p.kv.k_min + at + e);
+          const uint4 hi = *reinterpret_cast<const uint4*>(p.kv.k_max + at + e);
+          auto add = [&](uint32_t y, uint32_t l, uint32_t h) {
+            const float q0 = lo16_f32<BF16>(y), q1 = hi16_f32<BF16>(y);
+            x = fma((double)q0, (double)(q0 > 0.f ? lo16_f32<BF16>(h) : lo16_f32<BF16>(l)), x);
+            x = fma((double)q1, (double)(q1 > 0.f ? hi16_f32<BF16>(h) : hi16_f32<BF16>(l)), x);
+          };
+          add(wq.x, lo.x, hi.x);
+          add(wq.y, lo.y, hi.y);
+          add(wq.z, lo.z, hi.z);
+          add(wq.w, lo.w, hi.w);
+        }
       }
 #pragma unroll
-      for (int w = 16; w; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-      if (lane == 0) {
+      for (int w = 4; w; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
+      if (good && sub == 0) {
         const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.);   // (-0 as 0)
-        atomicMax(exact + at_list, u >> 63 ? ~u : u | 0x8000000000000000ull);
+        atomicMax(exact + mine, u >> 63 ? ~u : u | 0x8000000000000000ull);
       }
-      r += kWarps;
+      mine += step_page;
+      row += step_row;
+      if (row >= p.rows) row -= p.rows, ++mine;
     }
     __syncthreads();
+    // (the list is in page order: of equal scores the first are taken)
+    if (small) {
+      if (tid < n_near) {
+        const unsigned long long x = exact[tid];
+        int ahead = 0;
 #pragma unroll 1
-    for (int i = tid; i < n_near; i += kSelectThreads) {   // the list is in page order
-      const unsigned long long x = exact[i];
-      int ahead = 0;
+        for (int j = 0; j < n_near; ++j) ahead += exact[j] > x || (exact[j] == x && j < tid);
+        if (ahead < take) atomicOr(&mark[tid >> 5], 1u << (tid & 31));
+      }
+    } else {   // many alike: their take-th largest (take >= 1: fewer than `want` lie above the threshold)
+      unsigned long long top = 0;
 #pragma unroll 1
-      for (int j = 0; j < n_near; ++j) ahead += exact[j] > x || (exact[j] == x && j < i);
-      if (ahead < take) atomicOr(&mark[i >> 5], 1u << (i & 31));
+      for (int shift = 56; shift >= 0; shift -= 8) {
+#pragma unroll 1
+        for (int i = tid; i < n_near; i += kSelectThreads) {
+          const unsigned long long x = exact[i];
+          if (shift == 56 || x >> (shift + 8) == top) atomicAdd(&s_hist[(x >> shift) & 255], 1);
+        }
+        pick();
+        top = top << 8 | (unsigned)s_digit;
+      }
+      int before = 0;                    // of those that equal it
+#pragma unroll 1
+      for (int i0 = 0; i0 < n_near; i0 += kSelectThreads) {
+        const int i = i0 + tid;
+        const unsigned long long x = i < n_near ? exact[i] : 0;
+        const bool same = i < n_near && x == top;
+        const unsigned sames = __ballot_sync(0xffffffffu, same);
+        if (lane == 0) s_warp[warp].x = __popc(sames);
+        __syncthreads();
+        const int c = lane < kWarps ? s_warp[lane].x : 0;
+        const int at = before + __reduce_add_sync(0xffffffffu, lane < warp ? c : 0) + __popc(sames & ((1u << lane) - 1));
+        before += __reduce_add_sync(0xffffffffu, c);
+        const unsigned word = __ballot_sync(0xffffffffu, i < n_near && (x > top || (same && at < s_left)));
+        if (lane == 0 && i < n_near) mark[i >> 5] = word;
+        __syncthreads();
+      }
     }
     __syncthreads();
   }

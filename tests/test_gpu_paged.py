@@ -569,6 +569,30 @@ def test_select_many_near_the_threshold():
     assert np.array_equal(got.cpu().numpy(), P.select(q, lo, hi, c.table, [n * 16], 16, M))
 
 
+def test_select_pages_that_are_all_alike():
+    """So many equal scores that a pairwise ranking would take seconds: the
+    lowest page numbers among the equal, behind the few that are larger."""
+    import torch
+    import attention_forward_fa_gb300 as fa
+    n, M = 131072, 300
+    table = torch.randperm(64, device="cuda", dtype=torch.int32).repeat(n // 64).view(1, n)   # shared pages
+    pool = torch.zeros(64, 1, 16, 64, device="cuda", dtype=torch.bfloat16)
+    lo, hi = (torch.ones(64, 1, 64, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    cache = fa.PagedKV(pool, pool.clone(), table, lo, hi)
+    q = torch.ones(1, 4, 1, 64, device="cuda", dtype=torch.bfloat16)
+    lens = torch.tensor([16 * n], device="cuda", dtype=torch.int32)
+    got = fa.select_kv_pages(q, cache, lens, M, first=2, last=3)
+    assert _status() == 0
+    assert got.flatten().tolist() == list(range(M - 3)) + [n - 3, n - 2, n - 1]
+    best = int(table[0, 40])                          # one page of the pool, in 2048 places: less than
+    hi[best, 0, 7] = 1.0 + 2.0 ** -7                  # fp32's error above the rest with 2^20 beside it
+    lo[:, 0, 0] = hi[:, 0, 0] = 2.0 ** 20
+    places = (table[0] == best).nonzero().flatten().tolist()
+    got = fa.select_kv_pages(q, cache, lens, M, first=2, last=3)
+    assert _status() == 0
+    assert got.flatten().tolist() == [0, 1] + places[:M - 5] + [n - 3, n - 2, n - 1]
+
+
 def test_select_extreme_bounds_and_bad_pages():
     """Sums past the fp32 range of a score, and page ids outside the pool: no
     page is listed twice or out of range."""
