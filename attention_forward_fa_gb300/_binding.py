@@ -642,7 +642,8 @@ def flash_attention_decode(q, cache: PagedKV, kv_lens, *, scale: Optional[float]
     are in the cache already; kv_lens int32 [B], the tokens in the cache.  Row i is token
     t = kv_lens[b] - Sq + i and sees keys max(0, t - pre_tokens) .. t (pre_tokens None: from 0); a
     row that sees none gets 0 and LSE +inf.  page_idx: int32 [B, Hkv, max_sel] (select_kv_pages):
-    only these pages of each sequence are read.  Returns (o, lse fp32 [B, Hq, Sq])."""
+    only these pages of each sequence are read (of a list, as many entries count as the sequence
+    has pages: invalid ones belong at the end).  Returns (o, lse fp32 [B, Hq, Sq])."""
     import torch
     B, Hq, Sq, D = _query_of(q, cache)
     if not q.is_contiguous():

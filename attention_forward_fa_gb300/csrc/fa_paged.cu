@@ -311,9 +311,8 @@ int fa_decode(const void* q, const fa_paged_kv_t* kv, void* o, float* lse, int B
   if (!c.status) return cuda_fail(cudaGetLastError());
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // the most tiles that a unit can have: the lengths are known on the device only
-  const long long keys = (long long)(page_idx ? max_sel : kv->max_pages) * kv->page_size;
+  const long long keys = (long long)(page_idx ? std::min(max_sel, kv->max_pages) : kv->max_pages) * kv->page_size;
   const long long tiles = (keys + fa::kDecTile - 1) / fa::kDecTile;
-  c.sel_tiles = (int)tiles;
   if (D == 128)
     return fp16 ? launch_decode_rows<false, 128>(p, tiles, st) : launch_decode_rows<true, 128>(p, tiles, st);
   return fp16 ? launch_decode_rows<false, 64>(p, tiles, st) : launch_decode_rows<true, 64>(p, tiles, st);

@@ -483,8 +483,10 @@ int fa_kv_append(const fa_paged_kv_t* kv, const fa_kv_new_t* x, int B, int Hq, i
  *             only the listed pages (numbers p of the sequence's own pages, as
  *             in the page table's columns) are read; an entry < 0 or past the
  *             sequence's last page is an invalid slot; a page listed twice
- *             counts twice.  1 <= max_sel <= 2^20.  Pages and the mask above
- *             apply together.
+ *             counts twice.  Of a list the first n entries count, n the pages
+ *             that the sequence has: a list without repetitions needs no more,
+ *             with its invalid slots at the end.  1 <= max_sel <= 2^20.  Pages
+ *             and the mask above apply together.
  * What lies in the cache at positions that no row of a sequence sees is never
  * used and may be anything, NaN included; keys and values that some row sees
  * must be finite.

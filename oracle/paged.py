@@ -71,7 +71,7 @@ def decode(q, k_pages, v_pages, table, lens, scale, pre_tokens=None, page_idx=No
         for h in range(Hkv):
             pages = np.arange(n_pages)
             if page_idx is not None:
-                pages = page_idx[b, h]
+                pages = page_idx[b, h, :n_pages]     # as many entries count as there are pages
                 pages = pages[(pages >= 0) & (pages < n_pages)]
             pos = (pages[:, None] * page + np.arange(page)).reshape(-1)
             ids = table[b, pages]

@@ -352,10 +352,11 @@ def test_decode_never_uses_what_no_row_sees(dtype, Sq, pre, bad):
 @pytest.mark.parametrize("dtype,B,Hq,Hkv,D,page,Sq,lens,sel", [
     ("bf16", 2, 8, 2, 128, 64, 1, [1000, 300], 3), ("fp16", 1, 4, 4, 64, 16, 1, [3000], 40),
     ("bf16", 3, 8, 1, 64, 256, 3, [1000, 1, 257], 2), ("bf16", 1, 16, 4, 128, 32, 1, [5000], 100),
-    ("fp16", 2, 4, 2, 128, 128, 1, [129, 0], 5),
+    ("fp16", 2, 4, 2, 128, 128, 1, [129, 0], 5), ("bf16", 4, 8, 2, 64, 16, 2, [100, 17, 700, 3], 60),
 ])
 def test_decode_listed_pages(dtype, B, Hq, Hkv, D, page, Sq, lens, sel):
-    """Lists in any order, with invalid slots, repeats and an empty one."""
+    """Lists in any order, with invalid slots, repeats and an empty one, longer
+    than their sequences too."""
     import attention_forward_fa_gb300 as fa
     c = Cache(8, dtype, B, Hkv, D, page, lens)
     wide = c.table.shape[1]

@@ -69,6 +69,8 @@ def test_decode_limits():
     assert np.allclose(O[0, 0], v[0, 0, 38:40])               # each row sees itself alone
     O, _, _, _, _ = P.decode(0 * q, kp, vp, table, [40], 1.0, page_idx=np.array([[[1, -1, 1, 9]]]))
     assert np.allclose(O[0, 0, 0], v[0, 0, 16:32].mean(0))    # listed twice, invalid slots
+    O, _, _, _, _ = P.decode(0 * q, kp, vp, table, [40], 1.0, page_idx=np.array([[[1, -1, 9, 0]]]))
+    assert np.allclose(O[0, 0, 0], v[0, 0, 16:32].mean(0))    # three pages: the fourth entry is not read
 
 
 def test_append_then_decode_and_bounds():
