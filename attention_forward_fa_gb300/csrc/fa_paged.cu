@@ -181,7 +181,11 @@ int launch_select(fa::SelectParams& p, long long units, cudaStream_t st) {
   p.exact = reinterpret_cast<unsigned long long*>(scratch + pages * 8);
   p.near = reinterpret_cast<int32_t*>(scratch + pages * 16);
   p.mark = reinterpret_cast<uint32_t*>(scratch + pages * 20);
-  cudaError_t e = launch_dependent(fa::fa_page_score_kernel<BF16, D>, (unsigned)(units * p.chunks), 32, 0, st, p);
+  const int sms = fa_host::sm_count();
+  if (sms <= 0) return cuda_fail(cudaErrorInvalidDevice);
+  const long long runs = units * p.chunks, most = (long long)fa::kScoreBlocks * sms;
+  cudaError_t e = runs > most ? launch_dependent(fa::fa_page_score_kernel<BF16, D, true>, (unsigned)most, 32, 0, st, p)
+                              : launch_dependent(fa::fa_page_score_kernel<BF16, D, false>, (unsigned)runs, 32, 0, st, p);
   if (e == cudaSuccess)
     e = launch_dependent(fa::fa_select_kernel<BF16, D>, (unsigned)units, fa::kSelectThreads, 0, st, p);
   cudaFreeAsync(scratch, st);

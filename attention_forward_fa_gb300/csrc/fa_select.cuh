@@ -37,11 +37,12 @@ struct SelectParams {
   int32_t* near;          //   near the threshold: their 64-bit scores, their numbers and (a bit each)
   uint32_t* mark;         //   which of them are taken
   int B, Hkv, rows, max_sel, first, last;   // rows = G * Sq
-  int chunks;             // blocks per (sequence, KV head)
+  int chunks;             // runs of kScorePages per (sequence, KV head)
   int* status;
 };
 
-constexpr int kScorePages = 16;                 // pages per block of one warp
+constexpr int kScorePages = 16;                 // pages that a block of one warp scores at a time
+constexpr int kScoreBlocks = 56;                // blocks per SM at most
 constexpr int kSelectThreads = 512;
 constexpr int kKeys = 8;                        // scores per thread held in registers (4096 pages)
 constexpr int kNearCached = 256;                // pages near the threshold kept in shared memory
@@ -52,26 +53,19 @@ __device__ __forceinline__ int select_pages_of(const PagedKv& c, int len) {
   return (len + (1 << c.page_shift) - 1) >> c.page_shift;
 }
 
-// One warp per block of 16 pages.  Each lane copies to shared memory, all at once, the very 16-byte pieces that
+// A warp scores 16 pages.  Each lane copies to shared memory, all at once, the very 16-byte pieces that
 // it will feed to the matrix instructions, so that nothing has to be exchanged and no register waits
 // for memory: 8 KB in flight per warp (D 128), 24 warps per SM.  (Measured with the second kernel,
-// 2048 pages of 64 (sequence, KV head) pairs, D 128, 67 MB of bounds: this 22.5 us, of which 15.6 are
+// 2048 pages of 64 (sequence, KV head) pairs, D 128, 67 MB of bounds: this 22.7 us, of which 15.6 are
 // this kernel's; 32 pages per warp 24.4 us, 48 25.9 us, 64 25.5 us: fewer, longer blocks end
 // unevenly; bounds loaded to registers, 12 warps per SM, 38.6 us; one long run of pages per warp
 // through a ring of three groups 35 us: it leaves the latency of the matrix instructions bare.)
 template <bool BF16, int D>
-__global__ void __launch_bounds__(32) fa_page_score_kernel(const SelectParams p) {
+__device__ __forceinline__ void score_pages(const SelectParams& p, uint4 (&s_in)[2][2][D / 32][32], int unit, int b,
+                                            int first, int n) {
   constexpr int C = D / 32;
-  __shared__ __align__(16) uint4 s_in[2][2][C][32];   // [bound][page half][step][lane]
-  pdl_wait_prior();
-  pdl_launch_dependents();   // (after the wait: the next kernel may read the lengths as it starts)
-  const int unit = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
-  const int b = unit / p.Hkv, hk = unit % p.Hkv;
-  const int n = select_pages_of(p.kv, p.kv_lens[b]);
   const int lane = threadIdx.x, g = lane >> 2, t4 = lane & 3;
-  if (chunk == 0 && hk == 0 && lane == 0) (void)paged_len(p.kv, p.kv_lens[b], p.status);
-  const int first = chunk * kScorePages;
-  if (first >= n) return;
+  const int hk = unit - b * p.Hkv;
   const int ids = lane < 16 && first + lane < n ? paged_id(p.kv, b, first + lane, p.status) : -1;
   // of pages first + g and first + g + 8: 8 channels at 32 c + 8 t4 of either bound
   bool good[2];
@@ -142,6 +136,39 @@ __global__ void __launch_bounds__(32) fa_page_score_kernel(const SelectParams p)
     if (t4 == 0 && s < n)            // a page that is none scores below all others
       p.score[(long long)unit * p.kv.max_pages + s] =
           good[j] ? make_float2(odd[j] ? 0.f : best[j], odd[j] ? INFINITY : scale[j]) : make_float2(-INFINITY, 0.f);
+  }
+}
+
+// A block per run of 16 pages that the table has room for, or, where that were more than kScoreBlocks per
+// SM, so many blocks that each look at 32 of their runs at once for those that hold pages: tables
+// have room for more than most sequences use.  (64 sequences of 188 pages, 8 KV heads of 64, room for
+// 8192: 24 us, a block per run 277 us; where all room is used the loop costs, 23.4 us against 22.7 us
+// in the case above.)
+template <bool BF16, int D, bool MANY>
+__global__ void __launch_bounds__(32) fa_page_score_kernel(const SelectParams p) {
+  __shared__ __align__(16) uint4 s_in[2][2][D / 32][32];   // [bound][page half][step][lane]
+  pdl_wait_prior();
+  pdl_launch_dependents();   // (after the wait: the next kernel may read the lengths as it starts)
+  const int lane = threadIdx.x;
+  if constexpr (!MANY) {
+    const int unit = blockIdx.x / p.chunks, first = blockIdx.x % p.chunks * kScorePages, b = unit / p.Hkv;
+    const int len = p.kv_lens[b], n = select_pages_of(p.kv, len);
+    if (first == 0 && unit == b * p.Hkv && lane == 0) (void)paged_len(p.kv, len, p.status);
+    if (first >= n) return;
+    score_pages<BF16, D>(p, s_in, unit, b, first, n);
+  } else {
+    const unsigned runs = (unsigned)p.B * p.Hkv * p.chunks;   // (below 2^31)
+    for (unsigned run0 = blockIdx.x; run0 < runs; run0 += 32 * gridDim.x) {
+      const unsigned run = run0 + gridDim.x * lane;
+      const int unit = (int)(run / (unsigned)p.chunks), first = (int)(run % (unsigned)p.chunks) * kScorePages;
+      const int b = unit / p.Hkv, len = run < runs ? p.kv_lens[b] : 0, n = select_pages_of(p.kv, len);
+      if (run < runs && first == 0 && unit == b * p.Hkv) (void)paged_len(p.kv, len, p.status);
+      for (unsigned live = __ballot_sync(0xffffffffu, first < n); live; live &= live - 1) {
+        const int at = __ffs(live) - 1;
+        score_pages<BF16, D>(p, s_in, __shfl_sync(0xffffffffu, unit, at), __shfl_sync(0xffffffffu, b, at),
+                             __shfl_sync(0xffffffffu, first, at), __shfl_sync(0xffffffffu, n, at));
+      }
+    }
   }
 }
 

@@ -570,6 +570,31 @@ def test_select_many_near_the_threshold():
     assert np.array_equal(got.cpu().numpy(), P.select(q, lo, hi, c.table, [n * 16], 16, M))
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64)])
+def test_select_tables_with_room_to_spare(dtype, D):
+    """Tables for 32768 pages, sequences of none to a few hundred (one as long as
+    its table): the entries behind a sequence's last page may be anything."""
+    import torch
+    import attention_forward_fa_gb300 as fa
+    room, Hkv, M = 32768, 3, 9
+    c = Cache(31, dtype, 7, Hkv, D, 16, [0, 1, 16, 4000, 333, 5000, 64], bounds=True)
+    table = torch.full((8, room), -7, device="cuda", dtype=torch.int32)
+    table[:7, :c.table.shape[1]] = _dev(c.table)
+    table[:7, c.table.shape[1]:] = 2 ** 31 - 1
+    table[7] = torch.arange(room, device="cuda", dtype=torch.int32) % c.k.shape[0]
+    cache = fa.PagedKV(c.tk, c.tv, table, c.tlo, c.thi)
+    lens = [0, 1, 16, 4000, 333, 5000, 64, 16 * room]
+    q = _round(c.rng.standard_normal((8, 2 * Hkv, 1, D)), dtype)
+    got = fa.select_kv_pages(_dev(q, dtype), cache, c.ints(lens), M)
+    assert _status() == 0
+    assert np.array_equal(got.cpu().numpy(), P.select(q, c.lo, c.hi, table.cpu().numpy(), lens, 16, M))
+    lens[2], lens[5] = -1, 16 * room + 1
+    got = fa.select_kv_pages(_dev(q, dtype), cache, c.ints(lens), M)
+    assert _status() == fa.FA_ERR_INDEX
+    lens[2], lens[5] = 0, 0
+    assert np.array_equal(got.cpu().numpy(), P.select(q, c.lo, c.hi, table.cpu().numpy(), lens, 16, M))
+
+
 def test_select_pages_that_are_all_alike():
     """So many equal scores that a pairwise ranking would take seconds: the
     lowest page numbers among the equal, behind the few that are larger."""
