@@ -22,6 +22,7 @@
 namespace fa {
 
 constexpr int kAppendThreads = 256;
+constexpr int kAppendBlocks = 64;   // blocks per SM at most
 constexpr int kBatch = 2;      // rows per thread in flight (queries: heads, values: tokens)
 
 struct AppendParams {
@@ -44,16 +45,15 @@ struct AppendParams {
   int* status;
 };
 
+// Piece `at` of the work: one page of one sequence, some heads of its K, V or Q.
 template <bool BF16, int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const AppendParams p) {
+__device__ __forceinline__ void append_piece(const AppendParams& p, int at) {
   constexpr int L = D / 16;                    // threads per row
   constexpr int kRows = kAppendThreads / L;    // rows per step
   __shared__ uint4 s_red[4][8][L];             // [min A, min B, max A, max B][warp][thread of the row]
-  pdl_launch_dependents();
-  pdl_wait_prior();
   const int items = 2 * p.k_items + p.q_items;
-  const int item = blockIdx.x % items;
-  const int rest = blockIdx.x / items;
+  const int item = at % items;
+  const int rest = at / items;
   const int chunk = rest % p.chunks, b = rest / p.chunks;
 
   const int ps_shift = p.kv.page_shift, ps = 1 << ps_shift;
@@ -263,6 +263,35 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const A
       if (kept) widen(j, *lo, *hi);
       *lo = mn[j];
       *hi = mx[j];
+    }
+  }
+}
+
+// A block per piece that Snew has room for, or, where that were more than kAppendBlocks per SM, so many
+// blocks that each look at 32 of their pieces at once for those that hold tokens: a padded batch may
+// mix prompts with single tokens.  (32 sequences padded to 4096 tokens, pages of 16, one of them that
+// long and the others one token: 32 us, a block per piece 110 us; all of one token 15 and 100 us.  Fewer
+// blocks end unevenly where the pieces are full, 40 us against 31 us with 16 per SM.)
+template <bool BF16, int D, bool INTERLEAVED, bool MANY>
+__global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const AppendParams p, int pieces) {
+  pdl_launch_dependents();
+  pdl_wait_prior();
+  if constexpr (!MANY) {
+    append_piece<BF16, D, INTERLEAVED>(p, blockIdx.x);
+  } else {
+    for (unsigned at0 = blockIdx.x; at0 < (unsigned)pieces; at0 += 32 * gridDim.x) {
+      const unsigned at = at0 + gridDim.x * (threadIdx.x & 31);
+      bool some = false;
+      if (at < (unsigned)pieces) {
+        const int rest = at / (2 * p.k_items + p.q_items), chunk = rest % p.chunks, b = rest / p.chunks;
+        const int n = p.new_lens ? min(p.new_lens[b], p.Snew) : p.Snew, len = p.kv_lens[b];
+        // (whatever is to be reported, the piece of chunk 0 reports)
+        some = chunk == 0 || (n > 0 && len >= 0 && (long long)len + n > ((long long)(len >> p.kv.page_shift) + chunk) << p.kv.page_shift);
+      }
+      for (unsigned live = __ballot_sync(0xffffffffu, some); live; live &= live - 1) {
+        append_piece<BF16, D, INTERLEAVED>(p, (int)(at0 + gridDim.x * (__ffs(live) - 1)));
+        __syncthreads();           // (its shared memory)
+      }
     }
   }
 }

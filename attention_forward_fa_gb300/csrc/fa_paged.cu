@@ -85,10 +85,19 @@ fa::PagedKv device_cache(const fa_paged_kv_t* kv) {
   return c;
 }
 
+template <bool BF16, int D, bool INTERLEAVED>
+cudaError_t launch_append(const fa::AppendParams& p, long long pieces, cudaStream_t st) {
+  const int sms = fa_host::sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const long long most = (long long)fa::kAppendBlocks * sms;
+  return pieces > most ? launch_dependent(fa::fa_kv_append_kernel<BF16, D, INTERLEAVED, true>, (unsigned)most,
+                                          fa::kAppendThreads, 0, st, p, (int)pieces)
+                       : launch_dependent(fa::fa_kv_append_kernel<BF16, D, INTERLEAVED, false>, (unsigned)pieces,
+                                          fa::kAppendThreads, 0, st, p, (int)pieces);
+}
 template <bool BF16, int D>
-cudaError_t launch_append(const fa::AppendParams& p, bool interleaved, unsigned grid, cudaStream_t st) {
-  return interleaved ? launch_dependent(fa::fa_kv_append_kernel<BF16, D, true>, grid, fa::kAppendThreads, 0, st, p)
-                     : launch_dependent(fa::fa_kv_append_kernel<BF16, D, false>, grid, fa::kAppendThreads, 0, st, p);
+cudaError_t launch_append(const fa::AppendParams& p, bool interleaved, long long pieces, cudaStream_t st) {
+  return interleaved ? launch_append<BF16, D, true>(p, pieces, st) : launch_append<BF16, D, false>(p, pieces, st);
 }
 
 // 5-D view (64 channels, slots, D / 64, heads, pages) of a pool, in boxes of
@@ -258,17 +267,17 @@ int fa_kv_append(const fa_paged_kv_t* kv, const fa_kv_new_t* x, int B, int Hq, i
   p.q_heads = 2 * fa::kBatch * hp;
   p.k_items = (Hkv + hp - 1) / hp;
   p.q_items = x->q ? (Hq + p.q_heads - 1) / p.q_heads : 0;
-  const long long grid = (long long)B * p.chunks * (2 * p.k_items + p.q_items);
-  if (grid > 0x7FFFFFFFLL) return FA_ERR_SHAPE;
+  const long long per_b = (long long)p.chunks * (2 * p.k_items + p.q_items);
+  if (per_b > kMostRows / B) return FA_ERR_SHAPE;
+  const long long pieces = per_b * B;
   p.status = fa_host::status_ptr();
   if (!p.status) return cuda_fail(cudaGetLastError());
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool fp16 = (mask_mode & FA_DTYPE_FP16) != 0;
   const bool il = x->interleaved != 0;
-  const unsigned blocks = (unsigned)grid;
   const cudaError_t e =
-      D == 128 ? (fp16 ? launch_append<false, 128>(p, il, blocks, st) : launch_append<true, 128>(p, il, blocks, st))
-               : (fp16 ? launch_append<false, 64>(p, il, blocks, st) : launch_append<true, 64>(p, il, blocks, st));
+      D == 128 ? (fp16 ? launch_append<false, 128>(p, il, pieces, st) : launch_append<true, 128>(p, il, pieces, st))
+               : (fp16 ? launch_append<false, 64>(p, il, pieces, st) : launch_append<true, 64>(p, il, pieces, st));
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 

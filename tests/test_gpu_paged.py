@@ -119,6 +119,9 @@ APPEND = [
     ("bf16", 2, 16, 16, 64, 128, 129, [100, 127], [129, 65], 0, False, "halves"),
     ("fp16", 1, 33, 1, 64, 64, 70, [7], [70], 16, False, "hnd"),
     ("bf16", 1, 72, 9, 128, 32, 3, [30], [3], 112, True, "nhd"),
+    # much room, few tokens: a block looks for its pieces
+    ("bf16", 16, 1, 1, 64, 16, 4096, [5, 0] + [100] * 14, [900, 0, 4096, 33] + [1] * 12, 64, False, "hnd"),
+    ("fp16", 26, 1, 1, 128, 16, 2048, [15] * 25 + [0], [2, 2048] + [1, 0] * 12, 32, True, "nhd"),
 ]
 
 
