@@ -730,25 +730,42 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) fa_decode_join_kerne
   const long long row = (long long)blockIdx.x * (kWarps / WPR) + warp / WPR;
   const int part = warp % WPR;
   const long long per_b = (long long)p.Hkv * p.rows;
-  if (row >= per_b * p.B) return;
-  const int b = (int)(row / per_b);
+  const bool none = row >= per_b * p.B;                  // (a row for all warps of a block where WPR > 1)
+  const int b = none ? p.B - 1 : (int)(row / per_b);
   const int in_b = (int)(row % per_b);
   const int hk = in_b / p.rows, r = in_b % p.rows;
   const int rg = r / rows8, rr = r % rows8;
   long long total = 0, before = 0;
-  for (int base = 0; base < p.B; base += 32 * kChunks) {
+  auto add_up = [&](int base, int end) {                 // charges of 256 sequences, and of those before `end`
     int len[kChunks], c[kChunks];
     decode_charges(p, base, lane, len, c);
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
       total += c[i];
-      if (base + 32 * i + lane < b) before += c[i];
+      if (base + 32 * i + lane < end) before += c[i];
     }
+  };
+  if (p.B <= 32 * kChunks) {
+    add_up(0, b);
+    total = warp_sum(total);
+    before = warp_sum(before);
+  } else {   // shared by the block's warps, up to the sequence of its first row; the few from there by each
+    __shared__ long long s_sum[kWarps][2];
+    const int b0 = (int)((long long)blockIdx.x * (kWarps / WPR) / per_b);
+    for (int base = 32 * kChunks * warp; base < p.B; base += 32 * kChunks * kWarps) add_up(base, b0);
+    total = warp_sum(total);
+    before = warp_sum(before);
+    if (lane == 0) s_sum[warp][0] = total, s_sum[warp][1] = before;
+    __syncthreads();
+    total = warp_sum(lane < kWarps ? s_sum[lane][0] : 0);
+    before = (lane < kWarps ? s_sum[lane][1] : 0) + (b0 + lane < b ? decode_span(p, decode_len(p, b0 + lane)).n + kUnitTiles : 0);
+    before = warp_sum(before);                           // (b - b0 is less than the block's 8 rows)
   }
-  total = warp_sum(total) * p.units;
+  if (none) return;
+  total *= p.units;
   const int ctas = decode_ctas(p, total);
   const int n = decode_span(p, decode_len(p, b)).n;
-  const long long t0 = warp_sum(before) * p.units + (long long)(hk * p.groups + rg) * (n + kUnitTiles) + kUnitTiles;
+  const long long t0 = before * p.units + (long long)(hk * p.groups + rg) * (n + kUnitTiles) + kUnitTiles;
   const int c0 = decode_owner(total, ctas, t0), c1 = decode_owner(total, ctas, t0 + n - 1);
   pdl_wait_prior();
   if (c0 == c1) return;          // finished by its CTA

@@ -423,6 +423,22 @@ def test_decode_more_sequences_than_one_look_up():
     _check(o, l, P.decode(q, c.k, c.v, c.table, lens, 0.125), "fp16")
 
 
+@pytest.mark.parametrize("B,Hq", [(300, 1), (1300, 1), (513, 5)])
+def test_decode_joins_among_many_sequences(B, Hq):
+    """More sequences than one look-up holds, a few of them long: their pieces
+    are joined by blocks whose rows belong to one sequence or to several."""
+    import attention_forward_fa_gb300 as fa
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(0, 40, B)]
+    for b in (0, 1, 255, 256, B - 1):
+        lens[b] = 900 + b
+    c = Cache(25, "bf16", B, 1, 64, 32, lens)
+    q = _round(c.rng.standard_normal((B, Hq, 1, 64)), "bf16")
+    o, l = fa.flash_attention_decode(_dev(q, "bf16"), c.obj, c.ints(lens))
+    assert _status() == 0
+    _check(o, l, P.decode(q, c.k, c.v, c.table, lens, 0.125), "bf16")
+
+
 def test_two_streams_at_once():
     """Eager calls of all three operators on two streams, each with scratch of its own."""
     import torch
