@@ -53,6 +53,12 @@ __device__ __forceinline__ int select_pages_of(const PagedKv& c, int len) {
   return (len + (1 << c.page_shift) - 1) >> c.page_shift;
 }
 
+// Pages of a sequence that have to be scored: none where the list has room for all.
+__device__ __forceinline__ int scored_pages_of(const SelectParams& p, int len) {
+  const int n = select_pages_of(p.kv, len);
+  return n > p.max_sel ? n : 0;
+}
+
 // A warp scores 16 pages.  Each lane copies to shared memory, all at once, the very 16-byte pieces that
 // it will feed to the matrix instructions, so that nothing has to be exchanged and no register waits
 // for memory: 8 KB in flight per warp (D 128), 24 warps per SM.  (Measured with the second kernel,
@@ -152,7 +158,7 @@ __global__ void __launch_bounds__(32) fa_page_score_kernel(const SelectParams p)
   const int lane = threadIdx.x;
   if constexpr (!MANY) {
     const int unit = blockIdx.x / p.chunks, first = blockIdx.x % p.chunks * kScorePages, b = unit / p.Hkv;
-    const int len = p.kv_lens[b], n = select_pages_of(p.kv, len);
+    const int len = p.kv_lens[b], n = scored_pages_of(p, len);
     if (first == 0 && unit == b * p.Hkv && lane == 0) (void)paged_len(p.kv, len, p.status);
     if (first >= n) return;
     score_pages<BF16, D>(p, s_in, unit, b, first, n);
@@ -161,7 +167,7 @@ __global__ void __launch_bounds__(32) fa_page_score_kernel(const SelectParams p)
     for (unsigned run0 = blockIdx.x; run0 < runs; run0 += 32 * gridDim.x) {
       const unsigned run = run0 + gridDim.x * lane;
       const int unit = (int)(run / (unsigned)p.chunks), first = (int)(run % (unsigned)p.chunks) * kScorePages;
-      const int b = unit / p.Hkv, len = run < runs ? p.kv_lens[b] : 0, n = select_pages_of(p.kv, len);
+      const int b = unit / p.Hkv, len = run < runs ? p.kv_lens[b] : 0, n = scored_pages_of(p, len);
       if (run < runs && first == 0 && unit == b * p.Hkv) (void)paged_len(p.kv, len, p.status);
       for (unsigned live = __ballot_sync(0xffffffffu, first < n); live; live &= live - 1) {
         const int at = __ffs(live) - 1;

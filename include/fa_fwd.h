@@ -509,7 +509,8 @@ int fa_decode(const void* q, const fa_paged_kv_t* kv, void* o, float* lse, int B
  * equal scores by the lower page number, until max_sel pages are listed or
  * none is left.  page_idx [B, Hkv, max_sel] (DEVICE int32) gets the page
  * numbers in ascending order, then -1.  The choice is that of scores in 64-bit
- * arithmetic.  kv_lens as fa_decode; q [B, Hq, Sq, D] contiguous; q and the
+ * arithmetic (a sequence of at most max_sel pages is listed unscored: neither its
+ * table entries nor its bounds are read).  kv_lens as fa_decode; q [B, Hq, Sq, D] contiguous; q and the
  * bounds of a sequence's pages must be finite, k_min <= k_max.  first, last >= 0, first + last <= max_sel <= 2^20.
  * Scratch: stream-ordered, 24 bytes per (sequence, KV head, page
  * table column).

@@ -638,6 +638,21 @@ def test_select_pages_that_are_all_alike():
     assert got.flatten().tolist() == [0, 1] + places[:M - 5] + [n - 3, n - 2, n - 1]
 
 
+def test_select_lists_short_sequences_unscored():
+    """At most max_sel pages: all of them, without a look at table or bounds."""
+    import torch
+    import attention_forward_fa_gb300 as fa
+    c = Cache(32, "bf16", 2, 2, 64, 16, [320, 800], bounds=True)
+    c.obj.page_table[0] = -7
+    c.tlo[_dev(c.table[0, :20]).long()] = float("nan")
+    q = _round(c.rng.standard_normal((2, 4, 1, 64)), "bf16")
+    got = fa.select_kv_pages(_dev(q, "bf16"), c.obj, c.ints([320, 800]), 20).cpu().numpy()
+    assert _status() == 0
+    assert (got[0] == np.arange(20)).all()
+    assert np.array_equal(got[1], P.select(q[1:], c.lo, c.hi, c.table[1:], [800], 16, 20)[0])
+    torch.cuda.synchronize()
+
+
 def test_select_extreme_bounds_and_bad_pages():
     """Sums past the fp32 range of a score, and page ids outside the pool: no
     page is listed twice or out of range."""
