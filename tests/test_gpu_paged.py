@@ -259,6 +259,8 @@ DECODE = [
     ("bf16", 1, 20, 1, 128, 16, 2, [99], None, "hnd"),
     ("bf16", 1, 128, 1, 128, 256, 1, [500], None, "hnd"),
     ("fp16", 2, 16, 16, 64, 16, 1, [5000, 4999], 4097, "hnd"),
+    ("bf16", 3, 8, 2, 128, 64, 150, [400, 151, 100], None, "nhd"),       # a chunk of a prompt
+    ("fp16", 1, 6, 2, 64, 32, 333, [333], 64, "hnd"),
 ]
 
 
