@@ -420,8 +420,10 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
         if (in == 0) look_up((t0 + j + per) * nsub + lane, id2, slot2, key2);
       }
     }
-    // after an expired wait: copies in flight land before the CTA ends
-    if (dead && lane == 0)
+    // Every copy lands before the CTA ends, whether or not some wait expired: a consumer may give up
+    // on a copy in flight after the producer's last wait.  (Where none did, the consumers wait for the
+    // same phases.)
+    if (lane == 0)
       for (int i = max(0, it - NS); i < it; ++i) drain_bar(FULL(i % NS), (i / NS) & 1, wc.timeout);
     return;
   }
@@ -650,8 +652,10 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
           for (int i = 0; i < DT; ++i) mma_16x8<BF16>(o[n][i], v[q][i], pp.z, pp.w);
         }
       }
+      // A warp that gave up hands back no stage: its copy may still be in flight.  The producer's next
+      // wait for that stage then fails too, so that no stage is armed before its last copy has landed.
       __syncwarp();
-      if (lane == 0) mbar_arrive(EMPTY(st));
+      if (lane == 0 && !dead) mbar_arrive(EMPTY(st));
     }
 
     // ---- the unit's sums; each warp writes its channels
