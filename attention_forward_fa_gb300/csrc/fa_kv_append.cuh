@@ -17,12 +17,15 @@
 // of three loads, of which the tokens wait for one only.  One token each of 128
 // sequences: 2.3 us, a launch and that chain.
 #pragma once
+#include <type_traits>
+
 #include "fa_paged.cuh"
 
 namespace fa {
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendBlocks = 64;   // blocks per SM at most
+constexpr int kAppendBlocks = 64;       // pieces per SM up to which each has a block of its own
+constexpr int kAppendLoopBlocks = 32;   // blocks per SM past that
 constexpr int kBatch = 2;      // rows per thread in flight (queries: heads, values: tokens)
 
 struct AppendParams {
@@ -45,15 +48,13 @@ struct AppendParams {
   int* status;
 };
 
-// Piece `at` of the work: one page of one sequence, some heads of its K, V or Q.
-template <bool BF16, int D, bool INTERLEAVED>
-__device__ __forceinline__ void append_piece(const AppendParams& p, int at) {
+// A piece of the work: one page of one sequence (`rest`), some heads (`item`) of its K, V or Q.
+constexpr int kAppendK = 0, kAppendV = 1, kAppendQ = 2;
+template <bool BF16, int D, bool INTERLEAVED, int KIND>
+__device__ __forceinline__ void append_piece(const AppendParams& p, int item, int rest) {
   constexpr int L = D / 16;                    // threads per row
   constexpr int kRows = kAppendThreads / L;    // rows per step
   __shared__ uint4 s_red[4][8][L];             // [min A, min B, max A, max B][warp][thread of the row]
-  const int items = 2 * p.k_items + p.q_items;
-  const int item = at % items;
-  const int rest = at / items;
   const int chunk = rest % p.chunks, b = rest / p.chunks;
 
   const int ps_shift = p.kv.page_shift, ps = 1 << ps_shift;
@@ -140,7 +141,7 @@ __device__ __forceinline__ void append_piece(const AppendParams& p, int at) {
   auto ld = [](const uint16_t* x) { return *reinterpret_cast<const uint4*>(x); };
   auto st = [](uint16_t* x, uint4 w) { *reinterpret_cast<uint4*>(x) = w; };
 
-  if (item >= 2 * p.k_items) {   // ---------------- queries: one set of angles for all heads
+  if constexpr (KIND == kAppendQ) {   // ---------------- queries: one set of angles for all heads
     const int h0 = (item - 2 * p.k_items) * p.q_heads;
     const int h1 = min(p.Hq, h0 + p.q_heads);
     for (int t = t0 + tl; t < t1; t += tp) {
@@ -167,7 +168,7 @@ __device__ __forceinline__ void append_piece(const AppendParams& p, int at) {
     }
     return;
   }
-  if (item >= p.k_items) {       // ---------------- values: copied
+  if constexpr (KIND == kAppendV) {       // ---------------- values: copied
     const int h = (item - p.k_items) * hp + hl;
     if (h >= p.Hkv) return;
     const uint16_t* src = p.v + b * p.v_sb + h * p.v_sh + 16 * part;
@@ -267,33 +268,48 @@ __device__ __forceinline__ void append_piece(const AppendParams& p, int at) {
   }
 }
 
-// A block per piece that Snew has room for, or, where that were more than kAppendBlocks per SM, so many
-// blocks that each look at 32 of their pieces at once for those that hold tokens: a padded batch may
-// mix prompts with single tokens.  (32 sequences padded to 4096 tokens, pages of 16, one of them that
-// long and the others one token: 32 us, a block per piece 110 us; all of one token 15 and 100 us.  Fewer
-// blocks end unevenly where the pieces are full, 40 us against 31 us with 16 per SM.)
+// A block per piece that Snew has room for, or, where that were more than kAppendBlocks per SM,
+// kAppendLoopBlocks per SM (a multiple of the items) that each keep to one item and look at 32 of their
+// pages at once for those that hold tokens: a padded batch may mix prompts with single tokens.  Each
+// kind of piece has a loop of its own: one loop around all three needed 120 registers, spilled 150
+// bytes at the 64 that four blocks per SM leave, and took 22 % longer over full pieces.  (8 prompts of
+// 4096, pages of 64: 125.6 us, 6.41 TB/s, a block per piece 125.2; 32 sequences padded to 4096 tokens,
+// pages of 16, one of them that long and the others one token: 24.5 and 117 us; all of one token 9.8
+// and 104 us.  16 blocks per SM: 132, 24.2 and 8.0 us; 64: 127, 30.5 and 15.6.  Just below the limit a
+// block per piece is ahead: the four prompts above 33.0 us, looping 34.2.)
 template <bool BF16, int D, bool INTERLEAVED, bool MANY>
 __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const AppendParams p, int pieces) {
   pdl_launch_dependents();
   pdl_wait_prior();
-  if constexpr (!MANY) {
-    append_piece<BF16, D, INTERLEAVED>(p, blockIdx.x);
-  } else {
-    for (unsigned at0 = blockIdx.x; at0 < (unsigned)pieces; at0 += 32 * gridDim.x) {
-      const unsigned at = at0 + gridDim.x * (threadIdx.x & 31);
-      bool some = false;
-      if (at < (unsigned)pieces) {
-        const int rest = at / (2 * p.k_items + p.q_items), chunk = rest % p.chunks, b = rest / p.chunks;
-        const int n = p.new_lens ? min(p.new_lens[b], p.Snew) : p.Snew, len = p.kv_lens[b];
-        // (whatever is to be reported, the piece of chunk 0 reports)
-        some = chunk == 0 || (n > 0 && len >= 0 && (long long)len + n > ((long long)(len >> p.kv.page_shift) + chunk) << p.kv.page_shift);
-      }
-      for (unsigned live = __ballot_sync(0xffffffffu, some); live; live &= live - 1) {
-        append_piece<BF16, D, INTERLEAVED>(p, (int)(at0 + gridDim.x * (__ffs(live) - 1)));
-        __syncthreads();           // (its shared memory)
+  const unsigned items = 2 * p.k_items + p.q_items;
+  const int item = (int)(blockIdx.x % items);
+  auto run = [&](auto kind) {
+    constexpr int KIND = decltype(kind)::value;
+    if constexpr (!MANY) {
+      append_piece<BF16, D, INTERLEAVED, KIND>(p, item, (int)(blockIdx.x / items));
+    } else {
+      const unsigned pages = (unsigned)pieces / items, step = gridDim.x / items;
+#pragma unroll 1
+      for (unsigned at0 = blockIdx.x / items; at0 < pages; at0 += 32 * step) {
+        const unsigned at = at0 + step * (threadIdx.x & 31);
+        bool some = false;
+        if (at < pages) {
+          const int chunk = at % p.chunks, b = at / p.chunks;
+          const int n = p.new_lens ? min(p.new_lens[b], p.Snew) : p.Snew, len = p.kv_lens[b];
+          // (whatever is to be reported, the piece of chunk 0 reports)
+          some = chunk == 0 || (n > 0 && len >= 0 && (long long)len + n > ((long long)(len >> p.kv.page_shift) + chunk) << p.kv.page_shift);
+        }
+#pragma unroll 1
+        for (unsigned live = __ballot_sync(0xffffffffu, some); live; live &= live - 1) {
+          append_piece<BF16, D, INTERLEAVED, KIND>(p, item, (int)(at0 + step * (__ffs(live) - 1)));
+          if constexpr (KIND == kAppendK) __syncthreads();   // (its shared memory)
+        }
       }
     }
-  }
+  };
+  if (item >= 2 * p.k_items) run(std::integral_constant<int, kAppendQ>{});
+  else if (item >= p.k_items) run(std::integral_constant<int, kAppendV>{});
+  else run(std::integral_constant<int, kAppendK>{});
 }
 
 }  // namespace fa

@@ -89,11 +89,13 @@ template <bool BF16, int D, bool INTERLEAVED>
 cudaError_t launch_append(const fa::AppendParams& p, long long pieces, cudaStream_t st) {
   const int sms = fa_host::sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const long long most = (long long)fa::kAppendBlocks * sms;
-  return pieces > most ? launch_dependent(fa::fa_kv_append_kernel<BF16, D, INTERLEAVED, true>, (unsigned)most,
-                                          fa::kAppendThreads, 0, st, p, (int)pieces)
-                       : launch_dependent(fa::fa_kv_append_kernel<BF16, D, INTERLEAVED, false>, (unsigned)pieces,
-                                          fa::kAppendThreads, 0, st, p, (int)pieces);
+  const long long items = 2LL * p.k_items + p.q_items;
+  const long long loop = std::max(1LL, (long long)fa::kAppendLoopBlocks * sms / items) * items;   // (an item per block)
+  return pieces > (long long)fa::kAppendBlocks * sms
+             ? launch_dependent(fa::fa_kv_append_kernel<BF16, D, INTERLEAVED, true>, (unsigned)loop,
+                                fa::kAppendThreads, 0, st, p, (int)pieces)
+             : launch_dependent(fa::fa_kv_append_kernel<BF16, D, INTERLEAVED, false>, (unsigned)pieces,
+                                fa::kAppendThreads, 0, st, p, (int)pieces);
 }
 template <bool BF16, int D>
 cudaError_t launch_append(const fa::AppendParams& p, bool interleaved, long long pieces, cudaStream_t st) {
