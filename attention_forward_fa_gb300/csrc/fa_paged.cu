@@ -185,6 +185,8 @@ int launch_decode_rows(fa::DecodeParams& p, long long tiles_per_unit, cudaStream
 
 template <bool BF16, int D>
 int launch_select(fa::SelectParams& p, long long units, cudaStream_t st) {
+  const int sms = fa_host::sm_count();
+  if (sms <= 0) return cuda_fail(cudaErrorInvalidDevice);
   const size_t pages = (size_t)units * p.kv.max_pages;
   uint8_t* scratch = static_cast<uint8_t*>(fa_host::scratch_alloc(pages * 24, st));
   if (!scratch) return cuda_fail(cudaGetLastError());
@@ -192,8 +194,6 @@ int launch_select(fa::SelectParams& p, long long units, cudaStream_t st) {
   p.exact = reinterpret_cast<unsigned long long*>(scratch + pages * 8);
   p.near = reinterpret_cast<int32_t*>(scratch + pages * 16);
   p.mark = reinterpret_cast<uint32_t*>(scratch + pages * 20);
-  const int sms = fa_host::sm_count();
-  if (sms <= 0) return cuda_fail(cudaErrorInvalidDevice);
   const long long runs = units * p.chunks, most = (long long)fa::kScoreBlocks * sms;
   cudaError_t e = runs > most ? launch_dependent(fa::fa_page_score_kernel<BF16, D, true>, (unsigned)most, 32, 0, st, p)
                               : launch_dependent(fa::fa_page_score_kernel<BF16, D, false>, (unsigned)runs, 32, 0, st, p);
