@@ -456,10 +456,17 @@ def flash_attention_backward(q, k, v, o, lse, dout, *, o_lo=None, scale: Optiona
 
 
 # ------------------------------------------------------------------ paged key-value cache
+def _int(x) -> int:
+    """x as the library's 32-bit ints hold it: what does not fit is the nearest that does (ctypes would
+    take its lowest 32 bits: a window of 2**32 tokens would become one of none)."""
+    x = int(x)
+    return -2**31 if x < -2**31 else 2**31 - 1 if x > 2**31 - 1 else x
+
+
 def fa_kv_append(kv: fa_paged_kv_t, x: fa_kv_new_t, B: int, Hq: int, Hkv: int, Snew: int, D: int,
                  mask_mode: int, kv_lens, new_lens=None, stream=None) -> int:
     """Direct call of the C entry point (see include/fa_fwd.h).  Returns the FA_* code."""
-    return library().fa_kv_append(kv, x, B, Hq, Hkv, Snew, D, int(mask_mode), _ptr(kv_lens),
+    return library().fa_kv_append(kv, x, *map(_int, (B, Hq, Hkv, Snew, D, mask_mode)), _ptr(kv_lens),
                                   _ptr(new_lens), _stream(stream))
 
 
@@ -467,18 +474,18 @@ def fa_decode(q, kv: fa_paged_kv_t, o, lse, B: int, Hq: int, Hkv: int, Sq: int, 
               scale: float, mask_mode: int, kv_lens, pre_tokens: int = -1, page_idx=None,
               max_sel: int = 0, stream=None) -> int:
     """Direct call of the C entry point (see include/fa_fwd.h).  Returns the FA_* code."""
-    return library().fa_decode(_ptr(q), kv, _ptr(o), _ptr(lse), B, Hq, Hkv, Sq, D, float(scale),
-                               int(mask_mode), _ptr(kv_lens), int(pre_tokens), _ptr(page_idx),
-                               int(max_sel), _stream(stream))
+    return library().fa_decode(_ptr(q), kv, _ptr(o), _ptr(lse), *map(_int, (B, Hq, Hkv, Sq, D)), float(scale),
+                               _int(mask_mode), _ptr(kv_lens), _int(pre_tokens), _ptr(page_idx),
+                               _int(max_sel), _stream(stream))
 
 
 def fa_select_pages(q, kv: fa_paged_kv_t, page_idx, B: int, Hq: int, Hkv: int, Sq: int, D: int,
                     mask_mode: int, kv_lens, max_sel: int, first: int = 1, last: int = 1,
                     stream=None) -> int:
     """Direct call of the C entry point (see include/fa_fwd.h).  Returns the FA_* code."""
-    return library().fa_select_pages(_ptr(q), kv, _ptr(page_idx), B, Hq, Hkv, Sq, D,
-                                     int(mask_mode), _ptr(kv_lens), int(max_sel), int(first),
-                                     int(last), _stream(stream))
+    return library().fa_select_pages(_ptr(q), kv, _ptr(page_idx),
+                                     *map(_int, (B, Hq, Hkv, Sq, D, mask_mode)), _ptr(kv_lens),
+                                     *map(_int, (max_sel, first, last)), _stream(stream))
 
 
 class PagedKV:
@@ -532,8 +539,8 @@ class PagedKV:
         self._flags = FA_DTYPE_FP16 if self.dtype == torch.float16 else 0
         self._c = fa_paged_kv_t(
             k_pages.data_ptr(), v_pages.data_ptr(), *k_pages.stride()[:3], *v_pages.stride()[:3],
-            _ptr(k_min), _ptr(k_max), page_table.data_ptr(), page_table.stride(0), self.max_pages,
-            self.num_pages, self.page_size)
+            _ptr(k_min), _ptr(k_max), page_table.data_ptr(), page_table.stride(0), _int(self.max_pages),
+            _int(self.num_pages), self.page_size)
 
 
 def _int32_of(t, shape, device, name):
@@ -617,7 +624,7 @@ def paged_kv_append(cache: PagedKV, kv_lens, k, v, *, new_lens=None, q=None, q_o
         for t in (cos, sin):
             if t.dtype != torch.float32 or t.device != cache.device or not t.is_contiguous():
                 raise ValueError("cos and sin must be contiguous fp32 tensors on the cache's device")
-        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        max_pos, rot = _int(cos.shape[0]), _int(2 * cos.shape[1])
 
     def call(raw):
         qo = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q is not None and q_out is None else q_out
@@ -667,7 +674,7 @@ def flash_attention_decode(q, cache: PagedKV, kv_lens, *, scale: Optional[float]
         e = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device) if lse is None else lse
         _raise(library().fa_decode(q.data_ptr(), cache._c, o.data_ptr(), e.data_ptr(), B, Hq, cache.Hkv,
                                    Sq, D, 1.0 / math.sqrt(D) if scale is None else scale, cache._flags,
-                                   kv_lens.data_ptr(), -1 if pre_tokens is None else pre_tokens,
+                                   kv_lens.data_ptr(), -1 if pre_tokens is None else _int(pre_tokens),
                                    _ptr(page_idx), max_sel, raw))
         return o, e
 
@@ -695,7 +702,7 @@ def select_kv_pages(q, cache: PagedKV, kv_lens, max_sel: int, *, first: int = 1,
     def call(raw):
         idx = torch.empty(shape, dtype=torch.int32, device=q.device) if out is None else out
         _raise(library().fa_select_pages(q.data_ptr(), cache._c, idx.data_ptr(), B, Hq, cache.Hkv, Sq, D,
-                                         cache._flags, kv_lens.data_ptr(), max_sel, first, last, raw))
+                                         cache._flags, kv_lens.data_ptr(), max_sel, _int(first), _int(last), raw))
         return idx
 
     raw = _raw_here(cache.device) if stream is None else None
