@@ -290,7 +290,8 @@ int fa_decode(const void* q, const fa_paged_kv_t* kv, void* o, float* lse, int B
   if (rc == FA_OK) rc = validate_pools(kv, Hkv);
   if (rc != FA_OK) return rc;
   if (!q || !o || !lse || !kv_lens) return FA_ERR_NULL;
-  if (!std::isfinite(scale) || pre_tokens < -1) return FA_ERR_SHAPE;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!std::isfinite(scale) || !std::isfinite(scale_log2) || pre_tokens < -1) return FA_ERR_SHAPE;
   if (page_idx && (max_sel <= 0 || max_sel > kMostSel)) return FA_ERR_SHAPE;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(kv_lens, 4) || !aligned(page_idx, 4))
     return FA_ERR_ALIGN;
@@ -317,7 +318,7 @@ int fa_decode(const void* q, const fa_paged_kv_t* kv, void* o, float* lse, int B
   c.Sq = Sq;
   c.pre_tokens = pre_tokens;
   c.reach = pre_tokens < 0 ? -1 : (int)std::min<long long>((long long)Sq + pre_tokens, 0x7FFFFFFF);
-  c.scale_log2 = scale * 1.4426950408889634f;
+  c.scale_log2 = scale_log2;
   c.q = static_cast<const uint16_t*>(q);
   c.o = static_cast<uint16_t*>(o);
   c.lse = lse;

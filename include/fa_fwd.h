@@ -479,6 +479,7 @@ int fa_kv_append(const fa_paged_kv_t* kv, const fa_kv_new_t* x, int B, int Hq, i
  * pre_tokens >= 0, j >= t - pre_tokens; -1 is unbounded).  A row that sees no
  * key (t < 0, an empty sequence) gets O = 0 and LSE = +inf.  Query head h reads
  * KV head h / (Hq / Hkv).
+ *   scale     finite, also times log2(e) (FA_ERR_SHAPE otherwise).
  *   page_idx  NULL (every page), or DEVICE int32 [B, Hkv, max_sel], contiguous:
  *             only the listed pages (numbers p of the sequence's own pages, as
  *             in the page table's columns) are read; an entry < 0 or past the

@@ -93,3 +93,18 @@ def test_tables_of_more_positions_than_32_bits_count(lib):
     x = torch.zeros(1, 2, 1, 64, dtype=torch.bfloat16)
     B.paged_kv_append(cpu_cache(), N, x, x, cos=Rows, sin=Rows, stream=1)
     assert seen == {"max_pos": BIG, "rot": 16}
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -3e38, 1e39, float("nan")])
+def test_a_scale_past_fp32_in_log2_units_is_refused(scale):
+    """Scores are taken in log2 units: 2.4e38 * log2(e) is no fp32 number, and
+    every score would be infinite or NaN."""
+    if torch.cuda.is_available():
+        pytest.skip("stand-in device addresses: no GPU may be visible")
+    from attention_forward_fa_gb300 import build
+    build.build()
+    P = 0x10000
+    kv = B.fa_paged_kv_t(k=P, v=P, k_stride_page=8192, k_stride_head=2048, k_stride_slot=128, v_stride_page=8192,
+                         v_stride_head=2048, v_stride_slot=128, page_table=P, table_stride=8, max_pages=8,
+                         num_pages=64, page_size=16)
+    assert B.fa_decode(P, kv, P, P, 1, 8, 2, 1, 128, scale, 0, P, -1, None, 0, 0) == B.FA_ERR_SHAPE
