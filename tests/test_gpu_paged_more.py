@@ -87,3 +87,76 @@ def test_append_of_more_pieces_than_blocks(dtype, B, Hq, Hkv, D, page, S, rot, i
         assert torch.equal(hi[first], k[first, :, old:].amax(1).clamp(min=-9.0))
     keep = ~wrote[:, None, :, None].expand_as(k)
     assert torch.equal(k[keep], was_k[keep]) and torch.equal(v[keep], was_v[keep])
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,page,S,old,new,pre", [
+    ("bf16", 8, 2, 128, 16, 5, [40, 7, 0, 100], [5, 2, 3, 0], None),
+    ("fp16", 6, 6, 64, 32, 4, [0, 31, 700], [4, 1, 3], 20),
+    ("bf16", 16, 1, 128, 64, 9, [1000, 64], [1, 9], None),
+    ("bf16", 8, 4, 64, 16, 60, [0, 3], [60, 21], None),
+])
+def test_steps_of_different_lengths(dtype, Hq, Hkv, D, page, S, old, new, pre):
+    """A padded step: the append's rows lie at the front, the attention takes
+    them at the end of its rows; moved there and back by one gather each, every
+    sequence is answered as by a call of its own.  The rows in front belong to
+    no token and may hold anything: they reach no other row."""
+    import torch
+    import attention_forward_fa_gb300 as fa
+    B = len(old)
+    c = Cache(41, dtype, B, Hkv, D, page, [o + n for o, n in zip(old, new)])
+    x = _dev(_round(c.rng.standard_normal((B, Hq + 2 * Hkv, S, D)), dtype), dtype)
+    cos, sin = _tables(max(old) + S, D)
+    lens, n = c.ints(old), c.ints(new)
+    q = torch.full((B, Hq, S, D), float("nan"), dtype=x.dtype, device="cuda")
+    fa.paged_kv_append(c.obj, lens, x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], new_lens=n, q=x[:, :Hq], q_out=q, cos=_dev(cos), sin=_dev(sin))
+    lens = lens + n
+    i, gap = torch.arange(S, device="cuda"), (S - n)[:, None]
+    to_end = ((i - gap) % S)[:, None, :, None].expand_as(q)
+    o, l = fa.flash_attention_decode(q.gather(2, to_end), c.obj, lens, pre_tokens=pre)
+    to_front = (i + gap) % S
+    o = o.gather(2, to_front[:, None, :, None].expand_as(o))
+    l = l.gather(2, to_front[:, None].expand_as(l))
+    assert _status() == 0
+    k, v, qh = _host(c.tk), _host(c.tv), _host(q)
+    for b in range(B):
+        m = new[b]
+        if m:
+            ref = P.decode(qh[b:b + 1, :, :m], k, v, c.table[b:b + 1], [old[b] + m], D ** -0.5, pre)
+            _check(o[b:b + 1, :, :m], l[b:b + 1, :, :m], ref, dtype, f"sequence {b}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_bounds_after_tokens_are_taken_back(dtype):
+    """Draft tokens that are refused: kv_lens goes back inside a page and the
+    next tokens overwrite them.  The bounds stay those of all keys stored in the
+    page since its slot 0 was written, so that no score falls below a key's;
+    a page whose slot 0 is written again starts anew."""
+    import torch
+    import attention_forward_fa_gb300 as fa
+    page, D = 16, 64
+    c = Cache(42, dtype, 1, 2, D, page, [3 * page], bounds=True)
+    x = [_dev(_round(c.rng.standard_normal((1, 2, 12, D)), dtype), dtype) for _ in range(3)]
+    fa.paged_kv_append(c.obj, c.ints([0]), x[0], x[0])                   # tokens 0 .. 11
+    fa.paged_kv_append(c.obj, c.ints([12]), x[1], x[1])                  # 12 .. 23: 4 into page 0, 8 into page 1
+    fa.paged_kv_append(c.obj, c.ints([14]), x[2], x[2])                  # back to 14: 14 .. 25
+    assert _status() == 0
+    p0, p1 = int(c.table[0, 0]), int(c.table[0, 1])
+    every = torch.cat((x[0][0], x[1][0, :, :4], x[2][0, :, :2]), 1)      # whatever page 0 has held
+    assert torch.equal(c.tlo[p0], every.amin(1)) and torch.equal(c.thi[p0], every.amax(1))
+    assert torch.equal(c.tlo[p1], x[2][0, :, 2:].amin(1)) and torch.equal(c.thi[p1], x[2][0, :, 2:].amax(1))
+    for p in (p0, p1):
+        held = c.tk[p] if p == p0 else c.tk[p][:, :10]
+        assert bool((c.tlo[p][:, None] <= held).all()) and bool((c.thi[p][:, None] >= held).all())
+
+
+def test_a_window_past_32_bits_is_none():
+    import torch
+    import attention_forward_fa_gb300 as fa
+    c = Cache(43, "bf16", 2, 2, 64, 32, [300, 33])
+    q = _dev(_round(c.rng.standard_normal((2, 4, 3, 64)), "bf16"), "bf16")
+    n = c.ints([300, 33])
+    o, l = fa.flash_attention_decode(q, c.obj, n)
+    for pre in (300, 2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 1, 2 ** 63):
+        x, y = fa.flash_attention_decode(q, c.obj, n, pre_tokens=pre)
+        assert torch.equal(o, x) and torch.equal(l, y), pre
+    assert _status() == 0
