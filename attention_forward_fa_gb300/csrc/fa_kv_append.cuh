@@ -48,8 +48,10 @@ struct AppendParams {
   int* status;
 };
 
-// A piece of the work: one page of one sequence (`rest`), some heads (`item`) of its K, V or Q.
-constexpr int kAppendK = 0, kAppendV = 1, kAppendQ = 2;
+// A piece of the work: one page of one sequence (`rest`), some heads (`item`) of its K, V or Q.  KIND: which
+// of the three, or kAppendAny by the item (one way for all up to the tokens' loads: a copy for each kind
+// takes a call of few tokens 0.1 us longer, on its way through the instruction cache).
+constexpr int kAppendK = 0, kAppendV = 1, kAppendQ = 2, kAppendAny = 3;
 template <bool BF16, int D, bool INTERLEAVED, int KIND>
 __device__ __forceinline__ void append_piece(const AppendParams& p, int item, int rest) {
   constexpr int L = D / 16;                    // threads per row
@@ -141,7 +143,7 @@ __device__ __forceinline__ void append_piece(const AppendParams& p, int item, in
   auto ld = [](const uint16_t* x) { return *reinterpret_cast<const uint4*>(x); };
   auto st = [](uint16_t* x, uint4 w) { *reinterpret_cast<uint4*>(x) = w; };
 
-  if constexpr (KIND == kAppendQ) {   // ---------------- queries: one set of angles for all heads
+  if (KIND == kAppendQ || (KIND == kAppendAny && item >= 2 * p.k_items)) {   // ---------------- queries: one set of angles for all heads
     const int h0 = (item - 2 * p.k_items) * p.q_heads;
     const int h1 = min(p.Hq, h0 + p.q_heads);
     for (int t = t0 + tl; t < t1; t += tp) {
@@ -168,7 +170,7 @@ __device__ __forceinline__ void append_piece(const AppendParams& p, int item, in
     }
     return;
   }
-  if constexpr (KIND == kAppendV) {       // ---------------- values: copied
+  if (KIND == kAppendV || (KIND == kAppendAny && item >= p.k_items)) {       // ---------------- values: copied
     const int h = (item - p.k_items) * hp + hl;
     if (h >= p.Hkv) return;
     const uint16_t* src = p.v + b * p.v_sb + h * p.v_sh + 16 * part;
@@ -283,11 +285,11 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const A
   pdl_wait_prior();
   const unsigned items = 2 * p.k_items + p.q_items;
   const int item = (int)(blockIdx.x % items);
-  auto run = [&](auto kind) {
-    constexpr int KIND = decltype(kind)::value;
-    if constexpr (!MANY) {
-      append_piece<BF16, D, INTERLEAVED, KIND>(p, item, (int)(blockIdx.x / items));
-    } else {
+  if constexpr (!MANY) {
+    append_piece<BF16, D, INTERLEAVED, kAppendAny>(p, item, (int)(blockIdx.x / items));
+  } else {
+    auto loop = [&](auto kind) {
+      constexpr int KIND = decltype(kind)::value;
       const unsigned pages = (unsigned)pieces / items, step = gridDim.x / items;
 #pragma unroll 1
       for (unsigned at0 = blockIdx.x / items; at0 < pages; at0 += 32 * step) {
@@ -305,11 +307,11 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const A
           if constexpr (KIND == kAppendK) __syncthreads();   // (its shared memory)
         }
       }
-    }
-  };
-  if (item >= 2 * p.k_items) run(std::integral_constant<int, kAppendQ>{});
-  else if (item >= p.k_items) run(std::integral_constant<int, kAppendV>{});
-  else run(std::integral_constant<int, kAppendK>{});
+    };
+    if (item >= 2 * p.k_items) loop(std::integral_constant<int, kAppendQ>{});
+    else if (item >= p.k_items) loop(std::integral_constant<int, kAppendV>{});
+    else loop(std::integral_constant<int, kAppendK>{});
+  }
 }
 
 }  // namespace fa
