@@ -160,3 +160,63 @@ def test_a_window_past_32_bits_is_none():
         x, y = fa.flash_attention_decode(q, c.obj, n, pre_tokens=pre)
         assert torch.equal(o, x) and torch.equal(l, y), pre
     assert _status() == 0
+
+
+@pytest.mark.parametrize("dtype,B,Hq,Hkv,D,page", [("bf16", 5, 8, 2, 128, 16), ("fp16", 40, 4, 4, 64, 32)])
+def test_steps_in_flight(dtype, B, Hq, Hkv, D, page):
+    """Many steps with nothing between their calls: each kernel may start while
+    the one before it drains, and reads what that one wrote (pages, bounds, the
+    list of pages, its rotated queries).  The same bits as with a wait after
+    every call."""
+    import torch
+    import attention_forward_fa_gb300 as fa
+    steps, S = 60, 2
+    cos, sin = (_dev(x) for x in _tables(3 * steps + 200, D))
+    rng = np.random.default_rng(44)
+    start = [int(x) for x in rng.integers(0, 200, B)]
+    cap = [n + S * steps for n in start]
+    xs = [_dev(_round(rng.standard_normal((B, Hq + 2 * Hkv, S, D)), dtype), dtype) for _ in range(steps)]
+    first = _dev(_round(rng.standard_normal((B, Hkv, 200, D)), dtype), dtype)
+    lens = [_dev(np.asarray([n + S * i for n in start], dtype=np.int32)) for i in range(steps + 1)]
+    zero = torch.zeros_like(lens[0])
+
+    def run(wait):
+        c = Cache(45, dtype, B, Hkv, D, page, cap, bounds=True)
+        fa.paged_kv_append(c.obj, zero, first, first, new_lens=lens[0], cos=cos, sin=sin)
+        torch.cuda.synchronize()
+        out = []
+        outs = [(torch.empty(B, Hq, S, D, dtype=first.dtype, device="cuda"), torch.empty(B, Hkv, 7, dtype=torch.int32, device="cuda"),
+                 *(torch.empty(B, Hq, S, D, dtype=first.dtype, device="cuda") for _ in range(2)),
+                 *(torch.empty(B, Hq, S, device="cuda") for _ in range(2))) for _ in range(steps)]
+        torch.cuda.synchronize()
+        for i, (q, idx, o, o7, l, l7) in enumerate(outs):
+            x = xs[i]
+            for call in (lambda: fa.paged_kv_append(c.obj, lens[i], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], q=x[:, :Hq], q_out=q, cos=cos, sin=sin),
+                         lambda: fa.flash_attention_decode(q, c.obj, lens[i + 1], out=o, lse=l),
+                         lambda: fa.select_kv_pages(q, c.obj, lens[i + 1], 7, out=idx),
+                         lambda: fa.flash_attention_decode(q, c.obj, lens[i + 1], page_idx=idx, out=o7, lse=l7)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+            out += [q, idx, o, o7, l, l7]
+        torch.cuda.synchronize()
+        return out + [c.tk, c.tv, c.tlo, c.thi]
+
+    want = run(True)
+    for _ in range(5):
+        for i, (a, b) in enumerate(zip(run(False), want)):
+            assert torch.equal(a, b), f"output {i}"
+    assert _status() == 0
+    # appends alone, one behind the other: the bounds are read and written by each
+    for wait in (True, False, False, False):
+        c = Cache(46, dtype, B, Hkv, D, page, cap, bounds=True)
+        torch.cuda.synchronize()
+        for i in range(steps):
+            fa.paged_kv_append(c.obj, lens[i], xs[i][:, :Hkv], xs[i][:, :Hkv])
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (c.tk, c.tv, c.tlo, c.thi)]
+        if wait:
+            want = got
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
