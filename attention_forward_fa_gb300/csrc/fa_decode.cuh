@@ -633,23 +633,46 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
           v[q][i][3] &= keep1;
         }
       };
-      if (NT <= 4 && !whole) {
+      if constexpr (NT > 4) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) load_v(q);
+      }
+      if (!whole) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) keep_seen(q);
       }
+      // The tile's sum starts from zero and is added to O by itself: the matrix instructions cut off what
+      // they add (about 2^-24 of the sum so far each, always towards zero), and eight of them per tile on
+      // a running O lost 8.6e-4 of it over 131072 keys of one CTA, four times an fp16 rounding.  Columns
+      // of 8 rows are summed NB at a time, so that there are products that do not wait for each other.
+      // (16 sequences of 4096 tokens, 8 KV heads of 128: on a running O 57.0 us at 32 rows and 81.5 at 48,
+      // column by column 60.6 and 85, so 59.2 and 77.8; up to 24 rows all the same.)
+      constexpr int NB = NT > 4 ? 3 : NT > 2 ? 2 : 1;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if constexpr (NT > 4) {
-          load_v(q);
-          if (!whole) keep_seen(q);
-        }
+      for (int n0 = 0; n0 < NT; n0 += NB) {
+        float sum[NB][DT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint4 pp = s_p[(q * NT + n) * 32 + lane];
+        for (int j = 0; j < NB; ++j)
 #pragma unroll
-          for (int i = 0; i < DT; ++i) mma_16x8<BF16>(o[n][i], v[q][i], pp.x, pp.y);
+          for (int i = 0; i < DT; ++i) sum[j][i][0] = sum[j][i][1] = sum[j][i][2] = sum[j][i][3] = 0.f;
 #pragma unroll
-          for (int i = 0; i < DT; ++i) mma_16x8<BF16>(o[n][i], v[q][i], pp.z, pp.w);
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int j = 0; j < NB; ++j) {
+            if (n0 + j >= NT) break;
+            const uint4 pp = s_p[(q * NT + n0 + j) * 32 + lane];
+#pragma unroll
+            for (int i = 0; i < DT; ++i) mma_16x8<BF16>(sum[j][i], v[q][i], pp.x, pp.y);
+#pragma unroll
+            for (int i = 0; i < DT; ++i) mma_16x8<BF16>(sum[j][i], v[q][i], pp.z, pp.w);
+          }
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          if (n0 + j >= NT) break;
+#pragma unroll
+          for (int i = 0; i < DT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n0 + j][i][e] += sum[j][i][e];
         }
       }
       // A warp that gave up hands back no stage: its copy may still be in flight.  The producer's next

@@ -163,9 +163,10 @@ int launch_decode(fa::DecodeParams& p, long long most_tiles, cudaStream_t st) {
 template <bool BF16, int D>
 int launch_decode_rows(fa::DecodeParams& p, long long tiles_per_unit, cudaStream_t st) {
   // As few passes over the keys as 48 rows each allow, and as few columns of 8 as then hold a pass's
-  // rows.  Up to 32 rows the time is that of the keys, past that the matrix instructions', about 1.5
-  // us a row whatever the split (16 sequences of 4096 tokens, 8 KV heads of 128, bf16: 47 us at 4
-  // rows, 58 at 32, 69 at 40, 83 at 48, 101 at 64, 148 at 96; one pass of 64 rows spilled and took 127).
+  // rows.  Up to 32 rows the time is that of the keys, past that the matrix instructions', about 1.4
+  // us a row whatever the split (16 sequences of 4096 tokens, 8 KV heads of 128, bf16: 46 us at 4
+  // rows, 59 at 32, 68 at 40, 78 at 48, 105 at 64, 143 at 96; with 128 channels the passes of 40 and 48
+  // rows spill 4 and 12 bytes, one of 64 rows spilled far more and took 127 us).
   fa::DecodeCore& c = p.c;
   const int passes = (c.rows + 47) / 48;
   const int nt = ((c.rows + passes - 1) / passes + 7) / 8;

@@ -220,3 +220,40 @@ def test_steps_in_flight(dtype, B, Hq, Hkv, D, page):
         if wait:
             want = got
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype,D,B,G,n", [("fp16", 128, 304, 1, 131072), ("fp16", 64, 304, 8, 131072),
+                                           ("bf16", 128, 304, 1, 131072), ("fp16", 64, 160, 48, 65536),
+                                           ("fp16", 128, 160, 20, 65536)])
+def test_decode_long_sums_lose_nothing(dtype, D, B, G, n):
+    """So many long sequences that a block sums whole ones by itself, thousands of
+    tiles; values of one sign, so that whatever the sums cut off adds up.  The
+    bounds are those of the other decode tests: they know no length.  (Pages are
+    shared: the reference weighs each by how often it is listed.)"""
+    import torch
+    import attention_forward_fa_gb300 as fa
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float16
+    page, P_ = 256, 96
+    g = torch.Generator(device="cuda").manual_seed(47)
+    k = torch.randn(P_, 1, page, D, generator=g, device="cuda", dtype=dt)
+    v = (1 + torch.rand(P_, 1, page, D, generator=g, device="cuda")).to(dt)
+    t = torch.randint(P_, (B, n // page), generator=g, device="cuda").to(torch.int32)
+    q = (0.1 * torch.randn(B, G, 1, D, generator=g, device="cuda")).to(dt)
+    lens = torch.full((B,), n, device="cuda", dtype=torch.int32)
+    o, l = fa.flash_attention_decode(q, fa.PagedKV(k, v, t), lens)
+    assert _status() == 0
+    u, sub, small = (2.0 ** -8, 0.0, 0.0) if dtype == "bf16" else (2.0 ** -11, 2.0 ** -25, 2.0 ** -32)
+    for b in range(0, B, 9):
+        w = torch.bincount(t[b].long(), minlength=P_).double()
+        x = torch.einsum("gd,psd->gps", q[b, :, 0].double(), k[:, 0].double()) * D ** -0.5
+        X = (torch.einsum("gd,psd->gps", q[b, :, 0].double().abs(), k[:, 0].double().abs()) * D ** -0.5).amax((1, 2))
+        m = x.amax((1, 2))
+        e = torch.exp(x - m[:, None, None]) * w[:, None]
+        z = e.sum((1, 2))
+        ref = torch.einsum("gps,psd->gd", e, v[:, 0].double()) / z[:, None]
+        lim = (2 * 2.0 ** -16 * X + 2.0 ** -20 * X + 2.0 ** -15)[:, None] * ref + (u + 2.0 ** -20) * ref + sub
+        lim += small * torch.einsum("p,psd->d", w, v[:, 0].double())
+        err = (o[b, :, 0].double() - ref).abs()
+        assert bool((err <= lim).all()), f"sequence {b}: O off by {(err / lim).max().item():.3g} of its bound"
+        ll = (2.0 ** -16 + 2.0 ** -21) * X + 2.0 ** -20 * (1 + (m + torch.log(z)).abs())
+        assert bool(((l[b, :, 0].double() - m - torch.log(z)).abs() <= ll).all())
