@@ -592,8 +592,13 @@ def paged_kv_append(cache: PagedKV, kv_lens, k, v, *, new_lens=None, q=None, q_o
     q [B, Hq, S, D]: rotated by the same positions into q_out (allocated where None; may be q).
     cos, sin: fp32 [max_pos, r / 2] of the rotated channels r <= D, r a multiple of 16; None: no
     rotation.  interleaved: pairs (2j, 2j + 1) instead of (j, j + r / 2).
-    Updates cache.k_min / k_max where the cache has them.  Returns q_out (rows past new_lens as
-    they were: undefined in an allocated one), or None without q."""
+    Updates cache.k_min / k_max where the cache has them (then no two sequences may append to one
+    page).  Returns q_out (rows past new_lens as they were: undefined in an allocated one), or None
+    without q.  A sequence's rows are its first new_lens[b], flash_attention_decode wants them as the
+    last: where new_lens differ, row i moves to row i + S - new_lens[b] in between.
+
+    stream, of this and the other calls on a cache: as under torch.cuda.stream(stream); the caller
+    orders it behind what makes the inputs and keeps them until it has run."""
     import torch
     if k.dim() != 4 or k.shape != v.shape:
         raise ValueError("k and v must be [B, Hkv, S, D], of one shape")
@@ -648,7 +653,8 @@ def flash_attention_decode(q, cache: PagedKV, kv_lens, *, scale: Optional[float]
     q [B, Hq, Sq, D] contiguous, of the cache's type: the Sq newest tokens of each sequence, which
     are in the cache already; kv_lens int32 [B], the tokens in the cache.  Row i is token
     t = kv_lens[b] - Sq + i and sees keys max(0, t - pre_tokens) .. t (pre_tokens None: from 0); a
-    row that sees none gets 0 and LSE +inf.  page_idx: int32 [B, Hkv, max_sel] (select_kv_pages):
+    row that sees none gets 0 and LSE +inf.  A sequence with fewer new tokens has them in its last
+    rows (paged_kv_append leaves them in the first).  page_idx: int32 [B, Hkv, max_sel] (select_kv_pages):
     only these pages of each sequence are read (of a list, as many entries count as the sequence
     has pages: invalid ones belong at the end).  Returns (o, lse fp32 [B, Hq, Sq])."""
     import torch

@@ -22,7 +22,10 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // null where the driv
 
 // Launch with programmatic stream serialisation: the kernel may be scheduled
 // while the previous kernel on the stream drains; it waits for that kernel
-// (griddepcontrol.wait) before its first global memory access.
+// (griddepcontrol.wait) before it writes or reads global memory.  Ahead of that
+// wait it may read only what was final before the previous kernel let it go, so
+// that kernel has to wait for those before it first (fa_decode_join_kernel and
+// fa_select_kernel read the lengths early: their predecessors wait, then trigger).
 template <typename... Params, typename... Args>
 cudaError_t launch_dependent(void (*kern)(Params...), unsigned grid, unsigned block, size_t smem,
                              cudaStream_t st, Args&&... args) {

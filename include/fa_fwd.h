@@ -403,8 +403,10 @@ int fa_convert_v_fp16(const void* v_bf16, void* v_fp16, int64_t n_elems, void* s
  * max_pages entries per sequence, max_pages * page_size <= 2^31 - 65536; the same
  * limit holds for the rows of a call's queries (B * Hq * Sq) or new keys.
  * k_min / k_max: NULL, or [num_pages, Hkv, D] of the cache's type, contiguous,
- * 16-byte aligned: per page and channel the least and largest stored key,
- * written by fa_kv_append and read by fa_select_pages. */
+ * 16-byte aligned: per page and channel the least and largest key stored since
+ * the page's slot 0 was last written (which bounds the keys that the page holds,
+ * also after tokens were taken back by a smaller kv_lens), written by
+ * fa_kv_append and read by fa_select_pages. */
 typedef struct {
   void* k;
   void* v;
@@ -458,12 +460,17 @@ typedef struct {
  *   new_lens  NULL (n_b = Snew), or DEVICE int32[B] with n_b in [0, Snew]; a
  *             value outside is clamped and reported as FA_ERR_INDEX.  Tokens
  *             i >= n_b are padding: nothing of them is read, and their rows of
- *             q_out stay as they were.
+ *             q_out stay as they were.  The rows of a sequence's tokens are thus
+ *             its first n_b, where fa_decode takes its last ones (row i is token
+ *             kv_lens + n_b - Snew + i there): q_out goes to fa_decode as it is
+ *             only where every n_b is Snew; else row i of sequence b has to move
+ *             to row i + Snew - n_b (and the answers back).
  * With k_min / k_max set, the bounds of every page that got a token are
  * brought up to date from the keys as stored: anew for a page whose slot 0 was
  * written, widened otherwise.
  * No two appended tokens may share a page slot, nor two calls that overlap on
- * the GPU a page.  D in {64, 128}; mask_mode: 0 (bf16) or FA_DTYPE_FP16, the
+ * the GPU a page; with k_min / k_max set no two sequences of a call may append
+ * to one page (its bounds have one writer).  D in {64, 128}; mask_mode: 0 (bf16) or FA_DTYPE_FP16, the
  * type of the cache, k, v, q and q_out.  Allocates nothing.
  */
 int fa_kv_append(const fa_paged_kv_t* kv, const fa_kv_new_t* x, int B, int Hq, int Hkv, int Snew,
@@ -478,7 +485,9 @@ int fa_kv_append(const fa_paged_kv_t* kv, const fa_kv_new_t* x, int B, int Hq, i
  * Row i is the token t = kv_lens[b] - Sq + i and sees the keys j <= t (and, with
  * pre_tokens >= 0, j >= t - pre_tokens; -1 is unbounded).  A row that sees no
  * key (t < 0, an empty sequence) gets O = 0 and LSE = +inf.  Query head h reads
- * KV head h / (Hq / Hkv).
+ * KV head h / (Hq / Hkv).  A sequence with fewer than Sq new tokens has them in
+ * its last rows (fa_kv_append leaves them in the first); the rows in front are
+ * answered as the tokens before, whatever they hold, and reach no other row.
  *   scale     finite, also times log2(e) (FA_ERR_SHAPE otherwise).
  *   page_idx  NULL (every page), or DEVICE int32 [B, Hkv, max_sel], contiguous:
  *             only the listed pages (numbers p of the sequence's own pages, as
@@ -486,15 +495,18 @@ int fa_kv_append(const fa_paged_kv_t* kv, const fa_kv_new_t* x, int B, int Hq, i
  *             sequence's last page is an invalid slot; a page listed twice
  *             counts twice.  Of a list the first n entries count, n the pages
  *             that the sequence has: a list without repetitions needs no more,
- *             with its invalid slots at the end.  1 <= max_sel <= 2^20.  Pages
- *             and the mask above apply together.
+ *             with its invalid slots at the end (of [-1, -1, 1] for a sequence of
+ *             two pages nothing counts).  1 <= max_sel <= 2^20.  Pages and the
+ *             mask above apply together.
  * What lies in the cache at positions that no row of a sequence sees is never
  * used and may be anything, NaN included; keys and values that some row sees
  * must be finite.
  * D in {64, 128}; mask_mode: 0 (bf16) or FA_DTYPE_FP16, the type of q, o and the
  * cache.  P enters the value product as a hi + lo pair of that type.  The work
  * is split over the cache's length; the pieces (fp32) go to stream-ordered
- * scratch and are joined.  Results do not depend on what else runs.
+ * scratch and are joined.  The same call gives the same bits, whatever else
+ * runs; where a sequence is split follows the lengths of the whole batch, so
+ * that in another batch its last bits may differ.
  */
 int fa_decode(const void* q, const fa_paged_kv_t* kv, void* o, float* lse, int B, int Hq, int Hkv,
               int Sq, int D, float scale, int mask_mode, const int32_t* kv_lens, int pre_tokens,

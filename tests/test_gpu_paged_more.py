@@ -257,3 +257,23 @@ def test_decode_long_sums_lose_nothing(dtype, D, B, G, n):
         assert bool((err <= lim).all()), f"sequence {b}: O off by {(err / lim).max().item():.3g} of its bound"
         ll = (2.0 ** -16 + 2.0 ** -21) * X + 2.0 ** -20 * (1 + (m + torch.log(z)).abs())
         assert bool(((l[b, :, 0].double() - m - torch.log(z)).abs() <= ll).all())
+
+
+def test_front_page_drafts_run():
+    """The front page's padded step, behind its generation step, as written there."""
+    import re
+    from pathlib import Path
+    import torch
+    import attention_forward_fa_gb300 as fa
+    text = (Path(__file__).resolve().parents[1] / "README.md").read_text()
+    blocks = [b for b in re.findall(r"```python\n(.*?)```", text, re.S) if "paged_kv_append" in b]
+    env = {"torch": torch, "fa": fa}
+    torch.manual_seed(48)
+    for i, b in enumerate(blocks):
+        exec(compile(b, f"serving-example-{i}", "exec"), env)
+    k, v, t = _host(env["k_pages"]), _host(env["v_pages"]), env["table"].cpu().numpy()
+    for b, (m, n) in enumerate(((4, 1005), (2, 40))):
+        q = _host(env["q"])[b:b + 1, :, :m]
+        O, _, A, X, V = P.decode(q, k, v, t[b:b + 1], [n], 128 ** -0.5)
+        lim = (2 * 2.0 ** -16 * X + 2.0 ** -20 * X + 2.0 ** -15)[..., None] * A + (2.0 ** -8 + 2.0 ** -20) * np.abs(O)
+        assert (np.abs(_host(env["drafts"])[b:b + 1, :, :m] - O) <= lim).all()
