@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 from typing import Optional
 
@@ -459,14 +460,14 @@ def flash_attention_backward(q, k, v, o, lse, dout, *, o_lo=None, scale: Optiona
 def _int(x) -> int:
     """x as the library's 32-bit ints hold it: what does not fit is the nearest that does (ctypes would
     take its lowest 32 bits: a window of 2**32 tokens would become one of none)."""
-    x = int(x)
+    x = operator.index(x)
     return -2**31 if x < -2**31 else 2**31 - 1 if x > 2**31 - 1 else x
 
 
 def fa_kv_append(kv: fa_paged_kv_t, x: fa_kv_new_t, B: int, Hq: int, Hkv: int, Snew: int, D: int,
                  mask_mode: int, kv_lens, new_lens=None, stream=None) -> int:
     """Direct call of the C entry point (see include/fa_fwd.h).  Returns the FA_* code."""
-    return library().fa_kv_append(kv, x, *map(_int, (B, Hq, Hkv, Snew, D, mask_mode)), _ptr(kv_lens),
+    return library().fa_kv_append(kv, x, *map(_int, (B, Hq, Hkv, Snew, D, int(mask_mode))), _ptr(kv_lens),
                                   _ptr(new_lens), _stream(stream))
 
 
@@ -475,8 +476,8 @@ def fa_decode(q, kv: fa_paged_kv_t, o, lse, B: int, Hq: int, Hkv: int, Sq: int, 
               max_sel: int = 0, stream=None) -> int:
     """Direct call of the C entry point (see include/fa_fwd.h).  Returns the FA_* code."""
     return library().fa_decode(_ptr(q), kv, _ptr(o), _ptr(lse), *map(_int, (B, Hq, Hkv, Sq, D)), float(scale),
-                               _int(mask_mode), _ptr(kv_lens), _int(pre_tokens), _ptr(page_idx),
-                               _int(max_sel), _stream(stream))
+                               _int(int(mask_mode)), _ptr(kv_lens), _int(int(pre_tokens)), _ptr(page_idx),
+                               _int(int(max_sel)), _stream(stream))
 
 
 def fa_select_pages(q, kv: fa_paged_kv_t, page_idx, B: int, Hq: int, Hkv: int, Sq: int, D: int,
@@ -484,8 +485,8 @@ def fa_select_pages(q, kv: fa_paged_kv_t, page_idx, B: int, Hq: int, Hkv: int, S
                     stream=None) -> int:
     """Direct call of the C entry point (see include/fa_fwd.h).  Returns the FA_* code."""
     return library().fa_select_pages(_ptr(q), kv, _ptr(page_idx),
-                                     *map(_int, (B, Hq, Hkv, Sq, D, mask_mode)), _ptr(kv_lens),
-                                     *map(_int, (max_sel, first, last)), _stream(stream))
+                                     *map(_int, (B, Hq, Hkv, Sq, D, int(mask_mode))), _ptr(kv_lens),
+                                     *map(_int, map(int, (max_sel, first, last))), _stream(stream))
 
 
 class PagedKV:

@@ -70,6 +70,15 @@ def test_forced_pages_past_32_bits(lib, first, last):
         assert y == max(-2 ** 31, min(x, BIG))
 
 
+@pytest.mark.parametrize("bad", [3.5, "7", 2.0 ** 40])
+def test_what_is_no_whole_number_is_refused(lib, bad):
+    with pytest.raises((TypeError, ctypes.ArgumentError)):
+        B.flash_attention_decode(Q, cpu_cache(), N, pre_tokens=bad, stream=1)
+    with pytest.raises((TypeError, ctypes.ArgumentError)):
+        B.select_kv_pages(Q, cpu_cache(), N, 4, first=bad, stream=1)
+    assert not lib.calls
+
+
 def test_direct_calls(lib):
     kv, new = B.fa_paged_kv_t(), B.fa_kv_new_t()
     assert B.fa_decode(0, kv, 0, 0, 2 ** 32 + 1, 8, 2, 1, 128, 1.0, 0, 0, 2 ** 32, None, 2 ** 32 + 4, 0) == 0
