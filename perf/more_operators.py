@@ -8,7 +8,7 @@ operations in fp32, fp64 where values next to a rounding border matter) or, wher
 this package's calls.
 
 An 8-bit cache holds each row of D channels of one token and KV head as e4m3 or e5m2 codes and one
-scale 2^e, e the least integer >= -90 at which no code exceeds the format's largest value, kept as
+scale 2^e, e the least integer >= -80 at which no code exceeds the format's largest value, kept as
 the byte e + 127 (a float8_e8m0fnu number).
 """
 import math
@@ -18,7 +18,7 @@ import torch
 own = False
 
 GOLDEN = 0.6180339887498949
-LEAST = -90         # of a scale's exponent
+LEAST = -80         # of a scale's exponent
 FP8 = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
 TOP = {"e4m3": 9, "e5m2": 16}    # the largest value is 0.875 * 2^TOP
 
