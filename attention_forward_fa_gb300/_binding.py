@@ -82,6 +82,21 @@ class fa_kv_new_t(ctypes.Structure):
                 ("interleaved", ctypes.c_int32), ("max_pos", ctypes.c_int32)]
 
 
+class fa_kv_fp8_t(ctypes.Structure):
+    _fields_ = [("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("format", ctypes.c_int32)]
+
+
+class fa_tree_t(ctypes.Structure):
+    _fields_ = [("ancestors", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("new_lens", ctypes.c_void_p)]
+
+
+class fa_kv_rows_t(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_stride_b", ctypes.c_int64), ("k_stride_h", ctypes.c_int64),
+                ("k_stride_s", ctypes.c_int64), ("v_stride_b", ctypes.c_int64),
+                ("v_stride_h", ctypes.c_int64), ("v_stride_s", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -132,6 +147,22 @@ def library() -> ctypes.CDLL:
         lib.fa_select_pages.argtypes = [ctypes.c_void_p, ctypes.POINTER(fa_paged_kv_t),
                                         ctypes.c_void_p] + [ctypes.c_int] * 6 + [
             ctypes.c_void_p] + [ctypes.c_int] * 3 + [ctypes.c_void_p]
+        lib.fa_kv_append_ext.restype = ctypes.c_int
+        lib.fa_kv_append_ext.argtypes = [
+            ctypes.POINTER(fa_paged_kv_t), ctypes.POINTER(fa_kv_fp8_t), ctypes.POINTER(fa_kv_new_t)] + [
+            ctypes.c_int] * 6 + [ctypes.c_void_p] * 4
+        lib.fa_decode_ext.restype = ctypes.c_int
+        lib.fa_decode_ext.argtypes = [
+            ctypes.c_void_p, ctypes.POINTER(fa_paged_kv_t), ctypes.POINTER(fa_kv_fp8_t), ctypes.c_void_p,
+            ctypes.c_void_p] + [ctypes.c_int] * 5 + [
+            ctypes.c_float, ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+            ctypes.c_int, ctypes.POINTER(fa_tree_t), ctypes.c_void_p]
+        lib.fa_kv_read.restype = ctypes.c_int
+        lib.fa_kv_read.argtypes = [ctypes.POINTER(fa_paged_kv_t), ctypes.POINTER(fa_kv_fp8_t),
+                                   ctypes.POINTER(fa_kv_rows_t)] + [ctypes.c_int] * 5 + [ctypes.c_void_p] * 3
+        lib.fa_kv_keep.restype = ctypes.c_int
+        lib.fa_kv_keep.argtypes = [ctypes.POINTER(fa_paged_kv_t), ctypes.POINTER(fa_kv_fp8_t)] + [
+            ctypes.c_int] * 4 + [ctypes.c_void_p] * 2 + [ctypes.c_int] + [ctypes.c_void_p] * 2
         lib.fa_check_status.restype = ctypes.c_int
         lib.fa_check_status.argtypes = [ctypes.c_void_p]
         lib.fa_set_wait_timeout_ns.restype = None
@@ -489,6 +520,37 @@ def fa_select_pages(q, kv: fa_paged_kv_t, page_idx, B: int, Hq: int, Hkv: int, S
                                      *map(_int, map(int, (max_sel, first, last))), _stream(stream))
 
 
+def fa_kv_append_ext(kv: fa_paged_kv_t, fp8, x: fa_kv_new_t, B: int, Hq: int, Hkv: int, Snew: int, D: int,
+                     mask_mode: int, kv_lens, new_lens=None, positions=None, stream=None) -> int:
+    """Direct call of the C entry point (see include/fa_fwd.h); fp8: fa_kv_fp8_t or None.  Returns the FA_* code."""
+    return library().fa_kv_append_ext(kv, fp8, x, *map(_int, (B, Hq, Hkv, Snew, D, int(mask_mode))), _ptr(kv_lens),
+                                      _ptr(new_lens), _ptr(positions), _stream(stream))
+
+
+def fa_decode_ext(q, kv: fa_paged_kv_t, fp8, o, lse, B: int, Hq: int, Hkv: int, Sq: int, D: int,
+                  scale: float, mask_mode: int, kv_lens, pre_tokens: int = -1, page_idx=None,
+                  max_sel: int = 0, tree=None, stream=None) -> int:
+    """Direct call of the C entry point (see include/fa_fwd.h); fp8: fa_kv_fp8_t or None, tree: fa_tree_t or
+    None.  Returns the FA_* code."""
+    return library().fa_decode_ext(_ptr(q), kv, fp8, _ptr(o), _ptr(lse), *map(_int, (B, Hq, Hkv, Sq, D)), float(scale),
+                                   _int(int(mask_mode)), _ptr(kv_lens), _int(int(pre_tokens)), _ptr(page_idx),
+                                   _int(int(max_sel)), tree, _stream(stream))
+
+
+def fa_kv_read(kv: fa_paged_kv_t, fp8, out: fa_kv_rows_t, B: int, Hkv: int, S: int, D: int, mask_mode: int,
+               starts, lens, stream=None) -> int:
+    """Direct call of the C entry point (see include/fa_fwd.h); fp8: fa_kv_fp8_t or None.  Returns the FA_* code."""
+    return library().fa_kv_read(kv, fp8, out, *map(_int, (B, Hkv, S, D, int(mask_mode))), _ptr(starts), _ptr(lens),
+                                _stream(stream))
+
+
+def fa_kv_keep(kv: fa_paged_kv_t, fp8, B: int, Hkv: int, D: int, mask_mode: int, kv_lens, keep_idx,
+               max_keep: int, keep_lens, stream=None) -> int:
+    """Direct call of the C entry point (see include/fa_fwd.h); fp8: fa_kv_fp8_t or None.  Returns the FA_* code."""
+    return library().fa_kv_keep(kv, fp8, *map(_int, (B, Hkv, D, int(mask_mode))), _ptr(kv_lens), _ptr(keep_idx),
+                                _int(int(max_keep)), _ptr(keep_lens), _stream(stream))
+
+
 class PagedKV:
     """A paged key-value cache: what the paged calls need to know of it.
 
@@ -500,16 +562,28 @@ class PagedKV:
     k_min, k_max: None, or contiguous [num_pages, Hkv, D] of the cache's type: the page bounds that
     paged_kv_append keeps and select_kv_pages reads.
 
+    An 8-bit cache: k_pages, v_pages of torch.float8_e4m3fn or torch.float8_e5m2, and k_scale, v_scale
+    contiguous [num_pages, Hkv, page_size] of torch.uint8 or torch.float8_e8m0fnu: row (page, head, slot)
+    holds the values code * 2^(scale byte - 127).  dtype (bf16 where None, or fp16) is then the type of
+    the queries, new keys and values, answers and bounds that go with the cache.
+
     Holds the tensors, no copies: what is written into them between calls counts.  The object
     itself is never changed by a call and may serve several streams."""
 
     __slots__ = ("k_pages", "v_pages", "page_table", "k_min", "k_max", "dtype", "device", "B",
-                 "Hkv", "D", "page_size", "num_pages", "max_pages", "_flags", "_c")
+                 "Hkv", "D", "page_size", "num_pages", "max_pages", "_flags", "_c", "k_scale", "v_scale", "_fp8")
 
-    def __init__(self, k_pages, v_pages, page_table, k_min=None, k_max=None):
+    def __init__(self, k_pages, v_pages, page_table, k_min=None, k_max=None, *, k_scale=None, v_scale=None, dtype=None):
         import torch
-        if k_pages.dtype not in (torch.bfloat16, torch.float16):
-            raise TypeError("the cache must be bf16 or fp16")
+        formats = {torch.float8_e4m3fn: FA_FP8_E4M3, torch.float8_e5m2: FA_FP8_E5M2}
+        eight = k_pages.dtype in formats
+        if not eight and k_pages.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("the cache must be bf16 or fp16, or float8_e4m3fn or float8_e5m2 with scales")
+        if eight != (k_scale is not None) or eight != (v_scale is not None):
+            raise ValueError("k_scale and v_scale go with an 8-bit cache, and an 8-bit cache with them")
+        kind = (dtype or torch.bfloat16) if eight else k_pages.dtype
+        if kind not in (torch.bfloat16, torch.float16) or (not eight and dtype not in (None, kind)):
+            raise TypeError("dtype must be bf16 or fp16 (of a 16-bit cache: its own)")
         if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
             raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, D], of one shape")
         if (k_min is None) != (k_max is None):
@@ -520,12 +594,16 @@ class PagedKV:
         self.num_pages, self.Hkv, self.page_size, self.D = k_pages.shape
         self.B, self.max_pages = page_table.shape
         bounds = () if k_min is None else (k_min, k_max)
-        for t in (k_pages, v_pages, page_table) + bounds:
+        scales = (k_scale, v_scale) if eight else ()
+        for t in (k_pages, v_pages, page_table) + bounds + scales:
             if not t.is_cuda or t.device != k_pages.device:
                 raise ValueError("the cache's tensors must be on one CUDA device")
-        for t in (v_pages,) + bounds:
-            if t.dtype != k_pages.dtype:
-                raise ValueError("k_pages, v_pages, k_min and k_max must be of one type")
+        if v_pages.dtype != k_pages.dtype or any(t.dtype != kind for t in bounds):
+            raise ValueError("k_pages, v_pages, k_min and k_max must be of one type (k_min and k_max of an 8-bit cache: dtype)")
+        for t in scales:
+            if (t.dtype not in (torch.uint8, torch.float8_e8m0fnu) or not t.is_contiguous()
+                    or t.shape != (self.num_pages, self.Hkv, self.page_size)):
+                raise ValueError("k_scale and v_scale must be contiguous uint8 or float8_e8m0fnu [num_pages, Hkv, page_size]")
         for t in (k_pages, v_pages):
             if t.stride(3) != 1:
                 raise ValueError("k_pages and v_pages must have a contiguous last dimension")
@@ -536,12 +614,19 @@ class PagedKV:
             raise ValueError("D must be 64 or 128, page_size 16, 32, 64, 128 or 256")
         self.k_pages, self.v_pages, self.page_table = k_pages, v_pages, page_table
         self.k_min, self.k_max = k_min, k_max
-        self.dtype, self.device = k_pages.dtype, k_pages.device
+        self.dtype, self.device = kind, k_pages.device
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self._fp8 = fa_kv_fp8_t(k_scale.data_ptr(), v_scale.data_ptr(), formats[k_pages.dtype]) if eight else None
         self._flags = FA_DTYPE_FP16 if self.dtype == torch.float16 else 0
         self._c = fa_paged_kv_t(
             k_pages.data_ptr(), v_pages.data_ptr(), *k_pages.stride()[:3], *v_pages.stride()[:3],
             _ptr(k_min), _ptr(k_max), page_table.data_ptr(), page_table.stride(0), _int(self.max_pages),
             _int(self.num_pages), self.page_size)
+
+
+def _fp8_of(cache) -> Optional[fa_kv_fp8_t]:
+    """The scales of an 8-bit cache, None of a 16-bit one."""
+    return getattr(cache, "_fp8", None)
 
 
 def _int32_of(t, shape, device, name):
@@ -557,6 +642,16 @@ def _query_of(q, cache):
     if B != cache.B or D != cache.D or Hq % cache.Hkv:
         raise ValueError("q does not fit the cache: B, D or Hq % Hkv")
     return B, Hq, Sq, D
+
+
+def _answers_of(q, out, lse):
+    import torch
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or out.device != q.device
+                            or not out.is_contiguous()):
+        raise ValueError("out must be contiguous, of q's shape and type, on its device")
+    if lse is not None and (lse.shape != q.shape[:3] or lse.dtype != torch.float32
+                            or lse.device != q.device or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 tensor [B, Hq, Sq] on q's device")
 
 
 def _raw_here(device) -> Optional[int]:
@@ -584,15 +679,18 @@ def _elsewhere(device, stream, call):
 
 
 def paged_kv_append(cache: PagedKV, kv_lens, k, v, *, new_lens=None, q=None, q_out=None, cos=None,
-                    sin=None, interleaved: bool = False, stream=None):
-    """New tokens into a paged cache, rotated on the way (fa_kv_append).
+                    sin=None, interleaved: bool = False, positions=None, stream=None):
+    """New tokens into a paged cache, rotated on the way (fa_kv_append, fa_kv_append_ext).
 
     k, v [B, Hkv, S, D] of the cache's type, any strides with a contiguous last dimension; token i
     of sequence b takes position kv_lens[b] + i (kv_lens int32 [B], the tokens in the cache before;
     the caller adds the new ones).  new_lens: int32 [B], how many of the S are real (None: all).
     q [B, Hq, S, D]: rotated by the same positions into q_out (allocated where None; may be q).
     cos, sin: fp32 [max_pos, r / 2] of the rotated channels r <= D, r a multiple of 16; None: no
-    rotation.  interleaved: pairs (2j, 2j + 1) instead of (j, j + r / 2).
+    rotation.  interleaved: pairs (2j, 2j + 1) instead of (j, j + r / 2).  positions: int32 [B, S], by
+    which the tokens are rotated instead (a tree's drafts by their depth); where they are stored stays.
+    Into an 8-bit cache each row of D channels is quantised as it is written, with the scale that its
+    largest channel needs; a row that is not finite becomes NaN (FA_ERR_RANGE by fa_check_status).
     Updates cache.k_min / k_max where the cache has them (then no two sequences may append to one
     page).  Returns q_out (rows past new_lens as they were: undefined in an allocated one), or None
     without q.  A sequence's rows are its first new_lens[b], flash_attention_decode wants them as the
@@ -609,6 +707,8 @@ def paged_kv_append(cache: PagedKV, kv_lens, k, v, *, new_lens=None, q=None, q_o
     _int32_of(kv_lens, (B,), cache.device, "kv_lens")
     if new_lens is not None:
         _int32_of(new_lens, (B,), cache.device, "new_lens")
+    if positions is not None:
+        _int32_of(positions, (B, S), cache.device, "positions")
     if q is None:
         if q_out is not None:
             raise ValueError("q_out without q")
@@ -638,8 +738,13 @@ def paged_kv_append(cache: PagedKV, kv_lens, k, v, *, new_lens=None, q=None, q_o
         x = fa_kv_new_t(k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(qo), *k.stride()[:3], *v.stride()[:3],
                         *(none if q is None else q.stride()[:3]), *(none if q is None else qo.stride()[:3]),
                         _ptr(cos), _ptr(sin), rot, 1 if interleaved else 0, max_pos)
-        _raise(library().fa_kv_append(cache._c, x, B, Hq, Hkv, S, D, cache._flags, kv_lens.data_ptr(),
-                                      _ptr(new_lens), raw))
+        fp8 = _fp8_of(cache)
+        if fp8 is None and positions is None:
+            _raise(library().fa_kv_append(cache._c, x, B, Hq, Hkv, S, D, cache._flags, kv_lens.data_ptr(),
+                                          _ptr(new_lens), raw))
+        else:
+            _raise(library().fa_kv_append_ext(cache._c, fp8, x, B, Hq, Hkv, S, D, cache._flags, kv_lens.data_ptr(),
+                                              _ptr(new_lens), _ptr(positions), raw))
         return qo
 
     raw = _raw_here(cache.device) if stream is None else None
@@ -669,21 +774,116 @@ def flash_attention_decode(q, cache: PagedKV, kv_lens, *, scale: Optional[float]
         _int32_of(page_idx, (B, cache.Hkv, max_sel), cache.device, "page_idx")
     if pre_tokens is not None and pre_tokens < 0:
         raise ValueError("pre_tokens must be >= 0 (None: unbounded)")
-    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or out.device != q.device
-                            or not out.is_contiguous()):
-        raise ValueError("out must be contiguous, of q's shape and type, on its device")
-    if lse is not None and (lse.shape != (B, Hq, Sq) or lse.dtype != torch.float32
-                            or lse.device != q.device or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous fp32 tensor [B, Hq, Sq] on q's device")
+    _answers_of(q, out, lse)
 
     def call(raw):
         o = torch.empty_like(q) if out is None else out
         e = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device) if lse is None else lse
-        _raise(library().fa_decode(q.data_ptr(), cache._c, o.data_ptr(), e.data_ptr(), B, Hq, cache.Hkv,
-                                   Sq, D, 1.0 / math.sqrt(D) if scale is None else scale, cache._flags,
-                                   kv_lens.data_ptr(), -1 if pre_tokens is None else _int(pre_tokens),
-                                   _ptr(page_idx), max_sel, raw))
+        fp8 = _fp8_of(cache)
+        rest = (o.data_ptr(), e.data_ptr(), B, Hq, cache.Hkv, Sq, D, 1.0 / math.sqrt(D) if scale is None else scale,
+                cache._flags, kv_lens.data_ptr(), -1 if pre_tokens is None else _int(pre_tokens), _ptr(page_idx), max_sel)
+        _raise(library().fa_decode(q.data_ptr(), cache._c, *rest, raw) if fp8 is None else
+               library().fa_decode_ext(q.data_ptr(), cache._c, fp8, *rest, None, raw))
         return o, e
+
+    raw = _raw_here(cache.device) if stream is None else None
+    return _elsewhere(cache.device, stream, call) if raw is None else call(raw)
+
+
+def flash_attention_decode_tree(q, cache: PagedKV, kv_lens, ancestors, *, new_lens=None,
+                                scale: Optional[float] = None, out=None, lse=None, stream=None):
+    """Attention of each sequence's tree of drafted tokens over a paged cache (fa_decode_ext).
+
+    q [B, Hq, S, D] contiguous, of the cache's type: the drafts of each sequence, which are in the
+    cache already as its last new_lens[b] tokens (int32 [B]; None: S); kv_lens int32 [B], the tokens in
+    the cache, drafts included.  Row i < new_lens[b] is draft i, the token kv_lens[b] - new_lens[b] + i
+    (paged_kv_append leaves the rows so); it sees every token before the drafts, and of the drafts those
+    that row i of ancestors names: bool or uint8 [B, S, S], or [S, S] for one tree in every
+    sequence, True where draft i sees draft j (itself too, as a rule).  Rows past new_lens[b] are
+    padding: they are answered as rows that see the tokens before the drafts.
+    Returns (o, lse fp32 [B, Hq, S])."""
+    import torch
+    B, Hq, S, D = _query_of(q, cache)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    _int32_of(kv_lens, (B,), cache.device, "kv_lens")
+    if new_lens is not None:
+        _int32_of(new_lens, (B,), cache.device, "new_lens")
+    if (ancestors.dtype not in (torch.bool, torch.uint8) or ancestors.device != cache.device
+            or ancestors.shape not in ((S, S), (B, S, S))):
+        raise ValueError("ancestors must be bool or uint8 [B, S, S] or [S, S] on the cache's device")
+    each = ancestors[0] if ancestors.dim() == 3 else ancestors
+    if not each.is_contiguous():
+        raise ValueError("the trees of ancestors must be contiguous")
+    stride = ancestors.stride(0) if ancestors.dim() == 3 and B > 1 else 0
+    _answers_of(q, out, lse)
+
+    def call(raw):
+        o = torch.empty_like(q) if out is None else out
+        e = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device) if lse is None else lse
+        tree = fa_tree_t(ancestors.data_ptr(), stride, _ptr(new_lens))
+        _raise(library().fa_decode_ext(q.data_ptr(), cache._c, _fp8_of(cache), o.data_ptr(), e.data_ptr(), B, Hq,
+                                       cache.Hkv, S, D, 1.0 / math.sqrt(D) if scale is None else scale, cache._flags,
+                                       kv_lens.data_ptr(), -1, None, 0, tree, raw))
+        return o, e
+
+    raw = _raw_here(cache.device) if stream is None else None
+    return _elsewhere(cache.device, stream, call) if raw is None else call(raw)
+
+
+def paged_kv_read(cache: PagedKV, lens, *, starts=None, size: Optional[int] = None, k_out=None, v_out=None,
+                  stream=None):
+    """Tokens out of a paged cache into dense rows (fa_kv_read): row i < lens[b] of sequence b is its
+    token starts[b] + i (lens, starts int32 [B]; starts None: 0), of an 8-bit cache as the values that it
+    stands for.  Returns (k, v) [B, Hkv, S, D] of cache.dtype, any strides with a contiguous last
+    dimension: k_out and v_out where given, else allocated with S = size (rows past lens as they were:
+    undefined in allocated ones)."""
+    import torch
+    _int32_of(lens, (cache.B,), cache.device, "lens")
+    if starts is not None:
+        _int32_of(starts, (cache.B,), cache.device, "starts")
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out go together")
+    if (k_out is None) == (size is None):
+        raise ValueError("either size or k_out and v_out")
+    if k_out is None:
+        shape = (cache.B, cache.Hkv, operator.index(size), cache.D)
+    else:
+        shape = tuple(k_out.shape)
+        if len(shape) != 4 or v_out.shape != k_out.shape or (shape[0], shape[1], shape[3]) != (cache.B, cache.Hkv, cache.D):
+            raise ValueError("k_out and v_out must be [B, Hkv, S, D], of one shape, that of the cache")
+        for t in (k_out, v_out):
+            if t.dtype != cache.dtype or t.device != cache.device or t.stride(3) != 1:
+                raise ValueError("k_out and v_out must be of the cache's type, on its device, with a contiguous last dimension")
+
+    def call(raw):
+        k, v = ((torch.empty(shape, dtype=cache.dtype, device=cache.device) for _ in range(2)) if k_out is None
+                else (k_out, v_out))
+        rows = fa_kv_rows_t(k.data_ptr(), v.data_ptr(), *k.stride()[:3], *v.stride()[:3])
+        _raise(library().fa_kv_read(cache._c, _fp8_of(cache), rows, cache.B, cache.Hkv, shape[2], cache.D, cache._flags,
+                                    _ptr(starts), lens.data_ptr(), raw))
+        return k, v
+
+    raw = _raw_here(cache.device) if stream is None else None
+    return _elsewhere(cache.device, stream, call) if raw is None else call(raw)
+
+
+def paged_kv_keep(cache: PagedKV, kv_lens, keep_idx, keep_lens, *, stream=None):
+    """The accepted drafts of each sequence to the places behind the tokens before them (fa_kv_keep):
+    the token at kv_lens[b] + keep_idx[b, i] moves to kv_lens[b] + i for i < keep_lens[b], keys and
+    values as stored (with their scales), page bounds kept.  kv_lens int32 [B]: the tokens before the
+    drafts; keep_idx int32 [B, M], ascending in each sequence; keep_lens int32 [B].  The caller goes on
+    with kv_lens + keep_lens tokens."""
+    _int32_of(kv_lens, (cache.B,), cache.device, "kv_lens")
+    _int32_of(keep_lens, (cache.B,), cache.device, "keep_lens")
+    if keep_idx.dim() != 2:
+        raise ValueError("keep_idx must be [B, M]")
+    M = keep_idx.shape[1]
+    _int32_of(keep_idx, (cache.B, M), cache.device, "keep_idx")
+
+    def call(raw):
+        _raise(library().fa_kv_keep(cache._c, _fp8_of(cache), cache.B, cache.Hkv, cache.D, cache._flags,
+                                    kv_lens.data_ptr(), keep_idx.data_ptr(), _int(M), keep_lens.data_ptr(), raw))
 
     raw = _raw_here(cache.device) if stream is None else None
     return _elsewhere(cache.device, stream, call) if raw is None else call(raw)

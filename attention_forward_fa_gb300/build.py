@@ -10,7 +10,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfa_fwd.so")
-SOURCES = ["fa_fwd.cu", "fa_paged.cu"]
+SOURCES = ["fa_fwd.cu", "fa_paged.cu", "fa_paged8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -92,6 +92,11 @@ struct DecodeCore {
   float* part_o;               // [2 * ctas][8 NT][D], unnormalised: slot 2 c + 1 begins its unit
   float2* part_ml;             // [2 * ctas][8 NT]: reference (log2 units), sum
   long long timeout_ns;
+  // A tree of drafts: row i is draft i of the last new_lens[b] tokens and sees of them those that
+  // ancestors[b][i] names, and every token before; null: the rows are the newest tokens one after another.
+  const uint8_t* ancestors;    // [B, Sq, Sq]
+  long long anc_stride;        // of a sequence
+  const int32_t* new_lens;     // or null: Sq
 };
 struct DecodeParams {
   DecodeCore c;
@@ -127,14 +132,15 @@ struct DecodeSpan {
   int lo, hi, first, n;
   int listed;      // entries of the list that count
 };
+template <int TILE = kDecTile>
 __device__ __forceinline__ DecodeSpan decode_span(const DecodeCore& p, int len) {
   DecodeSpan s;
   s.hi = len;
   s.lo = p.reach >= 0 ? max(0, len - p.reach) : 0;
-  s.first = p.sel ? 0 : s.lo / kDecTile;
+  s.first = p.sel ? 0 : s.lo / TILE;
   s.listed = min(p.max_sel, (len + (1 << p.page_shift) - 1) >> p.page_shift);
   const int keys = p.sel ? s.listed << p.page_shift : len;
-  s.n = max(1, (keys + kDecTile - 1) / kDecTile - s.first);
+  s.n = max(1, (keys + TILE - 1) / TILE - s.first);
   return s;
 }
 __device__ __forceinline__ int decode_len(const DecodeCore& p, int b) {
@@ -143,8 +149,31 @@ __device__ __forceinline__ int decode_len(const DecodeCore& p, int b) {
   return len < 0 || len > p.max_len ? 0 : len;
 }
 
+// Drafts of a sequence's tree.
+__device__ __forceinline__ int decode_drafts(const DecodeCore& p, int b, int len) {
+  const int n = p.new_lens ? __ldcg(p.new_lens + b) : p.Sq;
+  return min(max(n, 0), min(p.Sq, len));
+}
+// Whether row i sees the key at position `key` >= base, the first draft's.
+__device__ __forceinline__ bool decode_ancestor(const DecodeCore& p, int b, int drafts, int i, int j) {
+  return i < drafts && j < drafts && p.ancestors[b * p.anc_stride + (long long)i * p.Sq + j] != 0;
+}
+// Lengths and numbers of drafts that the tables cannot hold are reported, once.
+__device__ __forceinline__ void decode_report(const DecodeCore& p) {
+  for (int i = threadIdx.x; i < p.B; i += 32 * kDecWarps) {
+    const int len = p.kv_lens[i];
+    bool bad = len < 0 || len > p.max_len;
+    if (p.ancestors && !bad) {
+      const int n = p.new_lens ? p.new_lens[i] : p.Sq;
+      bad = n < 0 || n > p.Sq || n > len;
+    }
+    if (bad) atomicOr(p.status, fa_host::kStatusIndex);
+  }
+}
+
 // The lengths and charges of sequences base + 32 i + lane: eight independent loads.
 constexpr int kChunks = 8;
+template <int TILE = kDecTile>
 __device__ __forceinline__ void decode_charges(const DecodeCore& p, int base, int lane, int (&len)[kChunks],
                                                int (&c)[kChunks]) {
 #pragma unroll
@@ -157,7 +186,7 @@ __device__ __forceinline__ void decode_charges(const DecodeCore& p, int base, in
   }
 #pragma unroll
   for (int i = 0; i < kChunks; ++i)
-    if (base + 32 * i + lane < p.B) c[i] = decode_span(p, len[i]).n + kUnitTiles;
+    if (base + 32 * i + lane < p.B) c[i] = decode_span<TILE>(p, len[i]).n + kUnitTiles;
 }
 // Sum over the warp of numbers below 2^59, in three pieces by the warp's reduction.
 __device__ __forceinline__ long long warp_sum(long long x) {
@@ -207,6 +236,103 @@ __device__ __forceinline__ DecodePiece decode_step(DecodeWalk& w, int n, int uni
   return d;
 }
 
+// This CTA's range of charged tiles and the sequence it starts in, by one warp.
+template <int TILE = kDecTile>
+__device__ __forceinline__ void decode_start(const DecodeCore& p, int lane, DecodeWalk* s_walk, int* s_len) {
+  int len[kChunks], c[kChunks];
+  int mine = 0, my_len = 0, inc;           // of the sequence `at + lane`, its chunk of 32 summed up
+  auto scan = [&](int x) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    return x;
+  };
+  long long total, start = 0, end = 0, first, before = 0;
+  int at = 0;
+  auto range = [&]() {
+    if ((int)blockIdx.x < decode_ctas(p, total)) {
+      start = decode_first(p, total, blockIdx.x);
+      end = decode_first(p, total, blockIdx.x + 1);
+    }
+    // in charges of one unit per sequence: the sequence is the last with at most so many before it
+    first = times_inverse(start, p.units_inv);
+  };
+  if (p.B <= 32) {
+    if (lane < p.B) {
+      my_len = decode_len(p, lane);
+      mine = decode_span<TILE>(p, my_len).n + kUnitTiles;
+    }
+    inc = scan(mine);
+    total = (long long)__shfl_sync(0xffffffffu, inc, 31) * p.units;
+    range();
+  } else {
+    long long sum = 0;
+    for (int base = 32 * kChunks; base < p.B; base += 32 * kChunks) {
+      decode_charges<TILE>(p, base, lane, len, c);
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) sum += c[i];
+    }
+    decode_charges<TILE>(p, 0, lane, len, c);         // (kept for the search)
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) sum += c[i];
+    total = warp_sum(sum) * p.units;
+    range();
+    at = -1;
+    for (int base = 0; at < 0; base += 32 * kChunks) {
+      if (base) decode_charges<TILE>(p, base, lane, len, c);
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        if (at >= 0) break;
+        const int in = __reduce_add_sync(0xffffffffu, (unsigned)c[i]);   // (32 of at most 2^25 + 2)
+        if (before + in > first || base + 32 * (i + 1) >= p.B) at = base + 32 * i, mine = c[i], my_len = len[i];
+        else before += in;
+      }
+    }
+    inc = scan(mine);
+  }
+  const unsigned here = __ballot_sync(0xffffffffu, mine > 0 && before + inc - mine <= first);
+  if (lane == 31 - __clz(here)) {
+    const long long off = start - (before + inc - mine) * p.units;
+    const int unit = (int)quotient(off, mine);
+    *s_walk = DecodeWalk{at + lane, unit, (int)(off - (long long)unit * mine), end - start};
+    *s_len = my_len;
+  }
+}
+
+// Sub-block c of a unit's tiles (2^box_shift keys; those from `end` on are another's): its page, first
+// slot and first key; id and key -1 where nothing of it is to be copied.
+template <int TILE = kDecTile>
+__device__ __forceinline__ void decode_look_up(const DecodeCore& p, const DecodeSpan& s, int b, int hk, int n_pages, int c,
+                                               int end, int box_shift, int& id, int& slot, int& key) {
+  id = -1, slot = 0, key = -1;
+  if (c >= end) return;
+  int page;
+  if (p.sel) {
+    const int spp = p.page_shift - box_shift;    // log2 sub-blocks per page
+    const int at = c >> spp;
+    if (at >= s.listed) return;
+    page = p.sel[((long long)b * p.Hkv + hk) * p.max_sel + at];
+    if (page < 0 || page >= n_pages) return;
+    slot = (c & ((1 << spp) - 1)) << box_shift;
+    key = (page << p.page_shift) + slot;
+  } else {
+    key = s.first * TILE + (c << box_shift);
+    page = key >> p.page_shift;
+    slot = key & ((1 << p.page_shift) - 1);
+  }
+  if (key >= s.hi || key + (1 << box_shift) <= s.lo) {   // (also any key of an empty sequence)
+    key = -1;
+    return;
+  }
+  id = p.table[(long long)b * p.table_stride + page];
+  if (id < 0 || id >= p.num_pages) {
+    atomicOr(p.status, fa_host::kStatusIndex);
+    id = key = -1;
+  }
+}
+
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, uint32_t bar, int slot,
                                             int head, int page) {
   asm volatile(
@@ -248,7 +374,9 @@ __device__ __forceinline__ void mma_16x8(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <bool BF16, int D, int NT>
+// TREE: the rows are a tree of drafts.  (Asked at run time instead, the plain form with 128 channels
+// and 48 rows spilled 48 bytes instead of 12.)
+template <bool BF16, int D, int NT, bool TREE = false>
 __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(const __grid_constant__ DecodeParams params) {
   const DecodeCore& p = params.c;
   using SM = DecodeSmem<D, NT>;
@@ -278,68 +406,9 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
   pdl_wait_prior();
   pdl_launch_dependents();
   if (warp == kDecWarps) {   // this CTA's range of charged tiles, and the sequence it starts in
-    int len[kChunks], c[kChunks];
-    int mine = 0, my_len = 0, inc;           // of the sequence `at + lane`, its chunk of 32 summed up
-    auto scan = [&](int x) {
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
-      }
-      return x;
-    };
-    long long total, start = 0, end = 0, first, before = 0;
-    int at = 0;
-    auto range = [&]() {
-      if ((int)blockIdx.x < decode_ctas(p, total)) {
-        start = decode_first(p, total, blockIdx.x);
-        end = decode_first(p, total, blockIdx.x + 1);
-      }
-      // in charges of one unit per sequence: the sequence is the last with at most so many before it
-      first = times_inverse(start, p.units_inv);
-    };
-    if (p.B <= 32) {
-      if (lane < p.B) {
-        my_len = decode_len(p, lane);
-        mine = decode_span(p, my_len).n + kUnitTiles;
-      }
-      inc = scan(mine);
-      total = (long long)__shfl_sync(0xffffffffu, inc, 31) * p.units;
-      range();
-    } else {
-      long long sum = 0;
-      for (int base = 32 * kChunks; base < p.B; base += 32 * kChunks) {
-        decode_charges(p, base, lane, len, c);
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) sum += c[i];
-      }
-      decode_charges(p, 0, lane, len, c);         // (kept for the search)
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i) sum += c[i];
-      total = warp_sum(sum) * p.units;
-      range();
-      at = -1;
-      for (int base = 0; at < 0; base += 32 * kChunks) {
-        if (base) decode_charges(p, base, lane, len, c);
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-          if (at >= 0) break;
-          const int in = __reduce_add_sync(0xffffffffu, (unsigned)c[i]);   // (32 of at most 2^25 + 2)
-          if (before + in > first || base + 32 * (i + 1) >= p.B) at = base + 32 * i, mine = c[i], my_len = len[i];
-          else before += in;
-        }
-      }
-      inc = scan(mine);
-    }
-    const unsigned here = __ballot_sync(0xffffffffu, mine > 0 && before + inc - mine <= first);
-    if (lane == 31 - __clz(here)) {
-      const long long off = start - (before + inc - mine) * p.units;
-      const int unit = (int)quotient(off, mine);
-      *s_walk = DecodeWalk{at + lane, unit, (int)(off - (long long)unit * mine), end - start};
-      *s_len = my_len;
-    }
-  } else if (blockIdx.x == 0) {   // lengths that the tables cannot hold are reported once
-    for (int i = threadIdx.x; i < p.B; i += 32 * kDecWarps) if (const int len = p.kv_lens[i]; len < 0 || len > p.max_len) atomicOr(p.status, fa_host::kStatusIndex);
+    decode_start(p, lane, s_walk, s_len);
+  } else if (blockIdx.x == 0) {
+    decode_report(p);
   }
   __syncthreads();
   DecodeWalk walk = *s_walk;
@@ -361,33 +430,8 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
       if (walk.b != b && walk.left > 0) len = decode_len(p, walk.b);
       const int t0 = d.t0, nt = d.nt;
       const int n_pages = (s.hi + (1 << p.page_shift) - 1) >> p.page_shift;
-      // Lane i looks up sub-block c0 + i of the unit (box keys each): page, first slot, first key.
       auto look_up = [&](int c, int& id, int& slot, int& key) {
-        id = -1, slot = 0, key = -1;
-        if (c >= (t0 + nt) * nsub) return;
-        int page;
-        if (p.sel) {
-          const int spp = p.page_shift - box_shift;    // log2 sub-blocks per page
-          const int at = c >> spp;
-          if (at >= s.listed) return;
-          page = p.sel[((long long)b * p.Hkv + hk) * p.max_sel + at];
-          if (page < 0 || page >= n_pages) return;
-          slot = (c & ((1 << spp) - 1)) << box_shift;
-          key = (page << p.page_shift) + slot;
-        } else {
-          key = s.first * kDecTile + (c << box_shift);
-          page = key >> p.page_shift;
-          slot = key & ((1 << p.page_shift) - 1);
-        }
-        if (key >= s.hi || key + box <= s.lo) {           // (also any key of an empty sequence)
-          key = -1;
-          return;
-        }
-        id = p.table[(long long)b * p.table_stride + page];
-        if (id < 0 || id >= p.num_pages) {
-          atomicOr(p.status, fa_host::kStatusIndex);
-          id = key = -1;
-        }
+        decode_look_up(p, s, b, hk, n_pages, c, (t0 + nt) * nsub, box_shift, id, slot, key);
       };
       int id, slot, key, id2 = -1, slot2 = 0, key2 = -1;
       const int per = 32 / nsub;                          // tiles per look-up
@@ -493,7 +537,9 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
 #pragma unroll
         for (int k2 = 0; k2 < KS / 2; ++k2) qf[n][k2] = load_q(n, k2);
     }
-    const int tok_min = len - p.Sq;                                       // the first row's token
+    const int drafts = TREE ? decode_drafts(p, b, len) : 0;
+    // the first row's token; the last before a tree, that all its rows see
+    const int tok_min = TREE ? len - drafts - 1 : len - p.Sq;
     const int low_max = p.pre_tokens >= 0 ? len - 1 - p.pre_tokens : 0;   // lowest key that all rows see
 
     float o[NT][DT][4], m[NT][2], l[NT][2];
@@ -549,8 +595,13 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = key0 + g + 8 * (e >> 1);
-            const int t = tok_min + (p.Sq == 1 ? 0 : (rg * 8 * NT + n * 8 + 2 * t4 + (e & 1)) % p.Sq);
-            if (key > t || (p.pre_tokens >= 0 && key < t - p.pre_tokens)) c[n][e] = -INFINITY;
+            const int i = p.Sq == 1 ? 0 : (rg * 8 * NT + n * 8 + 2 * t4 + (e & 1)) % p.Sq;
+            if constexpr (TREE) {
+              if (key > tok_min && !decode_ancestor(p, b, drafts, i, key - tok_min - 1)) c[n][e] = -INFINITY;
+            } else {
+              const int t = tok_min + i;
+              if (key > t || (p.pre_tokens >= 0 && key < t - p.pre_tokens)) c[n][e] = -INFINITY;
+            }
           }
       }
 #pragma unroll
@@ -746,7 +797,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
 // it alone (the same bits every time).  WPR warps per row: 1 where there are many
 // rows, 8 where there are few, 32 where a unit may have so many pieces (one KV
 // head over 131072 tokens has one per CTA, 304).
-template <bool BF16, int D, int WPR>
+template <bool BF16, int D, int WPR, int TILE = kDecTile>
 __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) fa_decode_join_kernel(const __grid_constant__ DecodeCore p, int rows8) {
   constexpr int kWarps = WPR > 8 ? WPR : 8;
   __shared__ __align__(16) float s_o[WPR][D];
@@ -766,7 +817,7 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) fa_decode_join_kerne
   long long total = 0, before = 0;
   auto add_up = [&](int base, int end) {                 // charges of 256 sequences, and of those before `end`
     int len[kChunks], c[kChunks];
-    decode_charges(p, base, lane, len, c);
+    decode_charges<TILE>(p, base, lane, len, c);
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
       total += c[i];
@@ -786,13 +837,13 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) fa_decode_join_kerne
     if (lane == 0) s_sum[warp][0] = total, s_sum[warp][1] = before;
     __syncthreads();
     total = warp_sum(lane < kWarps ? s_sum[lane][0] : 0);
-    before = (lane < kWarps ? s_sum[lane][1] : 0) + (b0 + lane < b ? decode_span(p, decode_len(p, b0 + lane)).n + kUnitTiles : 0);
+    before = (lane < kWarps ? s_sum[lane][1] : 0) + (b0 + lane < b ? decode_span<TILE>(p, decode_len(p, b0 + lane)).n + kUnitTiles : 0);
     before = warp_sum(before);                           // (b - b0 is less than the block's 8 rows)
   }
   if (none) return;
   total *= p.units;
   const int ctas = decode_ctas(p, total);
-  const int n = decode_span(p, decode_len(p, b)).n;
+  const int n = decode_span<TILE>(p, decode_len(p, b)).n;
   const long long t0 = before * p.units + (long long)(hk * p.groups + rg) * (n + kUnitTiles) + kUnitTiles;
   const int c0 = decode_owner(total, ctas, t0), c1 = decode_owner(total, ctas, t0 + n - 1);
   pdl_wait_prior();

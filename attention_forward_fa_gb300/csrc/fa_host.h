@@ -11,6 +11,7 @@
 
 namespace fa_host {
 
+constexpr int kStatusRange = 2;   // a value outside what its format holds
 constexpr int kStatusIndex = 4;   // a page id, length or position out of range met by a paged call
 
 int* status_ptr();                                        // device status word of the current device

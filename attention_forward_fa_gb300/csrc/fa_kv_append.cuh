@@ -20,6 +20,7 @@
 #include <type_traits>
 
 #include "fa_paged.cuh"
+#include "fa_paged8.cuh"
 
 namespace fa {
 
@@ -46,13 +47,21 @@ struct AppendParams {
   int q_heads;             // heads per block of the Q blocks (the K and V blocks: those of one step)
   int k_items, q_items;    // blocks per page for K (V as many), for Q
   int* status;
+  const int32_t* positions;   // [B, Snew] or null (kAppendPlaced, kAppend8)
+  uint8_t* k_scale;           // [num_pages, Hkv, page size] (kAppend8: kv.k and kv.v are codes)
+  uint8_t* v_scale;
+  int e5m2;                   // codes of e5m2 instead of e4m3
 };
+
+// FORM: a 16-bit cache with tokens turned by where they stand (kAppendPlain) or by positions that are
+// given (kAppendPlaced), or an 8-bit cache (kAppend8, positions given or not).
+constexpr int kAppendPlain = 0, kAppendPlaced = 1, kAppend8 = 2;
 
 // A piece of the work: one page of one sequence (`rest`), some heads (`item`) of its K, V or Q.  KIND: which
 // of the three, or kAppendAny by the item (one way for all up to the tokens' loads: a copy for each kind
 // takes a call of few tokens 0.1 us longer, on its way through the instruction cache).
 constexpr int kAppendK = 0, kAppendV = 1, kAppendQ = 2, kAppendAny = 3;
-template <bool BF16, int D, bool INTERLEAVED, int KIND>
+template <bool BF16, int D, bool INTERLEAVED, int KIND, int FORM>
 __device__ __forceinline__ void append_piece(const AppendParams& p, int item, int rest) {
   constexpr int L = D / 16;                    // threads per row
   constexpr int kRows = kAppendThreads / L;    // rows per step
@@ -84,7 +93,8 @@ __device__ __forceinline__ void append_piece(const AppendParams& p, int item, in
     atomicOr(p.status, fa_host::kStatusIndex);
     return true;
   };
-  if (p.rot_dim && t1 > p.max_pos) {
+  const bool placed = FORM != kAppendPlain && p.positions != nullptr;
+  if (p.rot_dim && !placed && t1 > p.max_pos) {
     if (threadIdx.x == 0) atomicOr(p.status, fa_host::kStatusIndex);
     t1 = p.max_pos;
     if (t0 >= t1) return;
@@ -100,6 +110,15 @@ __device__ __forceinline__ void append_piece(const AppendParams& p, int item, in
   const int offB = halves ? 8 * part + p.rot_dim / 2 : 16 * part + 8;
   const int half = p.rot_dim / 2;
 
+  // the position that token t is turned by; -1 (reported, the token is left out) where it has no row
+  auto position = [&](int t) {
+    if (!placed || p.rot_dim == 0) return t;
+    const int at = p.positions[(long long)b * p.Snew + (t - before)];
+    if (at >= 0 && at < p.max_pos) return at;
+    atomicOr(p.status, fa_host::kStatusIndex);
+    return -1;
+  };
+
   float c[8], s[8];
   auto angles = [&](int t) {
     if (!turns) return;
@@ -109,12 +128,7 @@ __device__ __forceinline__ void append_piece(const AppendParams& p, int item, in
     c[0] = c0.x; c[1] = c0.y; c[2] = c0.z; c[3] = c0.w; c[4] = c1.x; c[5] = c1.y; c[6] = c1.z; c[7] = c1.w;
     s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w; s[4] = s1.x; s[5] = s1.y; s[6] = s1.z; s[7] = s1.w;
   };
-  // in fp32, each channel rounded once to the cache's type
-  auto rotate = [&](uint4& wa, uint4& wb) {
-    if (!turns) return;
-    float a[8], d[8];
-    unpack8<BF16>(wa, a);
-    unpack8<BF16>(wb, d);
+  auto turn = [&](float (&a)[8], float (&d)[8]) {
     if constexpr (INTERLEAVED) {
       float x[16];
 #pragma unroll
@@ -135,6 +149,14 @@ __device__ __forceinline__ void append_piece(const AppendParams& p, int item, in
         d[j] = e * s[j] + o * c[j];
       }
     }
+  };
+  // in fp32, each channel rounded once to the cache's type
+  auto rotate = [&](uint4& wa, uint4& wb) {
+    if (!turns) return;
+    float a[8], d[8];
+    unpack8<BF16>(wa, a);
+    unpack8<BF16>(wb, d);
+    turn(a, d);
     wa = pack8<BF16>(a);
     wb = pack8<BF16>(d);
   };
@@ -149,7 +171,9 @@ __device__ __forceinline__ void append_piece(const AppendParams& p, int item, in
     for (int t = t0 + tl; t < t1; t += tp) {
       const uint16_t* src = p.q + b * p.q_sb + (long long)(t - before) * p.q_ss;
       uint16_t* dst = p.qo + b * p.o_sb + (long long)(t - before) * p.o_ss;
-      angles(t);
+      const int at = position(t);
+      if (FORM != kAppendPlain && at < 0) continue;
+      angles(at);
       for (int h = h0 + hl; h < h1; h += kBatch * hp) {
         uint4 wa[kBatch], wb[kBatch];
 #pragma unroll
@@ -184,10 +208,28 @@ __device__ __forceinline__ void append_piece(const AppendParams& p, int item, in
         wb[i] = ld(x + 8);
       }
       if (no_page()) return;
+      if constexpr (FORM == kAppend8) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          if (t + i * tp >= t1) break;
+          if (position(t + i * tp) < 0) continue;
+          float a[8], d[8];
+          unpack8<BF16>(wa[i], a);
+          unpack8<BF16>(wb[i], d);
+          const int slot = (t + i * tp) & (ps - 1);
+          uint2 qa, qd;
+          const uint32_t scale = quantise_row<L>(a, d, p.e5m2 != 0, qa, qd, p.status);
+          uint8_t* y = reinterpret_cast<uint8_t*>(p.kv.v) + (long long)id * p.kv.v_sp + h * p.kv.v_sh + (long long)slot * p.kv.v_ss;
+          *reinterpret_cast<uint4*>(y + 16 * part) = make_uint4(qa.x, qa.y, qd.x, qd.y);
+          if (part == 0) p.v_scale[(((long long)id * p.Hkv + h) << ps_shift) + slot] = (uint8_t)scale;
+        }
+        continue;
+      }
       uint16_t* dst = p.kv.v + (long long)id * p.kv.v_sp + h * p.kv.v_sh + 16 * part;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         if (t + i * tp >= t1) break;
+        if (FORM != kAppendPlain && position(t + i * tp) < 0) continue;
         uint16_t* y = dst + (long long)((t + i * tp) & (ps - 1)) * p.kv.v_ss;
         st(y, wa[i]);
         st(y + 8, wb[i]);
@@ -217,7 +259,31 @@ __device__ __forceinline__ void append_piece(const AppendParams& p, int item, in
     for (int t = t0 + tl; t < t1; t += tp) {
       const uint16_t* x = src + (long long)(t - before) * p.k_ss;
       uint4 wa = ld(x + offA), wb = ld(x + offB);
-      angles(t);
+      const int at = position(t);
+      if (FORM != kAppendPlain && at < 0) continue;
+      angles(at);
+      if constexpr (FORM == kAppend8) {
+        float a[8], d[8];
+        unpack8<BF16>(wa, a);
+        unpack8<BF16>(wb, d);
+        if (turns) turn(a, d);
+        if (no_page()) break;
+        const int slot = t & (ps - 1);
+        uint2 qa, qd;
+        const uint32_t scale = quantise_row<L>(a, d, p.e5m2 != 0, qa, qd, p.status);
+        uint8_t* y = reinterpret_cast<uint8_t*>(p.kv.k) + (long long)id * p.kv.k_sp + h * p.kv.k_sh + (long long)slot * p.kv.k_ss;
+        *reinterpret_cast<uint2*>(y + offA) = qa;
+        *reinterpret_cast<uint2*>(y + offB) = qd;
+        if (part == 0) p.k_scale[(((long long)id * p.Hkv + h) << ps_shift) + slot] = (uint8_t)scale;
+        if (p.kv.k_min) {
+          uint4 lo, hi;
+          stored_bounds<BF16>(qa, scale, p.e5m2 != 0, lo, hi);
+          widen(0, lo, hi);
+          stored_bounds<BF16>(qd, scale, p.e5m2 != 0, lo, hi);
+          widen(1, lo, hi);
+        }
+        continue;
+      }
       rotate(wa, wb);
       if (no_page()) break;
       uint16_t* y = p.kv.k + (long long)id * p.kv.k_sp + h * p.kv.k_sh + (long long)(t & (ps - 1)) * p.kv.k_ss;
@@ -279,14 +345,14 @@ __device__ __forceinline__ void append_piece(const AppendParams& p, int item, in
 // pages of 16, one of them that long and the others one token: 24.5 and 117 us; all of one token 9.8
 // and 104 us.  16 blocks per SM: 132, 24.2 and 8.0 us; 64: 127, 30.5 and 15.6.  Just below the limit a
 // block per piece is ahead: the four prompts above 33.0 us, looping 34.2.)
-template <bool BF16, int D, bool INTERLEAVED, bool MANY>
+template <bool BF16, int D, bool INTERLEAVED, bool MANY, int FORM = kAppendPlain>
 __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const AppendParams p, int pieces) {
   pdl_launch_dependents();
   pdl_wait_prior();
   const unsigned items = 2 * p.k_items + p.q_items;
   const int item = (int)(blockIdx.x % items);
   if constexpr (!MANY) {
-    append_piece<BF16, D, INTERLEAVED, kAppendAny>(p, item, (int)(blockIdx.x / items));
+    append_piece<BF16, D, INTERLEAVED, kAppendAny, FORM>(p, item, (int)(blockIdx.x / items));
   } else {
     auto loop = [&](auto kind) {
       constexpr int KIND = decltype(kind)::value;
@@ -303,7 +369,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const A
         }
 #pragma unroll 1
         for (unsigned live = __ballot_sync(0xffffffffu, some); live; live &= live - 1) {
-          append_piece<BF16, D, INTERLEAVED, KIND>(p, item, (int)(at0 + step * (__ffs(live) - 1)));
+          append_piece<BF16, D, INTERLEAVED, KIND, FORM>(p, item, (int)(at0 + step * (__ffs(live) - 1)));
           if constexpr (KIND == kAppendK) __syncthreads();   // (its shared memory)
         }
       }

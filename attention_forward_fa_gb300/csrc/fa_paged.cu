@@ -8,12 +8,14 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 #include <utility>
 
 #include "../../include/fa_fwd.h"
 #include "fa_decode.cuh"
 #include "fa_host.h"
 #include "fa_kv_append.cuh"
+#include "fa_paged_launch.h"
 #include "fa_select.cuh"
 
 namespace {
@@ -44,23 +46,28 @@ int validate_cache(const fa_paged_kv_t* kv, int B, int Hq, int Hkv, int S, int D
 }
 
 // A stride that steps over `n` things: refused where negative, 0 (things would share memory) or not
-// a multiple of 8; of no meaning, and any, where there is one thing only.
-int validate_stride(int64_t s, int64_t n, bool may_share) {
+// a multiple of `unit`; of no meaning, and any, where there is one thing only.
+int validate_stride(int64_t s, int64_t n, bool may_share, int unit = 8) {
   if (n <= 1) return FA_OK;
   if (s < 0 || s >= (1LL << 38) || (s == 0 && !may_share)) return FA_ERR_SHAPE;
-  return s % 8 ? FA_ERR_ALIGN : FA_OK;
+  return s % unit ? FA_ERR_ALIGN : FA_OK;
 }
 
-// The pools: bases and strides.
-int validate_pools(const fa_paged_kv_t* kv, int Hkv) {
+// The pools: bases and strides (rows start on 16 bytes), and what an 8-bit cache has besides.
+int validate_pools(const fa_paged_kv_t* kv, int Hkv, const fa_kv_fp8_t* fp8 = nullptr) {
   if (!kv->k || !kv->v) return FA_ERR_NULL;
   int rc = FA_OK;
   for (const auto& [s, n] : {std::pair<int64_t, int64_t>{kv->k_stride_page, kv->num_pages}, {kv->v_stride_page, kv->num_pages},
                              {kv->k_stride_head, Hkv}, {kv->v_stride_head, Hkv},
                              {kv->k_stride_slot, kv->page_size}, {kv->v_stride_slot, kv->page_size}})
-    if (rc == FA_OK) rc = validate_stride(s, n, false);
+    if (rc == FA_OK) rc = validate_stride(s, n, false, fp8 ? 16 : 8);
   if (rc != FA_OK) return rc;
   if (!aligned(kv->k, 16) || !aligned(kv->v, 16)) return FA_ERR_ALIGN;
+  if (fp8) {
+    if (!fp8->k_scale || !fp8->v_scale) return FA_ERR_NULL;
+    if (fp8->format != FA_FP8_E4M3 && fp8->format != FA_FP8_E5M2) return FA_ERR_SHAPE;
+    if (!aligned(fp8->k_scale, 16) || !aligned(fp8->v_scale, 16)) return FA_ERR_ALIGN;
+  }
   return FA_OK;
 }
 
@@ -85,23 +92,6 @@ fa::PagedKv device_cache(const fa_paged_kv_t* kv) {
   return c;
 }
 
-template <bool BF16, int D, bool INTERLEAVED>
-cudaError_t launch_append(const fa::AppendParams& p, long long pieces, cudaStream_t st) {
-  const int sms = fa_host::sm_count();
-  if (sms <= 0) return cudaErrorInvalidDevice;
-  const long long items = 2LL * p.k_items + p.q_items;
-  const long long loop = std::max(1LL, (long long)fa::kAppendLoopBlocks * sms / items) * items;   // (an item per block)
-  return pieces > (long long)fa::kAppendBlocks * sms
-             ? launch_dependent(fa::fa_kv_append_kernel<BF16, D, INTERLEAVED, true>, (unsigned)loop,
-                                fa::kAppendThreads, 0, st, p, (int)pieces)
-             : launch_dependent(fa::fa_kv_append_kernel<BF16, D, INTERLEAVED, false>, (unsigned)pieces,
-                                fa::kAppendThreads, 0, st, p, (int)pieces);
-}
-template <bool BF16, int D>
-cudaError_t launch_append(const fa::AppendParams& p, bool interleaved, long long pieces, cudaStream_t st) {
-  return interleaved ? launch_append<BF16, D, true>(p, pieces, st) : launch_append<BF16, D, false>(p, pieces, st);
-}
-
 // 5-D view (64 channels, slots, D / 64, heads, pages) of a pool, in boxes of
 // one page's and head's `box` slots with all channels, 128-byte swizzle: in
 // shared memory [D / 64][box][64].
@@ -123,9 +113,26 @@ bool encode_pool(CUtensorMap* tm, const void* base, bool fp16, int D, int Hkv, c
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool BF16, int D, int NT>
+// 4-D view (D bytes, slots, heads, pages) of an 8-bit pool, in boxes of `box` slots' rows, swizzled over
+// the row.
+bool encode_pool8(CUtensorMap* tm, const void* base, int D, int Hkv, const fa_paged_kv_t* kv, int64_t s_page,
+                  int64_t s_head, int64_t s_slot, int box) {
+  auto enc = fa_host::tensor_map_encoder();
+  if (!enc) return false;
+  if (Hkv == 1) s_head = 128;
+  if (kv->num_pages == 1) s_page = 128;
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)kv->page_size, (cuuint64_t)Hkv, (cuuint64_t)kv->num_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)s_slot, (cuuint64_t)s_head, (cuuint64_t)s_page};
+  cuuint32_t boxes[4] = {(cuuint32_t)D, (cuuint32_t)box, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, boxes, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool BF16, int D, int NT, bool TREE>
 int launch_decode(fa::DecodeParams& p, long long most_tiles, cudaStream_t st) {
-  auto kern = fa::fa_decode_kernel<BF16, D, NT>;
+  auto kern = fa::fa_decode_kernel<BF16, D, NT, TREE>;
   constexpr int smem = fa::DecodeSmem<D, NT>::kBytes;
   int dev = 0;
   cudaGetDevice(&dev);
@@ -160,7 +167,7 @@ int launch_decode(fa::DecodeParams& p, long long most_tiles, cudaStream_t st) {
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
-template <bool BF16, int D>
+template <bool BF16, int D, bool TREE>
 int launch_decode_rows(fa::DecodeParams& p, long long tiles_per_unit, cudaStream_t st) {
   // As few passes over the keys as 48 rows each allow, and as few columns of 8 as then hold a pass's
   // rows.  Up to 32 rows the time is that of the keys, past that the matrix instructions', about 1.4
@@ -175,12 +182,12 @@ int launch_decode_rows(fa::DecodeParams& p, long long tiles_per_unit, cudaStream
   c.units = c.Hkv * c.groups;
   const long long most = (tiles_per_unit + fa::kUnitTiles) * c.B * c.units;
   switch (nt) {
-    case 1: return launch_decode<BF16, D, 1>(p, most, st);
-    case 2: return launch_decode<BF16, D, 2>(p, most, st);
-    case 3: return launch_decode<BF16, D, 3>(p, most, st);
-    case 4: return launch_decode<BF16, D, 4>(p, most, st);
-    case 5: return launch_decode<BF16, D, 5>(p, most, st);
-    default: return launch_decode<BF16, D, 6>(p, most, st);
+    case 1: return launch_decode<BF16, D, 1, TREE>(p, most, st);
+    case 2: return launch_decode<BF16, D, 2, TREE>(p, most, st);
+    case 3: return launch_decode<BF16, D, 3, TREE>(p, most, st);
+    case 4: return launch_decode<BF16, D, 4, TREE>(p, most, st);
+    case 5: return launch_decode<BF16, D, 5, TREE>(p, most, st);
+    default: return launch_decode<BF16, D, 6, TREE>(p, most, st);
   }
 }
 
@@ -204,16 +211,12 @@ int launch_select(fa::SelectParams& p, long long units, cudaStream_t st) {
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
-}  // namespace
-
-extern "C" {
-
-int fa_kv_append(const fa_paged_kv_t* kv, const fa_kv_new_t* x, int B, int Hq, int Hkv, int Snew,
-                 int D, int mask_mode, const int32_t* kv_lens, const int32_t* new_lens,
-                 void* stream) {
+int append_call(const fa_paged_kv_t* kv, const fa_kv_fp8_t* fp8, const fa_kv_new_t* x, int B, int Hq, int Hkv,
+                int Snew, int D, int mask_mode, const int32_t* kv_lens, const int32_t* new_lens,
+                const int32_t* positions, void* stream) {
   if (!x) return FA_ERR_NULL;
   int rc = validate_cache(kv, B, Hq, Hkv, Snew, D, mask_mode);
-  if (rc == FA_OK) rc = validate_pools(kv, Hkv);
+  if (rc == FA_OK) rc = validate_pools(kv, Hkv, fp8);
   if (rc != FA_OK) return rc;
   if ((long long)B * (x->q ? Hq : Hkv) > kMostRows / Snew) return FA_ERR_SHAPE;
   if (!x->k || !x->v || !kv_lens || (x->q == nullptr) != (x->q_out == nullptr)) return FA_ERR_NULL;
@@ -239,7 +242,7 @@ int fa_kv_append(const fa_paged_kv_t* kv, const fa_kv_new_t* x, int B, int Hq, i
     return FA_ERR_SHAPE;
   if (!aligned(x->k, 16) || !aligned(x->v, 16) || !aligned(x->q, 16) || !aligned(x->q_out, 16) ||
       (x->rot_dim && (!aligned(x->cos, 16) || !aligned(x->sin, 16))) || !aligned(kv_lens, 4) ||
-      !aligned(new_lens, 4))
+      !aligned(new_lens, 4) || !aligned(positions, 4))
     return FA_ERR_ALIGN;
 
   fa::AppendParams p;
@@ -278,17 +281,23 @@ int fa_kv_append(const fa_paged_kv_t* kv, const fa_kv_new_t* x, int B, int Hq, i
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool fp16 = (mask_mode & FA_DTYPE_FP16) != 0;
   const bool il = x->interleaved != 0;
-  const cudaError_t e =
-      D == 128 ? (fp16 ? launch_append<false, 128>(p, il, pieces, st) : launch_append<true, 128>(p, il, pieces, st))
-               : (fp16 ? launch_append<false, 64>(p, il, pieces, st) : launch_append<true, 64>(p, il, pieces, st));
+  if (fp8) {
+    p.k_scale = fp8->k_scale;
+    p.v_scale = fp8->v_scale;
+    p.e5m2 = fp8->format == FA_FP8_E5M2;
+  }
+  p.positions = positions;
+  const cudaError_t e = fp8 ? fa_host::launch_append8(p, fp16, D, il, pieces, st)
+                        : positions ? fa_host::launch_append_placed(p, fp16, D, il, pieces, st)
+                                    : fa_host::launch_append<fa::kAppendPlain>(p, fp16, D, il, pieces, st);
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
-int fa_decode(const void* q, const fa_paged_kv_t* kv, void* o, float* lse, int B, int Hq, int Hkv,
-              int Sq, int D, float scale, int mask_mode, const int32_t* kv_lens, int pre_tokens,
-              const int32_t* page_idx, int max_sel, void* stream) {
+int decode_call(const void* q, const fa_paged_kv_t* kv, const fa_kv_fp8_t* fp8, void* o, float* lse, int B, int Hq,
+                int Hkv, int Sq, int D, float scale, int mask_mode, const int32_t* kv_lens, int pre_tokens,
+                const int32_t* page_idx, int max_sel, const fa_tree_t* tree, void* stream) {
   int rc = validate_cache(kv, B, Hq, Hkv, Sq, D, mask_mode);
-  if (rc == FA_OK) rc = validate_pools(kv, Hkv);
+  if (rc == FA_OK) rc = validate_pools(kv, Hkv, fp8);
   if (rc != FA_OK) return rc;
   if (!q || !o || !lse || !kv_lens) return FA_ERR_NULL;
   const float scale_log2 = scale * 1.4426950408889634f;
@@ -297,14 +306,31 @@ int fa_decode(const void* q, const fa_paged_kv_t* kv, void* o, float* lse, int B
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(kv_lens, 4) || !aligned(page_idx, 4))
     return FA_ERR_ALIGN;
   if ((long long)B * Hq > kMostRows / Sq) return FA_ERR_SHAPE;
+  if (tree) {
+    if (!tree->ancestors) return FA_ERR_NULL;
+    if (pre_tokens >= 0 || page_idx) return FA_ERR_UNSUPPORTED;
+    if (tree->stride_b < 0) return FA_ERR_SHAPE;
+    if (!aligned(tree->new_lens, 4)) return FA_ERR_ALIGN;
+  }
+  fa::Decode8Params p8;
   fa::DecodeParams p;
   std::memset(&p, 0, sizeof(p));
   const bool fp16 = (mask_mode & FA_DTYPE_FP16) != 0;
+  if (fp8) {
+    std::memset(&p8, 0, sizeof(p8));
+    const int box = std::min(kv->page_size, fa::kDec8Tile);
+    if (!encode_pool8(&p8.tm_k, kv->k, D, Hkv, kv, kv->k_stride_page, kv->k_stride_head, kv->k_stride_slot, box) ||
+        !encode_pool8(&p8.tm_v, kv->v, D, Hkv, kv, kv->v_stride_page, kv->v_stride_head, kv->v_stride_slot, box))
+      return cuda_fail(cudaErrorInvalidValue);
+    p8.k_scale = fp8->k_scale;
+    p8.v_scale = fp8->v_scale;
+    p8.e5m2 = fp8->format == FA_FP8_E5M2;
+  }
   const int box = std::min(kv->page_size, fa::kDecTile);
-  if (!encode_pool(&p.tm_k, kv->k, fp16, D, Hkv, kv, kv->k_stride_page, kv->k_stride_head, kv->k_stride_slot, box) ||
-      !encode_pool(&p.tm_v, kv->v, fp16, D, Hkv, kv, kv->v_stride_page, kv->v_stride_head, kv->v_stride_slot, box))
+  if (!fp8 && (!encode_pool(&p.tm_k, kv->k, fp16, D, Hkv, kv, kv->k_stride_page, kv->k_stride_head, kv->k_stride_slot, box) ||
+      !encode_pool(&p.tm_v, kv->v, fp16, D, Hkv, kv, kv->v_stride_page, kv->v_stride_head, kv->v_stride_slot, box)))
     return cuda_fail(cudaErrorInvalidValue);
-  fa::DecodeCore& c = p.c;
+  fa::DecodeCore& c = fp8 ? p8.c : p.c;
   c.kv_lens = kv_lens;
   c.table = kv->page_table;
   c.table_stride = kv->table_stride;
@@ -326,13 +352,123 @@ int fa_decode(const void* q, const fa_paged_kv_t* kv, void* o, float* lse, int B
   c.timeout_ns = fa_host::wait_timeout_ns();
   c.status = fa_host::status_ptr();
   if (!c.status) return cuda_fail(cudaGetLastError());
+  if (tree) {
+    c.ancestors = tree->ancestors;
+    c.anc_stride = tree->stride_b;
+    c.new_lens = tree->new_lens;
+  }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // the most tiles that a unit can have: the lengths are known on the device only
   const long long keys = (long long)(page_idx ? std::min(max_sel, kv->max_pages) : kv->max_pages) * kv->page_size;
+  if (fp8) return fa_host::launch_decode8(p8, fp16, D, keys, st);
   const long long tiles = (keys + fa::kDecTile - 1) / fa::kDecTile;
-  if (D == 128)
-    return fp16 ? launch_decode_rows<false, 128>(p, tiles, st) : launch_decode_rows<true, 128>(p, tiles, st);
-  return fp16 ? launch_decode_rows<false, 64>(p, tiles, st) : launch_decode_rows<true, 64>(p, tiles, st);
+  auto launch = [&](auto with_tree) {
+    constexpr bool T = decltype(with_tree)::value;
+    if (D == 128)
+      return fp16 ? launch_decode_rows<false, 128, T>(p, tiles, st) : launch_decode_rows<true, 128, T>(p, tiles, st);
+    return fp16 ? launch_decode_rows<false, 64, T>(p, tiles, st) : launch_decode_rows<true, 64, T>(p, tiles, st);
+  };
+  return tree ? launch(std::true_type{}) : launch(std::false_type{});
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_kv_append(const fa_paged_kv_t* kv, const fa_kv_new_t* x, int B, int Hq, int Hkv, int Snew,
+                 int D, int mask_mode, const int32_t* kv_lens, const int32_t* new_lens,
+                 void* stream) {
+  return append_call(kv, nullptr, x, B, Hq, Hkv, Snew, D, mask_mode, kv_lens, new_lens, nullptr, stream);
+}
+
+int fa_kv_append_ext(const fa_paged_kv_t* kv, const fa_kv_fp8_t* fp8, const fa_kv_new_t* x, int B, int Hq, int Hkv,
+                     int Snew, int D, int mask_mode, const int32_t* kv_lens, const int32_t* new_lens,
+                     const int32_t* positions, void* stream) {
+  return append_call(kv, fp8, x, B, Hq, Hkv, Snew, D, mask_mode, kv_lens, new_lens, positions, stream);
+}
+
+int fa_decode(const void* q, const fa_paged_kv_t* kv, void* o, float* lse, int B, int Hq, int Hkv,
+              int Sq, int D, float scale, int mask_mode, const int32_t* kv_lens, int pre_tokens,
+              const int32_t* page_idx, int max_sel, void* stream) {
+  return decode_call(q, kv, nullptr, o, lse, B, Hq, Hkv, Sq, D, scale, mask_mode, kv_lens, pre_tokens, page_idx, max_sel,
+                     nullptr, stream);
+}
+
+int fa_decode_ext(const void* q, const fa_paged_kv_t* kv, const fa_kv_fp8_t* fp8, void* o, float* lse, int B, int Hq,
+                  int Hkv, int Sq, int D, float scale, int mask_mode, const int32_t* kv_lens, int pre_tokens,
+                  const int32_t* page_idx, int max_sel, const fa_tree_t* tree, void* stream) {
+  return decode_call(q, kv, fp8, o, lse, B, Hq, Hkv, Sq, D, scale, mask_mode, kv_lens, pre_tokens, page_idx, max_sel,
+                     tree, stream);
+}
+
+int fa_kv_read(const fa_paged_kv_t* kv, const fa_kv_fp8_t* fp8, const fa_kv_rows_t* out, int B, int Hkv, int S, int D,
+               int mask_mode, const int32_t* starts, const int32_t* lens, void* stream) {
+  if (!out) return FA_ERR_NULL;
+  int rc = validate_cache(kv, B, Hkv, Hkv, S, D, mask_mode);
+  if (rc == FA_OK) rc = validate_pools(kv, Hkv, fp8);
+  if (rc != FA_OK) return rc;
+  if (!out->k || !out->v || !lens) return FA_ERR_NULL;
+  if ((long long)B * Hkv > kMostRows / S) return FA_ERR_SHAPE;
+  for (const auto& [s, n] : {std::pair<int64_t, int64_t>{out->k_stride_b, B}, {out->k_stride_h, Hkv}, {out->k_stride_s, S},
+                             {out->v_stride_b, B}, {out->v_stride_h, Hkv}, {out->v_stride_s, S}})
+    if (rc == FA_OK) rc = validate_stride(s, n, false);
+  if (rc != FA_OK) return rc;
+  if (!aligned(out->k, 16) || !aligned(out->v, 16) || !aligned(starts, 4) || !aligned(lens, 4)) return FA_ERR_ALIGN;
+  fa::ReadParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.kv = device_cache(kv);
+  if (fp8) {
+    p.k_scale = fp8->k_scale;
+    p.v_scale = fp8->v_scale;
+    p.e5m2 = fp8->format == FA_FP8_E5M2;
+  }
+  p.k = static_cast<uint16_t*>(out->k);
+  p.v = static_cast<uint16_t*>(out->v);
+  p.k_sb = out->k_stride_b, p.k_sh = out->k_stride_h, p.k_ss = out->k_stride_s;
+  p.v_sb = out->v_stride_b, p.v_sh = out->v_stride_h, p.v_ss = out->v_stride_s;
+  p.starts = starts;
+  p.lens = lens;
+  p.Hkv = Hkv;
+  p.S = S;
+  p.chunks = (S + fa::kReadTokens - 1) / fa::kReadTokens;
+  const long long blocks = (long long)p.chunks * Hkv * B;      // (below the rows' limit)
+  p.status = fa_host::status_ptr();
+  if (!p.status) return cuda_fail(cudaGetLastError());
+  const cudaError_t e = fa_host::launch_read(p, (mask_mode & FA_DTYPE_FP16) != 0, D, fp8 != nullptr, (unsigned)blocks,
+                                             reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e);
+}
+
+int fa_kv_keep(const fa_paged_kv_t* kv, const fa_kv_fp8_t* fp8, int B, int Hkv, int D, int mask_mode,
+               const int32_t* kv_lens, const int32_t* keep_idx, int max_keep, const int32_t* keep_lens, void* stream) {
+  int rc = validate_cache(kv, B, Hkv, Hkv, 1, D, mask_mode);
+  if (rc == FA_OK) rc = validate_pools(kv, Hkv, fp8);
+  if (rc != FA_OK) return rc;
+  if (!kv_lens || !keep_idx || !keep_lens) return FA_ERR_NULL;
+  if (max_keep <= 0) return FA_ERR_SHAPE;
+  if (!aligned(kv_lens, 4) || !aligned(keep_idx, 4) || !aligned(keep_lens, 4)) return FA_ERR_ALIGN;
+  fa::KeepParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.kv = device_cache(kv);
+  if (fp8) {
+    p.k_scale = fp8->k_scale;
+    p.v_scale = fp8->v_scale;
+    p.e5m2 = fp8->format == FA_FP8_E5M2;
+  }
+  p.kv_lens = kv_lens;
+  p.idx = keep_idx;
+  p.keep_lens = keep_lens;
+  p.Hkv = Hkv;
+  p.M = max_keep;
+  const long long columns = 2LL * Hkv * (D * (fp8 ? 1 : 2) / 16);
+  const long long parts = (columns + fa::kKeepThreads - 1) / fa::kKeepThreads;
+  if (columns > 0x7FFFFFFFLL || parts * B > 0x7FFFFFFFLL) return FA_ERR_SHAPE;
+  p.parts = (int)parts;
+  p.status = fa_host::status_ptr();
+  if (!p.status) return cuda_fail(cudaGetLastError());
+  const cudaError_t e = fa_host::launch_keep(p, (mask_mode & FA_DTYPE_FP16) != 0, D, fp8 != nullptr, (unsigned)(parts * B),
+                                             reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
 int fa_select_pages(const void* q, const fa_paged_kv_t* kv, int32_t* page_idx, int B, int Hq,

@@ -532,6 +532,109 @@ int fa_select_pages(const void* q, const fa_paged_kv_t* kv, int32_t* page_idx, i
                     int Hkv, int Sq, int D, int mask_mode, const int32_t* kv_lens, int max_sel,
                     int first, int last, void* stream);
 
+/* ---- an 8-bit cache ------------------------------------------------------ */
+/*
+ * k and v of fa_paged_kv_t are then codes of one byte (strides in elements,
+ * multiples of 16), D of them for each token and KV head, and a row's values are
+ * code * 2^e, its scale 2^e kept as the byte e + 127 at
+ *   k_scale[(page * Hkv + head) * page_size + slot],  v_scale alike,
+ * contiguous uint8 [num_pages, Hkv, page_size], 16-byte aligned.  mask_mode names
+ * the type of q, o, new and read tokens and of k_min / k_max as before (they
+ * bound the keys as stored; an fp16 bound of a stored key past 65504 is infinite).
+ * fa_kv_append_ext writes a row's e as the least integer >= -80 at which no
+ * code exceeds the format's largest value (448 or 57344; at e = 119 or 112, the
+ * largest, codes saturate) and each channel as the nearest code of
+ * x * 2^-e, ties to even, x in fp32 as rotated.  A row that holds an infinity
+ * or NaN becomes NaN (codes 0, scale byte 255) and is reported as FA_ERR_RANGE by
+ * fa_check_status.  Callers that write rows themselves: scale bytes 1 to 253, of
+ * values 47 to 253 (2^-80 to 2^126), codes finite.
+ */
+typedef struct {
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  int32_t format;     /* FA_FP8_E4M3 or FA_FP8_E5M2 */
+} fa_kv_fp8_t;
+
+/*
+ * fa_kv_append_ext -- fa_kv_append into an 8-bit cache (fp8; NULL: 16-bit), and
+ * with positions given: DEVICE int32 [B, Snew], contiguous, by which token i of
+ * sequence b is rotated in the place of kv_lens[b] + i (drafts of a tree lie one
+ * behind another in the cache and turn by their depth).  Where a token is stored
+ * does not change.  A position without a row in the rotation tables leaves its
+ * token out and is reported as FA_ERR_INDEX; positions of padding are not read.
+ */
+int fa_kv_append_ext(const fa_paged_kv_t* kv, const fa_kv_fp8_t* fp8, const fa_kv_new_t* x, int B,
+                     int Hq, int Hkv, int Snew, int D, int mask_mode, const int32_t* kv_lens,
+                     const int32_t* new_lens, const int32_t* positions, void* stream);
+
+/* A tree of drafted tokens per sequence (host struct).  The last n_b tokens of
+ * sequence b in the cache are its drafts, n_b = new_lens[b] in [0, min(Sq, kv_lens[b])]
+ * (DEVICE int32[B]; NULL: Sq); a value outside is clamped and reported as
+ * FA_ERR_INDEX.  ancestors: DEVICE uint8 [Sq, Sq] per sequence, stride_b elements
+ * apart (0: one tree for all); element (i, j) nonzero: draft i sees draft j.  A
+ * draft sees itself only where (i, i) is set; elements past n_b are not read. */
+typedef struct {
+  const uint8_t* ancestors;
+  int64_t stride_b;
+  const int32_t* new_lens;
+} fa_tree_t;
+
+/*
+ * fa_decode_ext -- fa_decode over an 8-bit cache (fp8; NULL: 16-bit) or for a tree
+ * of drafts (tree; NULL: the newest tokens one after another), or both.  With a
+ * tree, row i < n_b is draft i, the token kv_lens[b] - n_b + i: it sees every token
+ * before the drafts and those drafts that its row of ancestors names (kv_lens
+ * counts the drafts; rows are a sequence's first, as fa_kv_append leaves them).
+ * Rows i >= n_b are padding: whatever they hold, they are answered as rows that see
+ * the tokens before the drafts, and reach no other row.  A tree goes with neither
+ * pre_tokens nor page_idx (FA_ERR_UNSUPPORTED).
+ * Over an 8-bit cache the products take fp16 codes, Q as fp16 of a power of
+ * two times it (exact but for bf16 channels below 2^-29 of their row's largest) and P
+ * as one fp16; scores and sums are fp32.
+ */
+int fa_decode_ext(const void* q, const fa_paged_kv_t* kv, const fa_kv_fp8_t* fp8, void* o, float* lse,
+                  int B, int Hq, int Hkv, int Sq, int D, float scale, int mask_mode,
+                  const int32_t* kv_lens, int pre_tokens, const int32_t* page_idx, int max_sel,
+                  const fa_tree_t* tree, void* stream);
+
+/* Dense rows (host struct): element (b, h, i, d) at base[b * stride_b + h * stride_h +
+ * i * stride_s + d]; strides in elements, positive, multiples of 8, below 2^38
+ * (one over a size of 1 is not looked at); bases 16-byte aligned. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t k_stride_b, k_stride_h, k_stride_s;
+  int64_t v_stride_b, v_stride_h, v_stride_s;
+} fa_kv_rows_t;
+
+/*
+ * fa_kv_read -- tokens out of the cache: row i < lens[b] of sequence b becomes the
+ * key and value of its token starts[b] + i (starts NULL: 0), of an 8-bit cache
+ * (fp8) code * 2^e rounded once to the type of mask_mode.  Rows i >= lens[b] stay
+ * as they were.  lens, starts: DEVICE int32[B]; a length outside [0, S] is clamped,
+ * a run that the table cannot hold or a token whose page id is outside the pool is
+ * left out; each is reported as FA_ERR_INDEX.  k_min, k_max are not looked at.
+ */
+int fa_kv_read(const fa_paged_kv_t* kv, const fa_kv_fp8_t* fp8, const fa_kv_rows_t* out, int B,
+               int Hkv, int S, int D, int mask_mode, const int32_t* starts, const int32_t* lens,
+               void* stream);
+
+/*
+ * fa_kv_keep -- accepted drafts to their places: the token at kv_lens[b] +
+ * keep_idx[b, i] moves to kv_lens[b] + i, for i < keep_lens[b] (kv_lens: the tokens
+ * before the drafts).  keep_idx: DEVICE int32 [B, max_keep], contiguous, a
+ * sequence's entries ascending from >= 0; keep_lens: DEVICE int32[B] in [0, max_keep].
+ * Keys and values move as stored, with their scales.  Where the cache has bounds,
+ * those of a page that a key moved into take it in: anew where slot 0 was moved
+ * into, widened otherwise.  Places behind the last kept draft stay as they were.  An
+ * entry that is not ascending, a token past the table or a page id outside the pool
+ * ends its sequence's path there, a length outside is clamped; each is reported as
+ * FA_ERR_INDEX.  No two sequences of a call may share a page that is moved into.
+ */
+int fa_kv_keep(const fa_paged_kv_t* kv, const fa_kv_fp8_t* fp8, int B, int Hkv, int D, int mask_mode,
+               const int32_t* kv_lens, const int32_t* keep_idx, int max_keep,
+               const int32_t* keep_lens, void* stream);
+
 /* Synchronises `stream`, then returns and clears the device status word of
  * the current device: FA_OK, FA_ERR_DEVICE_TIMEOUT, FA_ERR_RANGE or
  * FA_ERR_INDEX (in that order where several were seen since the last call), or

@@ -12,6 +12,28 @@ from __future__ import annotations
 
 import numpy as np
 
+from oracle import fp8 as F
+
+LEAST = -80      # of a scale's exponent
+TOP = {"e4m3fn": (8, 119), "e5m2": (15, 112)}      # the largest code is 1.75 * 2^(first); the largest exponent
+
+
+def exponent(x, fmt):
+    """e of the scale 2^e of rows x [..., D] (finite): the least >= LEAST with
+    max |x| <= (largest code) 2^e."""
+    a = np.abs(np.asarray(x, dtype=np.float64)).max(-1)
+    m, k = np.frexp(np.where(a > 0, a, 1.0))             # a = 2 m * 2^(k - 1), 1 <= 2 m < 2
+    e = k - 1 - TOP[fmt][0] + (m > 0.875)
+    return np.where(a > 0, np.clip(e, LEAST, TOP[fmt][1]), LEAST).astype(np.int64)
+
+
+def quantise(x, fmt):
+    """(codes [..., D], exponents [...]) of rows: x is stored as codes * 2^e."""
+    e = exponent(x, fmt)
+    z = np.ldexp(np.asarray(x, dtype=np.float64), -e[..., None])
+    top = F.FORMATS[fmt][2]
+    return F.round_fp8(np.clip(z, -top, top), fmt), e
+
 
 def rotate(x, pos, cos, sin, interleaved: bool):
     """x [..., S, D] with the first r = 2 * cos.shape[1] channels turned by the
@@ -29,9 +51,11 @@ def rotate(x, pos, cos, sin, interleaved: bool):
 
 
 def append(k_pages, v_pages, table, lens, k, v, new_lens, cos=None, sin=None,
-           interleaved=False, store=lambda x: x, k_min=None, k_max=None):
+           interleaved=False, store=lambda x: x, k_min=None, k_max=None, positions=None,
+           store_v=lambda x: x):
     """The pools (and bounds, where given) after the append; the arguments are
-    left alone.  k, v [B, Hkv, S, D]."""
+    left alone.  k, v [B, Hkv, S, D].  positions [B, S]: the tokens turn by them
+    instead of by where they stand."""
     kp, vp = k_pages.copy(), v_pages.copy()
     lo = None if k_min is None else k_min.copy()
     hi = None if k_max is None else k_max.copy()
@@ -41,22 +65,26 @@ def append(k_pages, v_pages, table, lens, k, v, new_lens, cos=None, sin=None,
             t = int(lens[b]) + i
             x = k[b, :, i]
             if cos is not None:
-                x = rotate(x[:, None], np.array([t]), cos, sin, interleaved)[:, 0]
+                at = t if positions is None else int(positions[b, i])
+                x = rotate(x[:, None], np.array([at]), cos, sin, interleaved)[:, 0]
             x = store(x)
             p, slot = table[b, t // page], t % page
             kp[p, :, slot] = x
-            vp[p, :, slot] = v[b, :, i]
+            vp[p, :, slot] = store_v(v[b, :, i])
             if lo is not None:
                 lo[p] = x if slot == 0 else np.minimum(lo[p], x)
                 hi[p] = x if slot == 0 else np.maximum(hi[p], x)
     return kp, vp, lo, hi
 
 
-def decode(q, k_pages, v_pages, table, lens, scale, pre_tokens=None, page_idx=None):
+def decode(q, k_pages, v_pages, table, lens, scale, pre_tokens=None, page_idx=None, tree=None):
     """(O, LSE, A, X, V): the attention of q [B, Hq, Sq, D] over the pages, its
     log-sum-exp (+inf for a row that sees no key, O = 0 there), and for error
     bounds A = sum_j p_j |v_j| and V = sum_j |v_j| per output and X = max over
-    the row's keys of scale * sum_d |q_d k_jd|."""
+    the row's keys of scale * sum_d |q_d k_jd|.  tree: (ancestors [B, Sq, Sq],
+    drafts [B]): the last drafts[b] tokens are a tree, row i its draft i, which
+    sees the tokens before and the drafts of its row of ancestors; rows past
+    drafts[b] see the tokens before."""
     B, Hq, Sq, D = q.shape
     Hkv, page = k_pages.shape[1], k_pages.shape[2]
     G = Hq // Hkv
@@ -80,6 +108,11 @@ def decode(q, k_pages, v_pages, table, lens, scale, pre_tokens=None, page_idx=No
             for i in range(Sq):
                 t = n - Sq + i
                 see = pos <= t
+                if tree is not None:
+                    first = n - int(tree[1][b])
+                    see = pos < first
+                    if i < tree[1][b]:
+                        see = see | ((pos < n) & tree[0][b][i][np.clip(pos - first, 0, Sq - 1)].astype(bool))
                 if pre_tokens is not None:
                     see &= pos >= t - pre_tokens
                 if not see.any():
@@ -121,3 +154,38 @@ def select(q, k_min, k_max, table, lens, page, max_sel, first=1, last=1):
             take = sorted(forced + others[:max_sel - len(forced)])
             out[b, h, :len(take)] = take
     return out
+
+
+def read(k_pages, v_pages, table, starts, lens, k_out, v_out):
+    """(k, v) [B, Hkv, S, D]: row i < lens[b] is token starts[b] + i, the others
+    as in k_out, v_out."""
+    k, v, page = k_out.copy(), v_out.copy(), k_pages.shape[2]
+    for b in range(table.shape[0]):
+        for i in range(int(lens[b])):
+            t = int(starts[b]) + i
+            k[b, :, i] = k_pages[table[b, t // page], :, t % page]
+            v[b, :, i] = v_pages[table[b, t // page], :, t % page]
+    return k, v
+
+
+def keep(pools, table, lens, idx, keep_lens, page, keys=None, k_min=None, k_max=None):
+    """The pools [num_pages, Hkv, page, ...] after each sequence's accepted drafts
+    idx[b, :keep_lens[b]] moved behind its lens[b] tokens; with keys (what the
+    first pool's rows stand for, [num_pages, Hkv, page, D]) the bounds too."""
+    pools = [x.copy() for x in pools]
+    lo, hi = (None, None) if k_min is None else (k_min.copy(), k_max.copy())
+    for b in range(table.shape[0]):
+        n = int(lens[b])
+        path = [int(j) for j in idx[b, :int(keep_lens[b])]]
+        rows = [[x[table[b, (n + j) // page], :, (n + j) % page].copy() for x in pools + ([] if lo is None else [keys])]
+                for j in path]
+        for i, (j, row) in enumerate(zip(path, rows)):
+            if i == j:
+                continue
+            p, slot = table[b, (n + i) // page], (n + i) % page
+            for x, r in zip(pools, row):
+                x[p, :, slot] = r
+            if lo is not None:
+                lo[p] = row[-1] if slot == 0 else np.minimum(lo[p], row[-1])
+                hi[p] = row[-1] if slot == 0 else np.maximum(hi[p], row[-1])
+    return pools, lo, hi
