@@ -238,7 +238,7 @@ __device__ __forceinline__ DecodePiece decode_step(DecodeWalk& w, int n, int uni
 
 // This CTA's range of charged tiles and the sequence it starts in, by one warp.
 template <int TILE = kDecTile>
-__device__ __forceinline__ void decode_start(const DecodeCore& p, int lane, DecodeWalk* s_walk, int* s_len) {
+__device__ __forceinline__ void decode_start(const DecodeCore& p, int cta, int lane, DecodeWalk* s_walk, int* s_len) {
   int len[kChunks], c[kChunks];
   int mine = 0, my_len = 0, inc;           // of the sequence `at + lane`, its chunk of 32 summed up
   auto scan = [&](int x) {
@@ -252,9 +252,9 @@ __device__ __forceinline__ void decode_start(const DecodeCore& p, int lane, Deco
   long long total, start = 0, end = 0, first, before = 0;
   int at = 0;
   auto range = [&]() {
-    if ((int)blockIdx.x < decode_ctas(p, total)) {
-      start = decode_first(p, total, blockIdx.x);
-      end = decode_first(p, total, blockIdx.x + 1);
+    if (cta < decode_ctas(p, total)) {
+      start = decode_first(p, total, cta);
+      end = decode_first(p, total, cta + 1);
     }
     // in charges of one unit per sequence: the sequence is the last with at most so many before it
     first = times_inverse(start, p.units_inv);
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
   pdl_wait_prior();
   pdl_launch_dependents();
   if (warp == kDecWarps) {   // this CTA's range of charged tiles, and the sequence it starts in
-    decode_start(p, lane, s_walk, s_len);
+    decode_start(p, blockIdx.x, lane, s_walk, s_len);
   } else if (blockIdx.x == 0) {
     decode_report(p);
   }

@@ -32,8 +32,13 @@ namespace fa {
 
 constexpr int kDec8Tile = 128;      // keys per tile
 constexpr int kDec8Groups = 8;      // of 16 keys; a consumer scores two
+// Teams of four consumers and a producer, each with a ring and a range of its own, that share one CTA
+// per SM.  (As CTAs of their own, three per SM at 128 registers, they left an SM with two where the
+// kernel started beside the last CTAs of the one before it: five warps each fill the four register
+// files only from the right first one on.  The third then ran alone at the end, and 8 sequences of
+// 131072 tokens took 435 us back to back against 310 us one by one.)
 template <int NT>
-constexpr int kDec8CtasPerSm = NT <= 2 ? 3 : 2;
+constexpr int kDec8Teams = NT <= 2 ? 3 : 2;
 
 struct Decode8Params {
   DecodeCore c;
@@ -58,8 +63,9 @@ struct Decode8Smem {
   static constexpr int kMetaOff = kSumOff + kDecWarps * 8 * NT * 4;              // int [stages][8]
   static constexpr int kBarOff = kMetaOff + kStages * kDec8Groups * 4;
   static constexpr int kMiscOff = kBarOff + 2 * kStages * 8;
-  static constexpr int kBytes = kMiscOff + 64;
-  static_assert((kBytes + 1024) * kDec8CtasPerSm<NT> <= 228 * 1024, "CTAs that share an SM");
+  static constexpr int kTeam = (kMiscOff + 64 + 1023) / 1024 * 1024;   // (swizzled tiles start on 1024 bytes)
+  static constexpr int kBytes = kTeam * kDec8Teams<NT>;
+  static_assert(kBytes <= 227 * 1024, "one CTA per SM");
 };
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int slot, int head, int page) {
@@ -87,14 +93,17 @@ __device__ __forceinline__ void codes4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 }
 
 template <bool BF16, int D, int NT, bool E5M2>
-__global__ void __launch_bounds__(kDecThreads, kDec8CtasPerSm<NT>) fa_decode8_kernel(const __grid_constant__ Decode8Params params) {
+__global__ void __launch_bounds__(kDecThreads * kDec8Teams<NT>, 1) fa_decode8_kernel(const __grid_constant__ Decode8Params params) {
   const DecodeCore& p = params.c;
   using SM = Decode8Smem<D, NT>;
   constexpr int NS = SM::kStages;
   constexpr int KC = D / 16;                   // 16-byte chunks of a row
-  extern __shared__ __align__(1024) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem_all[];
+  const int team = threadIdx.x / kDecThreads;
+  uint8_t* smem = smem_all + team * SM::kTeam;
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = (threadIdx.x % kDecThreads) >> 5, lane = threadIdx.x & 31;
+  const int cta = team * gridDim.x + blockIdx.x;     // as the schedule counts: few ranges get an SM each
   auto FULL = [&](int s) { return sbase + SM::kBarOff + 8 * s; };
   auto EMPTY = [&](int s) { return sbase + SM::kBarOff + 8 * (NS + s); };
   int* s_meta = reinterpret_cast<int*>(smem + SM::kMetaOff);   // per stage: first key of each 16, or -1
@@ -102,7 +111,7 @@ __global__ void __launch_bounds__(kDecThreads, kDec8CtasPerSm<NT>) fa_decode8_ke
   int* s_len = reinterpret_cast<int*>(smem + SM::kMiscOff + 24);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + SM::kMiscOff + 28);
 
-  if (threadIdx.x == 0) {
+  if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&params.tm_k);
     tma_prefetch_desc(&params.tm_v);
     for (int s = 0; s < NS; ++s) {
@@ -115,8 +124,8 @@ __global__ void __launch_bounds__(kDecThreads, kDec8CtasPerSm<NT>) fa_decode8_ke
   // In this order: the join kernel may then read the lengths as soon as it runs.
   pdl_wait_prior();
   pdl_launch_dependents();
-  if (warp == kDecWarps) decode_start<kDec8Tile>(p, lane, s_walk, s_len);
-  else if (blockIdx.x == 0) decode_report(p);
+  if (warp == kDecWarps) decode_start<kDec8Tile>(p, cta, lane, s_walk, s_len);
+  else if (cta == 0) decode_report(p);
   __syncthreads();
   DecodeWalk walk = *s_walk;
   const WaitCtx wc{s_abort, p.status, p.timeout_ns};
@@ -190,7 +199,7 @@ __global__ void __launch_bounds__(kDecThreads, kDec8CtasPerSm<NT>) fa_decode8_ke
   float* s_fac = reinterpret_cast<float*>(smem + SM::kFacOff);
   float* s_max = reinterpret_cast<float*>(smem + SM::kMaxOff);
   float* s_sum = reinterpret_cast<float*>(smem + SM::kSumOff);
-  auto sync = [&]() { named_sync(1, 32 * kDecWarps); };
+  auto sync = [&]() { named_sync(1 + 2 * team, 32 * kDecWarps); };
   // Key r of a stage is row r, D bytes; its 16-byte chunk c lies at place c ^ turn(r) (128-byte swizzle
   // for rows of 128 bytes, 64-byte swizzle for rows of 64).
   auto turn = [](int r) { return (uint32_t)(D == 128 ? r & 7 : (r >> 1) & 3); };
@@ -361,7 +370,7 @@ __global__ void __launch_bounds__(kDecThreads, kDec8CtasPerSm<NT>) fa_decode8_ke
 #pragma unroll
           for (int e = 0; e < 4; ++e) over = fmaxf(over, c[u][n][e] - m[n][e & 1]);   // (NaN is dropped)
       }
-      if (named_or(2, 32 * kDecWarps, over > kMaxOver + kLift<false>)) {   // the references move up
+      if (named_or(2 + 2 * team, 32 * kDecWarps, over > kMaxOver + kLift<false>)) {   // the references move up
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float mx[2] = {fmaxf(fmaxf(c[0][n][0], c[0][n][2]), fmaxf(c[1][n][0], c[1][n][2])),
@@ -480,7 +489,7 @@ __global__ void __launch_bounds__(kDecThreads, kDec8CtasPerSm<NT>) fa_decode8_ke
     }
     sync();
     const bool direct = d.t0 == 0 && d.nt == s.n;
-    const long long part0 = (2LL * blockIdx.x + (d.t0 == 0 ? 1 : 0)) * (8 * NT);
+    const long long part0 = (2LL * cta + (d.t0 == 0 ? 1 : 0)) * (8 * NT);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float sum[2] = {0.f, 0.f};

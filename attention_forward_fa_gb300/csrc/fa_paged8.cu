@@ -53,7 +53,7 @@ int launch_decode8_rows(fa::Decode8Params& p, long long most_tiles, cudaStream_t
   if (attr_err[dev & 63] != cudaSuccess) return cuda_fail(attr_err[dev & 63]);
   const int sms = sm_count();
   if (sms <= 0) return cuda_fail(cudaErrorInvalidDevice);
-  p.c.ctas = (int)std::min<long long>(fa::kDec8CtasPerSm<NT> * sms, most_tiles);
+  p.c.ctas = (int)std::min<long long>(fa::kDec8Teams<NT> * sms, most_tiles);
   auto inverse = [](unsigned long long d) { return d == 1 ? 0ull : ~0ull / d + 1; };   // ceil(2^64 / d)
   p.c.ctas_inv = inverse(p.c.ctas);
   p.c.units_inv = inverse(p.c.units);
@@ -62,7 +62,8 @@ int launch_decode8_rows(fa::Decode8Params& p, long long most_tiles, cudaStream_t
   if (!scratch) return cuda_fail(cudaGetLastError());
   p.c.part_o = static_cast<float*>(scratch);
   p.c.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(scratch) + o_bytes);
-  cudaError_t e = launch_dependent(kern, (unsigned)p.c.ctas, fa::kDecThreads, smem, st, p);
+  const unsigned grid = (unsigned)std::min(p.c.ctas, sms);
+  cudaError_t e = launch_dependent(kern, grid, fa::kDecThreads * fa::kDec8Teams<NT>, smem, st, p);
   if (e == cudaSuccess) {   // (as for a 16-bit cache)
     const long long rows = (long long)p.c.B * p.c.Hkv * p.c.rows;
     constexpr int T = fa::kDec8Tile;
