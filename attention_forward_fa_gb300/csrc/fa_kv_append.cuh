@@ -218,7 +218,7 @@ __device__ __forceinline__ void append_piece(const AppendParams& p, int item, in
           unpack8<BF16>(wb[i], d);
           const int slot = (t + i * tp) & (ps - 1);
           uint2 qa, qd;
-          const uint32_t scale = quantise_row<L>(a, d, p.e5m2 != 0, qa, qd, p.status);
+          const uint32_t scale = quantise_row<L>(a, d, p.e5m2, qa, qd, p.status);
           uint8_t* y = reinterpret_cast<uint8_t*>(p.kv.v) + (long long)id * p.kv.v_sp + h * p.kv.v_sh + (long long)slot * p.kv.v_ss;
           *reinterpret_cast<uint4*>(y + 16 * part) = make_uint4(qa.x, qa.y, qd.x, qd.y);
           if (part == 0) p.v_scale[(((long long)id * p.Hkv + h) << ps_shift) + slot] = (uint8_t)scale;
@@ -270,17 +270,24 @@ __device__ __forceinline__ void append_piece(const AppendParams& p, int item, in
         if (no_page()) break;
         const int slot = t & (ps - 1);
         uint2 qa, qd;
-        const uint32_t scale = quantise_row<L>(a, d, p.e5m2 != 0, qa, qd, p.status);
+        const uint32_t scale = quantise_row<L>(a, d, p.e5m2, qa, qd, p.status);
         uint8_t* y = reinterpret_cast<uint8_t*>(p.kv.k) + (long long)id * p.kv.k_sp + h * p.kv.k_sh + (long long)slot * p.kv.k_ss;
         *reinterpret_cast<uint2*>(y + offA) = qa;
         *reinterpret_cast<uint2*>(y + offB) = qd;
         if (part == 0) p.k_scale[(((long long)id * p.Hkv + h) << ps_shift) + slot] = (uint8_t)scale;
         if (p.kv.k_min) {
           uint4 lo, hi;
-          stored_bounds<BF16>(qa, scale, p.e5m2 != 0, lo, hi);
-          widen(0, lo, hi);
-          stored_bounds<BF16>(qd, scale, p.e5m2 != 0, lo, hi);
-          widen(1, lo, hi);
+          if (p.e5m2) {
+            stored_bounds<BF16, true>(qa, scale, lo, hi);
+            widen(0, lo, hi);
+            stored_bounds<BF16, true>(qd, scale, lo, hi);
+            widen(1, lo, hi);
+          } else {
+            stored_bounds<BF16, false>(qa, scale, lo, hi);
+            widen(0, lo, hi);
+            stored_bounds<BF16, false>(qd, scale, lo, hi);
+            widen(1, lo, hi);
+          }
         }
         continue;
       }

@@ -83,8 +83,14 @@ __global__ void __launch_bounds__(kReadThreads) fa_kv_read_kernel(const ReadPara
       auto out = [&](uint16_t* to, uint4 w, uint32_t scale) {
         const float f = scale_of(scale);
         uint4* y = reinterpret_cast<uint4*>(to + 16 * part);
-        y[0] = read_codes<BF16>(make_uint2(w.x, w.y), f, p.e5m2 != 0);
-        y[1] = read_codes<BF16>(make_uint2(w.z, w.w), f, p.e5m2 != 0);
+        const uint2 c0 = make_uint2(w.x, w.y), c1 = make_uint2(w.z, w.w);
+        if (p.e5m2) {
+          y[0] = read_codes<BF16, true>(c0, f);
+          y[1] = read_codes<BF16, true>(c1, f);
+        } else {
+          y[0] = read_codes<BF16, false>(c0, f);
+          y[1] = read_codes<BF16, false>(c1, f);
+        }
       };
       out(ko, k[i], ks[i]);
       out(vo, v[i], vs[i]);
@@ -221,9 +227,10 @@ __global__ void __launch_bounds__(kKeepThreads) fa_kv_keep_kernel(const KeepPara
             }
             if constexpr (EIGHT) {
               uint4 lo, hi;
-              stored_bounds<BF16>(make_uint2(w[i].x, w[i].y), f[i], p.e5m2 != 0, lo, hi);
+              const uint2 c0 = make_uint2(w[i].x, w[i].y), c1 = make_uint2(w[i].z, w[i].w);
+              p.e5m2 ? stored_bounds<BF16, true>(c0, f[i], lo, hi) : stored_bounds<BF16, false>(c0, f[i], lo, hi);
               widen(0, lo, hi);
-              stored_bounds<BF16>(make_uint2(w[i].z, w[i].w), f[i], p.e5m2 != 0, lo, hi);
+              p.e5m2 ? stored_bounds<BF16, true>(c1, f[i], lo, hi) : stored_bounds<BF16, false>(c1, f[i], lo, hi);
               widen(1, lo, hi);
             } else {
               widen(0, w[i], w[i]);

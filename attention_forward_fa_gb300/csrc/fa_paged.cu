@@ -26,6 +26,7 @@ using fa_host::launch_dependent;
 constexpr long long kMostTokens = (1LL << 31) - 65536;   // of one sequence: positions are 32-bit
 constexpr long long kMostRows = (1LL << 31) - 65536;     // of a call (B * heads * tokens), counted in 32 bits
 constexpr int kMostSel = 1 << 20;                        // listed pages of one KV head
+constexpr int kWideRows = 32;                            // rows per KV head that decode without tcgen05
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -94,9 +95,9 @@ fa::PagedKv device_cache(const fa_paged_kv_t* kv) {
 
 // 5-D view (64 channels, slots, D / 64, heads, pages) of a pool, in boxes of
 // one page's and head's `box` slots with all channels, 128-byte swizzle: in
-// shared memory [D / 64][box][64].
+// shared memory [D / 64][box][64].  (one_chunk: 64 of the channels, [box][64].)
 bool encode_pool(CUtensorMap* tm, const void* base, bool fp16, int D, int Hkv, const fa_paged_kv_t* kv,
-                 int64_t s_page, int64_t s_head, int64_t s_slot, int box) {
+                 int64_t s_page, int64_t s_head, int64_t s_slot, int box, bool one_chunk = false) {
   auto enc = fa_host::tensor_map_encoder();
   if (!enc) return false;
   // a stride over a single head or page is never stepped; for the map it has to be valid
@@ -105,7 +106,7 @@ bool encode_pool(CUtensorMap* tm, const void* base, bool fp16, int D, int Hkv, c
   cuuint64_t dims[5] = {64, (cuuint64_t)kv->page_size, (cuuint64_t)(D / 64), (cuuint64_t)Hkv,
                         (cuuint64_t)kv->num_pages};
   cuuint64_t strides[4] = {(cuuint64_t)s_slot * 2, 128, (cuuint64_t)s_head * 2, (cuuint64_t)s_page * 2};
-  cuuint32_t boxes[5] = {64, (cuuint32_t)box, (cuuint32_t)(D / 64), 1, 1};
+  cuuint32_t boxes[5] = {64, (cuuint32_t)box, one_chunk ? 1u : (cuuint32_t)(D / 64), 1, 1};
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return enc(tm, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
              const_cast<void*>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -114,9 +115,9 @@ bool encode_pool(CUtensorMap* tm, const void* base, bool fp16, int D, int Hkv, c
 }
 
 // 4-D view (D bytes, slots, heads, pages) of an 8-bit pool, in boxes of `box` slots' rows, swizzled over
-// the row.
+// the row or as they are.
 bool encode_pool8(CUtensorMap* tm, const void* base, int D, int Hkv, const fa_paged_kv_t* kv, int64_t s_page,
-                  int64_t s_head, int64_t s_slot, int box) {
+                  int64_t s_head, int64_t s_slot, int box, bool swizzle) {
   auto enc = fa_host::tensor_map_encoder();
   if (!enc) return false;
   if (Hkv == 1) s_head = 128;
@@ -126,7 +127,8 @@ bool encode_pool8(CUtensorMap* tm, const void* base, int D, int Hkv, const fa_pa
   cuuint32_t boxes[4] = {(cuuint32_t)D, (cuuint32_t)box, 1, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, boxes, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -313,24 +315,31 @@ int decode_call(const void* q, const fa_paged_kv_t* kv, const fa_kv_fp8_t* fp8, 
     if (!aligned(tree->new_lens, 4)) return FA_ERR_ALIGN;
   }
   fa::Decode8Params p8;
+  fa::WideParams pw;
   fa::DecodeParams p;
-  std::memset(&p, 0, sizeof(p));
   const bool fp16 = (mask_mode & FA_DTYPE_FP16) != 0;
-  if (fp8) {
-    std::memset(&p8, 0, sizeof(p8));
-    const int box = std::min(kv->page_size, fa::kDec8Tile);
-    if (!encode_pool8(&p8.tm_k, kv->k, D, Hkv, kv, kv->k_stride_page, kv->k_stride_head, kv->k_stride_slot, box) ||
-        !encode_pool8(&p8.tm_v, kv->v, D, Hkv, kv, kv->v_stride_page, kv->v_stride_head, kv->v_stride_slot, box))
-      return cuda_fail(cudaErrorInvalidValue);
-    p8.k_scale = fp8->k_scale;
-    p8.v_scale = fp8->v_scale;
-    p8.e5m2 = fp8->format == FA_FP8_E5M2;
-  }
-  const int box = std::min(kv->page_size, fa::kDecTile);
-  if (!fp8 && (!encode_pool(&p.tm_k, kv->k, fp16, D, Hkv, kv, kv->k_stride_page, kv->k_stride_head, kv->k_stride_slot, box) ||
-      !encode_pool(&p.tm_v, kv->v, fp16, D, Hkv, kv, kv->v_stride_page, kv->v_stride_head, kv->v_stride_slot, box)))
-    return cuda_fail(cudaErrorInvalidValue);
-  fa::DecodeCore& c = fp8 ? p8.c : p.c;
+  const int rows = Hq / Hkv * Sq;
+  // More rows than the warp-level products take at the speed of the keys (fa_wide.cuh; the fa_decode of a
+  // 16-bit cache without a tree keeps to its passes of 48 rows and so to its bits).
+  const bool wide = rows > kWideRows && (fp8 || tree);
+  const int box = std::min(kv->page_size, wide || fp8 ? 128 : fa::kDecTile);
+  auto maps = [&](auto& x) {
+    std::memset(&x, 0, sizeof(x));
+    auto one = [&](CUtensorMap* tm, const void* base, int64_t page, int64_t head, int64_t slot) {
+      return fp8 ? encode_pool8(tm, base, D, Hkv, kv, page, head, slot, box, !wide)
+                 : encode_pool(tm, base, fp16, D, Hkv, kv, page, head, slot, box, wide);
+    };
+    return one(&x.tm_k, kv->k, kv->k_stride_page, kv->k_stride_head, kv->k_stride_slot) &&
+           one(&x.tm_v, kv->v, kv->v_stride_page, kv->v_stride_head, kv->v_stride_slot);
+  };
+  auto codes = [&](auto& x) {
+    x.k_scale = fp8->k_scale;
+    x.v_scale = fp8->v_scale;
+    x.e5m2 = fp8->format == FA_FP8_E5M2;
+  };
+  if (!(wide ? maps(pw) : fp8 ? maps(p8) : maps(p))) return cuda_fail(cudaErrorInvalidValue);
+  if (fp8) wide ? codes(pw) : codes(p8);
+  fa::DecodeCore& c = wide ? pw.c : fp8 ? p8.c : p.c;
   c.kv_lens = kv_lens;
   c.table = kv->page_table;
   c.table_stride = kv->table_stride;
@@ -341,7 +350,7 @@ int decode_call(const void* q, const fa_paged_kv_t* kv, const fa_kv_fp8_t* fp8, 
   c.max_sel = max_sel;
   c.B = B;
   c.Hkv = Hkv;
-  c.rows = Hq / Hkv * Sq;
+  c.rows = rows;
   c.Sq = Sq;
   c.pre_tokens = pre_tokens;
   c.reach = pre_tokens < 0 ? -1 : (int)std::min<long long>((long long)Sq + pre_tokens, 0x7FFFFFFF);
@@ -360,6 +369,7 @@ int decode_call(const void* q, const fa_paged_kv_t* kv, const fa_kv_fp8_t* fp8, 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // the most tiles that a unit can have: the lengths are known on the device only
   const long long keys = (long long)(page_idx ? std::min(max_sel, kv->max_pages) : kv->max_pages) * kv->page_size;
+  if (wide) return fa_host::launch_wide(pw, fp16, D, fp8 != nullptr, keys, st);
   if (fp8) return fa_host::launch_decode8(p8, fp16, D, keys, st);
   const long long tiles = (keys + fa::kDecTile - 1) / fa::kDecTile;
   auto launch = [&](auto with_tree) {

@@ -81,19 +81,15 @@ int launch_decode8_rows(fa::Decode8Params& p, long long most_tiles, cudaStream_t
 template <bool BF16, int D, bool E5M2>
 int launch_decode8_groups(fa::Decode8Params& p, long long keys, cudaStream_t st) {
   fa::DecodeCore& c = p.c;
-  const int passes = (c.rows + 47) / 48;
-  const int nt = ((c.rows + passes - 1) / passes + 7) / 8;
-  c.groups = (c.rows + 8 * nt - 1) / (8 * nt);
-  if ((long long)c.Hkv * c.groups > 0x7FFFFFFFLL) return FA_ERR_SHAPE;
-  c.units = c.Hkv * c.groups;
+  const int nt = (c.rows + 7) / 8;      // (more than 32 rows: launch_wide)
+  c.groups = 1;
+  c.units = c.Hkv;
   const long long most = ((keys + fa::kDec8Tile - 1) / fa::kDec8Tile + fa::kUnitTiles) * c.B * c.units;
   switch (nt) {
     case 1: return launch_decode8_rows<BF16, D, 1, E5M2>(p, most, st);
     case 2: return launch_decode8_rows<BF16, D, 2, E5M2>(p, most, st);
     case 3: return launch_decode8_rows<BF16, D, 3, E5M2>(p, most, st);
-    case 4: return launch_decode8_rows<BF16, D, 4, E5M2>(p, most, st);
-    case 5: return launch_decode8_rows<BF16, D, 5, E5M2>(p, most, st);
-    default: return launch_decode8_rows<BF16, D, 6, E5M2>(p, most, st);
+    default: return launch_decode8_rows<BF16, D, 4, E5M2>(p, most, st);
   }
 }
 template <bool BF16, int D>
@@ -102,6 +98,64 @@ int launch_decode8_format(fa::Decode8Params& p, long long keys, cudaStream_t st)
 }
 
 }  // namespace
+
+namespace {
+
+template <bool BF16, int D, bool EIGHT, int SLOTS>
+int launch_wide_slots(fa::WideParams& p, long long keys, cudaStream_t st) {
+  auto kern = fa::fa_wide_kernel<BF16, D, EIGHT, SLOTS>;
+  constexpr int smem = fa::WideSmem<D, EIGHT, SLOTS>::kBytes, rows8 = 128 * SLOTS;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  static std::once_flag once[64];
+  static cudaError_t attr_err[64];
+  std::call_once(once[dev & 63], [&] {
+    attr_err[dev & 63] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
+  if (attr_err[dev & 63] != cudaSuccess) return cuda_fail(attr_err[dev & 63]);
+  const int sms = sm_count();
+  if (sms <= 0) return cuda_fail(cudaErrorInvalidDevice);
+  fa::DecodeCore& c = p.c;
+  c.groups = (int)(((long long)c.rows + rows8 - 1) / rows8);
+  if ((long long)c.Hkv * c.groups > 0x7FFFFFFFLL) return FA_ERR_SHAPE;
+  c.units = c.Hkv * c.groups;
+  const long long most = ((keys + fa::kWideTile - 1) / fa::kWideTile + fa::kUnitTiles) * c.B * c.units;
+  c.ctas = (int)std::min<long long>(sms, most);
+  auto inverse = [](unsigned long long d) { return d == 1 ? 0ull : ~0ull / d + 1; };   // ceil(2^64 / d)
+  c.ctas_inv = inverse(c.ctas);
+  c.units_inv = inverse(c.units);
+  const size_t o_bytes = (size_t)2 * c.ctas * rows8 * D * 4;
+  void* scratch = scratch_alloc(o_bytes + (size_t)2 * c.ctas * rows8 * 8, st);
+  if (!scratch) return cuda_fail(cudaGetLastError());
+  c.part_o = static_cast<float*>(scratch);
+  c.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(scratch) + o_bytes);
+  cudaError_t e = launch_dependent(kern, (unsigned)c.ctas, fa::kWideThreads<EIGHT, SLOTS>, smem, st, p);
+  if (e == cudaSuccess) {   // (as fa_paged.cu joins)
+    const long long rows = (long long)c.B * c.Hkv * c.rows;
+    constexpr int T = fa::kWideTile;
+    if (rows > 8LL * sms)
+      e = launch_dependent(fa::fa_decode_join_kernel<BF16, D, 1, T>, (unsigned)((rows + 7) / 8), 256, 0, st, c, rows8);
+    else if (c.ctas / ((long long)c.B * c.units) < 32)
+      e = launch_dependent(fa::fa_decode_join_kernel<BF16, D, 8, T>, (unsigned)rows, 256, 0, st, c, rows8);
+    else
+      e = launch_dependent(fa::fa_decode_join_kernel<BF16, D, 32, T>, (unsigned)rows, 1024, 0, st, c, rows8);
+  }
+  cudaFreeAsync(scratch, st);
+  return e == cudaSuccess ? FA_OK : cuda_fail(e);
+}
+template <bool BF16, int D>
+int launch_wide_type(fa::WideParams& p, bool eight, long long keys, cudaStream_t st) {
+  const bool two = p.c.rows > 128;
+  if (eight) return two ? launch_wide_slots<BF16, D, true, 2>(p, keys, st) : launch_wide_slots<BF16, D, true, 1>(p, keys, st);
+  return two ? launch_wide_slots<BF16, D, false, 2>(p, keys, st) : launch_wide_slots<BF16, D, false, 1>(p, keys, st);
+}
+
+}  // namespace
+
+int launch_wide(fa::WideParams& p, bool fp16, int D, bool eight, long long keys, cudaStream_t st) {
+  if (D == 128) return fp16 ? launch_wide_type<false, 128>(p, eight, keys, st) : launch_wide_type<true, 128>(p, eight, keys, st);
+  return fp16 ? launch_wide_type<false, 64>(p, eight, keys, st) : launch_wide_type<true, 64>(p, eight, keys, st);
+}
 
 int launch_decode8(fa::Decode8Params& p, bool fp16, int D, long long keys, cudaStream_t st) {
   if (D == 128) return fp16 ? launch_decode8_format<false, 128>(p, keys, st) : launch_decode8_format<true, 128>(p, keys, st);

@@ -17,20 +17,30 @@ namespace fa {
 constexpr int kLeastExp = -80;          // of a scale: 2^31 times 2^(15 - e), a softmax's sum (fa_decode8.cuh), stays an fp32 number
 constexpr uint32_t kScaleNone = 255;    // the scale byte of a row that was not finite
 
-__device__ __forceinline__ uint32_t codes_f16x2(uint32_t two, bool e5m2) {   // two codes in bits 0-15, exactly
+template <bool E5M2>
+__device__ __forceinline__ uint32_t codes_f16x2(uint32_t two) {   // two codes in bits 0-15, exactly
   uint32_t r;
-  if (e5m2)
+  if constexpr (E5M2)
     asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.f16x2.e5m2x2 %0, t;\n}" : "=r"(r) : "r"(two));
   else
     asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}" : "=r"(r) : "r"(two));
   return r;
 }
-__device__ __forceinline__ uint32_t codes_of(float lo, float hi, bool e5m2) {   // to the nearest code, ties to even
-  uint16_t r;
-  if (e5m2)
-    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+template <bool E5M2>
+__device__ __forceinline__ uint32_t codes_of(float a, float b, float c, float d) {   // to the nearest codes, ties to even
+  uint32_t r;
+  if constexpr (E5M2)
+    asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e5m2x2.f32 l, %2, %1;\n cvt.rn.satfinite.e5m2x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}"
+        : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
   else
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}"
+        : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+// the largest magnitude of three, NaN where one of them is
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 // 2^e from the scale byte e + 127 (infinity from kScaleNone)
@@ -39,16 +49,16 @@ __device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_floa
 // The codes of a row that L neighbouring lanes hold, 16 channels each, and its scale byte.  A row that
 // is not finite becomes NaN (scale byte 255) and is reported: no code stands for an infinity.
 template <int L>
-__device__ __forceinline__ uint32_t quantise_row(const float (&a)[8], const float (&d)[8], bool e5m2, uint2& qa,
+__device__ __forceinline__ uint32_t quantise_row(const float (&a)[8], const float (&d)[8], int e5m2, uint2& qa,
                                                  uint2& qd, int* status) {
-  // (as whole numbers: of the magnitudes' bits NaN is the largest, infinity next)
-  uint32_t top = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) top = max(top, max(__float_as_uint(a[j]) & 0x7FFFFFFFu, __float_as_uint(d[j]) & 0x7FFFFFFFu));
+  float t0 = max3_abs_nan(a[0], a[1], a[2]), t1 = max3_abs_nan(d[0], d[1], d[2]);
+  t0 = max3_abs_nan(t0, a[3], a[4]), t1 = max3_abs_nan(t1, d[3], d[4]);
+  t0 = max3_abs_nan(t0, a[5], a[6]), t1 = max3_abs_nan(t1, d[5], d[6]);
+  uint32_t top = __float_as_uint(max3_abs_nan(max3_abs_nan(t0, a[7], d[7]), t1, t1));
   const unsigned lane = threadIdx.x & 31;
   const unsigned row = ((1u << L) - 1u) << (lane & ~(unsigned)(L - 1));   // (rows of a warp may be on their own)
 #pragma unroll
-  for (int m = 1; m < L; m <<= 1) top = max(top, __shfl_xor_sync(row, top, m));
+  for (int m = 1; m < L; m <<= 1) top = max(top, __shfl_xor_sync(row, top, m));   // (by its bits NaN is the largest)
   if (top >= 0x7F800000u) {
     qa = qd = make_uint2(0, 0);
     if ((lane & (L - 1)) == 0) atomicOr(status, fa_host::kStatusRange);
@@ -57,28 +67,32 @@ __device__ __forceinline__ uint32_t quantise_row(const float (&a)[8], const floa
   // the largest is m 2^x, 1 <= m < 2: it fits 1.75 * 2^(8 or 15) at e = x - (8 or 15), one more where m > 1.75
   // (no more than keeps the largest code an fp32 and bf16 number; there it saturates)
   const int fit = e5m2 ? 15 : 8;
-  int e = (int)(top >> 23) - 127 - fit + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  int e = (int)((top + 0x1FFFFFu) >> 23) - 127 - fit;      // (0x1FFFFF carries a mantissa above 0x600000)
   e = min(max(e, kLeastExp), 127 - fit);
   const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-  auto pack = [&](const float (&x)[8]) {
-    return make_uint2(codes_of(x[0] * f, x[1] * f, e5m2) | codes_of(x[2] * f, x[3] * f, e5m2) << 16,
-                      codes_of(x[4] * f, x[5] * f, e5m2) | codes_of(x[6] * f, x[7] * f, e5m2) << 16);
-  };
-  qa = pack(a);
-  qd = pack(d);
+  float x[8], y[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = a[j] * f, y[j] = d[j] * f;
+  if (e5m2) {
+    qa = make_uint2(codes_of<true>(x[0], x[1], x[2], x[3]), codes_of<true>(x[4], x[5], x[6], x[7]));
+    qd = make_uint2(codes_of<true>(y[0], y[1], y[2], y[3]), codes_of<true>(y[4], y[5], y[6], y[7]));
+  } else {
+    qa = make_uint2(codes_of<false>(x[0], x[1], x[2], x[3]), codes_of<false>(x[4], x[5], x[6], x[7]));
+    qd = make_uint2(codes_of<false>(y[0], y[1], y[2], y[3]), codes_of<false>(y[4], y[5], y[6], y[7]));
+  }
   return (uint32_t)(e + 127);
 }
 
 // The cache type's numbers around the eight values that codes stand for: a bf16 is the value itself, of
 // fp16 (too narrow for some) the next below and above.
-template <bool BF16>
-__device__ __forceinline__ void stored_bounds(uint2 codes, uint32_t scale, bool e5m2, uint4& lo, uint4& hi) {
+template <bool BF16, bool E5M2>
+__device__ __forceinline__ void stored_bounds(uint2 codes, uint32_t scale, uint4& lo, uint4& hi) {
   const float f = scale_of(scale);
   uint32_t l[4], h[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint32_t two = (j < 2 ? codes.x : codes.y) >> (16 * (j & 1));
-    const uint32_t x = codes_f16x2(two & 0xFFFFu, e5m2);
+    const uint32_t x = codes_f16x2<E5M2>(two);
     const float x0 = f16_lo_to_f32(x) * f, x1 = f16_hi_to_f32(x) * f;
     if constexpr (BF16) {
       l[j] = h[j] = pack_bf16x2(x0, x1);
@@ -97,13 +111,13 @@ __device__ __forceinline__ void stored_bounds(uint2 codes, uint32_t scale, bool 
 }
 
 // Eight codes as the cache's type, rounded once (exact in bf16).
-template <bool BF16>
-__device__ __forceinline__ uint4 read_codes(uint2 codes, float f, bool e5m2) {
+template <bool BF16, bool E5M2>
+__device__ __forceinline__ uint4 read_codes(uint2 codes, float f) {
   float x[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint32_t two = (j < 2 ? codes.x : codes.y) >> (16 * (j & 1));
-    const uint32_t h = codes_f16x2(two & 0xFFFFu, e5m2);
+    const uint32_t h = codes_f16x2<E5M2>(two);
     x[2 * j] = f16_lo_to_f32(h) * f;
     x[2 * j + 1] = f16_hi_to_f32(h) * f;
   }

@@ -7,6 +7,7 @@
 #include "fa_host.h"
 #include "fa_kv_append.cuh"
 #include "fa_kv_move.cuh"
+#include "fa_wide.cuh"
 
 namespace fa_host {
 
@@ -34,6 +35,7 @@ cudaError_t launch_append(const fa::AppendParams& p, bool fp16, int D, bool inte
 cudaError_t launch_append_placed(const fa::AppendParams& p, bool fp16, int D, bool interleaved, long long pieces, cudaStream_t st);
 cudaError_t launch_append8(const fa::AppendParams& p, bool fp16, int D, bool interleaved, long long pieces, cudaStream_t st);
 int launch_decode8(fa::Decode8Params& p, bool fp16, int D, long long keys, cudaStream_t st);   // an FA_* code
+int launch_wide(fa::WideParams& p, bool fp16, int D, bool eight, long long keys, cudaStream_t st);   // an FA_* code
 cudaError_t launch_read(const fa::ReadParams& p, bool fp16, int D, bool eight, unsigned blocks, cudaStream_t st);
 cudaError_t launch_keep(const fa::KeepParams& p, bool fp16, int D, bool eight, unsigned blocks, cudaStream_t st);
 

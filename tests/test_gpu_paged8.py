@@ -398,14 +398,15 @@ def test_decode8(case):
 
 @pytest.mark.parametrize("dtype,fmt,D", [("bf16", "e4m3fn", 128), ("fp16", "e4m3fn", 64), ("fp16", "e5m2", 128)])
 @pytest.mark.parametrize("spread", [3.0, 12.0])
-def test_decode8_values_of_any_size(dtype, fmt, D, spread):
+@pytest.mark.parametrize("Sq", [1, 12, 40])
+def test_decode8_values_of_any_size(dtype, fmt, D, spread, Sq):
     """Values whose rows differ by many powers of two: small ones with large
     probabilities beside large ones with small, rows of zeros among them."""
     lens = [700, 33, 130]
     for scale in (0.05, D ** -0.5, 1.0):
         c = Cache8(7, dtype, fmt, 3, 2, D, 32, lens, spread=spread)
-        if dtype == "fp16":              # (the answers must fit)
-            shift = max(0, int(c.ve.max()) - 4)
+        if dtype == "fp16":              # (the answers must fit: 448 * 2^4, 57344 * 2^0)
+            shift = max(0, int(c.ve.max()) - (4 if fmt == "e4m3fn" else 0))
             c.ve -= shift
         zero = c.rng.random(c.ve.shape) < 0.1
         c.vc[zero], c.ve[zero] = 0, P.LEAST
@@ -413,7 +414,7 @@ def test_decode8_values_of_any_size(dtype, fmt, D, spread):
         c.v = np.ldexp(c.vc, c.ve[..., None])
         c.bv.copy_(_codes(c.vc, fmt).view(c.bv.dtype))
         c.sv.copy_(_dev((c.ve + 127).astype(np.uint8)))
-        q = _round(c.rng.standard_normal((3, 8, 1, D)), dtype)
+        q = _round(c.rng.standard_normal((3, 8, Sq, D)), dtype)
         _decode8(c, q, lens, f"spread {spread} scale {scale}", scale=scale)
 
 
@@ -442,6 +443,8 @@ def test_decode8_all_values_zero_and_queries_of_any_size():
     ("fp16", "e5m2", 2, 6, 3, 64, 16, 3, [500, 40], 12),
     ("bf16", "e4m3fn", 1, 4, 1, 128, 256, 2, [1500], 3),
     ("bf16", "e4m3fn", 70, 2, 2, 64, 32, 1, [100] * 70, 64),
+    ("bf16", "e4m3fn", 3, 8, 2, 128, 64, 10, [1000, 130, 5], 4),
+    ("fp16", "e5m2", 2, 6, 1, 64, 16, 30, [500, 40], 12),
 ])
 def test_decode8_listed_pages(dtype, fmt, B, Hq, Hkv, D, page, Sq, lens, sel):
     c = Cache8(9, dtype, fmt, B, Hkv, D, page, lens, stale=True)
@@ -493,11 +496,12 @@ def test_decode8_many_sequences(B, Hq, Hkv, page, Sq):
     _decode8(c, _round(rng.standard_normal((B, Hq, Sq, 64)), "bf16"), lens, "many")
 
 
-def test_decode8_leaves_out_bad_pages():
+@pytest.mark.parametrize("Sq", [1, 20])
+def test_decode8_leaves_out_bad_pages(Sq):
     import attention_forward_fa_gb300 as fa
     lens = [200, 200, 200]
     c = Cache8(13, "bf16", "e4m3fn", 3, 2, 128, 16, lens)
-    q = _round(c.rng.standard_normal((3, 4, 1, 128)), "bf16")
+    q = _round(c.rng.standard_normal((3, 4, Sq, 128)), "bf16")
     c.table[0, 2], c.table[1, 12] = c.k.shape[0], -1
     c.obj.page_table.copy_(_dev(c.table))
     o, l = fa.flash_attention_decode(_dev(q, "bf16"), c.obj, c.ints(lens))
@@ -510,6 +514,46 @@ def test_decode8_leaves_out_bad_pages():
     o, l = fa.flash_attention_decode(_dev(q, "bf16"), c.obj, c.ints([-3, 200000, 200]))
     assert _status() == fa.FA_ERR_INDEX
     assert bool((o[:2] == 0).all()) and bool((l[:2] == math.inf).all())
+
+
+@pytest.mark.parametrize("dtype,fmt,G,Sq,n,grow", [
+    ("fp16", "e4m3fn", 5, 8, 20000, 0.0), ("bf16", "e5m2", 4, 40, 9000, 0.0), ("fp16", "e4m3fn", 34, 1, 26000, 2e-3),
+    ("bf16", None, 3, 13, 20000, 0.0), ("fp16", None, 5, 30, 17000, 3e-3),
+])
+def test_many_rows_over_long_pieces(dtype, fmt, G, Sq, n, grow):
+    """More tiles of one unit in one CTA than add up in the accumulator, with scores that
+    grow along the keys too: 160 sequences over the same pages, the same queries."""
+    import torch
+    import attention_forward_fa_gb300 as fa
+    B, page, D = 160, 64, 64
+    c = Cache(30, dtype, 1, 1, D, page, [n]) if fmt is None else Cache8(30, dtype, fmt, 1, 1, D, page, [n], spread=2.0)
+    if grow:
+        k = c.k[c.table[0], 0].reshape(-1, D)
+        k[:, 0] = np.arange(k.shape[0]) * grow
+        if fmt is None:
+            c.k[c.table[0], 0] = _round(k, dtype).reshape(-1, page, D)
+            c.tk.copy_(_dev(c.k, dtype))
+        else:
+            c.kc[c.table[0], 0], c.ke[c.table[0], 0] = P.quantise(k.reshape(-1, page, D), fmt)
+            c.k = np.ldexp(c.kc, c.ke[..., None])
+            c.bk.copy_(_codes(c.kc, fmt).view(c.bk.dtype))
+            c.sk.copy_(_dev((c.ke + 127).astype(np.uint8)))
+    q = _round(c.rng.standard_normal((1, G, Sq, D)), dtype)
+    q[..., 0] = np.abs(q[..., 0])
+    anc, _ = _trees(c.rng, 1, Sq)
+    table = c.obj.page_table.expand(B, -1).contiguous()
+    many = (fa.PagedKV(c.obj.k_pages, c.obj.v_pages, table) if fmt is None else
+            fa.PagedKV(c.obj.k_pages, c.obj.v_pages, table, k_scale=c.sk, v_scale=c.sv, dtype=_torch_type(dtype)))
+    o, l = fa.flash_attention_decode_tree(_dev(q, dtype).expand(B, -1, -1, -1).contiguous(), many,
+                                          torch.full((B,), n, dtype=torch.int32, device="cuda"), _dev(anc[0]))
+    assert _status() == 0
+    a = (c.table, [n], D ** -0.5)
+    ref = P.decode(q, c.k, c.v, *a, tree=(anc, [Sq]))
+    for b in (0, 1, 77, 151, 152, 159):
+        if fmt is None:
+            _check(o[b:b + 1], l[b:b + 1], ref, dtype, f"sequence {b}")
+        else:
+            _check8(o[b:b + 1], l[b:b + 1], ref, *_spread(c, q, *a, (anc, [Sq])), dtype, f"sequence {b}")
 
 
 # ------------------------------------------------------------------ trees
