@@ -101,16 +101,21 @@ int launch_decode8_format(fa::Decode8Params& p, long long keys, cudaStream_t st)
 
 namespace {
 
-template <bool BF16, int D, bool EIGHT, int SLOTS>
-int launch_wide_slots(fa::WideParams& p, long long keys, cudaStream_t st) {
-  auto kern = fa::fa_wide_kernel<BF16, D, EIGHT, SLOTS>;
-  constexpr int smem = fa::WideSmem<D, EIGHT, SLOTS>::kBytes, rows8 = 128 * SLOTS;
+template <bool BF16, int D, bool EIGHT, bool SPLIT>
+int launch_wide_rows(fa::WideParams& p, long long keys, cudaStream_t st) {
+  auto kern = fa::fa_wide_kernel<BF16, D, EIGHT, SPLIT>;
+  constexpr int smem = fa::WideSmem<D, EIGHT, SPLIT>::kBytes, rows8 = SPLIT ? 128 : 256;
   int dev = 0;
   cudaGetDevice(&dev);
   static std::once_flag once[64];
   static cudaError_t attr_err[64];
   std::call_once(once[dev & 63], [&] {
-    attr_err[dev & 63] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t& e = attr_err[dev & 63];
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // The warps trade registers with setmaxnreg, which would wait forever for more than the launch gave.
+    cudaFuncAttributes a;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, kern);
+    if (e == cudaSuccess && a.numRegs < fa::kWideRegs<EIGHT>) e = cudaErrorInvalidConfiguration;
   });
   if (attr_err[dev & 63] != cudaSuccess) return cuda_fail(attr_err[dev & 63]);
   const int sms = sm_count();
@@ -125,11 +130,13 @@ int launch_wide_slots(fa::WideParams& p, long long keys, cudaStream_t st) {
   c.ctas_inv = inverse(c.ctas);
   c.units_inv = inverse(c.units);
   const size_t o_bytes = (size_t)2 * c.ctas * rows8 * D * 4;
-  void* scratch = scratch_alloc(o_bytes + (size_t)2 * c.ctas * rows8 * 8, st);
+  const size_t ml_bytes = (size_t)2 * c.ctas * rows8 * 8;
+  void* scratch = scratch_alloc(o_bytes + ml_bytes + (size_t)2 * c.ctas * 128 * D * 4, st);
   if (!scratch) return cuda_fail(cudaGetLastError());
   c.part_o = static_cast<float*>(scratch);
   c.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(scratch) + o_bytes);
-  cudaError_t e = launch_dependent(kern, (unsigned)c.ctas, fa::kWideThreads<EIGHT, SLOTS>, smem, st, p);
+  p.gone = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + o_bytes + ml_bytes);
+  cudaError_t e = launch_dependent(kern, (unsigned)c.ctas, fa::kWideThreads<EIGHT>, smem, st, p);
   if (e == cudaSuccess) {   // (as fa_paged.cu joins)
     const long long rows = (long long)c.B * c.Hkv * c.rows;
     constexpr int T = fa::kWideTile;
@@ -145,9 +152,9 @@ int launch_wide_slots(fa::WideParams& p, long long keys, cudaStream_t st) {
 }
 template <bool BF16, int D>
 int launch_wide_type(fa::WideParams& p, bool eight, long long keys, cudaStream_t st) {
-  const bool two = p.c.rows > 128;
-  if (eight) return two ? launch_wide_slots<BF16, D, true, 2>(p, keys, st) : launch_wide_slots<BF16, D, true, 1>(p, keys, st);
-  return two ? launch_wide_slots<BF16, D, false, 2>(p, keys, st) : launch_wide_slots<BF16, D, false, 1>(p, keys, st);
+  const bool split = p.c.rows <= 128;
+  if (eight) return split ? launch_wide_rows<BF16, D, true, true>(p, keys, st) : launch_wide_rows<BF16, D, true, false>(p, keys, st);
+  return split ? launch_wide_rows<BF16, D, false, true>(p, keys, st) : launch_wide_rows<BF16, D, false, false>(p, keys, st);
 }
 
 }  // namespace

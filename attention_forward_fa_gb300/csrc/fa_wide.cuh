@@ -6,13 +6,17 @@
 // the keys' bytes (1.4 us a row for 16 sequences of 4096 tokens on 8 KV heads).
 // Here up to 128 rows are the lanes of one accumulator, a row per softmax thread,
 // and a tile of 128 keys costs about 1000 cycles of the tensor cores whatever the
-// rows, below the 2900 that its 64 KB take from memory (an 8-bit tile: 1450); a
-// unit of up to 256 rows has two such slots, which share every key tile.
+// rows (over a 16-bit cache 1500), below the 2900 that its 64 KB take from memory (an
+// 8-bit tile: 1450).
 //
-//   * One CTA per SM; per slot four softmax warps, a producer warp, a warp whose
-//     first lane issues the MMAs, and over an 8-bit cache four converter warps.
-//     All hand-offs are mbarriers with bounded waits; no role waits for another in
-//     any other way, so that an expired wait ends every role by the abort flag.
+//   * One CTA per SM with two accumulators and two groups of softmax warps, which take
+//     turns with the tensor cores.  A unit of up to 256 rows has 128 in each and shares
+//     every key tile; with up to 128 rows (SPLIT) both have all rows and take every other
+//     tile, and the first group joins the two at a piece's end.
+//   * A producer warp, a warp whose first lane issues the MMAs, and over an 8-bit cache
+//     four converter warps.  All hand-offs are mbarriers with bounded waits; no role waits
+//     for another in any other way, so that an expired wait ends every role by the
+//     abort flag.
 //   * Loads K(0), V(0), K(1), ... go through one ring of operand tiles (128 keys,
 //     D / 64 chunks of 64 channels, 128-byte swizzle).  A 16-bit tile comes by TMA, a box
 //     per page part and chunk; an 8-bit one comes as codes into a second ring, and
@@ -24,13 +28,13 @@
 //     exponent of the probabilities as in fa_decode8.cuh, but only in tiles whose values'
 //     scales are within those limits, so that every product's operand is exact; in others
 //     the codes stay and the softmax threads take each key's exponent, which is slow.
-//   * S(t, j + 1) is issued behind P V (t, j), so that its commit says that O is at rest:
-//     the softmax threads may then move their references and rescale O.
-//   * P is written over S: as a hi + lo pair of the cache's type (16-bit: 64 + 64 columns,
-//     which takes the upper half of S first), or as one fp16 (8-bit).
+//   * The next S of a group is issued behind its P V, so that its commit says that O is at
+//     rest: the softmax threads may then move their references and rescale O.
+//   * P is written over S: as a hi + lo pair of the cache's type (16-bit: 64 + 64 columns),
+//     or as one fp16 (8-bit).
 //   * Up to kWideFlush tiles of a piece add up in TMEM, where the adder cuts off what it adds
 //     (about 2^-24 of the sum each 16 keys, always towards zero: 2^-15 over 8192 keys);
-//     then the softmax threads add O to the piece's place in scratch in fp32.
+//     then the softmax threads add O to a place in scratch in fp32.
 #pragma once
 #include <type_traits>
 
@@ -39,7 +43,7 @@
 namespace fa {
 
 constexpr int kWideTile = 128;
-constexpr int kWideInfo = 8;       // tiles whose keys and scales are kept: a producer is at most six ahead
+constexpr int kWideInfo = 8;       // tiles whose keys and scales are kept: the producer is at most seven ahead
 
 constexpr int kWideFlush = 64;     // tiles that add up in TMEM
 
@@ -48,6 +52,7 @@ struct WideParams {
   const uint8_t* k_scale;          // 8-bit caches
   const uint8_t* v_scale;
   int e5m2;
+  float* gone;                     // [ctas][groups][128][D]: sums that have left the accumulators
   CUtensorMap tm_k;                // 16-bit: (64 channels, slots, D / 64, heads, pages); 8-bit: (D, slots, heads, pages)
   CUtensorMap tm_v;
 };
@@ -59,25 +64,36 @@ struct WideTileInfo {              // of an 8-bit tile
   int each;                        // the values' exponents are taken key by key
 };
 
-template <int D, bool EIGHT, int SLOTS>
+template <int D, bool EIGHT, bool SPLIT>
 struct WideSmem {
-  static constexpr int kOp = 128 * D * 2;                        // an operand tile: Q of a slot, K or V
-  static constexpr int kStages = EIGHT ? (D == 128 ? 3 : 4) : (D == 128 ? (SLOTS == 2 ? 5 : 6) : 10);
-  static constexpr int kRawStages = !EIGHT ? 0 : D == 128 ? (SLOTS == 2 ? 3 : 5) : 8;
+  static constexpr int kOp = 128 * D * 2;                        // an operand tile: 128 rows of Q, K or V
+  static constexpr int kStages = D == 64 ? (EIGHT ? 4 : 10) : EIGHT ? (SPLIT ? 4 : 3) : SPLIT ? 6 : 5;
+  static constexpr int kRawStages = !EIGHT ? 0 : D == 128 ? 3 : 8;
   static constexpr int kRaw = 128 * D;                           // codes of K or V of a tile
-  static constexpr int kRingOff = SLOTS * kOp;
+  static constexpr int kRingOff = (SPLIT ? 1 : 2) * kOp;         // (behind Q)
   static constexpr int kRawOff = kRingOff + kStages * kOp;
   static constexpr int kScaleOff = kRawOff + kRawStages * kRaw;  // bytes [kWideInfo][K, V][128]
   static constexpr int kMetaOff = kScaleOff + (EIGHT ? kWideInfo * 256 : 0);     // int [kWideInfo][8]
   static constexpr int kInfoOff = kMetaOff + kWideInfo * 32;     // WideTileInfo [kWideInfo]
-  static constexpr int kBarOff = kInfoOff + kWideInfo * 16;
-  static constexpr int kBars = 2 * kStages + 2 * kRawStages + 3 * SLOTS + 2;
+  static constexpr int kMlOff = kInfoOff + kWideInfo * 16;       // float2 [128]: the second group's reference and sum
+  static constexpr int kBarOff = kMlOff + (SPLIT ? 1024 : 0);
+  static constexpr int kBars = 2 * kStages + 2 * kRawStages + 9;
   static constexpr int kMiscOff = kBarOff + kBars * 8;
   static constexpr int kBytes = kMiscOff + 64;
   static_assert(kBytes <= 227 * 1024, "one CTA per SM");
 };
-template <bool EIGHT, int SLOTS>
-constexpr int kWideThreads = 32 * (4 * SLOTS + 2 + (EIGHT ? 4 : 0));
+// Two groups of four softmax warps, one of producer and issuer (and two idle warps), one of converters.
+template <bool EIGHT>
+constexpr int kWideThreads = EIGHT ? 512 : 384;
+// Registers per thread at launch, and of the softmax warps and the others after they have traded.
+template <bool EIGHT>
+constexpr int kWideRegs = EIGHT ? 128 : 168;
+template <bool EIGHT>
+constexpr int kWideSoftmaxRegs = EIGHT ? 200 : 208;
+template <bool EIGHT>
+constexpr int kWideOtherRegs = EIGHT ? 56 : 88;
+static_assert(256 * kWideSoftmaxRegs<true> + 256 * kWideOtherRegs<true> <= 512 * kWideRegs<true>, "what the CTA has");
+static_assert(256 * kWideSoftmaxRegs<false> + 128 * kWideOtherRegs<false> <= 384 * kWideRegs<false>, "what the CTA has");
 
 __device__ __forceinline__ void tma_load_5d_chunk(uint32_t dst, const void* tmap, uint32_t bar, int slot, int chunk,
                                                   int head, int page) {
@@ -93,15 +109,15 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-template <bool BF16, int D, bool EIGHT, int SLOTS>
-__global__ void __launch_bounds__(kWideThreads<EIGHT, SLOTS>, 1) fa_wide_kernel(const __grid_constant__ WideParams params) {
+template <bool BF16, int D, bool EIGHT, bool SPLIT>
+__global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const __grid_constant__ WideParams params) {
   const DecodeCore& p = params.c;
-  using SM = WideSmem<D, EIGHT, SLOTS>;
+  using SM = WideSmem<D, EIGHT, SPLIT>;
   constexpr int NS = SM::kStages, RS = EIGHT ? SM::kRawStages : 1;
-  constexpr int kRows = 128 * SLOTS;
+  constexpr int kRows = SPLIT ? 128 : 256;            // of a unit
   constexpr bool kP16 = EIGHT || !BF16;               // the type of P (and of Q, K and V as operands): fp16 or bf16
   constexpr float kLiftP = kLift<!kP16>;
-  constexpr int kProducer = 4 * SLOTS, kIssuer = kProducer + 1, kConvert = kIssuer + 1;
+  constexpr int kProducer = 8, kIssuer = 9, kConvert = 12;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -111,10 +127,10 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT, SLOTS>, 1) fa_wide_kernel(
   auto RFULL = [&](int s) { return BAR(2 * NS + s); };             // codes are there
   auto REMPTY = [&](int s) { return BAR(2 * NS + RS + s); };       // they are converted
   constexpr int kB = 2 * NS + 2 * SM::kRawStages;
-  auto SFULL = [&](int t) { return BAR(kB + t); };                 // S of slot t
-  auto PREADY = [&](int t) { return BAR(kB + SLOTS + t); };        // P of slot t, O rescaled
-  auto OFULL = [&](int t) { return BAR(kB + 2 * SLOTS + t); };     // O of slot t, at a piece's end
-  const uint32_t QREADY = BAR(kB + 3 * SLOTS), DRAIN = BAR(kB + 3 * SLOTS + 1);
+  auto SFULL = [&](int t) { return BAR(kB + t); };                 // S of group t
+  auto PREADY = [&](int t) { return BAR(kB + 2 + t); };            // P of group t, O rescaled
+  auto OFULL = [&](int t) { return BAR(kB + 4 + t); };             // O of group t, at a piece's end
+  const uint32_t QREADY = BAR(kB + 6), DRAIN = BAR(kB + 7), JOIN = BAR(kB + 8);
   int* s_meta = reinterpret_cast<int*>(smem + SM::kMetaOff);       // per tile: first key of each 16, or -1
   WideTileInfo* s_info = reinterpret_cast<WideTileInfo*>(smem + SM::kInfoOff);
   DecodeWalk* s_walk = reinterpret_cast<DecodeWalk*>(smem + SM::kMiscOff);
@@ -134,18 +150,19 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT, SLOTS>, 1) fa_wide_kernel(
         mbar_init(RFULL(s), 1);
         mbar_init(REMPTY(s), 4);
       }
-    for (int t = 0; t < SLOTS; ++t) {
+    for (int t = 0; t < 2; ++t) {
       mbar_init(SFULL(t), 1);
       mbar_init(PREADY(t), 4);
       mbar_init(OFULL(t), 1);
     }
-    mbar_init(QREADY, 4 * SLOTS);
+    mbar_init(QREADY, 8);
     mbar_init(DRAIN, 1);
+    mbar_init(JOIN, 4);
     fence_mbar_init();
     *s_abort = 0;
   }
   if (warp == kIssuer) {
-    tmem_alloc(smem_u32(s_tmem), 256 * SLOTS);
+    tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
     tc_fence_before();
   }
@@ -162,7 +179,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT, SLOTS>, 1) fa_wide_kernel(
   const WaitCtx wc{s_abort, p.status, p.timeout_ns};
   const int box_shift = min(p.page_shift, 7);     // slots per copy
   const int box = 1 << box_shift;
-  // The next piece: its sequence, unit, span and tiles, and its number among this role's tiles.
+  // The next piece: its sequence, unit, span and tiles.
   struct Piece {
     int b, unit, len;
     DecodeSpan s;
@@ -181,9 +198,9 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT, SLOTS>, 1) fa_wide_kernel(
     return false;
   };
   Piece x;
-
   if (warp == kProducer) {
     // ============================================================ producer
+    regs_dec<kWideOtherRegs<EIGHT>>();
     int tile = 0;                                     // of this CTA; its loads are 2 tile (K) and 2 tile + 1 (V)
     bool dead = false;
     const int nsub = kWideTile >> box_shift;
@@ -258,57 +275,88 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT, SLOTS>, 1) fa_wide_kernel(
     __syncwarp();
   } else if (warp == kIssuer) {
     // ============================================================ MMA issue
+    regs_dec<kWideOtherRegs<EIGHT>>();
     if (lane == 0) {
       constexpr uint32_t kIdescS = idesc_f16(128, 128, !kP16, false);
       constexpr uint32_t kIdescO = idesc_f16(128, D, !kP16, true);
       const uint64_t q0 = sw128_desc(sbase, 16, 1024);
       const uint64_t k0 = sw128_desc(sbase + SM::kRingOff, 16, 1024);
       const uint64_t v0 = sw128_desc(sbase + SM::kRingOff, 128 * 128, 1024);
-      int tile = 0, piece = 0;
+      int tile = 0, piece = 0, done[2] = {0, 0};       // tiles whose P group t has made
       bool ok = true;
-      int p_phase = 0;                                 // of PREADY: tiles so far
-      auto scores = [&](int t, int ld) {
-        const uint64_t a = q0 + ((t * SM::kOp) >> 4), b = k0 + (((ld % NS) * SM::kOp) >> 4);
+      // S of group t from the K of `tl`, whose stage is given back behind the last group that reads it
+      auto scores = [&](int t, int tl, bool last) {
+        const int ld = 2 * tl;
+        const uint64_t a = q0 + (SPLIT ? 0 : (t * SM::kOp) >> 4), b = k0 + (((ld % NS) * SM::kOp) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
           mma_ss(tmem + 128 * t, a + off, b + off, kIdescS, kk > 0);
         }
         mma_commit(SFULL(t));
+        if (last) mma_commit(EMPTY(ld % NS));
+      };
+      auto values = [&](int t, int tl, int i, bool last) {     // i: the group's tiles of the piece before this one
+        const int ld = 2 * tl + 1;
+        const uint64_t b = v0 + (((ld % NS) * SM::kOp) >> 4);
+        const uint32_t o = tmem + 256 + 128 * t, s = tmem + 128 * t;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) mma_ts(o, s + 8 * kk, b + (kk * 2048 >> 4), kIdescO, i % kWideFlush || kk);
+        if constexpr (!EIGHT) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) mma_ts(o, s + 64 + 8 * kk, b + (kk * 2048 >> 4), kIdescO, 1);
+        }
+        if (last) mma_commit(EMPTY(ld % NS));
+      };
+      auto landed = [&](int ld) {
+        const bool got = wait_bar(FULL(ld % NS), (ld / NS) & 1, wc);
+        tc_fence_after();
+        return got;
+      };
+      auto ready = [&](int t) {
+        const bool got = wait_bar(PREADY(t), done[t]++ & 1, wc);
+        tc_fence_after();
+        return got;
       };
       while (ok && next_piece(x)) {
-        ok = wait_bar(QREADY, piece & 1, wc);
-        if (ok) ok = wait_bar(FULL((2 * tile) % NS), ((2 * tile) / NS) & 1, wc);
+        const int nt = x.d.nt;
+        ok = wait_bar(QREADY, piece & 1, wc) && landed(2 * tile);
         if (!ok) break;
-        tc_fence_after();
-        for (int t = 0; t < SLOTS; ++t) scores(t, 2 * tile);
-        mma_commit(EMPTY((2 * tile) % NS));
-        for (int j = 0; j < x.d.nt && ok; ++j, ++tile, ++p_phase) {
-          const int vl = 2 * tile + 1, kl = 2 * tile + 2;
-          ok = wait_bar(FULL(vl % NS), (vl / NS) & 1, wc);
-          const bool more = j + 1 < x.d.nt;
-          for (int t = 0; t < SLOTS && ok; ++t) {
-            ok = wait_bar(PREADY(t), p_phase & 1, wc);
+        if constexpr (SPLIT) {
+          scores(0, tile, true);
+          if (nt > 1) {
+            ok = landed(2 * tile + 2);
+            if (ok) scores(1, tile + 1, true);
+          }
+        } else {
+          scores(0, tile, false);
+          scores(1, tile, true);
+        }
+        for (int j = 0; j < nt && ok; ++j, ++tile) {
+          ok = landed(2 * tile + 1);
+          if constexpr (SPLIT) {
+            const int t = j & 1;
+            ok = ok && ready(t);
             if (!ok) break;
-            tc_fence_after();
-            const uint64_t b = v0 + (((vl % NS) * SM::kOp) >> 4);
-            const uint32_t o = tmem + 128 * SLOTS + 128 * t, s = tmem + 128 * t;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) mma_ts(o, s + 8 * kk, b + (kk * 2048 >> 4), kIdescO, j % kWideFlush || kk);
-            if constexpr (!EIGHT) {
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk) mma_ts(o, s + 64 + 8 * kk, b + (kk * 2048 >> 4), kIdescO, 1);
-            }
-            if (t == SLOTS - 1) mma_commit(EMPTY(vl % NS));
-            if (!more) {
+            values(t, tile, j >> 1, true);
+            if (j + 2 < nt) {
+              ok = landed(2 * tile + 4);
+              if (ok) scores(t, tile + 2, true);
+            } else {
               mma_commit(OFULL(t));
-              continue;
             }
-            if (t == 0) ok = wait_bar(FULL(kl % NS), (kl / NS) & 1, wc);
-            if (!ok) break;
-            if (t == 0) tc_fence_after();
-            scores(t, kl);
-            if (t == SLOTS - 1) mma_commit(EMPTY(kl % NS));
+          } else {
+            for (int t = 0; t < 2 && ok; ++t) {
+              ok = ready(t);
+              if (!ok) break;
+              values(t, tile, j, t == 1);
+              if (j + 1 < nt) {
+                if (t == 0) ok = landed(2 * tile + 2);
+                if (ok) scores(t, tile + 1, t == 1);
+              } else {
+                mma_commit(OFULL(t));
+              }
+            }
           }
         }
         ++piece;
@@ -318,8 +366,11 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT, SLOTS>, 1) fa_wide_kernel(
       drain_bar(DRAIN, 0, wc.timeout);
     }
     __syncwarp();
+  } else if (warp == kIssuer + 1 || warp == kIssuer + 2) {
+    regs_dec<kWideOtherRegs<EIGHT>>();               // (idle: registers are traded by groups of four warps)
   } else if (EIGHT && warp >= kConvert) {
     // ============================================================ converters
+    regs_dec<kWideOtherRegs<EIGHT>>();
     const int tid = threadIdx.x - 32 * kConvert;
     int tile = 0;
     bool dead = false;
@@ -329,6 +380,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT, SLOTS>, 1) fa_wide_kernel(
         uint8_t* scales = smem + SM::kScaleOff + at * 256;
         const int* meta = s_meta + at * 8;
         int top_k = 0, top_v = 0;
+        bool whole = false;                  // every key is seen
 #pragma unroll
         for (int kind = 0; kind < 2; ++kind) {
           const int ld = 2 * tile + kind, rs = ld % RS, st = ld % NS;
@@ -341,51 +393,57 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT, SLOTS>, 1) fa_wide_kernel(
           };
           if (kind == 0) {           // every warp for itself: the largest exponents of the seen keys, the values' least
             int low_v = 255;
+            unsigned on = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int r = 32 * i + lane;
               if (!seen(r)) continue;
+              ++on;
               const int ks = scales[r], vs = scales[128 + r];
               top_k = max(top_k, ks), top_v = max(top_v, vs), low_v = min(low_v, vs);
             }
             top_k = __reduce_max_sync(0xffffffffu, top_k);
             top_v = __reduce_max_sync(0xffffffffu, top_v);
             low_v = __reduce_min_sync(0xffffffffu, low_v);
+            whole = __all_sync(0xffffffffu, on == 4);
             const bool each = top_v - low_v > (params.e5m2 ? 8 : 15);
-            if (top_v == 0 || each) top_v = 0;                     // (0: the codes of V stay as they are)
+            if (each) top_v = 0;                     // (0: the codes of V stay as they are)
             if (tid == 0)
               s_info[at] = WideTileInfo{scale_of(top_k), top_v ? (float)(top_v - 127) : 0.f,
                                         top_v ? __uint_as_float((uint32_t)(254 - top_v) << 23) : 1.f, each};
           }
-          const uint8_t* raw = smem + SM::kRawOff + rs * SM::kRaw;
-          const uint32_t op = sbase + SM::kRingOff + st * SM::kOp;
+          // a thread keeps to one 16-byte chunk of codes and to the rows `row` + kStep i, whose places in the
+          // operand tile are kStep rows apart
+          constexpr int kChunks = D / 16, kStep = 128 / kChunks;
+          const int c = tid % kChunks, row = tid / kChunks;
+          const uint8_t* raw = smem + SM::kRawOff + rs * SM::kRaw + tid * 16;
+          const uint32_t to = sbase + SM::kRingOff + st * SM::kOp + (c >> 2) * (128 * 128) + row * 128;
+          // (the two halves of a chunk, for the second 64 channels in the other order: no bank twice)
+          const bool swap = (c >> 2) & 1;
+          const uint32_t first = to + (((2 * (c & 3) + swap) ^ (row & 7)) << 4), second = first ^ 16u;
           const int top = kind ? top_v : top_k;
+          const uint8_t* scale = scales + 128 * kind + row;
           auto convert = [&](auto format) {
             constexpr bool E5M2 = decltype(format)::value;
 #pragma unroll 4
-            for (int i = tid; i < 128 * (D / 16); i += 128) {
-              const int r = i / (D / 16), c = i % (D / 16);
-              const bool on = seen(r);
-              uint4 w = *reinterpret_cast<const uint4*>(raw + i * 16);
-              if (!on) w = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < kChunks; ++i) {
+              uint4 w = *reinterpret_cast<const uint4*>(raw + i * (kStep * D));
+              const int e = (int)scale[kStep * i] - top;                  // (<= 0 where the row is seen)
+              // 2^e as an fp16, exactly down to 2^-24
+              uint32_t f = e < -24 ? 0u : e < -14 ? 1u << ((24 + e) & 31) : (uint32_t)(15 + e) << 10;
+              if (top == 0) f = 0x3C00u;
+              if (!whole && !seen(row + kStep * i)) w = make_uint4(0, 0, 0, 0), f = 0;
+              f |= f << 16;
               uint32_t h[8];
               codes4<E5M2>(w.x, h[0], h[1]);
               codes4<E5M2>(w.y, h[2], h[3]);
               codes4<E5M2>(w.z, h[4], h[5]);
               codes4<E5M2>(w.w, h[6], h[7]);
-              if (top && on) {       // 2^(e - E) as an fp16, exactly, down to 2^-24
-                const int e = (int)scales[128 * kind + r] - top;
-                const uint32_t f = pack_f16x2(0.f, e < -126 ? 0.f : __uint_as_float((uint32_t)(127 + e) << 23)) >> 16;
-                const uint32_t f2 = f | f << 16;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) h[q] = mul_f16x2(h[q], f2);
-              }
-              const uint32_t to = op + (c >> 2) * (128 * 128) + r * 128;
-              const uint32_t a = ((2 * (c & 3)) ^ (r & 7)) << 4, b = a ^ 16u;
+              for (int q = 0; q < 8; ++q) h[q] = mul_f16x2(h[q], f);
               const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-              const bool swap = (c >> 2) & 1;      // (the two chunks of a row in the two orders: no bank twice)
-              st_shared_v4(to + (swap ? b : a), swap ? hi : lo);
-              st_shared_v4(to + (swap ? a : b), swap ? lo : hi);
+              st_shared_v4(first + i * (kStep * 128), swap ? hi : lo);
+              st_shared_v4(second + i * (kStep * 128), swap ? lo : hi);
             }
           };
           if (params.e5m2) convert(std::true_type{});
@@ -401,22 +459,34 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT, SLOTS>, 1) fa_wide_kernel(
     }
   } else {
     // ============================================================ softmax: a row per thread
+    regs_inc<kWideSoftmaxRegs<EIGHT>>();
     const int t = warp >> 2;
-    const int row = threadIdx.x & 127;                 // of the slot
+    const int row = threadIdx.x & 127;                 // of the group's 128
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + 128 * t + lanes, tO = tmem + 128 * SLOTS + 128 * t + lanes;
-    int tile = 0, piece = 0;
+    const uint32_t tS = tmem + 128 * t + lanes, tO = tmem + 256 + 128 * t + lanes;
+    int tile0 = 0, made = 0, pieces = 0, joins = 0;    // the piece's first tile; tiles and pieces of this group
     bool dead = false;
+    // fp32 numbers of scratch times g plus a row's 32 columns
+    auto plus = [&](uint4 a, float g, const uint32_t* u) {
+      return make_uint4(__float_as_uint(fmaf(__uint_as_float(a.x), g, __uint_as_float(u[0]))),
+                        __float_as_uint(fmaf(__uint_as_float(a.y), g, __uint_as_float(u[1]))),
+                        __float_as_uint(fmaf(__uint_as_float(a.z), g, __uint_as_float(u[2]))),
+                        __float_as_uint(fmaf(__uint_as_float(a.w), g, __uint_as_float(u[3]))));
+    };
+    auto gone_of = [&](int group) {                    // this row's sum that has left group's accumulator
+      return reinterpret_cast<uint4*>(params.gone + (((long long)blockIdx.x * 2 + group) * 128 + row) * D);
+    };
     while (!dead && next_piece(x)) {
-      const int hk = x.unit / p.groups, rg = x.unit % p.groups;
-      const int r0 = rg * kRows + 128 * t;             // this slot's first row of the KV head
+      const int hk = x.unit / p.groups, rg = x.unit % p.groups, nt = x.d.nt;
+      const int r0 = rg * kRows + (SPLIT ? 0 : 128 * t);   // this group's first row of the KV head
       const long long at0 = ((long long)x.b * p.Hkv + hk) * p.rows + r0;
       const bool mine = r0 + row < p.rows;
-      // Q into its slot (the last piece's S products of it are done), as fp16 of a power of two times it
-      // over an 8-bit cache
-      float fac = p.scale_log2;
+      // Q into its place (the last piece's S products of it are done), with the sign of the scale and, over an
+      // 8-bit cache, as fp16 of a power of two times it
+      float fac = fabsf(p.scale_log2);
       {
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (at0 + row) * D);
+        const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
         uint4 w[D / 8];
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) w[c] = mine ? src[c] : make_uint4(0, 0, 0, 0);
@@ -435,9 +505,12 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT, SLOTS>, 1) fa_wide_kernel(
           for (int c = 0; c < D / 8; ++c) w[c] = make_uint4(half(w[c].x), half(w[c].y), half(w[c].z), half(w[c].w));
           fac *= __uint_as_float((uint32_t)(127 + e) << 23);
         }
+        if (!SPLIT || t == 0) {
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          st_shared_v4(sbase + t * SM::kOp + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4), w[c]);
+          for (int c = 0; c < D / 8; ++c)
+            st_shared_v4(sbase + t * SM::kOp + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                         make_uint4(w[c].x ^ sign, w[c].y ^ sign, w[c].z ^ sign, w[c].w ^ sign));
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(QREADY);
@@ -449,44 +522,46 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT, SLOTS>, 1) fa_wide_kernel(
       const int all_hi = p.ancestors ? base - 1 : x.len - p.Sq;               // by every row
       const int all_lo = p.pre_tokens >= 0 ? x.len - 1 - p.pre_tokens : 0;    // and from here on
       const int low = p.pre_tokens >= 0 ? tok - p.pre_tokens : 0;
-      float m = kNoScore, l = 0.f, m_acc = kNoScore;   // m_acc: the reference of what has left TMEM
-      const bool direct = x.d.t0 == 0 && x.d.nt == x.s.n;
-      // this row's place in scratch: a piece's answer, before that the sum that has left TMEM (of a unit that is
-      // finished here the place of the one that begins after it)
-      const long long part = (2LL * blockIdx.x + (x.d.t0 == 0 ? 1 : 0)) * kRows + 128 * t + row;
-      uint4* acc = reinterpret_cast<uint4*>(p.part_o + part * D);
-      auto plus = [&](uint4 a, float g, const uint32_t* u) {      // a g + u
-        return make_uint4(__float_as_uint(fmaf(__uint_as_float(a.x), g, __uint_as_float(u[0]))),
-                          __float_as_uint(fmaf(__uint_as_float(a.y), g, __uint_as_float(u[1]))),
-                          __float_as_uint(fmaf(__uint_as_float(a.z), g, __uint_as_float(u[2]))),
-                          __float_as_uint(fmaf(__uint_as_float(a.w), g, __uint_as_float(u[3]))));
-      };
+      float m = kNoScore, l = 0.f, m_gone = kNoScore;  // m_gone: the reference of what has left the accumulator
+      int n = 0;                                       // tiles of the piece in this group
 
-      for (int j = 0; j < x.d.nt; ++j, ++tile) {
-        if (!__all_sync(0xffffffffu, wait_bar(SFULL(t), tile & 1, wc))) {
+#pragma unroll 1
+      for (int j = SPLIT ? t : 0; j < nt; j += SPLIT ? 2 : 1, ++n) {
+        const int tile = tile0 + j;
+        if (!__all_sync(0xffffffffu, wait_bar(SFULL(t), made & 1, wc))) {
           dead = true;
           break;
         }
+        ++made;
         tc_fence_after();
+        uint32_t su[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&su[32 * c]));
         const int* meta = s_meta + (tile % kWideInfo) * 8;
         const int4 ka = *reinterpret_cast<const int4*>(meta), kb = *reinterpret_cast<const int4*>(meta + 4);
         const int first = min(min(min(ka.x, ka.y), min(ka.z, ka.w)), min(min(kb.x, kb.y), min(kb.z, kb.w)));
         const int last = max(max(max(ka.x, ka.y), max(ka.z, ka.w)), max(max(kb.x, kb.y), max(kb.z, kb.w))) + 15;
         const bool all = first >= max(all_lo, 0) && last <= all_hi;
-        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-        if (!all) {
-          auto group = [&](int k0) -> uint32_t {       // the keys of 16 that this row sees before a tree
-            if (k0 < 0) return 0;
-            const int n = min(max(tok + 1 - k0, 0), 16), z = min(max(low - k0, 0), 16);
-            return ((1u << n) - 1u) & ~((1u << z) - 1u);
-          };
+        WideTileInfo info{1.f, 0.f, 1.f, 0};
+        if constexpr (EIGHT) info = s_info[tile % kWideInfo];
+        const uint8_t* vs = smem + SM::kScaleOff + (tile % kWideInfo) * 256 + 128;
+        // a score in log2 units with its value's exponent is s f + v
+        float f = fac * info.k_scale, v = info.v_exp;
+        tmem_wait_ld();
+        float sv[128];
+#pragma unroll
+        for (int i = 0; i < 128; ++i) sv[i] = __uint_as_float(su[i]);
+        if (!all || (EIGHT && info.each)) {            // (few tiles: a piece's ends)
           const int keys[8] = {ka.x, ka.y, ka.z, ka.w, kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) vis[c] = group(keys[2 * c]) | group(keys[2 * c + 1]) << 16;
-          if (p.ancestors) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              if (max(keys[2 * c], keys[2 * c + 1]) + 15 < base) continue;
+          for (int c = 0; c < 4; ++c) {
+            auto group = [&](int k0) -> uint32_t {     // the keys of 16 that this row sees before a tree
+              if (k0 < 0) return 0;
+              const int y = min(max(tok + 1 - k0, 0), 16), z = min(max(low - k0, 0), 16);
+              return ((1u << y) - 1u) & ~((1u << z) - 1u);
+            };
+            uint32_t vis = group(keys[2 * c]) | group(keys[2 * c + 1]) << 16;
+            if (p.ancestors && max(keys[2 * c], keys[2 * c + 1]) + 15 >= base) {
               // lane: one of the 32 keys; the warp's rows one by one
               const int k0 = lane < 16 ? keys[2 * c] : keys[2 * c + 1];
               const int draft = k0 < 0 ? -1 : k0 + (lane & 15) - base;
@@ -495,14 +570,21 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT, SLOTS>, 1) fa_wide_kernel(
               for (int r = 0; r < 32; ++r) {
                 const bool see = draft >= 0 && decode_ancestor(p, x.b, drafts, i, draft);
                 const uint32_t bits = __ballot_sync(0xffffffffu, see);
-                if (lane == r) vis[c] |= bits;
+                if (lane == r) vis |= bits;
                 if (++i == p.Sq) i = 0;
               }
             }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float y = fmaf(sv[32 * c + i], f, v);
+              if (EIGHT && info.each) y += (float)((int)vs[32 * c + i] - 127);
+              sv[32 * c + i] = (vis >> i) & 1u ? y : -INFINITY;
+            }
           }
+          f = 1.f, v = 0.f;
           if constexpr (!EIGHT) {
-            // V of keys that no row sees may hold anything: its rows become 0 (P is 0 there), by each slot
-            const int k0 = keys[row >> 4], k = k0 < 0 ? -1 : k0 + (row & 15);
+            // V of keys that no row sees may hold anything: its rows become 0 (P is 0 there), by each group
+            const int k0 = meta[row >> 4], k = k0 < 0 ? -1 : k0 + (row & 15);
             const int ld = 2 * tile + 1;
             if (!__all_sync(0xffffffffu, wait_bar(FULL(ld % NS), (ld / NS) & 1, wc))) {
               dead = true;
@@ -511,155 +593,172 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT, SLOTS>, 1) fa_wide_kernel(
             if (k < x.s.lo || k >= x.s.hi) {
 #pragma unroll
               for (int c = 0; c < D / 64; ++c)
+#pragma unroll
                 for (int q = 0; q < 8; ++q)
                   st_shared_v4(sbase + SM::kRingOff + (ld % NS) * SM::kOp + c * (128 * 128) + row * 128 + q * 16, make_uint4(0, 0, 0, 0));
             }
             fence_proxy_async_smem();
           }
         }
-        WideTileInfo info{1.f, 0.f, 1.f, 0};
-        if constexpr (EIGHT) info = s_info[tile % kWideInfo];
-        const float f = fac * info.k_scale;
-        const uint8_t* vs = smem + SM::kScaleOff + (tile % kWideInfo) * 256 + 128;
-        // scores in log2 units, the values' exponents added
-        auto load = [&](int c, float (&s)[32]) {
-          uint32_t u[32];
-          tmem_ld32(tS + 32 * c, u);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) s[i] = fmaf(__uint_as_float(u[i]), f, info.v_exp);
-          if (EIGHT && info.each) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] += (float)((int)vs[32 * c + i] - 127);
-          }
-          if (!all) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((vis[c] >> i) & 1u)) s[i] = -INFINITY;
-          }
-        };
-        if (j && j % kWideFlush == 0) {
-          const float g = ex2_approx(m_acc - m);
-          m_acc = m;
+        if (n && n % kWideFlush == 0) {                // (O is at rest; the next P V starts from zero)
+          const float g = ex2_approx(m_gone - m);
+          m_gone = m;
+          uint4* gone = gone_of(t);
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t u[32];
-            tmem_ld32(tO + 32 * c, u);
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t u[16];
+            tmem_ld16(tO + 16 * c, u);
             tmem_wait_ld();
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              acc[8 * c + q] = plus(j == kWideFlush ? make_uint4(0, 0, 0, 0) : acc[8 * c + q], g, u + 4 * q);
+            for (int q = 0; q < 4; ++q)
+              gone[4 * c + q] = plus(n == kWideFlush ? make_uint4(0, 0, 0, 0) : gone[4 * c + q], g, u + 4 * q);
           }
         }
-        float top = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float s[32];
-          load(c, s);
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) top = fmaxf(top, fmaxf(s[i], s[i + 1]));     // (NaN is dropped)
-        }
+        const float top = fmaf(row_max(sv), f, v);     // (f >= 0; NaN is dropped)
         if (__any_sync(0xffffffffu, top - m > kMaxOver + kLiftP)) {                    // references move up
           const float to = top - m > kMaxOver + kLiftP ? top - kLiftP : m;
           const float g = ex2_approx(m - to);
           m = to;
           l *= g;
-          if (j % kWideFlush) {
+          if (n % kWideFlush) {
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t u[32];
-              tmem_ld32(tO + 32 * c, u);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t u[16];
+              tmem_ld16(tO + 16 * c, u);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * g);
-              tmem_st32(tO + 32 * c, u);
+              for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * g);
+              tmem_st16(tO + 16 * c, u);
             }
           }
         }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        // chunk c as P: 16 registers of hi, 16 of lo
-        auto exps = [&](int c, uint32_t (&hi)[16], uint32_t (&lo)[16]) {
-          float s[32];
-          load(c, s);
+        if (EIGHT && info.each) {                      // the sum key by key, each with its value's 2^-e
+#pragma unroll 1
+          for (int c = 0; c < 16; ++c)
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float a = ex2_approx(s[i] - m), b = ex2_approx(s[i + 1] - m);
-            if (EIGHT && info.each) {
-              const uint32_t va = vs[32 * c + i], vb = vs[32 * c + i + 1];
-              if (a > 0.f) sum[0] = fmaf(a, __uint_as_float((254u - va) << 23), sum[0]);
-              if (b > 0.f) sum[1] = fmaf(b, __uint_as_float((254u - vb) << 23), sum[1]);
-            } else {
-              sum[(i >> 1) & 3] += a + b;
+            for (int i = 0; i < 8; ++i) {
+              float y = -INFINITY;
+#pragma unroll
+              for (int q = 0; q < 16; ++q) y = q == c ? sv[8 * q + i] : y;
+              const float a = ex2_approx(y - m);
+              if (a > 0.f) l = fmaf(a, __uint_as_float((254u - vs[8 * c + i]) << 23), l);
             }
-            hi[i / 2] = kP16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
-            if constexpr (!EIGHT) lo[i / 2] = pack_residual_x2(a, b, hi[i / 2], !kP16);
-          }
-        };
-        uint32_t h0[16], h1[16], lo[16];
-        if constexpr (EIGHT) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {      // (chunk c lies over chunk c / 2 of S, read by then)
-            exps(c, h0, lo);
-            tmem_st16(tS + 16 * c, h0);
-          }
-        } else {
-          // lo of the upper half over the upper half of S, its hi once the lower half has been read
-          exps(2, h0, lo);
-          uint32_t lo2[16];
-          exps(3, h1, lo2);
-          tmem_st16(tS + 64 + 32, lo);
-          tmem_st16(tS + 64 + 48, lo2);
-          uint32_t h[16];
-          exps(0, h, lo);
-          tmem_st16(tS, h);
-          tmem_st16(tS + 64, lo);
-          exps(1, h, lo);
-          tmem_st16(tS + 16, h);
-          tmem_st16(tS + 64 + 16, lo);
-          tmem_st16(tS + 32, h0);
-          tmem_st16(tS + 48, h1);
         }
-        const float all_sum = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        l = EIGHT && !info.each ? fmaf(all_sum, info.v_back, l) : l + all_sum;
+        const float neg = v - m;
+        const uint64_t f2 = f2_pack(f, f), neg2 = f2_pack(neg, neg);
+        uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float a, b;
+            f2_unpack(f2_fma(f2_pack(sv[32 * c + 2 * i], sv[32 * c + 2 * i + 1]), f2, neg2), a, b);
+            a = ex2_approx(a);
+            b = ex2_approx(b);
+            sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(a, b));
+            hi[i] = kP16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+            if constexpr (!EIGHT) lo[i] = pack_residual_x2(a, b, hi[i], !kP16);
+          }
+          tmem_st16(tS + 16 * c, hi);
+          if constexpr (!EIGHT) tmem_st16(tS + 64 + 16 * c, lo);
+        }
+        if (!(EIGHT && info.each)) {
+          float a, b, c, d;
+          f2_unpack(sum2[0], a, b);
+          f2_unpack(sum2[1], c, d);
+          l = fmaf((a + b) + (c + d), info.v_back, l);
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(PREADY(t));
       }
       if (dead) break;
+      tile0 += nt;
       // ---- the piece's answer
-      if (!__all_sync(0xffffffffu, wait_bar(OFULL(t), piece & 1, wc))) break;
-      ++piece;
-      tc_fence_after();
+      const bool direct = x.d.t0 == 0 && nt == x.s.n;
+      const long long part = (2LL * blockIdx.x + (x.d.t0 == 0 ? 1 : 0)) * kRows + (SPLIT ? 0 : 128 * t) + row;
+      float2* s_ml = reinterpret_cast<float2*>(smem + SM::kMlOff);
+      const bool other = SPLIT && nt > 1;              // the second group has tiles of the piece, too
+      if (n) {
+        if (!__all_sync(0xffffffffu, wait_bar(OFULL(t), pieces & 1, wc))) break;
+        ++pieces;
+        tc_fence_after();
+      }
+      if (SPLIT && t == 1) {                           // the first group joins the two
+        if (!n) continue;
+        s_ml[row] = make_float2(m, l);
+        // what has left the accumulator comes back to this group's place in scratch as of m
+        if (n > kWideFlush) {
+          const float g = ex2_approx(m_gone - m);
+          uint4* gone = gone_of(1);
+          const uint32_t none[4] = {0, 0, 0, 0};
+          for (int q = 0; q < D / 4; ++q) gone[q] = plus(gone[q], g, none);
+          __threadfence_block();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(JOIN);
+        continue;                                      // (O stays until the next piece's Q is ready)
+      }
+      float g0 = 1.f, g1 = 0.f;                        // the groups' weights
+      bool gone1 = false;
+      if (other) {
+        if (!__all_sync(0xffffffffu, wait_bar(OFULL(1), joins & 1, wc) && wait_bar(JOIN, joins & 1, wc))) break;
+        ++joins;
+        tc_fence_after();
+        const float2 ml = s_ml[row];
+        const float to = fmaxf(m, ml.x);
+        g0 = ex2_approx(m - to), g1 = ex2_approx(ml.x - to);
+        l = fmaf(l, g0, ml.y * g1);
+        m_gone = m_gone - m;                           // (relative to this group's own reference)
+        m = to;
+        gone1 = (nt / 2) > kWideFlush;
+      } else {
+        m_gone = m_gone - m;
+      }
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float g = ex2_approx(m_acc - m);
+      const float g = ex2_approx(m_gone) * g0;
+      uint4* to = reinterpret_cast<uint4*>(p.part_o + part * D);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t u[32];
-        tmem_ld32(tO + 32 * c, u);
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t u[16], u1[16];
+        tmem_ld16(tO + 16 * c, u);
+        if (other) tmem_ld16(tO + 128 + 16 * c, u1);
         tmem_wait_ld();
-        if (x.d.nt > kWideFlush) {
+        if (other) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const uint4 y = plus(acc[8 * c + q], g, u + 4 * q);
+          for (int i = 0; i < 16; ++i)
+            u[i] = __float_as_uint(fmaf(__uint_as_float(u[i]), g0, __uint_as_float(u1[i]) * g1));
+        }
+        if (n > kWideFlush) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint4 y = plus(gone_of(t)[4 * c + q], g, u + 4 * q);
             u[4 * q] = y.x, u[4 * q + 1] = y.y, u[4 * q + 2] = y.z, u[4 * q + 3] = y.w;
           }
         }
-        if (direct) {
-          if (mine) {
-            uint4* dst = reinterpret_cast<uint4*>(p.o + (at0 + row) * D + 32 * c);
+        if (gone1) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t y[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                y[e] = pack16x2<BF16>(__uint_as_float(u[8 * q + 2 * e]) * inv, __uint_as_float(u[8 * q + 2 * e + 1]) * inv);
-              dst[q] = make_uint4(y[0], y[1], y[2], y[3]);
-            }
+          for (int q = 0; q < 4; ++q) {
+            const uint4 y = plus(gone_of(1)[4 * c + q], g1, u + 4 * q);
+            u[4 * q] = y.x, u[4 * q + 1] = y.y, u[4 * q + 2] = y.z, u[4 * q + 3] = y.w;
           }
-        } else if (mine) {
+        }
+        if (!mine) continue;
+        if (direct) {
+          uint4* dst = reinterpret_cast<uint4*>(p.o + (at0 + row) * D + 16 * c);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) acc[8 * c + q] = make_uint4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
+          for (int q = 0; q < 2; ++q) {
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              y[e] = pack16x2<BF16>(__uint_as_float(u[8 * q + 2 * e]) * inv, __uint_as_float(u[8 * q + 2 * e + 1]) * inv);
+            dst[q] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) to[4 * c + q] = make_uint4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
         }
       }
       if (mine) {
@@ -673,7 +772,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT, SLOTS>, 1) fa_wide_kernel(
   __syncthreads();
   if (warp == kIssuer) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256 * SLOTS);
+    tmem_dealloc(tmem, 512);
   }
 }
 
