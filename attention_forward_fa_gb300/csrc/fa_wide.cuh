@@ -46,6 +46,7 @@ constexpr int kWideTile = 128;
 constexpr int kWideInfo = 8;       // tiles whose keys and scales are kept: the producer is at most seven ahead
 
 constexpr int kWideFlush = 64;     // tiles that add up in TMEM
+constexpr int kWideDrafts = 64;    // drafts whose ancestors are kept as words; of larger trees they are looked up tile by tile
 
 struct WideParams {
   DecodeCore c;
@@ -76,7 +77,8 @@ struct WideSmem {
   static constexpr int kMetaOff = kScaleOff + (EIGHT ? kWideInfo * 256 : 0);     // int [kWideInfo][8]
   static constexpr int kInfoOff = kMetaOff + kWideInfo * 32;     // WideTileInfo [kWideInfo]
   static constexpr int kMlOff = kInfoOff + kWideInfo * 16;       // float2 [128]: the second group's reference and sum
-  static constexpr int kBarOff = kMlOff + (SPLIT ? 1024 : 0);
+  static constexpr int kTreeOff = kMlOff + (SPLIT ? 1024 : 0);   // uint2 [2][kWideDrafts]: what each draft sees, per piece's parity
+  static constexpr int kBarOff = kTreeOff + 16 * kWideDrafts;
   static constexpr int kBars = 2 * kStages + 2 * kRawStages + 9;
   static constexpr int kMiscOff = kBarOff + kBars * 8;
   static constexpr int kBytes = kMiscOff + 64;
@@ -89,9 +91,9 @@ constexpr int kWideThreads = EIGHT ? 512 : 384;
 template <bool EIGHT>
 constexpr int kWideRegs = EIGHT ? 128 : 168;
 template <bool EIGHT>
-constexpr int kWideSoftmaxRegs = EIGHT ? 200 : 208;
+constexpr int kWideSoftmaxRegs = EIGHT ? 192 : 200;
 template <bool EIGHT>
-constexpr int kWideOtherRegs = EIGHT ? 56 : 88;
+constexpr int kWideOtherRegs = EIGHT ? 64 : 104;
 static_assert(256 * kWideSoftmaxRegs<true> + 256 * kWideOtherRegs<true> <= 512 * kWideRegs<true>, "what the CTA has");
 static_assert(256 * kWideSoftmaxRegs<false> + 128 * kWideOtherRegs<false> <= 384 * kWideRegs<false>, "what the CTA has");
 
@@ -276,13 +278,16 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
   } else if (warp == kIssuer) {
     // ============================================================ MMA issue
     regs_dec<kWideOtherRegs<EIGHT>>();
-    if (lane == 0) {
+    // (the whole warp runs the loop, one lane's MMAs count: their descriptors stay in uniform registers)
+    {
+      const uint32_t lead = elect_lane();
       constexpr uint32_t kIdescS = idesc_f16(128, 128, !kP16, false);
       constexpr uint32_t kIdescO = idesc_f16(128, D, !kP16, true);
       const uint64_t q0 = sw128_desc(sbase, 16, 1024);
       const uint64_t k0 = sw128_desc(sbase + SM::kRingOff, 16, 1024);
       const uint64_t v0 = sw128_desc(sbase + SM::kRingOff, 128 * 128, 1024);
-      int tile = 0, piece = 0, done[2] = {0, 0};       // tiles whose P group t has made
+      int tile = 0, piece = 0;
+      uint32_t phases = 0;                             // bit t: the parity of group t's next P
       bool ok = true;
       // S of group t from the K of `tl`, whose stage is given back behind the last group that reads it
       auto scores = [&](int t, int tl, bool last) {
@@ -291,36 +296,38 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
-          mma_ss(tmem + 128 * t, a + off, b + off, kIdescS, kk > 0);
+          mma_ss_if(tmem + 128 * t, a + off, b + off, kIdescS, kk > 0, lead);
         }
-        mma_commit(SFULL(t));
-        if (last) mma_commit(EMPTY(ld % NS));
+        mma_commit_if(SFULL(t), lead);
+        if (last) mma_commit_if(EMPTY(ld % NS), lead);
       };
       auto values = [&](int t, int tl, int i, bool last) {     // i: the group's tiles of the piece before this one
         const int ld = 2 * tl + 1;
         const uint64_t b = v0 + (((ld % NS) * SM::kOp) >> 4);
         const uint32_t o = tmem + 256 + 128 * t, s = tmem + 128 * t;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) mma_ts(o, s + 8 * kk, b + (kk * 2048 >> 4), kIdescO, i % kWideFlush || kk);
+        for (int kk = 0; kk < 8; ++kk) mma_ts_if(o, s + 8 * kk, b + (kk * 2048 >> 4), kIdescO, i % kWideFlush || kk, lead);
         if constexpr (!EIGHT) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) mma_ts(o, s + 64 + 8 * kk, b + (kk * 2048 >> 4), kIdescO, 1);
+          for (int kk = 0; kk < 8; ++kk) mma_ts_if(o, s + 64 + 8 * kk, b + (kk * 2048 >> 4), kIdescO, 1, lead);
         }
-        if (last) mma_commit(EMPTY(ld % NS));
+        if (last) mma_commit_if(EMPTY(ld % NS), lead);
       };
       auto landed = [&](int ld) {
-        const bool got = wait_bar(FULL(ld % NS), (ld / NS) & 1, wc);
+        const bool got = __all_sync(0xffffffffu, wait_bar(FULL(ld % NS), (ld / NS) & 1, wc));
         tc_fence_after();
         return got;
       };
       auto ready = [&](int t) {
-        const bool got = wait_bar(PREADY(t), done[t]++ & 1, wc);
+        const bool got = __all_sync(0xffffffffu, wait_bar(PREADY(t), (phases >> t) & 1, wc));
+        phases ^= 1u << t;
         tc_fence_after();
         return got;
       };
       while (ok && next_piece(x)) {
         const int nt = x.d.nt;
-        ok = wait_bar(QREADY, piece & 1, wc) && landed(2 * tile);
+        ok = __all_sync(0xffffffffu, wait_bar(QREADY, piece & 1, wc));
+        ok = ok && landed(2 * tile);
         if (!ok) break;
         if constexpr (SPLIT) {
           scores(0, tile, true);
@@ -343,7 +350,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
               ok = landed(2 * tile + 4);
               if (ok) scores(t, tile + 2, true);
             } else {
-              mma_commit(OFULL(t));
+              mma_commit_if(OFULL(t), lead);
             }
           } else {
             for (int t = 0; t < 2 && ok; ++t) {
@@ -354,7 +361,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
                 if (t == 0) ok = landed(2 * tile + 2);
                 if (ok) scores(t, tile + 1, t == 1);
               } else {
-                mma_commit(OFULL(t));
+                mma_commit_if(OFULL(t), lead);
               }
             }
           }
@@ -362,7 +369,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
         ++piece;
       }
       // whatever is in flight ends before the tensor memory and the tiles are given up
-      mma_commit(DRAIN);
+      mma_commit_if(DRAIN, lead);
       drain_bar(DRAIN, 0, wc.timeout);
     }
     __syncwarp();
@@ -425,25 +432,34 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
           const uint8_t* scale = scales + 128 * kind + row;
           auto convert = [&](auto format) {
             constexpr bool E5M2 = decltype(format)::value;
-#pragma unroll 4
-            for (int i = 0; i < kChunks; ++i) {
-              uint4 w = *reinterpret_cast<const uint4*>(raw + i * (kStep * D));
-              const int e = (int)scale[kStep * i] - top;                  // (<= 0 where the row is seen)
-              // 2^e as an fp16, exactly down to 2^-24
-              uint32_t f = e < -24 ? 0u : e < -14 ? 1u << ((24 + e) & 31) : (uint32_t)(15 + e) << 10;
-              if (top == 0) f = 0x3C00u;
-              if (!whole && !seen(row + kStep * i)) w = make_uint4(0, 0, 0, 0), f = 0;
-              f |= f << 16;
-              uint32_t h[8];
-              codes4<E5M2>(w.x, h[0], h[1]);
-              codes4<E5M2>(w.y, h[2], h[3]);
-              codes4<E5M2>(w.z, h[4], h[5]);
-              codes4<E5M2>(w.w, h[6], h[7]);
+#pragma unroll 1
+            for (int i0 = 0; i0 < kChunks; i0 += 4) {
+              uint4 w[4];                              // (four loads, then their stores: one order of memory for all)
+              int e[4];
 #pragma unroll
-              for (int q = 0; q < 8; ++q) h[q] = mul_f16x2(h[q], f);
-              const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-              st_shared_v4(first + i * (kStep * 128), swap ? hi : lo);
-              st_shared_v4(second + i * (kStep * 128), swap ? lo : hi);
+              for (int y = 0; y < 4; ++y) {
+                w[y] = *reinterpret_cast<const uint4*>(raw + (i0 + y) * (kStep * D));
+                e[y] = (int)scale[kStep * (i0 + y)] - top;                // (<= 0 where the row is seen)
+              }
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int i = i0 + y;
+                // 2^e as an fp16, exactly down to 2^-24
+                uint32_t f = e[y] < -24 ? 0u : e[y] < -14 ? 1u << ((24 + e[y]) & 31) : (uint32_t)(15 + e[y]) << 10;
+                if (top == 0) f = 0x3C00u;
+                if (!whole && !seen(row + kStep * i)) w[y] = make_uint4(0, 0, 0, 0), f = 0;
+                f |= f << 16;
+                uint32_t h[8];
+                codes4<E5M2>(w[y].x, h[0], h[1]);
+                codes4<E5M2>(w[y].y, h[2], h[3]);
+                codes4<E5M2>(w[y].z, h[4], h[5]);
+                codes4<E5M2>(w[y].w, h[6], h[7]);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) h[q] = mul_f16x2(h[q], f);
+                const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                st_shared_v4(first + i * (kStep * 128), swap ? hi : lo);
+                st_shared_v4(second + i * (kStep * 128), swap ? lo : hi);
+              }
             }
           };
           if (params.e5m2) convert(std::true_type{});
@@ -464,7 +480,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
     const int row = threadIdx.x & 127;                 // of the group's 128
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + 128 * t + lanes, tO = tmem + 256 + 128 * t + lanes;
-    int tile0 = 0, made = 0, pieces = 0, joins = 0;    // the piece's first tile; tiles and pieces of this group
+    int tile0 = 0, made = 0, piece = 0, pieces = 0, joins = 0;   // the piece's first tile; tiles, pieces, pieces of this group
     bool dead = false;
     // fp32 numbers of scratch times g plus a row's 32 columns
     auto plus = [&](uint4 a, float g, const uint32_t* u) {
@@ -481,42 +497,61 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
       const int r0 = rg * kRows + (SPLIT ? 0 : 128 * t);   // this group's first row of the KV head
       const long long at0 = ((long long)x.b * p.Hkv + hk) * p.rows + r0;
       const bool mine = r0 + row < p.rows;
-      // Q into its place (the last piece's S products of it are done), with the sign of the scale and, over an
-      // 8-bit cache, as fp16 of a power of two times it
-      float fac = fabsf(p.scale_log2);
-      {
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (at0 + row) * D);
-        const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-        uint4 w[D / 8];
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) w[c] = mine ? src[c] : make_uint4(0, 0, 0, 0);
-        if constexpr (EIGHT && BF16) {
-          uint32_t top = 0;
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            top = max_u16x2(top, max_u16x2(w[c].x & 0x7FFF7FFFu, w[c].y & 0x7FFF7FFFu));
-            top = max_u16x2(top, max_u16x2(w[c].z & 0x7FFF7FFFu, w[c].w & 0x7FFF7FFFu));
-          }
-          top = max(top & 0xFFFFu, top >> 16);
-          const int e = max((int)(top >> 7), 127 - 100) - 127 - 14;       // as in fa_decode8_kernel
-          const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-          auto half = [&](uint32_t u) { return pack_f16x2(lo16_f32<true>(u) * f, hi16_f32<true>(u) * f); };
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) w[c] = make_uint4(half(w[c].x), half(w[c].y), half(w[c].z), half(w[c].w));
-          fac *= __uint_as_float((uint32_t)(127 + e) << 23);
-        }
-        if (!SPLIT || t == 0) {
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c)
-            st_shared_v4(sbase + t * SM::kOp + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                         make_uint4(w[c].x ^ sign, w[c].y ^ sign, w[c].z ^ sign, w[c].w ^ sign));
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(QREADY);
-      }
       const int drafts = p.ancestors ? decode_drafts(p, x.b, x.len) : 0;
       const int base = x.len - drafts;                                        // a tree's first draft
+      const bool small_tree = drafts > 0 && p.Sq <= kWideDrafts;
+      uint2* s_tree = reinterpret_cast<uint2*>(smem + SM::kTreeOff) + (piece & 1) * kWideDrafts;
+      ++piece;
+      if (small_tree && (x.s.first + x.d.t0 + nt) * kWideTile > base) {       // the piece has drafts' keys
+#pragma unroll
+        for (int y = 0; y < kWideDrafts / 8; ++y) {                           // (a warp's drafts all at once)
+          const int i = warp + 8 * y;
+          const uint32_t a = __ballot_sync(0xffffffffu, decode_ancestor(p, x.b, drafts, i, lane));
+          const uint32_t c = __ballot_sync(0xffffffffu, decode_ancestor(p, x.b, drafts, i, 32 + lane));
+          if (lane == 0) s_tree[i] = make_uint2(a, c);
+        }
+      }
+      // Q into its place (the last piece's S products of it are done), with the sign of the scale and, over an
+      // 8-bit cache, as fp16 of a power of two times it: kLanes lanes per row, so that a load is whole lines
+      float fac = fabsf(p.scale_log2);
+      if (!SPLIT || t == 0 || (EIGHT && BF16)) {
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+        const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+        const int c = lane % kLanes;
+#pragma unroll
+        for (int y0 = 0; y0 < kLanes; y0 += 8) {
+          uint4 w[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const int r = (warp & 3) * 32 + (y0 + y) * kAtOnce + lane / kLanes;
+            w[y] = r0 + r < p.rows ? reinterpret_cast<const uint4*>(p.q + (at0 + r) * D)[c] : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const int r = (warp & 3) * 32 + (y0 + y) * kAtOnce + lane / kLanes;
+            if constexpr (EIGHT && BF16) {
+              uint32_t top = max_u16x2(max_u16x2(w[y].x & 0x7FFF7FFFu, w[y].y & 0x7FFF7FFFu),
+                                       max_u16x2(w[y].z & 0x7FFF7FFFu, w[y].w & 0x7FFF7FFFu));
+              top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+              for (int q = 1; q < kLanes; q <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, q));
+              const int e = max((int)(top >> 7), 127 - 100) - 127 - 14;       // as in fa_decode8_kernel
+              const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+              auto half = [&](uint32_t u) { return pack_f16x2(lo16_f32<true>(u) * f, hi16_f32<true>(u) * f); };
+              w[y] = make_uint4(half(w[y].x), half(w[y].y), half(w[y].z), half(w[y].w));
+              // to the thread of the row
+              const int its = __shfl_sync(0xffffffffu, e, (lane % kAtOnce) * kLanes);
+              if (lane / kAtOnce == y0 + y) fac *= __uint_as_float((uint32_t)(127 + its) << 23);
+            }
+            if (!SPLIT || t == 0)
+              st_shared_v4(sbase + t * SM::kOp + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                           make_uint4(w[y].x ^ sign, w[y].y ^ sign, w[y].z ^ sign, w[y].w ^ sign));
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(QREADY);
       const int i_row = p.Sq == 1 ? 0 : (r0 + row) % p.Sq;
       const int tok = p.ancestors ? base - 1 : x.len - p.Sq + i_row;          // keys up to it are seen
       const int all_hi = p.ancestors ? base - 1 : x.len - p.Sq;               // by every row
@@ -561,7 +596,16 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
               return ((1u << y) - 1u) & ~((1u << z) - 1u);
             };
             uint32_t vis = group(keys[2 * c]) | group(keys[2 * c + 1]) << 16;
-            if (p.ancestors && max(keys[2 * c], keys[2 * c + 1]) + 15 >= base) {
+            if (small_tree) {
+              const uint2 y = s_tree[i_row];
+              const unsigned long long w = y.x | (unsigned long long)y.y << 32;
+              auto sees = [&](int k0) -> uint32_t {    // the drafts among 16 keys that this row sees
+                const int d = k0 - base;
+                if (k0 < 0 || d <= -16 || d >= kWideDrafts) return 0;
+                return (uint32_t)(d < 0 ? w << -d : w >> d) & 0xFFFFu;
+              };
+              vis |= sees(keys[2 * c]) | sees(keys[2 * c + 1]) << 16;
+            } else if (p.ancestors && max(keys[2 * c], keys[2 * c + 1]) + 15 >= base) {
               // lane: one of the 32 keys; the warp's rows one by one
               const int k0 = lane < 16 ? keys[2 * c] : keys[2 * c + 1];
               const int draft = k0 < 0 ? -1 : k0 + (lane & 15) - base;
@@ -719,46 +763,75 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
       }
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const float g = ex2_approx(m_gone) * g0;
-      uint4* to = reinterpret_cast<uint4*>(p.part_o + part * D);
-#pragma unroll 1
-      for (int c = 0; c < D / 16; ++c) {
-        uint32_t u[16], u1[16];
+      // 16 columns of the row: both groups' and what has left the accumulators
+      auto answer = [&](int c, uint32_t (&u)[16]) {
         tmem_ld16(tO + 16 * c, u);
-        if (other) tmem_ld16(tO + 128 + 16 * c, u1);
-        tmem_wait_ld();
-        if (other) {
+        if constexpr (SPLIT) {
+          uint32_t u1[16];
+          tmem_ld16(tO + 128 + 16 * c, u1);            // (whatever it is where the second group had no tile)
+          tmem_wait_ld();
+          if (other) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            u[i] = __float_as_uint(fmaf(__uint_as_float(u[i]), g0, __uint_as_float(u1[i]) * g1));
+            for (int i = 0; i < 16; ++i)
+              u[i] = __float_as_uint(fmaf(__uint_as_float(u[i]), g0, __uint_as_float(u1[i]) * g1));
+          }
+        } else {
+          tmem_wait_ld();
         }
-        if (n > kWideFlush) {
+        auto add = [&](const uint4* from, float f) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint4 y = plus(gone_of(t)[4 * c + q], g, u + 4 * q);
+            const uint4 y = plus(from[4 * c + q], f, u + 4 * q);
             u[4 * q] = y.x, u[4 * q + 1] = y.y, u[4 * q + 2] = y.z, u[4 * q + 3] = y.w;
           }
-        }
-        if (gone1) {
+        };
+        if (n > kWideFlush) add(gone_of(t), g);
+        if (gone1) add(gone_of(1), g1);
+      };
+      // The warp's rows leave through where its rows of Q were (their last product is done; D / 64 areas of 128
+      // bytes a row, 16-byte chunks turned by the row), so that the stores are whole lines.
+      const uint32_t area = sbase + t * SM::kOp + ((warp & 3) * 32) * 128;
+      auto stage = [&](int chunk, uint4 y) {           // the chunk-th 16 bytes of this row's D / 64 areas
+        st_shared_v4(area + (chunk >> 3) * (128 * 128) + lane * 128 + (((chunk & 7) ^ (lane & 7)) << 4), y);
+      };
+      constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+      auto leave = [&](uint8_t* to, int pitch) {       // to: where this warp's first row begins
+        __syncwarp();
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint4 y = plus(gone_of(1)[4 * c + q], g1, u + 4 * q);
-            u[4 * q] = y.x, u[4 * q + 1] = y.y, u[4 * q + 2] = y.z, u[4 * q + 3] = y.w;
-          }
+        for (int y = 0; y < kLanes; ++y) {
+          const int r = y * kAtOnce + lane / kLanes, c = lane % kLanes;
+          const uint4 w = *reinterpret_cast<const uint4*>(smem + (area - sbase) + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+          if (r0 + (warp & 3) * 32 + r < p.rows) *reinterpret_cast<uint4*>(to + (long long)r * pitch + c * 16) = w;
         }
-        if (!mine) continue;
-        if (direct) {
-          uint4* dst = reinterpret_cast<uint4*>(p.o + (at0 + row) * D + 16 * c);
+        __syncwarp();
+      };
+      if (direct) {
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t u[16];
+          answer(c, u);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             uint32_t y[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               y[e] = pack16x2<BF16>(__uint_as_float(u[8 * q + 2 * e]) * inv, __uint_as_float(u[8 * q + 2 * e + 1]) * inv);
-            dst[q] = make_uint4(y[0], y[1], y[2], y[3]);
+            stage(2 * c + q, make_uint4(y[0], y[1], y[2], y[3]));
           }
-        } else {
+        }
+        leave(reinterpret_cast<uint8_t*>(p.o + (at0 + (warp & 3) * 32) * D), D * 2);
+      } else {
+        uint8_t* to = reinterpret_cast<uint8_t*>(p.part_o + (part - lane) * D);
+#pragma unroll 1
+        for (int z = 0; z < 2; ++z) {                  // (in fp32 half a row at a time)
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t u[16];
+            answer(z * (D / 32) + c, u);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) to[4 * c + q] = make_uint4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
+            for (int q = 0; q < 4; ++q) stage(4 * c + q, make_uint4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]));
+          }
+          leave(to + z * D * 2, D * 4);
         }
       }
       if (mine) {
