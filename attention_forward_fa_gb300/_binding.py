@@ -812,10 +812,10 @@ def flash_attention_decode_tree(q, cache: PagedKV, kv_lens, ancestors, *, new_le
     if (ancestors.dtype not in (torch.bool, torch.uint8) or ancestors.device != cache.device
             or ancestors.shape not in ((S, S), (B, S, S))):
         raise ValueError("ancestors must be bool or uint8 [B, S, S] or [S, S] on the cache's device")
-    each = ancestors[0] if ancestors.dim() == 3 else ancestors
-    if not each.is_contiguous():
-        raise ValueError("the trees of ancestors must be contiguous")
-    stride = ancestors.stride(0) if ancestors.dim() == 3 and B > 1 else 0
+    *batch, rows, cols = ancestors.stride()
+    if S > 1 and (rows, cols) != (S, 1):
+        raise ValueError("each tree of ancestors must be contiguous")
+    stride = batch[0] if batch and B > 1 else 0
     _answers_of(q, out, lse)
 
     def call(raw):

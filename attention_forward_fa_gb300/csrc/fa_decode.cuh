@@ -173,7 +173,7 @@ __device__ __forceinline__ void decode_report(const DecodeCore& p) {
 
 // The lengths and charges of sequences base + 32 i + lane: eight independent loads.
 constexpr int kChunks = 8;
-template <int TILE = kDecTile>
+template <int TILE = kDecTile, int CHARGE = kUnitTiles>
 __device__ __forceinline__ void decode_charges(const DecodeCore& p, int base, int lane, int (&len)[kChunks],
                                                int (&c)[kChunks]) {
 #pragma unroll
@@ -186,7 +186,7 @@ __device__ __forceinline__ void decode_charges(const DecodeCore& p, int base, in
   }
 #pragma unroll
   for (int i = 0; i < kChunks; ++i)
-    if (base + 32 * i + lane < p.B) c[i] = decode_span<TILE>(p, len[i]).n + kUnitTiles;
+    if (base + 32 * i + lane < p.B) c[i] = decode_span<TILE>(p, len[i]).n + CHARGE;
 }
 // Sum over the warp of numbers below 2^59, in three pieces by the warp's reduction.
 __device__ __forceinline__ long long warp_sum(long long x) {
@@ -224,12 +224,13 @@ struct DecodeWalk {
 struct DecodePiece {
   int t0, nt;
 };
+template <int CHARGE = kUnitTiles>
 __device__ __forceinline__ DecodePiece decode_step(DecodeWalk& w, int n, int units) {
   DecodePiece d;
-  const int charge = n + kUnitTiles;
+  const int charge = n + CHARGE;
   const int take = (int)min((long long)(charge - w.off), w.left);
-  d.t0 = max(0, w.off - kUnitTiles);
-  d.nt = max(0, w.off + take - kUnitTiles) - d.t0;
+  d.t0 = max(0, w.off - CHARGE);
+  d.nt = max(0, w.off + take - CHARGE) - d.t0;
   w.left -= take;
   w.off = 0;                    // (whatever is left starts with a unit)
   if (++w.unit == units) w.unit = 0, ++w.b;
@@ -237,7 +238,7 @@ __device__ __forceinline__ DecodePiece decode_step(DecodeWalk& w, int n, int uni
 }
 
 // This CTA's range of charged tiles and the sequence it starts in, by one warp.
-template <int TILE = kDecTile>
+template <int TILE = kDecTile, int CHARGE = kUnitTiles>
 __device__ __forceinline__ void decode_start(const DecodeCore& p, int cta, int lane, DecodeWalk* s_walk, int* s_len) {
   int len[kChunks], c[kChunks];
   int mine = 0, my_len = 0, inc;           // of the sequence `at + lane`, its chunk of 32 summed up
@@ -262,7 +263,7 @@ __device__ __forceinline__ void decode_start(const DecodeCore& p, int cta, int l
   if (p.B <= 32) {
     if (lane < p.B) {
       my_len = decode_len(p, lane);
-      mine = decode_span<TILE>(p, my_len).n + kUnitTiles;
+      mine = decode_span<TILE>(p, my_len).n + CHARGE;
     }
     inc = scan(mine);
     total = (long long)__shfl_sync(0xffffffffu, inc, 31) * p.units;
@@ -270,18 +271,18 @@ __device__ __forceinline__ void decode_start(const DecodeCore& p, int cta, int l
   } else {
     long long sum = 0;
     for (int base = 32 * kChunks; base < p.B; base += 32 * kChunks) {
-      decode_charges<TILE>(p, base, lane, len, c);
+      decode_charges<TILE, CHARGE>(p, base, lane, len, c);
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) sum += c[i];
     }
-    decode_charges<TILE>(p, 0, lane, len, c);         // (kept for the search)
+    decode_charges<TILE, CHARGE>(p, 0, lane, len, c);         // (kept for the search)
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) sum += c[i];
     total = warp_sum(sum) * p.units;
     range();
     at = -1;
     for (int base = 0; at < 0; base += 32 * kChunks) {
-      if (base) decode_charges<TILE>(p, base, lane, len, c);
+      if (base) decode_charges<TILE, CHARGE>(p, base, lane, len, c);
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         if (at >= 0) break;
@@ -797,7 +798,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
 // it alone (the same bits every time).  WPR warps per row: 1 where there are many
 // rows, 8 where there are few, 32 where a unit may have so many pieces (one KV
 // head over 131072 tokens has one per CTA, 304).
-template <bool BF16, int D, int WPR, int TILE = kDecTile>
+template <bool BF16, int D, int WPR, int TILE = kDecTile, int CHARGE = kUnitTiles>
 __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) fa_decode_join_kernel(const __grid_constant__ DecodeCore p, int rows8) {
   constexpr int kWarps = WPR > 8 ? WPR : 8;
   __shared__ __align__(16) float s_o[WPR][D];
@@ -817,7 +818,7 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) fa_decode_join_kerne
   long long total = 0, before = 0;
   auto add_up = [&](int base, int end) {                 // charges of 256 sequences, and of those before `end`
     int len[kChunks], c[kChunks];
-    decode_charges<TILE>(p, base, lane, len, c);
+    decode_charges<TILE, CHARGE>(p, base, lane, len, c);
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
       total += c[i];
@@ -837,14 +838,14 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) fa_decode_join_kerne
     if (lane == 0) s_sum[warp][0] = total, s_sum[warp][1] = before;
     __syncthreads();
     total = warp_sum(lane < kWarps ? s_sum[lane][0] : 0);
-    before = (lane < kWarps ? s_sum[lane][1] : 0) + (b0 + lane < b ? decode_span<TILE>(p, decode_len(p, b0 + lane)).n + kUnitTiles : 0);
+    before = (lane < kWarps ? s_sum[lane][1] : 0) + (b0 + lane < b ? decode_span<TILE>(p, decode_len(p, b0 + lane)).n + CHARGE : 0);
     before = warp_sum(before);                           // (b - b0 is less than the block's 8 rows)
   }
   if (none) return;
   total *= p.units;
   const int ctas = decode_ctas(p, total);
   const int n = decode_span<TILE>(p, decode_len(p, b)).n;
-  const long long t0 = before * p.units + (long long)(hk * p.groups + rg) * (n + kUnitTiles) + kUnitTiles;
+  const long long t0 = before * p.units + (long long)(hk * p.groups + rg) * (n + CHARGE) + CHARGE;
   const int c0 = decode_owner(total, ctas, t0), c1 = decode_owner(total, ctas, t0 + n - 1);
   pdl_wait_prior();
   if (c0 == c1) return;          // finished by its CTA

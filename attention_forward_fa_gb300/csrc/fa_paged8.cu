@@ -124,7 +124,7 @@ int launch_wide_rows(fa::WideParams& p, long long keys, cudaStream_t st) {
   c.groups = (int)(((long long)c.rows + rows8 - 1) / rows8);
   if ((long long)c.Hkv * c.groups > 0x7FFFFFFFLL) return FA_ERR_SHAPE;
   c.units = c.Hkv * c.groups;
-  const long long most = ((keys + fa::kWideTile - 1) / fa::kWideTile + fa::kUnitTiles) * c.B * c.units;
+  const long long most = ((keys + fa::kWideTile - 1) / fa::kWideTile + fa::kWideCharge) * c.B * c.units;
   c.ctas = (int)std::min<long long>(sms, most);
   auto inverse = [](unsigned long long d) { return d == 1 ? 0ull : ~0ull / d + 1; };   // ceil(2^64 / d)
   c.ctas_inv = inverse(c.ctas);
@@ -139,13 +139,13 @@ int launch_wide_rows(fa::WideParams& p, long long keys, cudaStream_t st) {
   cudaError_t e = launch_dependent(kern, (unsigned)c.ctas, fa::kWideThreads<EIGHT>, smem, st, p);
   if (e == cudaSuccess) {   // (as fa_paged.cu joins)
     const long long rows = (long long)c.B * c.Hkv * c.rows;
-    constexpr int T = fa::kWideTile;
+    constexpr int T = fa::kWideTile, C = fa::kWideCharge;
     if (rows > 8LL * sms)
-      e = launch_dependent(fa::fa_decode_join_kernel<BF16, D, 1, T>, (unsigned)((rows + 7) / 8), 256, 0, st, c, rows8);
+      e = launch_dependent(fa::fa_decode_join_kernel<BF16, D, 1, T, C>, (unsigned)((rows + 7) / 8), 256, 0, st, c, rows8);
     else if (c.ctas / ((long long)c.B * c.units) < 32)
-      e = launch_dependent(fa::fa_decode_join_kernel<BF16, D, 8, T>, (unsigned)rows, 256, 0, st, c, rows8);
+      e = launch_dependent(fa::fa_decode_join_kernel<BF16, D, 8, T, C>, (unsigned)rows, 256, 0, st, c, rows8);
     else
-      e = launch_dependent(fa::fa_decode_join_kernel<BF16, D, 32, T>, (unsigned)rows, 1024, 0, st, c, rows8);
+      e = launch_dependent(fa::fa_decode_join_kernel<BF16, D, 32, T, C>, (unsigned)rows, 1024, 0, st, c, rows8);
   }
   cudaFreeAsync(scratch, st);
   return e == cudaSuccess ? FA_OK : cuda_fail(e);

@@ -45,6 +45,9 @@ namespace fa {
 constexpr int kWideTile = 128;
 constexpr int kWideInfo = 8;       // tiles whose keys and scales are kept: the producer is at most seven ahead
 
+// A unit's own cost in tiles: its rows, its ends, its answer.  (16 trees of up to 12 drafts over up to 8192
+// tokens: 90 us at 2, 78 at 3, 70 at 5, 69 at 8; 4 of up to 64 over an 8-bit cache 88, 86, 87, 89.)
+constexpr int kWideCharge = 6;
 constexpr int kWideFlush = 64;     // tiles that add up in TMEM
 constexpr int kWideDrafts = 64;    // drafts whose ancestors are kept as words; of larger trees they are looked up tile by tile
 
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
   // In this order: the join kernel may then read the lengths as soon as it runs.
   pdl_wait_prior();
   pdl_launch_dependents();
-  if (warp == kProducer) decode_start<kWideTile>(p, blockIdx.x, lane, s_walk, s_len);
+  if (warp == kProducer) decode_start<kWideTile, kWideCharge>(p, blockIdx.x, lane, s_walk, s_len);
   else if (blockIdx.x == 0 && warp < kDecWarps) decode_report(p);
   __syncthreads();
   tc_fence_after();
@@ -193,7 +196,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
       x.b = walk.b;
       x.unit = walk.unit;
       x.s = decode_span<kWideTile>(p, x.len);
-      x.d = decode_step(walk, x.s.n, p.units);
+      x.d = decode_step<kWideCharge>(walk, x.s.n, p.units);
       if (walk.b != x.b && walk.left > 0) next_len = decode_len(p, walk.b);
       if (x.d.nt) return true;
     }
