@@ -21,10 +21,13 @@
 //     into the value product is 2^(s' - m), the weight of the value's codes, and
 //     the sum of the softmax takes 2^(s' - m) 2^-e.  So the product's operands are
 //     as large as what they add, whatever the scales.
-//   * P is one fp16, not a hi + lo pair: a value's code is off by up to 2^-4 of
-//     the value, and the rounding of P, 2^-12 of each key's contribution, stays
-//     below the rounding of a bf16 output and at that of an fp16 one.
+//   * P is one fp16 where the answer is bf16: its rounding, 2^-11 of each key's
+//     contribution at most, is a quarter of the answer's own.  An fp16 answer gets a
+//     hi + lo pair (one fp16 would add as much as its own rounding: 2.9e-4 against 2.1e-4
+//     of the answer over 64 sequences of up to 8192 tokens).
 #pragma once
+#include <type_traits>
+
 #include "fa_decode.cuh"
 #include "fa_paged8.cuh"
 
@@ -37,8 +40,9 @@ constexpr int kDec8Groups = 8;      // of 16 keys; a consumer scores two
 // kernel started beside the last CTAs of the one before it: five warps each fill the four register
 // files only from the right first one on.  The third then ran alone at the end, and 8 sequences of
 // 131072 tokens took 435 us back to back against 310 us one by one.)
-template <int NT>
-constexpr int kDec8Teams = NT <= 2 ? 3 : 2;
+// (Two where a third's shared memory or registers do not fit.)
+template <bool BF16, int NT>
+constexpr int kDec8Teams = NT == 1 || (NT == 2 && BF16) ? 3 : 2;
 
 struct Decode8Params {
   DecodeCore c;
@@ -49,14 +53,15 @@ struct Decode8Params {
   CUtensorMap tm_v;
 };
 
-template <int D, int NT>
+template <bool BF16, int D, int NT>
 struct Decode8Smem {
+  using P = std::conditional_t<BF16, uint2, uint4>;              // 16 keys' P of a lane: hi, or hi and lo
   static constexpr int kHalf = kDec8Tile * D;                    // K or V of a tile
   static constexpr int kStages = 2 * (128 / D);                  // 64 KB
   static constexpr bool kQShared = NT > 2;
   static constexpr int kScaleOff = kStages * 2 * kHalf;          // bytes [stages][K, V][128]
-  static constexpr int kPOff = kScaleOff + kStages * 2 * kDec8Tile;              // uint2 [8 x 16 keys][NT][lane]
-  static constexpr int kQOff = kPOff + kDec8Groups * NT * 256;                   // uint2 [NT][D / 16][lane]
+  static constexpr int kPOff = kScaleOff + kStages * 2 * kDec8Tile;              // P [8 x 16 keys][NT][lane]
+  static constexpr int kQOff = kPOff + kDec8Groups * NT * 32 * (int)sizeof(P);   // uint2 [NT][D / 16][lane]
   static constexpr int kFacOff = kQOff + (kQShared ? NT * (D / 16) * 256 : 0);   // float [8 NT]: Q's scales
   static constexpr int kMaxOff = kFacOff + 8 * NT * 4;                           // float [warps][8 NT]
   static constexpr int kSumOff = kMaxOff + kDecWarps * 8 * NT * 4;
@@ -64,7 +69,7 @@ struct Decode8Smem {
   static constexpr int kBarOff = kMetaOff + kStages * kDec8Groups * 4;
   static constexpr int kMiscOff = kBarOff + 2 * kStages * 8;
   static constexpr int kTeam = (kMiscOff + 64 + 1023) / 1024 * 1024;   // (swizzled tiles start on 1024 bytes)
-  static constexpr int kBytes = kTeam * kDec8Teams<NT>;
+  static constexpr int kBytes = kTeam * kDec8Teams<BF16, NT>;
   static_assert(kBytes <= 227 * 1024, "one CTA per SM");
 };
 
@@ -93,9 +98,10 @@ __device__ __forceinline__ void codes4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 }
 
 template <bool BF16, int D, int NT, bool E5M2>
-__global__ void __launch_bounds__(kDecThreads * kDec8Teams<NT>, 1) fa_decode8_kernel(const __grid_constant__ Decode8Params params) {
+__global__ void __launch_bounds__(kDecThreads * kDec8Teams<BF16, NT>, 1) fa_decode8_kernel(const __grid_constant__ Decode8Params params) {
   const DecodeCore& p = params.c;
-  using SM = Decode8Smem<D, NT>;
+  using SM = Decode8Smem<BF16, D, NT>;
+  using P = typename SM::P;
   constexpr int NS = SM::kStages;
   constexpr int KC = D / 16;                   // 16-byte chunks of a row
   extern __shared__ __align__(1024) uint8_t smem_all[];
@@ -194,7 +200,7 @@ __global__ void __launch_bounds__(kDecThreads * kDec8Teams<NT>, 1) fa_decode8_ke
   // ============================================================ consumers
   constexpr int DC = D / 64;                         // 16-channel chunks of this warp's quarter of O
   const int g = lane >> 2, t4 = lane & 3;
-  uint2* s_p = reinterpret_cast<uint2*>(smem + SM::kPOff);
+  P* s_p = reinterpret_cast<P*>(smem + SM::kPOff);
   uint2* s_q = reinterpret_cast<uint2*>(smem + SM::kQOff);
   float* s_fac = reinterpret_cast<float*>(smem + SM::kFacOff);
   float* s_max = reinterpret_cast<float*>(smem + SM::kMaxOff);
@@ -415,7 +421,13 @@ __global__ void __launch_bounds__(kDecThreads * kDec8Teams<NT>, 1) fa_decode8_ke
           const float p2 = ex2_approx(c[u][n][2] - m[n][0]), p3 = ex2_approx(c[u][n][3] - m[n][1]);
           l[n][0] = fmaf(p0, back[u][0], fmaf(p2, back[u][1], l[n][0]));
           l[n][1] = fmaf(p1, back[u][0], fmaf(p3, back[u][1], l[n][1]));
-          s_p[((2 * warp + u) * NT + n) * 32 + lane] = make_uint2(transpose8(pack_f16x2(p0, p1)), transpose8(pack_f16x2(p2, p3)));
+          const uint32_t h0 = pack_f16x2(p0, p1), h1 = pack_f16x2(p2, p3);
+          P& at = s_p[((2 * warp + u) * NT + n) * 32 + lane];
+          if constexpr (BF16)
+            at = make_uint2(transpose8(h0), transpose8(h1));
+          else
+            at = make_uint4(transpose8(h0), transpose8(h1), transpose8(pack_residual_x2(p0, p1, h0, false)),
+                            transpose8(pack_residual_x2(p2, p3, h1, false)));
         }
       sync();
       // Keys that no row sees have P = 0, and their V may hold anything (or be stale): it becomes 0.
@@ -462,9 +474,13 @@ __global__ void __launch_bounds__(kDecThreads * kDec8Teams<NT>, 1) fa_decode8_ke
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const uint2 pp = s_p[((2 * q2 + u) * NT + n) * 32 + lane];
+            const P pp = s_p[((2 * q2 + u) * NT + n) * 32 + lane];
 #pragma unroll
             for (int i = 0; i < DC; ++i) mma_16x8<false>(sum[n][i], v[u][i], pp.x, pp.y);
+            if constexpr (!BF16) {
+#pragma unroll
+              for (int i = 0; i < DC; ++i) mma_16x8<false>(sum[n][i], v[u][i], pp.z, pp.w);
+            }
           }
       }
 #pragma unroll

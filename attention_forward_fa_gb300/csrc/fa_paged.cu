@@ -188,8 +188,8 @@ int launch_decode_rows(fa::DecodeParams& p, long long tiles_per_unit, cudaStream
     case 2: return launch_decode<BF16, D, 2, TREE>(p, most, st);
     case 3: return launch_decode<BF16, D, 3, TREE>(p, most, st);
     case 4: return launch_decode<BF16, D, 4, TREE>(p, most, st);
-    case 5: return launch_decode<BF16, D, 5, TREE>(p, most, st);
-    default: return launch_decode<BF16, D, 6, TREE>(p, most, st);
+    case 5: return launch_decode<BF16, D, TREE ? 4 : 5, TREE>(p, most, st);      // (trees of more rows: launch_wide)
+    default: return launch_decode<BF16, D, TREE ? 4 : 6, TREE>(p, most, st);
   }
 }
 

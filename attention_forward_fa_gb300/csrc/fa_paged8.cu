@@ -42,7 +42,7 @@ namespace {
 template <bool BF16, int D, int NT, bool E5M2>
 int launch_decode8_rows(fa::Decode8Params& p, long long most_tiles, cudaStream_t st) {
   auto kern = fa::fa_decode8_kernel<BF16, D, NT, E5M2>;
-  constexpr int smem = fa::Decode8Smem<D, NT>::kBytes;
+  constexpr int smem = fa::Decode8Smem<BF16, D, NT>::kBytes;
   int dev = 0;
   cudaGetDevice(&dev);
   static std::once_flag once[64];
@@ -53,7 +53,7 @@ int launch_decode8_rows(fa::Decode8Params& p, long long most_tiles, cudaStream_t
   if (attr_err[dev & 63] != cudaSuccess) return cuda_fail(attr_err[dev & 63]);
   const int sms = sm_count();
   if (sms <= 0) return cuda_fail(cudaErrorInvalidDevice);
-  p.c.ctas = (int)std::min<long long>(fa::kDec8Teams<NT> * sms, most_tiles);
+  p.c.ctas = (int)std::min<long long>(fa::kDec8Teams<BF16, NT> * sms, most_tiles);
   auto inverse = [](unsigned long long d) { return d == 1 ? 0ull : ~0ull / d + 1; };   // ceil(2^64 / d)
   p.c.ctas_inv = inverse(p.c.ctas);
   p.c.units_inv = inverse(p.c.units);
@@ -63,7 +63,7 @@ int launch_decode8_rows(fa::Decode8Params& p, long long most_tiles, cudaStream_t
   p.c.part_o = static_cast<float*>(scratch);
   p.c.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(scratch) + o_bytes);
   const unsigned grid = (unsigned)std::min(p.c.ctas, sms);
-  cudaError_t e = launch_dependent(kern, grid, fa::kDecThreads * fa::kDec8Teams<NT>, smem, st, p);
+  cudaError_t e = launch_dependent(kern, grid, fa::kDecThreads * fa::kDec8Teams<BF16, NT>, smem, st, p);
   if (e == cudaSuccess) {   // (as for a 16-bit cache)
     const long long rows = (long long)p.c.B * p.c.Hkv * p.c.rows;
     constexpr int T = fa::kDec8Tile;

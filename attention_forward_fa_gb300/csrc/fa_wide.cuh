@@ -6,7 +6,7 @@
 // the keys' bytes (1.4 us a row for 16 sequences of 4096 tokens on 8 KV heads).
 // Here up to 128 rows are the lanes of one accumulator, a row per softmax thread,
 // and a tile of 128 keys costs about 1000 cycles of the tensor cores whatever the
-// rows (over a 16-bit cache 1500), below the 2900 that its 64 KB take from memory (an
+// rows (1500 where P is a pair), below the 2900 that its 64 KB take from memory (an
 // 8-bit tile: 1450).
 //
 //   * One CTA per SM with two accumulators and two groups of softmax warps, which take
@@ -30,8 +30,8 @@
 //     the codes stay and the softmax threads take each key's exponent, which is slow.
 //   * The next S of a group is issued behind its P V, so that its commit says that O is at
 //     rest: the softmax threads may then move their references and rescale O.
-//   * P is written over S: as a hi + lo pair of the cache's type (16-bit: 64 + 64 columns),
-//     or as one fp16 (8-bit).
+//   * P is written over S, as a hi + lo pair of the operands' type (64 + 64 columns) or, over an
+//     8-bit cache with bf16 answers, as one fp16.
 //   * Up to kWideFlush tiles of a piece add up in TMEM, where the adder cuts off what it adds
 //     (about 2^-24 of the sum each 16 keys, always towards zero: 2^-15 over 8192 keys);
 //     then the softmax threads add O to a place in scratch in fp32.
@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
   constexpr int NS = SM::kStages, RS = EIGHT ? SM::kRawStages : 1;
   constexpr int kRows = SPLIT ? 128 : 256;            // of a unit
   constexpr bool kP16 = EIGHT || !BF16;               // the type of P (and of Q, K and V as operands): fp16 or bf16
+  constexpr bool kPair = !EIGHT || !BF16;             // P as hi + lo (fa_decode.cuh, fa_decode8.cuh)
   constexpr float kLiftP = kLift<!kP16>;
   constexpr int kProducer = 8, kIssuer = 9, kConvert = 12;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
         const uint32_t o = tmem + 256 + 128 * t, s = tmem + 128 * t;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) mma_ts_if(o, s + 8 * kk, b + (kk * 2048 >> 4), kIdescO, i % kWideFlush || kk, lead);
-        if constexpr (!EIGHT) {
+        if constexpr (kPair) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) mma_ts_if(o, s + 64 + 8 * kk, b + (kk * 2048 >> 4), kIdescO, 1, lead);
         }
@@ -705,10 +706,10 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
             b = ex2_approx(b);
             sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(a, b));
             hi[i] = kP16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
-            if constexpr (!EIGHT) lo[i] = pack_residual_x2(a, b, hi[i], !kP16);
+            if constexpr (kPair) lo[i] = pack_residual_x2(a, b, hi[i], !kP16);
           }
           tmem_st16(tS + 16 * c, hi);
-          if constexpr (!EIGHT) tmem_st16(tS + 64 + 16 * c, lo);
+          if constexpr (kPair) tmem_st16(tS + 64 + 16 * c, lo);
         }
         if (!(EIGHT && info.each)) {
           float a, b, c, d;

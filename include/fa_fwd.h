@@ -590,7 +590,7 @@ typedef struct {
  * pre_tokens nor page_idx (FA_ERR_UNSUPPORTED).
  * Over an 8-bit cache the products take fp16 codes, Q as fp16 of a power of
  * two times it (exact but for bf16 channels below 2^-29 of their row's largest) and P
- * as one fp16; scores and sums are fp32.
+ * as one fp16, for fp16 answers as a hi + lo pair; scores and sums are fp32.
  */
 int fa_decode_ext(const void* q, const fa_paged_kv_t* kv, const fa_kv_fp8_t* fp8, void* o, float* lse,
                   int B, int Hq, int Hkv, int Sq, int D, float scale, int mask_mode,
