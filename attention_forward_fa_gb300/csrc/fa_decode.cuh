@@ -159,15 +159,16 @@ __device__ __forceinline__ bool decode_ancestor(const DecodeCore& p, int b, int 
   return i < drafts && j < drafts && p.ancestors[b * p.anc_stride + (long long)i * p.Sq + j] != 0;
 }
 // Lengths and numbers of drafts that the tables cannot hold are reported, once.
+template <bool TREE>
 __device__ __forceinline__ void decode_report(const DecodeCore& p) {
   for (int i = threadIdx.x; i < p.B; i += 32 * kDecWarps) {
     const int len = p.kv_lens[i];
-    bool bad = len < 0 || len > p.max_len;
-    if (p.ancestors && !bad) {
+    if (len < 0 || len > p.max_len) {
+      atomicOr(p.status, fa_host::kStatusIndex);
+    } else if (TREE && p.ancestors) {
       const int n = p.new_lens ? p.new_lens[i] : p.Sq;
-      bad = n < 0 || n > p.Sq || n > len;
+      if (n < 0 || n > p.Sq || n > len) atomicOr(p.status, fa_host::kStatusIndex);
     }
-    if (bad) atomicOr(p.status, fa_host::kStatusIndex);
   }
 }
 
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
   if (warp == kDecWarps) {   // this CTA's range of charged tiles, and the sequence it starts in
     decode_start(p, blockIdx.x, lane, s_walk, s_len);
   } else if (blockIdx.x == 0) {
-    decode_report(p);
+    decode_report<TREE>(p);
   }
   __syncthreads();
   DecodeWalk walk = *s_walk;
