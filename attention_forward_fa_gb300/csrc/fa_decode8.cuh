@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kDecThreads * kDec8Teams<BF16, NT>, 1) fa_deco
   pdl_wait_prior();
   pdl_launch_dependents();
   if (warp == kDecWarps) decode_start<kDec8Tile>(p, cta, lane, s_walk, s_len);
-  else if (cta == 0) decode_report<true>(p);
+  else if (cta == 0) decode_report(p);
   __syncthreads();
   DecodeWalk walk = *s_walk;
   const WaitCtx wc{s_abort, p.status, p.timeout_ns};

@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
   pdl_wait_prior();
   pdl_launch_dependents();
   if (warp == kProducer) decode_start<kWideTile, kWideCharge>(p, blockIdx.x, lane, s_walk, s_len);
-  else if (blockIdx.x == 0 && warp < kDecWarps) decode_report<true>(p);
+  else if (blockIdx.x == 0 && warp < kDecWarps) decode_report(p);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
