@@ -434,40 +434,45 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
           const uint32_t first = to + (((2 * (c & 3) + swap) ^ (row & 7)) << 4), second = first ^ 16u;
           const int top = kind ? top_v : top_k;
           const uint8_t* scale = scales + 128 * kind + row;
-          auto convert = [&](auto format) {
+          auto convert = [&](auto format, auto every) {
             constexpr bool E5M2 = decltype(format)::value;
 #pragma unroll 1
             for (int i0 = 0; i0 < kChunks; i0 += 4) {
               uint4 w[4];                              // (four loads, then their stores: one order of memory for all)
-              int e[4];
+              uint32_t f[4];
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
                 w[y] = *reinterpret_cast<const uint4*>(raw + (i0 + y) * (kStep * D));
-                e[y] = (int)scale[kStep * (i0 + y)] - top;                // (<= 0 where the row is seen)
+                f[y] = scale[kStep * (i0 + y)];
               }
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
-                const int i = i0 + y;
-                // 2^e as an fp16, exactly down to 2^-24
-                uint32_t f = e[y] < -24 ? 0u : e[y] < -14 ? 1u << ((24 + e[y]) & 31) : (uint32_t)(15 + e[y]) << 10;
-                if (top == 0) f = 0x3C00u;
-                if (!whole && !seen(row + kStep * i)) w[y] = make_uint4(0, 0, 0, 0), f = 0;
-                f |= f << 16;
+                // 2^(e - E) as an fp16 pair, exactly down to 2^-24 (e <= E where the row is seen)
+                const float x = top ? scale_of(max((int)f[y] - top, -100) + 127) : 1.f;
+                f[y] = pack_f16x2(x, x);
+                if (!decltype(every)::value && !seen(row + kStep * (i0 + y))) w[y] = make_uint4(0, 0, 0, 0), f[y] = 0;
+                if (D == 128 && swap) w[y] = make_uint4(w[y].z, w[y].w, w[y].x, w[y].y);
+              }
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
                 uint32_t h[8];
                 codes4<E5M2>(w[y].x, h[0], h[1]);
                 codes4<E5M2>(w[y].y, h[2], h[3]);
                 codes4<E5M2>(w[y].z, h[4], h[5]);
                 codes4<E5M2>(w[y].w, h[6], h[7]);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) h[q] = mul_f16x2(h[q], f);
-                const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                st_shared_v4(first + i * (kStep * 128), swap ? hi : lo);
-                st_shared_v4(second + i * (kStep * 128), swap ? lo : hi);
+                for (int q = 0; q < 8; ++q) h[q] = mul_f16x2(h[q], f[y]);
+                st_shared_v4(first + (i0 + y) * (kStep * 128), make_uint4(h[0], h[1], h[2], h[3]));
+                st_shared_v4(second + (i0 + y) * (kStep * 128), make_uint4(h[4], h[5], h[6], h[7]));
               }
             }
           };
-          if (params.e5m2) convert(std::true_type{});
-          else convert(std::false_type{});
+          auto of = [&](auto format) {
+            if (whole) convert(format, std::true_type{});
+            else convert(format, std::false_type{});
+          };
+          if (params.e5m2) of(std::true_type{});
+          else of(std::false_type{});
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
