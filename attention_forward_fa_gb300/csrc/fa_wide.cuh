@@ -13,10 +13,9 @@
 //     turns with the tensor cores.  A unit of up to 256 rows has 128 in each and shares
 //     every key tile; with up to 128 rows (SPLIT) both have all rows and take every other
 //     tile, and the first group joins the two at a piece's end.
-//   * A producer warp, a warp whose first lane issues the MMAs, and over an 8-bit cache
-//     four converter warps.  All hand-offs are mbarriers with bounded waits; no role waits
-//     for another in any other way, so that an expired wait ends every role by the
-//     abort flag.
+//   * A producer warp, a warp that issues the MMAs, and over an 8-bit cache six converter
+//     warps.  All hand-offs are mbarriers with bounded waits; no role waits for another in
+//     any other way, so that an expired wait ends every role by the abort flag.
 //   * Loads K(0), V(0), K(1), ... go through one ring of operand tiles (128 keys,
 //     D / 64 chunks of 64 channels, 128-byte swizzle).  A 16-bit tile comes by TMA, a box
 //     per page part and chunk; an 8-bit one comes as codes into a second ring, and
@@ -76,8 +75,8 @@ struct WideSmem {
   static constexpr int kRaw = 128 * D;                           // codes of K or V of a tile
   static constexpr int kRingOff = (SPLIT ? 1 : 2) * kOp;         // (behind Q)
   static constexpr int kRawOff = kRingOff + kStages * kOp;
-  static constexpr int kScaleOff = kRawOff + kRawStages * kRaw;  // bytes [kWideInfo][K, V][128]
-  static constexpr int kMetaOff = kScaleOff + (EIGHT ? kWideInfo * 256 : 0);     // int [kWideInfo][8]
+  static constexpr int kScaleOff = kRawOff + kRawStages * kRaw;  // bytes [kWideInfo][K, V with K, V with V][128]
+  static constexpr int kMetaOff = kScaleOff + (EIGHT ? kWideInfo * 384 : 0);     // int [kWideInfo][8]
   static constexpr int kInfoOff = kMetaOff + kWideInfo * 32;     // WideTileInfo [kWideInfo]
   static constexpr int kMlOff = kInfoOff + kWideInfo * 16;       // float2 [128]: the second group's reference and sum
   static constexpr int kTreeOff = kMlOff + (SPLIT ? 1024 : 0);   // uint2 [2][kWideDrafts]: what each draft sees, per piece's parity
@@ -87,7 +86,8 @@ struct WideSmem {
   static constexpr int kBytes = kMiscOff + 64;
   static_assert(kBytes <= 227 * 1024, "one CTA per SM");
 };
-// Two groups of four softmax warps, one of producer and issuer (and two idle warps), one of converters.
+// Two groups of four softmax warps, producer, issuer, and six converters or two idle warps.
+constexpr int kWideConverters = 3;      // of K, and as many of V
 template <bool EIGHT>
 constexpr int kWideThreads = EIGHT ? 512 : 384;
 // Registers per thread at launch, and of the softmax warps and the others after they have traded.
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
   constexpr bool kP16 = EIGHT || !BF16;               // the type of P (and of Q, K and V as operands): fp16 or bf16
   constexpr bool kPair = !EIGHT || !BF16;             // P as hi + lo (fa_decode.cuh, fa_decode8.cuh)
   constexpr float kLiftP = kLift<!kP16>;
-  constexpr int kProducer = 8, kIssuer = 9, kConvert = 12;
+  constexpr int kProducer = 8, kIssuer = 9, kConvert = 10;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -148,13 +148,13 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
     tma_prefetch_desc(&params.tm_k);
     tma_prefetch_desc(&params.tm_v);
     for (int s = 0; s < NS; ++s) {
-      mbar_init(FULL(s), EIGHT ? 4 : 1);
+      mbar_init(FULL(s), EIGHT ? kWideConverters : 1);
       mbar_init(EMPTY(s), 1);
     }
     if constexpr (EIGHT)
       for (int s = 0; s < RS; ++s) {
         mbar_init(RFULL(s), 1);
-        mbar_init(REMPTY(s), 4);
+        mbar_init(REMPTY(s), kWideConverters);
       }
     for (int t = 0; t < 2; ++t) {
       mbar_init(SFULL(t), 1);
@@ -247,19 +247,18 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
           if (kind == 0 && lane < 8) s_meta[at * 8 + lane] = first < 0 ? -1 : first + (off & (box - 1));
           __syncwarp();
           const uint32_t bar = EIGHT ? RFULL(st) : FULL(st);
-          const uint32_t each = EIGHT ? (uint32_t)box * D + (kind == 0 ? 2u * box : 0u) : (uint32_t)box * D * 2;
+          const uint32_t each = EIGHT ? (uint32_t)box * D + (kind == 0 ? 2u * box : (uint32_t)box) : (uint32_t)box * D * 2;
           if (lane == 0) mbar_arrive_expect_tx(bar, each * __popc(live));
           __syncwarp();
           if (mine) {
             const void* tm = kind ? &params.tm_v : &params.tm_k;
             if constexpr (EIGHT) {
               tma_load_4d(sbase + SM::kRawOff + st * SM::kRaw + sub * box * D, tm, bar, slot, hk, id);
-              if (kind == 0) {       // both scales with K: the softmax needs the values' before V
-                const long long from = (((long long)id * p.Hkv + hk) << p.page_shift) + slot;
-                const uint32_t to = sbase + SM::kScaleOff + at * 256 + sub * box;
-                bulk_load(to, params.k_scale + from, box, bar);
-                bulk_load(to + 128, params.v_scale + from, box, bar);
-              }
+              // both scales with K, as the softmax needs the values' before V; theirs with V again
+              const long long from = (((long long)id * p.Hkv + hk) << p.page_shift) + slot;
+              const uint32_t to = sbase + SM::kScaleOff + at * 384 + sub * box;
+              if (kind == 0) bulk_load(to, params.k_scale + from, box, bar);
+              bulk_load(to + (kind ? 256 : 128), params.v_scale + from, box, bar);
             } else {
 #pragma unroll
               for (int c = 0; c < D / 64; ++c)
@@ -377,108 +376,107 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
       drain_bar(DRAIN, 0, wc.timeout);
     }
     __syncwarp();
-  } else if (warp == kIssuer + 1 || warp == kIssuer + 2) {
+  } else if (!EIGHT && warp >= kConvert) {
     regs_dec<kWideOtherRegs<EIGHT>>();               // (idle: registers are traded by groups of four warps)
   } else if (EIGHT && warp >= kConvert) {
     // ============================================================ converters
+    // Half of them take the K tiles, half the V tiles: a tile's way through registers is latency (loads, two
+    // conversions and a product deep, stores, the fence), so that two at a time go twice as fast.
     regs_dec<kWideOtherRegs<EIGHT>>();
-    const int tid = threadIdx.x - 32 * kConvert;
+    constexpr int kThreads = 32 * kWideConverters;
+    const int tid = (threadIdx.x - 32 * kConvert) % kThreads, kind = (threadIdx.x - 32 * kConvert) / kThreads;
     int tile = 0;
     bool dead = false;
     while (!dead && next_piece(x)) {
-      for (int j = 0; j < x.d.nt && !dead; ++j, ++tile) {
-        const int at = tile % kWideInfo;
-        uint8_t* scales = smem + SM::kScaleOff + at * 256;
+      for (int j = 0; j < x.d.nt; ++j, ++tile) {
+        const int at = tile % kWideInfo, ld = 2 * tile + kind, rs = ld % RS, st = ld % NS;
+        if (!__all_sync(0xffffffffu, wait_bar(RFULL(rs), (ld / RS) & 1, wc))) dead = true;
+        if (!dead && ld >= NS && !__all_sync(0xffffffffu, wait_bar(EMPTY(st), (ld / NS - 1) & 1, wc))) dead = true;
+        if (dead) break;
         const int* meta = s_meta + at * 8;
-        int top_k = 0, top_v = 0;
-        bool whole = false;                  // every key is seen
+        auto seen = [&](int r) {
+          const int k = meta[r >> 4] < 0 ? -1 : meta[r >> 4] + (r & 15);
+          return k >= x.s.lo && k < x.s.hi;
+        };
+        // every warp for itself: the largest exponents of the seen keys, the values' least
+        const uint8_t* scales = smem + SM::kScaleOff + at * 384;           // K's, V's as they came with K, with V
+        int top_k = 0, top_v = 0, low_v = 255;
+        unsigned on = 0;
 #pragma unroll
-        for (int kind = 0; kind < 2; ++kind) {
-          const int ld = 2 * tile + kind, rs = ld % RS, st = ld % NS;
-          if (!__all_sync(0xffffffffu, wait_bar(RFULL(rs), (ld / RS) & 1, wc))) dead = true;
-          if (!dead && ld >= NS && !__all_sync(0xffffffffu, wait_bar(EMPTY(st), (ld / NS - 1) & 1, wc))) dead = true;
-          if (dead) break;
-          auto seen = [&](int r) {
-            const int k = meta[r >> 4] < 0 ? -1 : meta[r >> 4] + (r & 15);
-            return k >= x.s.lo && k < x.s.hi;
-          };
-          if (kind == 0) {           // every warp for itself: the largest exponents of the seen keys, the values' least
-            int low_v = 255;
-            unsigned on = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = 32 * i + lane;
-              if (!seen(r)) continue;
-              ++on;
-              const int ks = scales[r], vs = scales[128 + r];
-              top_k = max(top_k, ks), top_v = max(top_v, vs), low_v = min(low_v, vs);
-            }
-            top_k = __reduce_max_sync(0xffffffffu, top_k);
-            top_v = __reduce_max_sync(0xffffffffu, top_v);
-            low_v = __reduce_min_sync(0xffffffffu, low_v);
-            whole = __all_sync(0xffffffffu, on == 4);
-            const bool each = top_v - low_v > (params.e5m2 ? 8 : 15);
-            if (each) top_v = 0;                     // (0: the codes of V stay as they are)
-            if (tid == 0)
-              s_info[at] = WideTileInfo{scale_of(top_k), top_v ? (float)(top_v - 127) : 0.f,
-                                        top_v ? __uint_as_float((uint32_t)(254 - top_v) << 23) : 1.f, each};
-          }
-          // a thread keeps to one 16-byte chunk of codes and to the rows `row` + kStep i, whose places in the
-          // operand tile are kStep rows apart
-          constexpr int kChunks = D / 16, kStep = 128 / kChunks;
-          const int c = tid % kChunks, row = tid / kChunks;
-          const uint8_t* raw = smem + SM::kRawOff + rs * SM::kRaw + tid * 16;
-          const uint32_t to = sbase + SM::kRingOff + st * SM::kOp + (c >> 2) * (128 * 128) + row * 128;
-          // (the two halves of a chunk, for the second 64 channels in the other order: no bank twice)
-          const bool swap = (c >> 2) & 1;
-          const uint32_t first = to + (((2 * (c & 3) + swap) ^ (row & 7)) << 4), second = first ^ 16u;
-          const int top = kind ? top_v : top_k;
-          const uint8_t* scale = scales + 128 * kind + row;
-          auto convert = [&](auto format, auto every) {
-            constexpr bool E5M2 = decltype(format)::value;
+        for (int i = 0; i < 4; ++i) {
+          const int r = 32 * i + lane;
+          if (!seen(r)) continue;
+          ++on;
+          const int ks = scales[r], vs = scales[(kind ? 256 : 128) + r];
+          top_k = max(top_k, ks), top_v = max(top_v, vs), low_v = min(low_v, vs);
+        }
+        top_v = __reduce_max_sync(0xffffffffu, top_v);
+        low_v = __reduce_min_sync(0xffffffffu, low_v);
+        const bool whole = __all_sync(0xffffffffu, on == 4);               // every key is seen
+        const bool each = top_v - low_v > (params.e5m2 ? 8 : 15);
+        if (each) top_v = 0;                                               // (0: the codes of V stay as they are)
+        int top = top_v;
+        if (kind == 0) {
+          top = __reduce_max_sync(0xffffffffu, top_k);
+          if (tid == 0)
+            s_info[at] = WideTileInfo{scale_of(top), top_v ? (float)(top_v - 127) : 0.f,
+                                      top_v ? __uint_as_float((uint32_t)(254 - top_v) << 23) : 1.f, each};
+        }
+        // a thread keeps to one 16-byte chunk of codes and to the rows `row` + kStep i
+        constexpr int kChunks = D / 16, kStep = kThreads / kChunks, kTurns = (127 + kStep) / kStep;
+        static_assert(kStep % 8 == 0 || kStep % 8 == 4, "a row's place among a swizzled eight, and that of the next");
+        const int c = tid % kChunks, row = tid / kChunks;
+        const uint8_t* raw = smem + SM::kRawOff + rs * SM::kRaw + tid * 16;
+        const uint8_t* scale = scales + (kind ? 256 : 0) + row;
+        // (the two halves of a chunk, for the second 64 channels in the other order: no bank twice)
+        const bool swap = (c >> 2) & 1;
+        const uint32_t to = sbase + SM::kRingOff + st * SM::kOp + (c >> 2) * (128 * 128) + row * 128;
+        const uint32_t first = to + (((2 * (c & 3) + swap) ^ (row & 7)) << 4);
+        auto convert = [&](auto format, auto every) {
+          constexpr bool E5M2 = decltype(format)::value;
 #pragma unroll 1
-            for (int i0 = 0; i0 < kChunks; i0 += 4) {
-              uint4 w[4];                              // (four loads, then their stores: one order of memory for all)
-              uint32_t f[4];
+          for (int y0 = 0; y0 < kTurns; y0 += 4) {
+            uint4 w[4];                                // (four loads, then their stores: one order of memory for all)
+            uint32_t f[4];
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                w[y] = *reinterpret_cast<const uint4*>(raw + (i0 + y) * (kStep * D));
-                f[y] = scale[kStep * (i0 + y)];
-              }
+            for (int y = 0; y < 4; ++y) {
+              const bool there = row + kStep * (y0 + y) < 128;
+              w[y] = there ? *reinterpret_cast<const uint4*>(raw + (y0 + y) * (kStep * D)) : make_uint4(0, 0, 0, 0);
+              f[y] = there ? scale[kStep * (y0 + y)] : 0;
+            }
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                // 2^(e - E) as an fp16 pair, exactly down to 2^-24 (e <= E where the row is seen)
-                const float x = top ? scale_of(max((int)f[y] - top, -100) + 127) : 1.f;
-                f[y] = pack_f16x2(x, x);
-                if (!decltype(every)::value && !seen(row + kStep * (i0 + y))) w[y] = make_uint4(0, 0, 0, 0), f[y] = 0;
-                if (D == 128 && swap) w[y] = make_uint4(w[y].z, w[y].w, w[y].x, w[y].y);
-              }
+            for (int y = 0; y < 4; ++y) {
+              // 2^(e - E) as an fp16 pair, exactly down to 2^-24 (e <= E where the row is seen)
+              const float z = top ? scale_of(max((int)f[y] - top, -100) + 127) : 1.f;
+              f[y] = pack_f16x2(z, z);
+              if (!decltype(every)::value && !seen(min(row + kStep * (y0 + y), 127))) w[y] = make_uint4(0, 0, 0, 0), f[y] = 0;
+              if (D == 128 && swap) w[y] = make_uint4(w[y].z, w[y].w, w[y].x, w[y].y);
+              uint32_t h[8];
+              codes4<E5M2>(w[y].x, h[0], h[1]);
+              codes4<E5M2>(w[y].y, h[2], h[3]);
+              codes4<E5M2>(w[y].z, h[4], h[5]);
+              codes4<E5M2>(w[y].w, h[6], h[7]);
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                uint32_t h[8];
-                codes4<E5M2>(w[y].x, h[0], h[1]);
-                codes4<E5M2>(w[y].y, h[2], h[3]);
-                codes4<E5M2>(w[y].z, h[4], h[5]);
-                codes4<E5M2>(w[y].w, h[6], h[7]);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) h[q] = mul_f16x2(h[q], f[y]);
-                st_shared_v4(first + (i0 + y) * (kStep * 128), make_uint4(h[0], h[1], h[2], h[3]));
-                st_shared_v4(second + (i0 + y) * (kStep * 128), make_uint4(h[4], h[5], h[6], h[7]));
+              for (int q = 0; q < 8; ++q) h[q] = mul_f16x2(h[q], f[y]);
+              if (row + kStep * (y0 + y) < 128) {
+                const uint32_t p0 = (first + (y0 + y) * (kStep * 128)) ^ (kStep % 8 && (y & 1) ? 64u : 0u);
+                st_shared_v4(p0, make_uint4(h[0], h[1], h[2], h[3]));
+                st_shared_v4(p0 ^ 16u, make_uint4(h[4], h[5], h[6], h[7]));
               }
             }
-          };
-          auto of = [&](auto format) {
-            if (whole) convert(format, std::true_type{});
-            else convert(format, std::false_type{});
-          };
-          if (params.e5m2) of(std::true_type{});
-          else of(std::false_type{});
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(FULL(st));
-            mbar_arrive(REMPTY(rs));
           }
+        };
+        auto of = [&](auto format) {
+          if (whole) convert(format, std::true_type{});
+          else convert(format, std::false_type{});
+        };
+        if (params.e5m2) of(std::true_type{});
+        else of(std::false_type{});
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(FULL(st));
+          mbar_arrive(REMPTY(rs));
         }
       }
     }
@@ -588,7 +586,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
         const bool all = first >= max(all_lo, 0) && last <= all_hi;
         WideTileInfo info{1.f, 0.f, 1.f, 0};
         if constexpr (EIGHT) info = s_info[tile % kWideInfo];
-        const uint8_t* vs = smem + SM::kScaleOff + (tile % kWideInfo) * 256 + 128;
+        const uint8_t* vs = smem + SM::kScaleOff + (tile % kWideInfo) * 384 + 128;
         // a score in log2 units with its value's exponent is s f + v
         float f = fac * info.k_scale, v = info.v_exp;
         tmem_wait_ld();
