@@ -504,6 +504,9 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
       const int r0 = rg * kRows + (SPLIT ? 0 : 128 * t);   // this group's first row of the KV head
       const long long at0 = ((long long)x.b * p.Hkv + hk) * p.rows + r0;
       const bool mine = r0 + row < p.rows;
+      // The second group may have had no tile of the last piece: it stays at most one piece ahead of the first
+      // (it would else stand for it at QREADY, and for its rows of Q).
+      if (SPLIT && t == 1 && piece > 0 && !__all_sync(0xffffffffu, wait_bar(QREADY, (piece - 1) & 1, wc))) break;
       const int drafts = p.ancestors ? decode_drafts(p, x.b, x.len) : 0;
       const int base = x.len - drafts;                                        // a tree's first draft
       const bool small_tree = drafts > 0 && p.Sq <= kWideDrafts;

@@ -572,6 +572,10 @@ TREE = [
     ("bf16", "e4m3fn", 2, 4, 4, 128, 16, 64, [64, 900], [64, 61], False),
     ("fp16", "e4m3fn", 2, 3, 1, 64, 256, 33, [300, 33], [33, 33], True),
     ("bf16", "e4m3fn", 1, 8, 1, 128, 32, 150, [2100], [147], False),
+    # many units of one tile or two per CTA, 33 to 128 rows
+    ("bf16", None, 420, 4, 1, 64, 16, 10, [10 + 7 * b % 150 for b in range(420)], [10] * 420, True),
+    ("bf16", "e4m3fn", 420, 4, 1, 64, 32, 10, [10 + 7 * b % 150 for b in range(420)], [10 - b % 3 for b in range(420)], False),
+    ("fp16", "e4m3fn", 90, 66, 6, 128, 64, 4, [4 + 11 * b % 300 for b in range(90)], [4] * 90, True),
 ]
 
 
