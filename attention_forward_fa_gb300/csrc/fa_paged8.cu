@@ -81,9 +81,11 @@ int launch_decode8_rows(fa::Decode8Params& p, long long most_tiles, cudaStream_t
 template <bool BF16, int D, bool E5M2>
 int launch_decode8_groups(fa::Decode8Params& p, long long keys, cudaStream_t st) {
   fa::DecodeCore& c = p.c;
-  const int nt = (c.rows + 7) / 8;      // (more than 32 rows: launch_wide)
-  c.groups = 1;
-  c.units = c.Hkv;
+  // (passes of up to 32 rows: at 40 and 48 one of all rows spills 118 and 342 bytes)
+  const int passes = (c.rows + 31) / 32, nt = ((c.rows + passes - 1) / passes + 7) / 8;   // (more rows: launch_wide)
+  c.groups = (c.rows + 8 * nt - 1) / (8 * nt);
+  if ((long long)c.Hkv * c.groups > 0x7FFFFFFFLL) return FA_ERR_SHAPE;
+  c.units = c.Hkv * c.groups;
   const long long most = ((keys + fa::kDec8Tile - 1) / fa::kDec8Tile + fa::kUnitTiles) * c.B * c.units;
   switch (nt) {
     case 1: return launch_decode8_rows<BF16, D, 1, E5M2>(p, most, st);

@@ -398,7 +398,7 @@ def test_decode8(case):
 
 @pytest.mark.parametrize("dtype,fmt,D", [("bf16", "e4m3fn", 128), ("fp16", "e4m3fn", 64), ("fp16", "e5m2", 128)])
 @pytest.mark.parametrize("spread", [3.0, 12.0])
-@pytest.mark.parametrize("Sq", [1, 12, 40])
+@pytest.mark.parametrize("Sq", [1, 12, 24, 40])
 def test_decode8_values_of_any_size(dtype, fmt, D, spread, Sq):
     """Values whose rows differ by many powers of two: small ones with large
     probabilities beside large ones with small, rows of zeros among them."""
@@ -445,6 +445,7 @@ def test_decode8_all_values_zero_and_queries_of_any_size():
     ("bf16", "e4m3fn", 70, 2, 2, 64, 32, 1, [100] * 70, 64),
     ("bf16", "e4m3fn", 3, 8, 2, 128, 64, 10, [1000, 130, 5], 4),
     ("fp16", "e5m2", 2, 6, 1, 64, 16, 30, [500, 40], 12),
+    ("bf16", "e4m3fn", 2, 8, 1, 128, 64, 10, [700, 140], 6),
 ])
 def test_decode8_listed_pages(dtype, fmt, B, Hq, Hkv, D, page, Sq, lens, sel):
     c = Cache8(9, dtype, fmt, B, Hkv, D, page, lens, stale=True)
@@ -496,7 +497,7 @@ def test_decode8_many_sequences(B, Hq, Hkv, page, Sq):
     _decode8(c, _round(rng.standard_normal((B, Hq, Sq, 64)), "bf16"), lens, "many")
 
 
-@pytest.mark.parametrize("Sq", [1, 20])
+@pytest.mark.parametrize("Sq", [1, 20, 40])
 def test_decode8_leaves_out_bad_pages(Sq):
     import attention_forward_fa_gb300 as fa
     lens = [200, 200, 200]
@@ -517,7 +518,7 @@ def test_decode8_leaves_out_bad_pages(Sq):
 
 
 @pytest.mark.parametrize("dtype,fmt,G,Sq,n,grow", [
-    ("fp16", "e4m3fn", 5, 8, 20000, 0.0), ("bf16", "e5m2", 4, 40, 9000, 0.0), ("fp16", "e4m3fn", 34, 1, 26000, 2e-3),
+    ("fp16", "e4m3fn", 5, 16, 20000, 0.0), ("bf16", "e5m2", 4, 40, 9000, 0.0), ("fp16", "e4m3fn", 70, 1, 26000, 2e-3),
     ("bf16", None, 3, 13, 20000, 0.0), ("fp16", None, 5, 30, 17000, 3e-3),
 ])
 def test_many_rows_over_long_pieces(dtype, fmt, G, Sq, n, grow):
@@ -572,9 +573,10 @@ TREE = [
     ("bf16", "e4m3fn", 2, 4, 4, 128, 16, 64, [64, 900], [64, 61], False),
     ("fp16", "e4m3fn", 2, 3, 1, 64, 256, 33, [300, 33], [33, 33], True),
     ("bf16", "e4m3fn", 1, 8, 1, 128, 32, 150, [2100], [147], False),
-    # many units of one tile or two per CTA, 33 to 128 rows
+    # many units of one tile or two per CTA, and two passes of rows
     ("bf16", None, 420, 4, 1, 64, 16, 10, [10 + 7 * b % 150 for b in range(420)], [10] * 420, True),
-    ("bf16", "e4m3fn", 420, 4, 1, 64, 32, 10, [10 + 7 * b % 150 for b in range(420)], [10 - b % 3 for b in range(420)], False),
+    ("bf16", "e4m3fn", 420, 4, 1, 64, 32, 20, [20 + 7 * b % 150 for b in range(420)], [20 - b % 3 for b in range(420)], False),
+    ("bf16", "e4m3fn", 20, 4, 1, 128, 32, 12, [12 + 7 * b % 450 for b in range(20)], [12 - b % 3 for b in range(20)], False),
     ("fp16", "e4m3fn", 90, 66, 6, 128, 64, 4, [4 + 11 * b % 300 for b in range(90)], [4] * 90, True),
 ]
 
