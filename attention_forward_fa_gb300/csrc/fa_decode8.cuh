@@ -25,6 +25,12 @@
 //     contribution at most, is a quarter of the answer's own.  An fp16 answer gets a
 //     hi + lo pair (one fp16 would add as much as its own rounding: 2.9e-4 against 2.1e-4
 //     of the answer over 64 sequences of up to 8192 tokens).
+//
+// Measured (32 query heads on 8 KV heads of 128, both kernels): 8 sequences of 131072
+// tokens, e4m3, bf16 313 us, 6.92 TB/s of codes and scales (the 16-bit cache: 600 us);
+// 64 of mixed lengths up to 8192, e5m2, fp16, pages of 16 95 us, 5.9 TB/s; one of 517
+// tokens 6.3 us.  Up to 16 rows bound by HBM; at 32 rows by the warp-level products (16
+// trees over up to 8192 tokens: 44 us at 24 rows, 57 at 32, of which the bytes are 21).
 #pragma once
 #include <type_traits>
 

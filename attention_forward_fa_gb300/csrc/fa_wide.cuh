@@ -34,6 +34,16 @@
 //   * Up to kWideFlush tiles of a piece add up in TMEM, where the adder cuts off what it adds
 //     (about 2^-24 of the sum each 16 keys, always towards zero: 2^-15 over 8192 keys);
 //     then the softmax threads add O to a place in scratch in fp32.
+//
+// Measured (32 query heads on 8 KV heads of 128, bf16, with the join): 16 trees of up to 12
+// drafts over up to 8192 tokens (48 rows) 71 us, 41 of which are the bytes', over 32768 tokens
+// each 352 us, 6.1 TB/s; 4 trees of up to 64 (256 rows) over an 8-bit cache of up to 16384
+// tokens 73 us, over 65536 each 257 us, 1068 TF/s; the same over a 16-bit cache 69 and 277 us.
+// A unit costs about 13000 cycles beside its tiles (rows in, the last P V, the groups' join, the
+// answer out); with 256 rows a group's chain (S 512 cycles, softmax 2500, P V 512) sets the step,
+// 4000 cycles a tile, half of which the tensor cores work; with up to 128 rows over an 8-bit cache
+// the conversion does (16 trees over 32768 tokens 438 us): 96 KB a tile through shared memory, which
+// the S products want too.
 #pragma once
 #include <type_traits>
 

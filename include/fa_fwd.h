@@ -378,11 +378,15 @@ int fa_convert_v_fp16(const void* v_bf16, void* v_fp16, int64_t n_elems, void* s
 /*
  * The cache is a pool of pages of page_size tokens; sequence b's tokens
  * [p * page_size, (p + 1) * page_size) of every KV head lie in page
- * page_table[b * table_stride + p].  Three operators read and write it:
+ * page_table[b * table_stride + p].  Operators that read and write it:
  *   fa_kv_append     writes new tokens' K (rotated) and V into their pages,
  *   fa_decode        attention of a sequence's newest tokens over its pages,
- *   fa_select_pages  the pages that fa_decode may restrict itself to.
- * All three share the conventions above (device memory of the current device,
+ *   fa_select_pages  the pages that fa_decode may restrict itself to,
+ *   fa_kv_append_ext, fa_decode_ext   the first two over an 8-bit cache, and for
+ *                    trees of drafted tokens,
+ *   fa_kv_read       tokens out of their pages,
+ *   fa_kv_keep       accepted drafts to their places.
+ * All share the conventions above (device memory of the current device,
  * asynchronous on `stream`, argument errors synchronous).  Their kernels read
  * lengths and page ids on the device: an entry that they need and that is
  * outside [0, num_pages), a length outside [0, max_pages * page_size], or a

@@ -1076,3 +1076,37 @@ def test_wrappers_refuse_what_does_not_fit8():
         fa.flash_attention_decode(q, fa.PagedKV(pool, pool, c.obj.page_table, k_scale=s8, v_scale=s8), n)
     assert e.value.code == fa.FA_ERR_ALIGN
     assert _status() == 0
+
+
+def test_front_page_tree_runs():
+    """The front page's step over an 8-bit cache, behind the blocks before it, as written there."""
+    import re
+    from pathlib import Path
+    import torch
+    import attention_forward_fa_gb300 as fa
+    text = (Path(__file__).resolve().parents[1] / "README.md").read_text()
+    blocks = [b for b in re.findall(r"```python\n(.*?)```", text, re.S) if "paged_kv_append" in b]
+    env = {"torch": torch, "fa": fa}
+    torch.manual_seed(31)
+    for i, b in enumerate(blocks):
+        if "paged_kv_keep" in b:
+            b, rest = b.split("path = ")
+            exec(compile(b, f"serving-example-{i}", "exec"), env)
+
+            class Now:
+                fmt, D = "e4m3fn", 128
+            c = Now()
+            (c.kc, c.vc), (c.ke, c.ve) = ([_host(t) for t in env["codes"]], [t.cpu().numpy().astype(np.int64) - 127 for t in env["scales"]])
+            c.k, c.v = np.ldexp(c.kc, c.ke[..., None]), np.ldexp(c.vc, c.ve[..., None])
+            t, q = env["table"].cpu().numpy(), _host(env["qt"])
+            tree = (env["sees"].cpu().numpy()[None].repeat(2, 0), [8, 8])
+            a = (t, [1008, 45], 128 ** -0.5)
+            _check8(env["ot"], env["lt"], P.decode(q, c.k, c.v, *a, tree=tree), *_spread(c, q, *a, tree), "bf16")
+            exec(compile("path = " + rest, f"serving-example-{i}", "exec"), env)
+            (c.k, c.v), _, _ = P.keep([c.k, c.v], t, [1000, 37], env["path"].cpu().numpy(), [3, 2], 64)
+            k, v = P.read(c.k, c.v, t, [0, 0], [1003, 39], *(np.zeros((2, 8, 1003, 128)) for _ in range(2)))
+            for seq, n in ((0, 1003), (1, 39)):
+                assert np.array_equal(_host(env["k16"])[seq, :, :n], k[seq, :, :n])
+                assert np.array_equal(_host(env["v16"])[seq, :, :n], v[seq, :, :n])
+        else:
+            exec(compile(b, f"serving-example-{i}", "exec"), env)
