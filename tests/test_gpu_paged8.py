@@ -346,6 +346,25 @@ def test_append_at_given_positions():
             assert bool((q[seq, :, i] == 0).all()) and bool((q[seq, :, i + 1] != 0).any())
 
 
+def test_append_at_given_positions_of_more_pieces_than_blocks():
+    """Room for more pieces than blocks: a block looks for its pieces; the same bits as without positions."""
+    import torch
+    import attention_forward_fa_gb300 as fa
+    B, S, D = 26, 2048, 128
+    old, new = [15] * 25 + [0], [2, 2048] + [1, 0] * 12
+    a, b = (Cache(32, "bf16", B, 1, D, 16, [o + n for o, n in zip(old, new)], bounds=True) for _ in range(2))
+    x = _dev(_round(a.rng.standard_normal((B, 3, S, D)), "bf16"), "bf16")
+    cos, sin = (_dev(t) for t in _tables(2100, D))
+    to, tn = a.ints(old), a.ints(new)
+    kw = dict(new_lens=tn, cos=cos, sin=sin)
+    qa = fa.paged_kv_append(a.obj, to, x[:, 1:2], x[:, 2:], q=x[:, :1], q_out=torch.zeros_like(x[:, :1]), **kw)
+    pos = (to[:, None] + torch.arange(S, device="cuda", dtype=torch.int32)).contiguous()
+    qb = fa.paged_kv_append(b.obj, to, x[:, 1:2], x[:, 2:], q=x[:, :1], q_out=torch.zeros_like(x[:, :1]), positions=pos, **kw)
+    assert _status() == 0
+    for s, t in ((qa, qb), (a.tk, b.tk), (a.tv, b.tv), (a.tlo, b.tlo), (a.thi, b.thi)):
+        assert torch.equal(s, t)
+
+
 # ------------------------------------------------------------------ decode
 DECODE = [
     # dtype, fmt, B, Hq, Hkv, D, page, Sq, lens, pre, layout
@@ -573,6 +592,11 @@ TREE = [
     ("bf16", "e4m3fn", 2, 4, 4, 128, 16, 64, [64, 900], [64, 61], False),
     ("fp16", "e4m3fn", 2, 3, 1, 64, 256, 33, [300, 33], [33, 33], True),
     ("bf16", "e4m3fn", 1, 8, 1, 128, 32, 150, [2100], [147], False),
+    # sequences without tokens or drafts, by warps and by tcgen05
+    ("bf16", None, 4, 48, 1, 128, 16, 1, [0, 1, 300, 129], [0, 1, 1, 0], True),
+    ("fp16", "e4m3fn", 4, 72, 1, 64, 32, 2, [0, 2, 300, 129], [0, 2, 1, 0], False),
+    ("bf16", "e4m3fn", 4, 12, 4, 128, 32, 2, [0, 2, 300, 129], [0, 2, 1, 0], False),
+    ("bf16", "e5m2", 3, 140, 1, 128, 128, 2, [2, 0, 260], [2, 0, 2], False),
     # many units of one tile or two per CTA, and two passes of rows
     ("bf16", None, 420, 4, 1, 64, 16, 10, [10 + 7 * b % 150 for b in range(420)], [10] * 420, True),
     ("bf16", "e4m3fn", 420, 4, 1, 64, 32, 20, [20 + 7 * b % 150 for b in range(420)], [20 - b % 3 for b in range(420)], False),
@@ -619,6 +643,68 @@ def test_tree(case, kind):
     for b in range(B):                    # padding reaches no other row
         assert torch.equal(o[b, :, :drafts[b]], o3[b, :, :drafts[b]]) and torch.equal(l[b, :, :drafts[b]], l3[b, :, :drafts[b]])
     assert _status() == 0
+
+
+@pytest.mark.parametrize("dtype,fmt,Hq,S", [("bf16", None, 2, 6), ("fp16", None, 8, 20), ("bf16", None, 40, 11), ("bf16", "e4m3fn", 2, 6),
+                                            ("fp16", "e5m2", 8, 20), ("bf16", "e4m3fn", 40, 11)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_tree_scales_and_unseen_places(dtype, fmt, Hq, S, bad):
+    """Scales from flat to one-hot and a negative one; keys and values behind a sequence's tokens, in its own
+    pages too, are anything."""
+    import torch
+    import attention_forward_fa_gb300 as fa
+    lens, drafts, D, page = [333, 40, S], [S, S - 2, S], 64, 32
+    cap = [-(-n // page) * page for n in lens]
+    c = Cache(33, dtype, 3, 1, D, page, cap) if fmt is None else Cache8(33, dtype, fmt, 3, 1, D, page, cap)
+    for b, n in enumerate(lens):
+        for t in range(n, cap[b]):
+            p, s = int(c.table[b, t // page]), t % page
+            if fmt is None:
+                c.tk[p, :, s] = bad
+                c.tv[p, :, s] = -bad
+            else:
+                c.bk[p, :, s], c.bv[p, :, s] = 0x7F, 0xFE
+                c.sk[p, :, s], c.sv[p, :, s] = 255, 255 if t % 2 else 0
+    anc, _ = _trees(c.rng, 3, S)
+    q = _round(c.rng.standard_normal((3, Hq, S, D)), dtype)
+    for scale in (0.0, -0.2, 0.125, 3.0):
+        o, l = fa.flash_attention_decode_tree(_dev(q, dtype), c.obj, c.ints(lens), _dev(anc), new_lens=c.ints(drafts), scale=scale)
+        assert _status() == 0
+        a = (c.table, lens, scale)
+        ref = P.decode(q, c.k, c.v, *a, tree=(anc, drafts))
+        if fmt is None:
+            _check(o, l, ref, dtype, f"scale {scale}")
+        else:
+            _check8(o, l, ref, *_spread(c, q, *a, (anc, drafts)), dtype, f"scale {scale}")
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3fn"])
+def test_trees_on_two_streams_at_once(fmt):
+    """Calls with many rows on two streams beside a matrix product of torch's on a third: each has scratch and
+    accumulators of its own."""
+    import torch
+    import attention_forward_fa_gb300 as fa
+    lens, S = [2000, 700], 24
+    cs = [Cache(34 + i, "bf16", 2, 4, 128, 64, lens) if fmt is None else Cache8(34 + i, "bf16", fmt, 2, 4, 128, 64, lens) for i in range(2)]
+    qs = [_dev(_round(c.rng.standard_normal((2, (16, 32)[i], S, 128)), "bf16"), "bf16") for i, c in enumerate(cs)]
+    anc = [_dev(_trees(c.rng, 2, S)[0]) for c in cs]
+    n = cs[0].ints(lens)
+    want = [fa.flash_attention_decode_tree(q, c.obj, n, a) for q, c, a in zip(qs, cs, anc)]
+    m = torch.randn(1024, 1024, device="cuda", dtype=torch.bfloat16)
+    prod = m @ m
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(3)], [[], []]
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(fa.flash_attention_decode_tree(qs[i], cs[i].obj, n, anc[i]))
+        with torch.cuda.stream(streams[2]):
+            other = m @ m
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, l in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
+    assert torch.equal(other, prod) and _status() == 0
 
 
 @pytest.mark.parametrize("fmt", [None, "e4m3fn"])
