@@ -5,6 +5,7 @@ import ctypes
 import math
 import operator
 import os
+import struct
 from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -80,6 +81,10 @@ class fa_kv_new_t(ctypes.Structure):
                 ("qo_stride_h", ctypes.c_int64), ("qo_stride_s", ctypes.c_int64),
                 ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
                 ("interleaved", ctypes.c_int32), ("max_pos", ctypes.c_int32)]
+
+
+_KV_NEW = struct.Struct("@4Q12q2Q3i4x")      # fa_kv_new_t's fields
+assert _KV_NEW.size == ctypes.sizeof(fa_kv_new_t)
 
 
 class fa_kv_fp8_t(ctypes.Structure):
@@ -629,23 +634,35 @@ def _fp8_of(cache) -> Optional[fa_kv_fp8_t]:
     return getattr(cache, "_fp8", None)
 
 
+_torch = None
+
+
+def _t():
+    """torch, imported with the first call (an import statement in every call costs more than its checks)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _int32_of(t, shape, device, name):
-    import torch
-    if t.dtype != torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not _t().int32 or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor {tuple(shape)} on the cache's device")
 
 
 def _query_of(q, cache):
-    if q.dtype != cache.dtype or q.device != cache.device or q.dim() != 4:
+    shape = q.shape
+    if q.dtype is not cache.dtype or q.device != cache.device or len(shape) != 4:
         raise ValueError("q must be [B, Hq, Sq, D] of the cache's type, on its device")
-    B, Hq, Sq, D = q.shape
+    B, Hq, Sq, D = shape
     if B != cache.B or D != cache.D or Hq % cache.Hkv:
         raise ValueError("q does not fit the cache: B, D or Hq % Hkv")
     return B, Hq, Sq, D
 
 
 def _answers_of(q, out, lse):
-    import torch
+    torch = _t()
     if out is not None and (out.shape != q.shape or out.dtype != q.dtype or out.device != q.device
                             or not out.is_contiguous()):
         raise ValueError("out must be contiguous, of q's shape and type, on its device")
@@ -656,7 +673,7 @@ def _answers_of(q, out, lse):
 
 def _raw_here(device) -> Optional[int]:
     """The raw current stream where `device` is the current device, else None."""
-    import torch
+    torch = _t()
     if torch.cuda.current_device() != device.index:
         return None
     fast = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # a tenth of current_stream()'s time
@@ -698,53 +715,63 @@ def paged_kv_append(cache: PagedKV, kv_lens, k, v, *, new_lens=None, q=None, q_o
 
     stream, of this and the other calls on a cache: as under torch.cuda.stream(stream); the caller
     orders it behind what makes the inputs and keeps them until it has run."""
-    import torch
-    if k.dim() != 4 or k.shape != v.shape:
+    torch = _t()
+    shape, dtype, device = k.shape, cache.dtype, cache.device
+    if len(shape) != 4 or shape != v.shape:
         raise ValueError("k and v must be [B, Hkv, S, D], of one shape")
-    B, Hkv, S, D = k.shape
+    B, Hkv, S, D = shape
     if B != cache.B or Hkv != cache.Hkv or D != cache.D:
         raise ValueError("k and v do not fit the cache: B, Hkv or D")
-    _int32_of(kv_lens, (B,), cache.device, "kv_lens")
+    _int32_of(kv_lens, (B,), device, "kv_lens")
     if new_lens is not None:
-        _int32_of(new_lens, (B,), cache.device, "new_lens")
+        _int32_of(new_lens, (B,), device, "new_lens")
     if positions is not None:
-        _int32_of(positions, (B, S), cache.device, "positions")
+        _int32_of(positions, (B, S), device, "positions")
+    ks, vs = k.stride(), v.stride()
+    rows = [(k, ks), (v, vs)]
     if q is None:
         if q_out is not None:
             raise ValueError("q_out without q")
-        Hq = Hkv
+        Hq, qs = Hkv, None
     else:
-        _query_of(q, cache)
-        Hq = q.shape[1]
+        Hq = _query_of(q, cache)[1]
+        qs = q.stride()
+        rows.append((q, qs))
         if q.shape[2] != S or (q_out is not None and q_out.shape != q.shape):
             raise ValueError("q and q_out must be [B, Hq, S, D] with k's S")
-    for t in (k, v) + (() if q is None else (q,)) + (() if q_out is None else (q_out,)):
-        if t.dtype != cache.dtype or t.device != cache.device or t.stride(3) != 1:
+        if q_out is not None:
+            rows.append((q_out, q_out.stride()))
+    for t, st in rows:
+        if t.dtype is not dtype or t.device != device or st[3] != 1:
             raise ValueError("k, v, q, q_out must be of the cache's type, on its device, with a contiguous last dimension")
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
-    rot, max_pos = 0, 0
+    rot, max_pos, angles = 0, 0, (0, 0)
     if cos is not None:
-        if cos.shape != sin.shape or cos.dim() != 2:
+        table = cos.shape
+        if table != sin.shape or len(table) != 2:
             raise ValueError("cos and sin must be [max_pos, rotated channels / 2]")
         for t in (cos, sin):
-            if t.dtype != torch.float32 or t.device != cache.device or not t.is_contiguous():
+            if t.dtype is not torch.float32 or t.device != device or not t.is_contiguous():
                 raise ValueError("cos and sin must be contiguous fp32 tensors on the cache's device")
-        max_pos, rot = _int(cos.shape[0]), _int(2 * cos.shape[1])
+        max_pos, rot, angles = _int(table[0]), _int(2 * table[1]), (cos.data_ptr(), sin.data_ptr())
 
     def call(raw):
-        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q is not None and q_out is None else q_out
-        none = (0, 0, 0)
-        x = fa_kv_new_t(k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(qo), *k.stride()[:3], *v.stride()[:3],
-                        *(none if q is None else q.stride()[:3]), *(none if q is None else qo.stride()[:3]),
-                        _ptr(cos), _ptr(sin), rot, 1 if interleaved else 0, max_pos)
+        qo = torch.empty(q.shape, dtype=dtype, device=device) if q is not None and q_out is None else q_out
+        q_at = (0, 0) if q is None else (q.data_ptr(), qo.data_ptr())
+        q_by = (0, 0, 0, 0, 0, 0) if q is None else qs[:3] + (rows[3][1] if q_out is not None else qo.stride())[:3]
+        # (packed at once: the struct's own constructor takes twice the time)
+        x = fa_kv_new_t.from_buffer_copy(_KV_NEW.pack(k.data_ptr(), v.data_ptr(), *q_at, *ks[:3], *vs[:3], *q_by, *angles,
+                                                      rot, 1 if interleaved else 0, max_pos))
         fp8 = _fp8_of(cache)
         if fp8 is None and positions is None:
-            _raise(library().fa_kv_append(cache._c, x, B, Hq, Hkv, S, D, cache._flags, kv_lens.data_ptr(),
-                                          _ptr(new_lens), raw))
+            code = library().fa_kv_append(cache._c, x, B, Hq, Hkv, S, D, cache._flags, kv_lens.data_ptr(),
+                                          _ptr(new_lens), raw)
         else:
-            _raise(library().fa_kv_append_ext(cache._c, fp8, x, B, Hq, Hkv, S, D, cache._flags, kv_lens.data_ptr(),
-                                              _ptr(new_lens), _ptr(positions), raw))
+            code = library().fa_kv_append_ext(cache._c, fp8, x, B, Hq, Hkv, S, D, cache._flags, kv_lens.data_ptr(),
+                                              _ptr(new_lens), _ptr(positions), raw)
+        if code:
+            _raise(code)
         return qo
 
     raw = _raw_here(cache.device) if stream is None else None
@@ -763,7 +790,7 @@ def flash_attention_decode(q, cache: PagedKV, kv_lens, *, scale: Optional[float]
     rows (paged_kv_append leaves them in the first).  page_idx: int32 [B, Hkv, max_sel] (select_kv_pages):
     only these pages of each sequence are read (of a list, as many entries count as the sequence
     has pages: invalid ones belong at the end).  Returns (o, lse fp32 [B, Hq, Sq])."""
-    import torch
+    torch = _t()
     B, Hq, Sq, D = _query_of(q, cache)
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
@@ -802,7 +829,7 @@ def flash_attention_decode_tree(q, cache: PagedKV, kv_lens, ancestors, *, new_le
     sequence, True where draft i sees draft j (itself too, as a rule).  Rows past new_lens[b] are
     padding: they are answered as rows that see the tokens before the drafts.
     Returns (o, lse fp32 [B, Hq, S])."""
-    import torch
+    torch = _t()
     B, Hq, S, D = _query_of(q, cache)
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
@@ -838,7 +865,7 @@ def paged_kv_read(cache: PagedKV, lens, *, starts=None, size: Optional[int] = No
     stands for.  Returns (k, v) [B, Hkv, S, D] of cache.dtype, any strides with a contiguous last
     dimension: k_out and v_out where given, else allocated with S = size (rows past lens as they were:
     undefined in allocated ones)."""
-    import torch
+    torch = _t()
     _int32_of(lens, (cache.B,), cache.device, "lens")
     if starts is not None:
         _int32_of(starts, (cache.B,), cache.device, "starts")
@@ -895,7 +922,7 @@ def select_kv_pages(q, cache: PagedKV, kv_lens, max_sel: int, *, first: int = 1,
     of flash_attention_decode: int32 [B, Hkv, max_sel], ascending, -1 behind the last.  The cache
     needs page bounds (k_min, k_max).  first, last: so many first and last pages are always
     chosen."""
-    import torch
+    torch = _t()
     B, Hq, Sq, D = _query_of(q, cache)
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
