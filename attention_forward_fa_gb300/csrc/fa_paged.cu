@@ -270,6 +270,9 @@ int append_call(const fa_paged_kv_t* kv, const fa_kv_fp8_t* fp8, const fa_kv_new
   const int ps = kv->page_size;
   p.chunks = (int)(((long long)Snew + ps - 2) / ps) + 1;
   const int rows = fa::kAppendThreads / (D / 16);
+  // As many tokens of one head per step as there are rows, the page and the call allow. Half as many
+  // tokens of two heads, D = 128 into 8 bits: 8 x 4096 tokens 122.5 us instead of 128.8 (8 KV heads),
+  // 3 x 1111 tokens 18.5 instead of 17.3 and, with 2 KV heads, 12.7 instead of 8.8: not taken.
   while ((1 << p.tp_shift) < rows && (1 << p.tp_shift) < std::min(Snew, ps)) ++p.tp_shift;
   const int hp = rows >> p.tp_shift;
   p.q_heads = 2 * fa::kBatch * hp;
