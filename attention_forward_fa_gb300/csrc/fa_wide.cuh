@@ -83,6 +83,12 @@ struct WideSmem {
   static constexpr int kStages = D == 64 ? (EIGHT ? 4 : 10) : EIGHT ? (SPLIT ? 4 : 3) : SPLIT ? 6 : 5;
   static constexpr int kRawStages = !EIGHT ? 0 : D == 128 ? 3 : 8;
   static constexpr int kRaw = 128 * D;                           // codes of K or V of a tile
+  // Barriers of a ring: one per stage, or two in turn where the stages are odd in number.  A wait on a phase's
+  // parity also passes two phases too early, so that whoever waits has to have seen the phase before.  The
+  // converters of K and those of V see every other load each, whose copies land in any order: with an even
+  // number of barriers each of them belongs to one of the two kinds.
+  static constexpr int kOpBars = EIGHT && kStages % 2 ? 2 * kStages : kStages;
+  static constexpr int kRawBars = kRawStages % 2 ? 2 * kRawStages : kRawStages;
   static constexpr int kRingOff = (SPLIT ? 1 : 2) * kOp;         // (behind Q)
   static constexpr int kRawOff = kRingOff + kStages * kOp;
   static constexpr int kScaleOff = kRawOff + kRawStages * kRaw;  // bytes [kWideInfo][K, V with K, V with V][128]
@@ -91,7 +97,7 @@ struct WideSmem {
   static constexpr int kMlOff = kInfoOff + kWideInfo * 16;       // float2 [128]: the second group's reference and sum
   static constexpr int kTreeOff = kMlOff + (SPLIT ? 1024 : 0);   // uint2 [2][kWideDrafts]: what each draft sees, per piece's parity
   static constexpr int kBarOff = kTreeOff + 16 * kWideDrafts;
-  static constexpr int kBars = 2 * kStages + 2 * kRawStages + 9;
+  static constexpr int kBars = 2 * kOpBars + 2 * kRawBars + 9;
   static constexpr int kMiscOff = kBarOff + kBars * 8;
   static constexpr int kBytes = kMiscOff + 64;
   static_assert(kBytes <= 227 * 1024, "one CTA per SM");
@@ -128,7 +134,8 @@ template <bool BF16, int D, bool EIGHT, bool SPLIT>
 __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const __grid_constant__ WideParams params) {
   const DecodeCore& p = params.c;
   using SM = WideSmem<D, EIGHT, SPLIT>;
-  constexpr int NS = SM::kStages, RS = EIGHT ? SM::kRawStages : 1;
+  constexpr int ST = SM::kStages, NS = SM::kOpBars;   // load ld: stage ld % ST, barriers of ld % NS;
+  constexpr int RS = EIGHT ? SM::kRawStages : 1, RB = EIGHT ? SM::kRawBars : 1;   // its codes alike
   constexpr int kRows = SPLIT ? 128 : 256;            // of a unit
   constexpr bool kP16 = EIGHT || !BF16;               // the type of P (and of Q, K and V as operands): fp16 or bf16
   constexpr bool kPair = !EIGHT || !BF16;             // P as hi + lo (fa_decode.cuh, fa_decode8.cuh)
@@ -141,8 +148,8 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
   auto FULL = [&](int s) { return BAR(s); };                       // an operand tile is there
   auto EMPTY = [&](int s) { return BAR(NS + s); };                 // its MMAs are done
   auto RFULL = [&](int s) { return BAR(2 * NS + s); };             // codes are there
-  auto REMPTY = [&](int s) { return BAR(2 * NS + RS + s); };       // they are converted
-  constexpr int kB = 2 * NS + 2 * SM::kRawStages;
+  auto REMPTY = [&](int s) { return BAR(2 * NS + RB + s); };       // they are converted
+  constexpr int kB = 2 * NS + 2 * SM::kRawBars;
   auto SFULL = [&](int t) { return BAR(kB + t); };                 // S of group t
   auto PREADY = [&](int t) { return BAR(kB + 2 + t); };            // P of group t, O rescaled
   auto OFULL = [&](int t) { return BAR(kB + 4 + t); };             // O of group t, at a piece's end
@@ -162,7 +169,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
       mbar_init(EMPTY(s), 1);
     }
     if constexpr (EIGHT)
-      for (int s = 0; s < RS; ++s) {
+      for (int s = 0; s < RB; ++s) {
         mbar_init(RFULL(s), 1);
         mbar_init(REMPTY(s), kWideConverters);
       }
@@ -220,6 +227,8 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
     int tile = 0;                                     // of this CTA; its loads are 2 tile (K) and 2 tile + 1 (V)
     bool dead = false;
     const int nsub = kWideTile >> box_shift;
+    constexpr int R = EIGHT ? RS : ST, B = EIGHT ? RB : NS;     // the ring that the copies go to
+    auto there = [&](int ld) { return EIGHT ? RFULL(ld % B) : FULL(ld % B); };
     while (!dead && next_piece(x)) {
       const int hk = x.unit / p.groups;
       const int n_pages = (x.s.hi + (1 << p.page_shift) - 1) >> p.page_shift;
@@ -241,38 +250,35 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
 #pragma unroll
         for (int kind = 0; kind < 2; ++kind) {
           const int ld = 2 * tile + kind;
-          const int st = ld % (EIGHT ? RS : NS), n = ld / (EIGHT ? RS : NS);
+          const int st = (ld + B - R) % B, n = (ld + B - R) / B;   // (the barrier of load ld - R, which had the stage)
           bool ok = true;
           if (lane == 0 && n > 0) ok = wait_bar(EIGHT ? REMPTY(st) : EMPTY(st), (n - 1) & 1, wc);
           if (!__shfl_sync(0xffffffffu, ok, 0)) {
             dead = true;
             // (the loads up to here land below; `tile` counts whole tiles, a K without its V is waited for here)
-            if (kind == 1 && lane == 0) {
-              const int k = ld - 1, ks = k % (EIGHT ? RS : NS);
-              drain_bar(EIGHT ? RFULL(ks) : FULL(ks), (k / (EIGHT ? RS : NS)) & 1, wc.timeout);
-            }
+            if (kind == 1 && lane == 0) drain_bar(there(ld - 1), ((ld - 1) / B) & 1, wc.timeout);
             break;
           }
           // (the place of tile - kWideInfo: all its readers are done, see kWideInfo)
           if (kind == 0 && lane < 8) s_meta[at * 8 + lane] = first < 0 ? -1 : first + (off & (box - 1));
           __syncwarp();
-          const uint32_t bar = EIGHT ? RFULL(st) : FULL(st);
+          const uint32_t bar = there(ld), to = ld % R;
           const uint32_t each = EIGHT ? (uint32_t)box * D + (kind == 0 ? 2u * box : (uint32_t)box) : (uint32_t)box * D * 2;
           if (lane == 0) mbar_arrive_expect_tx(bar, each * __popc(live));
           __syncwarp();
           if (mine) {
             const void* tm = kind ? &params.tm_v : &params.tm_k;
             if constexpr (EIGHT) {
-              tma_load_4d(sbase + SM::kRawOff + st * SM::kRaw + sub * box * D, tm, bar, slot, hk, id);
+              tma_load_4d(sbase + SM::kRawOff + to * SM::kRaw + sub * box * D, tm, bar, slot, hk, id);
               // both scales with K, as the softmax needs the values' before V; theirs with V again
               const long long from = (((long long)id * p.Hkv + hk) << p.page_shift) + slot;
-              const uint32_t to = sbase + SM::kScaleOff + at * 384 + sub * box;
-              if (kind == 0) bulk_load(to, params.k_scale + from, box, bar);
-              bulk_load(to + (kind ? 256 : 128), params.v_scale + from, box, bar);
+              const uint32_t scales = sbase + SM::kScaleOff + at * 384 + sub * box;
+              if (kind == 0) bulk_load(scales, params.k_scale + from, box, bar);
+              bulk_load(scales + (kind ? 256 : 128), params.v_scale + from, box, bar);
             } else {
 #pragma unroll
               for (int c = 0; c < D / 64; ++c)
-                tma_load_5d_chunk(sbase + SM::kRingOff + st * SM::kOp + c * (128 * 128) + sub * box * 128, tm, bar, slot, c, hk, id);
+                tma_load_5d_chunk(sbase + SM::kRingOff + to * SM::kOp + c * (128 * 128) + sub * box * 128, tm, bar, slot, c, hk, id);
             }
           }
         }
@@ -283,9 +289,8 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
     }
     // every copy lands before the CTA ends, whether or not some wait expired
     if (lane == 0) {
-      constexpr int N = EIGHT ? RS : NS;
       const int end = 2 * tile;
-      for (int i = max(0, end - N); i < end; ++i) drain_bar(EIGHT ? RFULL(i % N) : FULL(i % N), (i / N) & 1, wc.timeout);
+      for (int i = max(0, end - R); i < end; ++i) drain_bar(there(i), (i / B) & 1, wc.timeout);
     }
     __syncwarp();
   } else if (warp == kIssuer) {
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
       // S of group t from the K of `tl`, whose stage is given back behind the last group that reads it
       auto scores = [&](int t, int tl, bool last) {
         const int ld = 2 * tl;
-        const uint64_t a = q0 + (SPLIT ? 0 : (t * SM::kOp) >> 4), b = k0 + (((ld % NS) * SM::kOp) >> 4);
+        const uint64_t a = q0 + (SPLIT ? 0 : (t * SM::kOp) >> 4), b = k0 + (((ld % ST) * SM::kOp) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
@@ -316,7 +321,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
       };
       auto values = [&](int t, int tl, int i, bool last) {     // i: the group's tiles of the piece before this one
         const int ld = 2 * tl + 1;
-        const uint64_t b = v0 + (((ld % NS) * SM::kOp) >> 4);
+        const uint64_t b = v0 + (((ld % ST) * SM::kOp) >> 4);
         const uint32_t o = tmem + 256 + 128 * t, s = tmem + 128 * t;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) mma_ts_if(o, s + 8 * kk, b + (kk * 2048 >> 4), kIdescO, i % kWideFlush || kk, lead);
@@ -399,9 +404,9 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
     bool dead = false;
     while (!dead && next_piece(x)) {
       for (int j = 0; j < x.d.nt; ++j, ++tile) {
-        const int at = tile % kWideInfo, ld = 2 * tile + kind, rs = ld % RS, st = ld % NS;
-        if (!__all_sync(0xffffffffu, wait_bar(RFULL(rs), (ld / RS) & 1, wc))) dead = true;
-        if (!dead && ld >= NS && !__all_sync(0xffffffffu, wait_bar(EMPTY(st), (ld / NS - 1) & 1, wc))) dead = true;
+        const int at = tile % kWideInfo, ld = 2 * tile + kind, rs = ld % RS, st = ld % ST;
+        if (!__all_sync(0xffffffffu, wait_bar(RFULL(ld % RB), (ld / RB) & 1, wc))) dead = true;
+        if (!dead && ld >= ST && !__all_sync(0xffffffffu, wait_bar(EMPTY((ld - ST) % NS), ((ld - ST) / NS) & 1, wc))) dead = true;
         if (dead) break;
         const int* meta = s_meta + at * 8;
         auto seen = [&](int r) {
@@ -485,8 +490,8 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(FULL(st));
-          mbar_arrive(REMPTY(rs));
+          mbar_arrive(FULL(ld % NS));
+          mbar_arrive(REMPTY(ld % RB));
         }
       }
     }
@@ -659,7 +664,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
               for (int c = 0; c < D / 64; ++c)
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
-                  st_shared_v4(sbase + SM::kRingOff + (ld % NS) * SM::kOp + c * (128 * 128) + row * 128 + q * 16, make_uint4(0, 0, 0, 0));
+                  st_shared_v4(sbase + SM::kRingOff + (ld % ST) * SM::kOp + c * (128 * 128) + row * 128 + q * 16, make_uint4(0, 0, 0, 0));
             }
             fence_proxy_async_smem();
           }
