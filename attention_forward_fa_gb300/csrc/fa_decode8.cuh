@@ -21,6 +21,9 @@
 //     into the value product is 2^(s' - m), the weight of the value's codes, and
 //     the sum of the softmax takes 2^(s' - m) 2^-e.  So the product's operands are
 //     as large as what they add, whatever the scales.
+//   * A value row that is not finite (scale byte 255, codes 0) weighs in the sum as
+//     any other and has a NaN for its P in the rows that see it, so that their
+//     answers are NaN and no other row's.
 //   * P is one fp16 where the answer is bf16: its rounding, 2^-11 of each key's
 //     contribution at most, is a quarter of the answer's own.  An fp16 answer gets a
 //     hi + lo pair (one fp16 would add as much as its own rounding: 2.9e-4 against 2.1e-4
@@ -341,6 +344,7 @@ __global__ void __launch_bounds__(kDecThreads * kDec8Teams<BF16, NT>, 1) fa_deco
       // (c2, c3) of each 16, rows 2 t4, 2 t4 + 1
       float over = -INFINITY;        // the most that one exceeds its row's reference by
       float back[2][2];              // 2^-e of the lane's keys' values
+      bool odd = false;              // whether one of them is not finite
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int kq = meta[2 * warp + u];
@@ -356,6 +360,8 @@ __global__ void __launch_bounds__(kDecThreads * kDec8Teams<BF16, NT>, 1) fa_deco
             const int key = key0 + g + 8 * x;
             if (key >= s.hi || key < s.lo) ks = vs = 127;
           }
+          odd = odd || vs == kScaleNone;
+          if (vs == kScaleNone) vs = 127;
           kf[x] = scale_of(ks);
           ve[x] = (float)((int)vs - 127);
           back[u][x] = __uint_as_float((254u - vs) << 23);
@@ -418,6 +424,25 @@ __global__ void __launch_bounds__(kDecThreads * kDec8Teams<BF16, NT>, 1) fa_deco
             o[n][i][3] *= f[1];
           }
         }
+      }
+      if (__any_sync(0xffffffffu, odd)) {
+        // Values that are not finite: the key's weight joins the sum here, and P becomes 2^100, an fp16
+        // infinity, which times the row's codes of 0 is NaN.  (What a row does not see stays -infinity.)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (scales[kDec8Tile + 32 * warp + 16 * u + 8 * x + g] != kScaleNone) continue;
+            back[u][x] = 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float& y = c[u][n][2 * x + e];
+                l[n][e] += ex2_approx(y - m[n][e]);
+                if (y != -INFINITY) y = m[n][e] + 100.f;
+              }
+          }
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u)

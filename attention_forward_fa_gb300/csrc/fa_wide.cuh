@@ -70,12 +70,14 @@ struct WideParams {
   CUtensorMap tm_v;
 };
 
-struct WideTileInfo {              // of an 8-bit tile
+struct alignas(16) WideTileInfo {  // of an 8-bit tile
   float k_scale;                   // 2^E_k
   float v_exp;                     // E_v
   float v_back;                    // 2^-E_v
-  int each;                        // the values' exponents are taken key by key
+  int flags;                       // kWide...
 };
+constexpr int kWideEachV = 1;      // the values' exponents are taken key by key
+constexpr int kWideNoneV = 2;      // (with kWideEachV) some are of rows that are not finite
 
 template <int D, bool EIGHT, bool SPLIT>
 struct WideSmem {
@@ -428,14 +430,17 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
         top_v = __reduce_max_sync(0xffffffffu, top_v);
         low_v = __reduce_min_sync(0xffffffffu, low_v);
         const bool whole = __all_sync(0xffffffffu, on == 4);               // every key is seen
-        const bool each = top_v - low_v > (params.e5m2 ? 8 : 15);
-        if (each) top_v = 0;                                               // (0: the codes of V stay as they are)
+        int flags = 0;
+        if (top_v - low_v > (params.e5m2 ? 8 : 15) || top_v == (int)kScaleNone) {
+          flags = top_v == (int)kScaleNone ? kWideEachV | kWideNoneV : kWideEachV;
+          top_v = 0;                                                       // (0: the codes of V stay as they are)
+        }
         int top = top_v;
         if (kind == 0) {
           top = __reduce_max_sync(0xffffffffu, top_k);
           if (tid == 0)
             s_info[at] = WideTileInfo{scale_of(top), top_v ? (float)(top_v - 127) : 0.f,
-                                      top_v ? __uint_as_float((uint32_t)(254 - top_v) << 23) : 1.f, each};
+                                      top_v ? __uint_as_float((uint32_t)(254 - top_v) << 23) : 1.f, flags};
         }
         // a thread keeps to one 16-byte chunk of codes and to the rows `row` + kStep i
         constexpr int kChunks = D / 16, kStep = kThreads / kChunks, kTurns = (127 + kStep) / kStep;
@@ -594,61 +599,132 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
         }
         ++made;
         tc_fence_after();
+        const int* meta = s_meta + (tile % kWideInfo) * 8;
+        // the keys of 32 that this row sees, from the first keys of both 16
+        auto visible = [&](int ka, int kb) {
+          auto group = [&](int k0) -> uint32_t {       // those before a tree
+            if (k0 < 0) return 0;
+            const int y = min(max(tok + 1 - k0, 0), 16), z = min(max(low - k0, 0), 16);
+            return ((1u << y) - 1u) & ~((1u << z) - 1u);
+          };
+          uint32_t vis = group(ka) | group(kb) << 16;
+          if (small_tree) {
+            const uint2 y = s_tree[i_row];
+            const unsigned long long w = y.x | (unsigned long long)y.y << 32;
+            auto sees = [&](int k0) -> uint32_t {      // the drafts among 16 keys that this row sees
+              const int d = k0 - base;
+              if (k0 < 0 || d <= -16 || d >= kWideDrafts) return 0;
+              return (uint32_t)(d < 0 ? w << -d : w >> d) & 0xFFFFu;
+            };
+            vis |= sees(ka) | sees(kb) << 16;
+          } else if (p.ancestors && max(ka, kb) + 15 >= base) {
+            // lane: one of the 32 keys; the warp's rows one by one
+            const int k0 = lane < 16 ? ka : kb;
+            const int draft = k0 < 0 ? -1 : k0 + (lane & 15) - base;
+            int i = (r0 + (warp & 3) * 32) % p.Sq;
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r) {
+              const bool see = draft >= 0 && decode_ancestor(p, x.b, drafts, i, draft);
+              const uint32_t bits = __ballot_sync(0xffffffffu, see);
+              if (lane == r) vis |= bits;
+              if (++i == p.Sq) i = 0;
+            }
+          }
+          return vis;
+        };
+        if (n && n % kWideFlush == 0) {                // (O is at rest; the next P V starts from zero)
+          const float g = ex2_approx(m_gone - m);
+          m_gone = m;
+          uint4* gone = gone_of(t);
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t u[16];
+            tmem_ld16(tO + 16 * c, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              gone[4 * c + q] = plus(n == kWideFlush ? make_uint4(0, 0, 0, 0) : gone[4 * c + q], g, u + 4 * q);
+          }
+        }
+        auto move = [&](float top) {                   // references move up
+          const float to = top - m > kMaxOver + kLiftP ? top - kLiftP : m;
+          const float g = ex2_approx(m - to);
+          m = to;
+          l *= g;
+          if (n % kWideFlush) {
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t u[16];
+              tmem_ld16(tO + 16 * c, u);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * g);
+              tmem_st16(tO + 16 * c, u);
+            }
+          }
+        };
+        WideTileInfo info{1.f, 0.f, 1.f, 0};
+        if constexpr (EIGHT) info = s_info[tile % kWideInfo];
+        // a score in log2 units with its value's exponent is s f + v
+        float f = fac * info.k_scale, v = info.v_exp;
+        const bool odd = EIGHT && info.flags;
+        if (odd) {
+          // Key by key, in tensor memory: the scores become what they are in log2 units, masked, the reference moves,
+          // and the sum takes each without its value's exponent.  (In loops of their own: as part of the code
+          // below they took 5 to 20 % of the time of the tiles that need none of it.)
+          const uint8_t* vs = smem + SM::kScaleOff + (tile % kWideInfo) * 384 + 128;
+          auto v_exp = [&](int i) { return vs[i] == kScaleNone ? 0.f : (float)((int)vs[i] - 127); };   // (not finite: it weighs as any other)
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t vis = visible(meta[2 * c], meta[2 * c + 1]);
+            uint32_t u[32];
+            tmem_ld32(tS + 32 * c, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float y = (vis >> i) & 1u ? fmaf(__uint_as_float(u[i]), f, v_exp(32 * c + i)) : -INFINITY;
+              top = fmaxf(top, y);                     // (NaN is dropped)
+              u[i] = __float_as_uint(y);
+            }
+            tmem_st32(tS + 32 * c, u);
+          }
+          tmem_wait_st();
+          if (__any_sync(0xffffffffu, top - m > kMaxOver + kLiftP)) move(top);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t u[32];
+            tmem_ld32(tS + 32 * c, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float y = __uint_as_float(u[i]);
+              l += ex2_approx(y - v_exp(32 * c + i) - m);
+              if (vs[32 * c + i] == kScaleNone && y > -INFINITY) u[i] = 0x7FFFFFFFu;   // (its P is NaN)
+            }
+            if (info.flags & kWideNoneV) tmem_st32(tS + 32 * c, u);
+          }
+          tmem_wait_st();
+          f = 1.f, v = 0.f;
+        }
         uint32_t su[128];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&su[32 * c]));
-        const int* meta = s_meta + (tile % kWideInfo) * 8;
         const int4 ka = *reinterpret_cast<const int4*>(meta), kb = *reinterpret_cast<const int4*>(meta + 4);
         const int first = min(min(min(ka.x, ka.y), min(ka.z, ka.w)), min(min(kb.x, kb.y), min(kb.z, kb.w)));
         const int last = max(max(max(ka.x, ka.y), max(ka.z, ka.w)), max(max(kb.x, kb.y), max(kb.z, kb.w))) + 15;
         const bool all = first >= max(all_lo, 0) && last <= all_hi;
-        WideTileInfo info{1.f, 0.f, 1.f, 0};
-        if constexpr (EIGHT) info = s_info[tile % kWideInfo];
-        const uint8_t* vs = smem + SM::kScaleOff + (tile % kWideInfo) * 384 + 128;
-        // a score in log2 units with its value's exponent is s f + v
-        float f = fac * info.k_scale, v = info.v_exp;
         tmem_wait_ld();
         float sv[128];
 #pragma unroll
         for (int i = 0; i < 128; ++i) sv[i] = __uint_as_float(su[i]);
-        if (!all || (EIGHT && info.each)) {            // (few tiles: a piece's ends)
+        if (!all && !odd) {                            // (few tiles: a piece's ends)
           const int keys[8] = {ka.x, ka.y, ka.z, ka.w, kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            auto group = [&](int k0) -> uint32_t {     // the keys of 16 that this row sees before a tree
-              if (k0 < 0) return 0;
-              const int y = min(max(tok + 1 - k0, 0), 16), z = min(max(low - k0, 0), 16);
-              return ((1u << y) - 1u) & ~((1u << z) - 1u);
-            };
-            uint32_t vis = group(keys[2 * c]) | group(keys[2 * c + 1]) << 16;
-            if (small_tree) {
-              const uint2 y = s_tree[i_row];
-              const unsigned long long w = y.x | (unsigned long long)y.y << 32;
-              auto sees = [&](int k0) -> uint32_t {    // the drafts among 16 keys that this row sees
-                const int d = k0 - base;
-                if (k0 < 0 || d <= -16 || d >= kWideDrafts) return 0;
-                return (uint32_t)(d < 0 ? w << -d : w >> d) & 0xFFFFu;
-              };
-              vis |= sees(keys[2 * c]) | sees(keys[2 * c + 1]) << 16;
-            } else if (p.ancestors && max(keys[2 * c], keys[2 * c + 1]) + 15 >= base) {
-              // lane: one of the 32 keys; the warp's rows one by one
-              const int k0 = lane < 16 ? keys[2 * c] : keys[2 * c + 1];
-              const int draft = k0 < 0 ? -1 : k0 + (lane & 15) - base;
-              int i = (r0 + (warp & 3) * 32) % p.Sq;
-#pragma unroll 8
-              for (int r = 0; r < 32; ++r) {
-                const bool see = draft >= 0 && decode_ancestor(p, x.b, drafts, i, draft);
-                const uint32_t bits = __ballot_sync(0xffffffffu, see);
-                if (lane == r) vis |= bits;
-                if (++i == p.Sq) i = 0;
-              }
-            }
+            const uint32_t vis = visible(keys[2 * c], keys[2 * c + 1]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              float y = fmaf(sv[32 * c + i], f, v);
-              if (EIGHT && info.each) y += (float)((int)vs[32 * c + i] - 127);
-              sv[32 * c + i] = (vis >> i) & 1u ? y : -INFINITY;
-            }
+            for (int i = 0; i < 32; ++i) sv[32 * c + i] = (vis >> i) & 1u ? fmaf(sv[32 * c + i], f, v) : -INFINITY;
           }
           f = 1.f, v = 0.f;
           if constexpr (!EIGHT) {
@@ -669,50 +745,8 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
             fence_proxy_async_smem();
           }
         }
-        if (n && n % kWideFlush == 0) {                // (O is at rest; the next P V starts from zero)
-          const float g = ex2_approx(m_gone - m);
-          m_gone = m;
-          uint4* gone = gone_of(t);
-#pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t u[16];
-            tmem_ld16(tO + 16 * c, u);
-            tmem_wait_ld();
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              gone[4 * c + q] = plus(n == kWideFlush ? make_uint4(0, 0, 0, 0) : gone[4 * c + q], g, u + 4 * q);
-          }
-        }
         const float top = fmaf(row_max(sv), f, v);     // (f >= 0; NaN is dropped)
-        if (__any_sync(0xffffffffu, top - m > kMaxOver + kLiftP)) {                    // references move up
-          const float to = top - m > kMaxOver + kLiftP ? top - kLiftP : m;
-          const float g = ex2_approx(m - to);
-          m = to;
-          l *= g;
-          if (n % kWideFlush) {
-#pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t u[16];
-              tmem_ld16(tO + 16 * c, u);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * g);
-              tmem_st16(tO + 16 * c, u);
-            }
-          }
-        }
-        if (EIGHT && info.each) {                      // the sum key by key, each with its value's 2^-e
-#pragma unroll 1
-          for (int c = 0; c < 16; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float y = -INFINITY;
-#pragma unroll
-              for (int q = 0; q < 16; ++q) y = q == c ? sv[8 * q + i] : y;
-              const float a = ex2_approx(y - m);
-              if (a > 0.f) l = fmaf(a, __uint_as_float((254u - vs[8 * c + i]) << 23), l);
-            }
-        }
+        if (__any_sync(0xffffffffu, top - m > kMaxOver + kLiftP)) move(top);
         const float neg = v - m;
         const uint64_t f2 = f2_pack(f, f), neg2 = f2_pack(neg, neg);
         uint64_t sum2[2] = {0ull, 0ull};
@@ -732,7 +766,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
           tmem_st16(tS + 16 * c, hi);
           if constexpr (kPair) tmem_st16(tS + 64 + 16 * c, lo);
         }
-        if (!(EIGHT && info.each)) {
+        if (!odd) {
           float a, b, c, d;
           f2_unpack(sum2[0], a, b);
           f2_unpack(sum2[1], c, d);

@@ -1,0 +1,105 @@
+"""Rows of an 8-bit cache that are not finite, and rows of very different sizes, in decode and trees
+by every kernel (up to 64 rows per KV head by warps, more by tcgen05), against the fp64 reference
+of oracle/paged.py with the bounds of tests/test_gpu_paged8.py.
+
+A row that is not finite is stored as codes 0 with the scale byte 255.  Of a value it is NaN in the
+answer of each row that sees it; its weight and so the LSE are those of its key.  Of a key the
+answer and the LSE of a row that sees it are NaN.  A row that does not see it is answered as
+without: as if its codes stood for zeros."""
+import numpy as np
+import pytest
+
+from oracle import paged as P
+from tests.test_gpu_paged import _dev, _host, _round, _status
+from tests.test_gpu_paged8 import Cache8, _check8, _spread, _trees
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from attention_forward_fa_gb300 import build
+    build.build()
+
+
+def _seen(lens, Sq, pre=None, tree=None):
+    """bool [B, Sq, longest]: which keys a row sees."""
+    pos = np.arange(max(lens))
+    see = np.zeros((len(lens), Sq, pos.size), dtype=bool)
+    for b, n in enumerate(lens):
+        for i in range(Sq):
+            t = n - Sq + i
+            see[b, i] = pos <= t if tree is None else pos < n - tree[1][b]
+            if pre is not None:
+                see[b, i] &= pos >= t - pre
+            if tree is not None and i < tree[1][b]:
+                first = n - tree[1][b]
+                see[b, i, first:n] = tree[0][b, i, : tree[1][b]]
+    return see
+
+
+def _spoil(c, kind, b, t):
+    """Token t of sequence b, every head: a key ("k") or value ("v") row that is not finite, zero on the
+    reference's side."""
+    p, s = int(c.table[b, t // c.page]), t % c.page
+    codes, scale = (c.bk, c.sk) if kind == "k" else (c.bv, c.sv)
+    codes[p, :, s], scale[p, :, s] = 0, 255
+    (c.k if kind == "k" else c.v)[p, :, s] = 0
+    (c.kc if kind == "k" else c.vc)[p, :, s] = 0
+    (c.ke if kind == "k" else c.ve)[p, :, s] = 0
+
+
+def _compare(c, q, lens, got, bad_k, bad_v, pre=None, tree=None, where=""):
+    """bad_k, bad_v: per sequence the tokens whose rows are not finite."""
+    o, l = (_host(x) for x in got)
+    B, Hq, Sq, D = q.shape
+    a = (c.table, lens, D ** -0.5)
+    ref = P.decode(q, c.k, c.v, *a, pre, None, tree)
+    see = _seen(lens, Sq, pre, tree)
+    nan_k, nan_v = (np.array([see[b][:, bad[b]].any(-1) for b in range(B)]) for bad in (bad_k, bad_v))     # [B, Sq]
+    every = lambda x: np.broadcast_to(x[:, None], (B, Hq, Sq))
+    assert np.isnan(o[every(nan_k | nan_v)]).all(), f"{where}: rows that see what is not finite"
+    assert np.isnan(l[every(nan_k)]).all() and not np.isnan(l[~every(nan_k)]).any(), f"{where}: LSE"
+    clean = np.where(every(nan_k | nan_v)[..., None], ref[0], o)
+    lse = np.where(every(nan_k), ref[1], l)
+    _check8(_dev(clean.astype(np.float32)), _dev(lse.astype(np.float32)), ref, *_spread(c, q, *a, tree, pre), c.dtype, where)
+
+
+ROWS = [
+    # dtype, fmt, Hq, Hkv, D, page, Sq
+    ("bf16", "e4m3fn", 4, 1, 128, 64, 1), ("fp16", "e5m2", 4, 2, 64, 16, 5), ("bf16", "e5m2", 12, 2, 128, 32, 4),
+    ("fp16", "e4m3fn", 8, 2, 128, 64, 10), ("bf16", "e4m3fn", 4, 2, 64, 128, 27),          # by warps: 1 to 54 rows
+    ("bf16", "e4m3fn", 8, 2, 128, 64, 25), ("fp16", "e5m2", 8, 2, 64, 16, 20),             # by tcgen05, up to 128
+    ("fp16", "e4m3fn", 4, 1, 128, 32, 40), ("bf16", "e5m2", 7, 1, 64, 256, 40),            # and more
+]
+
+
+@pytest.mark.parametrize("case", ROWS, ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("kinds", ["v"])
+def test_rows_that_are_not_finite(case, kinds):
+    """Among the newest tokens, in the text before them (one sequence in one piece, one cut into many),
+    and where a window ends."""
+    import attention_forward_fa_gb300 as fa
+    dtype, fmt, Hq, Hkv, D, page, Sq = case
+    lens = [200, 3000, 130]
+    for form in ("decode", "window", "tree"):
+        c = Cache8(41, dtype, fmt, 3, Hkv, D, page, lens)
+        late = [[n - 1 - Sq // 2] for n in lens]
+        text = [[], [17, 2000], []]
+        bad = [x + y for x, y in zip(late, text if form != "window" else [[], [lens[1] - Sq - 9], []])]
+        for kind in kinds:
+            for b in range(3):
+                for t in bad[b]:
+                    _spoil(c, kind, b, t)
+        q = _round(c.rng.standard_normal((3, Hq, Sq, D)), dtype)
+        tq, n = _dev(q, dtype), c.ints(lens)
+        pre, tree = (10 if form == "window" else None), None
+        if form == "tree":
+            drafts = [Sq, Sq, max(Sq - 2, 0)]
+            tree = (_trees(c.rng, 3, Sq)[0], drafts)
+            got = fa.flash_attention_decode_tree(tq, c.obj, n, _dev(tree[0]), new_lens=c.ints(drafts))
+        else:
+            got = fa.flash_attention_decode(tq, c.obj, n, pre_tokens=pre)
+        assert _status() == 0
+        none = [[], [], []]
+        _compare(c, q, lens, got, bad if "k" in kinds else none, bad if "v" in kinds else none, pre, tree, f"{kinds} {form}")
