@@ -921,7 +921,8 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) fa_decode_join_kerne
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D) + (E / 2) * lane;
 #pragma unroll
   for (int e = 0; e < E; e += 2) dst[e / 2] = pack16x2<BF16>(o[e] * inv, o[e + 1] * inv);
-  if (lane == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : INFINITY;
+  const bool empty = TILE == kDecTile ? !(l > 0.f) : l == 0.f;     // (over an 8-bit cache a NaN key's stays NaN)
+  if (lane == 0) p.lse[row] = empty ? INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 }  // namespace fa

@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kDecThreads * kDec8Teams<BF16, NT>, 1) fa_deco
         if (warp == 0 && g == 0) {
           if (!direct) p.part_ml[part0 + row] = make_float2(m[n][e], sum[e]);
           else if (row < rows)
-            p.lse[row0 + row] = sum[e] > 0.f ? (m[n][e] + log2f(sum[e])) * 0.6931471805599453f : INFINITY;
+            p.lse[row0 + row] = sum[e] == 0.f ? INFINITY : (m[n][e] + log2f(sum[e])) * 0.6931471805599453f;   // (NaN stays)
         }
       }
     }

@@ -21,12 +21,12 @@
 //     per page part and chunk; an 8-bit one comes as codes into a second ring, and
 //     the converters write it as fp16 into the operand ring.
 //   * The K codes of a tile are multiplied by 2^(e_k - E_k), E_k the largest exponent
-//     of its seen keys, which leaves one factor per tile for the scores.  (Exact while
-//     a row's scale is within 2^15, of e5m2 2^8, of the tile's largest; of smaller rows what
-//     is below 2^-33 of the largest key is lost.)  Values alike with E_v, which joins the
-//     exponent of the probabilities as in fa_decode8.cuh, but only in tiles whose values'
-//     scales are within those limits, so that every product's operand is exact; in others
-//     the codes stay and the softmax threads take each key's exponent, which is slow.
+//     of its seen keys, which leaves one factor per tile for the scores; values alike
+//     with E_v, which joins the exponent of the probabilities as in fa_decode8.cuh.
+//     That is exact where the tile's scales are within 2^15, of e5m2 2^8, of each other.
+//     In other tiles (the keys', the values', or both) the codes stay and the softmax
+//     threads take each key's exponent, which is slow.  A row of zeros (e = -80) beside
+//     others makes a tile one of those, and so does a row that is not finite.
 //   * The next S of a group is issued behind its P V, so that its commit says that O is at
 //     rest: the softmax threads may then move their references and rescale O.
 //   * P is written over S, as a hi + lo pair of the operands' type (64 + 64 columns) or, over an
@@ -78,6 +78,7 @@ struct alignas(16) WideTileInfo {  // of an 8-bit tile
 };
 constexpr int kWideEachV = 1;      // the values' exponents are taken key by key
 constexpr int kWideNoneV = 2;      // (with kWideEachV) some are of rows that are not finite
+constexpr int kWideEachK = 4;      // the keys' scales are taken key by key
 
 template <int D, bool EIGHT, bool SPLIT>
 struct WideSmem {
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
         };
         // every warp for itself: the largest exponents of the seen keys, the values' least
         const uint8_t* scales = smem + SM::kScaleOff + at * 384;           // K's, V's as they came with K, with V
-        int top_k = 0, top_v = 0, low_v = 255;
+        int top_k = 0, low_k = 255, top_v = 0, low_v = 255;
         unsigned on = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -425,21 +426,24 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
           if (!seen(r)) continue;
           ++on;
           const int ks = scales[r], vs = scales[(kind ? 256 : 128) + r];
-          top_k = max(top_k, ks), top_v = max(top_v, vs), low_v = min(low_v, vs);
+          top_k = max(top_k, ks), low_k = min(low_k, ks), top_v = max(top_v, vs), low_v = min(low_v, vs);
         }
         top_v = __reduce_max_sync(0xffffffffu, top_v);
         low_v = __reduce_min_sync(0xffffffffu, low_v);
         const bool whole = __all_sync(0xffffffffu, on == 4);               // every key is seen
+        const int apart = params.e5m2 ? 8 : 15;
         int flags = 0;
-        if (top_v - low_v > (params.e5m2 ? 8 : 15) || top_v == (int)kScaleNone) {
+        if (top_v - low_v > apart || top_v == (int)kScaleNone) {
           flags = top_v == (int)kScaleNone ? kWideEachV | kWideNoneV : kWideEachV;
           top_v = 0;                                                       // (0: the codes of V stay as they are)
         }
         int top = top_v;
         if (kind == 0) {
           top = __reduce_max_sync(0xffffffffu, top_k);
+          low_k = __reduce_min_sync(0xffffffffu, low_k);
+          if (top - low_k > apart || top == (int)kScaleNone) flags |= kWideEachK, top = 0;
           if (tid == 0)
-            s_info[at] = WideTileInfo{scale_of(top), top_v ? (float)(top_v - 127) : 0.f,
+            s_info[at] = WideTileInfo{flags & kWideEachK ? 1.f : scale_of(top), top_v ? (float)(top_v - 127) : 0.f,
                                       top_v ? __uint_as_float((uint32_t)(254 - top_v) << 23) : 1.f, flags};
         }
         // a thread keeps to one 16-byte chunk of codes and to the rows `row` + kStep i
@@ -672,37 +676,42 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
           // Key by key, in tensor memory: the scores become what they are in log2 units, masked, the reference moves,
           // and the sum takes each without its value's exponent.  (In loops of their own: as part of the code
           // below they took 5 to 20 % of the time of the tiles that need none of it.)
-          const uint8_t* vs = smem + SM::kScaleOff + (tile % kWideInfo) * 384 + 128;
-          auto v_exp = [&](int i) { return vs[i] == kScaleNone ? 0.f : (float)((int)vs[i] - 127); };   // (not finite: it weighs as any other)
+          const uint8_t* ks = smem + SM::kScaleOff + (tile % kWideInfo) * 384;
+          const bool each_k = info.flags & kWideEachK, each_v = info.flags & kWideEachV;
+          // byte i, or what stands for the tile's one (a key's scale is in f then)
+          auto k_byte = [&](int i) -> uint32_t { return each_k ? ks[i] : 127u; };
+          auto v_byte = [&](int i) -> uint32_t { return each_v ? ks[128 + i] : (uint32_t)((int)info.v_exp + 127); };
+          auto v_exp = [&](int i) { const uint32_t y = v_byte(i); return y == kScaleNone ? 0.f : (float)((int)y - 127); };
           float top = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t vis = visible(meta[2 * c], meta[2 * c + 1]);
-            uint32_t u[32];
-            tmem_ld32(tS + 32 * c, u);
+          for (int c = 0; c < 8; ++c) {
+            const uint32_t vis = visible(meta[c], -1);
+            uint32_t u[16];
+            tmem_ld16(tS + 16 * c, u);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float y = (vis >> i) & 1u ? fmaf(__uint_as_float(u[i]), f, v_exp(32 * c + i)) : -INFINITY;
+            for (int i = 0; i < 16; ++i) {
+              // (not finite: infinity times 0 of a key, of a value no exponent, so that it weighs as any other)
+              const float y = (vis >> i) & 1u ? fmaf(__uint_as_float(u[i]) * f, scale_of(k_byte(16 * c + i)), v_exp(16 * c + i)) : -INFINITY;
               top = fmaxf(top, y);                     // (NaN is dropped)
               u[i] = __float_as_uint(y);
             }
-            tmem_st32(tS + 32 * c, u);
+            tmem_st16(tS + 16 * c, u);
           }
           tmem_wait_st();
           if (__any_sync(0xffffffffu, top - m > kMaxOver + kLiftP)) move(top);
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t u[32];
-            tmem_ld32(tS + 32 * c, u);
+          for (int c = 0; c < 8; ++c) {
+            uint32_t u[16];
+            tmem_ld16(tS + 16 * c, u);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < 16; ++i) {
               const float y = __uint_as_float(u[i]);
-              l += ex2_approx(y - v_exp(32 * c + i) - m);
-              if (vs[32 * c + i] == kScaleNone && y > -INFINITY) u[i] = 0x7FFFFFFFu;   // (its P is NaN)
+              l += ex2_approx(y - v_exp(16 * c + i) - m);
+              if (v_byte(16 * c + i) == kScaleNone && y > -INFINITY) u[i] = 0x7FFFFFFFu;   // (its P is NaN)
             }
-            if (info.flags & kWideNoneV) tmem_st32(tS + 32 * c, u);
+            tmem_st16(tS + 16 * c, u);
           }
           tmem_wait_st();
           f = 1.f, v = 0.f;
@@ -894,7 +903,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
         }
       }
       if (mine) {
-        if (direct) p.lse[at0 + row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : INFINITY;
+        if (direct) p.lse[at0 + row] = l == 0.f ? INFINITY : (m + log2f(l)) * 0.6931471805599453f;   // (NaN stays)
         else p.part_ml[part] = make_float2(m, l);
       }
       tc_fence_before();

@@ -75,7 +75,7 @@ ROWS = [
 
 
 @pytest.mark.parametrize("case", ROWS, ids=lambda c: "-".join(map(str, c)))
-@pytest.mark.parametrize("kinds", ["v"])
+@pytest.mark.parametrize("kinds", ["v", "k", "kv"])
 def test_rows_that_are_not_finite(case, kinds):
     """Among the newest tokens, in the text before them (one sequence in one piece, one cut into many),
     and where a window ends."""
@@ -103,3 +103,68 @@ def test_rows_that_are_not_finite(case, kinds):
         assert _status() == 0
         none = [[], [], []]
         _compare(c, q, lens, got, bad if "k" in kinds else none, bad if "v" in kinds else none, pre, tree, f"{kinds} {form}")
+
+
+def _set_keys(c, k):
+    """The cache's keys become k [num_pages, Hkv, page, D], quantised."""
+    c.kc, c.ke = P.quantise(k, c.fmt)
+    c.k = np.ldexp(c.kc, c.ke[..., None])
+    from tests.test_gpu_paged8 import _codes
+    c.bk.copy_(_codes(c.kc, c.fmt).view(c.bk.dtype))
+    c.sk.copy_(_dev((c.ke + 127).astype(np.uint8)))
+
+
+@pytest.mark.parametrize("case", ROWS, ids=lambda c: "-".join(map(str, c)))
+def test_small_keys_beside_large_ones(case):
+    """Keys up to 2^60 times the others, orthogonal to every query, so that the answers are the small
+    keys' own; zero rows among them."""
+    import attention_forward_fa_gb300 as fa
+    dtype, fmt, Hq, Hkv, D, page, Sq = case
+    lens = [200, 3000, 130]
+    c = Cache8(42, dtype, fmt, 3, Hkv, D, page, lens)
+    q = _round(c.rng.standard_normal((3, Hq, Sq, D)), dtype)
+    q[..., 0] = 0
+    for share in (0.02, 0.5):
+        k = c.rng.standard_normal(c.k.shape)
+        large = c.rng.random(c.k.shape[:3]) < share
+        k[large] = 0
+        k[large, 0] = 2.0 ** c.rng.integers(5, 60, int(large.sum()))
+        k[c.rng.random(c.k.shape[:3]) < 0.02] = 0
+        _set_keys(c, k)
+        for tree in (None, (_trees(c.rng, 3, Sq)[0], [Sq, Sq, max(Sq - 2, 0)])):
+            tq, n = _dev(q, dtype), c.ints(lens)
+            got = (fa.flash_attention_decode(tq, c.obj, n) if tree is None else
+                   fa.flash_attention_decode_tree(tq, c.obj, n, _dev(tree[0]), new_lens=c.ints(tree[1])))
+            assert _status() == 0
+            none = [[], [], []]
+            _compare(c, q, lens, got, none, none, None, tree, f"share {share} tree {tree is not None}")
+
+
+@pytest.mark.parametrize("case", ROWS, ids=lambda c: "-".join(map(str, c)))
+def test_a_large_draft_reaches_no_other_branch(case):
+    """One draft's key of 2^70: rows that do not see it are answered to the usual bounds."""
+    import attention_forward_fa_gb300 as fa
+    dtype, fmt, Hq, Hkv, D, page, Sq = case
+    if Sq < 4:
+        pytest.skip("no branches")
+    lens, drafts = [200, 3000, 130], [Sq, Sq, Sq - 1]
+    c = Cache8(43, dtype, fmt, 3, Hkv, D, page, lens)
+    k = c.k.copy()
+    for b in range(3):
+        t = lens[b] - drafts[b] + 1
+        k[c.table[b, t // page], :, t % page] *= 2.0 ** 70
+    _set_keys(c, k)
+    anc = _trees(c.rng, 3, Sq)[0]
+    anc[:, 2:, 1] = c.rng.random((3, Sq - 2)) < 0.3
+    q = _round(c.rng.standard_normal((3, Hq, Sq, D)), dtype)
+    o, l = fa.flash_attention_decode_tree(_dev(q, dtype), c.obj, c.ints(lens), _dev(anc), new_lens=c.ints(drafts))
+    assert _status() == 0
+    a = (c.table, lens, D ** -0.5)
+    ref = P.decode(q, c.k, c.v, *a, tree=(anc, drafts))
+    W, E = _spread(c, q, *a, (anc, drafts))
+    clear = np.array([[i >= drafts[b] or not anc[b, i, 1] for i in range(Sq)] for b in range(3)])
+    assert clear.any() and not clear.all()
+    rows = np.broadcast_to(clear[:, None], (3, Hq, Sq))
+    pick = lambda x: x[rows][None, None]
+    got = [_dev(np.ascontiguousarray(pick(_host(x))).astype(np.float32)) for x in (o, l)]
+    _check8(*got, [pick(x) for x in ref], pick(W), E, dtype, "clear rows")
