@@ -795,6 +795,11 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
   }
 }
 
+// The exponent's part down to where 2^d is the least normal fp32 number: x 2^d as (x 2^(d - a)) 2^a, a = ex2_floor(d),
+// is right for d below it too.  (Over an 8-bit cache a sum may be as large as 2^126 beside a reference that falls behind by
+// as much: fa_decode8.cuh.)
+__device__ __forceinline__ float ex2_floor(float d) { return fmaxf(d, -126.f); }
+
 // Joins the pieces of the units that several CTAs shared: the schedule is
 // computed anew from the lengths, the pieces summed in an order that depends on
 // it alone (the same bits every time).  WPR warps per row: 1 where there are many
@@ -857,6 +862,14 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) fa_decode_join_kerne
   float m = kNoScore, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
+  auto add = [&](float2 ml, float to, float f) {       // f = 2^(ml.x - to)
+    if constexpr (TILE != kDecTile) {
+      const float d = ml.x - to, a = ex2_floor(d);
+      l = fmaf(ex2_approx(a), ml.y * ex2_approx(d - a), l);
+    } else {
+      l = fmaf(f, ml.y, l);
+    }
+  };
   for (int cb = c0 + part; cb <= c1; cb += WPR * kPieces) {
     float2 ml[kPieces];
     float x[kPieces][E];
@@ -883,14 +896,15 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) fa_decode_join_kerne
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) top = fmaxf(top, ml[i].x);
     const float keep = ex2_approx(m - top);
+    if constexpr (TILE != kDecTile) l *= ex2_approx(m - top - ex2_floor(m - top));
+    l *= TILE != kDecTile ? ex2_approx(ex2_floor(m - top)) : keep;
     m = top;
-    l *= keep;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] *= keep;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const float f = ex2_approx(ml[i].x - top);     // (a piece that is none is all 0)
-      l = fmaf(f, ml[i].y, l);
+      add(ml[i], top, f);
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = fmaf(f, x[i][e], o[e]);
     }
@@ -912,7 +926,7 @@ __global__ void __launch_bounds__(WPR > 8 ? 32 * WPR : 256) fa_decode_join_kerne
 #pragma unroll 8
     for (int w = 0; w < WPR; ++w) {
       const float f = ex2_approx(s_ml[w].x - m);
-      l = fmaf(f, s_ml[w].y, l);
+      add(s_ml[w], m, f);
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = fmaf(f, s_o[w][E * lane + e], o[e]);
     }

@@ -20,7 +20,9 @@
 //     (log2 units) and the running reference m over s', the probability that goes
 //     into the value product is 2^(s' - m), the weight of the value's codes, and
 //     the sum of the softmax takes 2^(s' - m) 2^-e.  So the product's operands are
-//     as large as what they add, whatever the scales.
+//     as large as what they add, whatever the scales.  Where 2^(s' - m) could be below
+//     2^-126 of a key whose part of the sum counts (its e more than kFarScales below
+//     that of a key that the reference followed) the sum takes 2^(s' - e - m) instead.
 //   * A value row that is not finite (scale byte 255, codes 0) weighs in the sum as
 //     any other and has a NaN for its P in the rows that see it, so that their
 //     answers are NaN and no other row's.
@@ -52,6 +54,12 @@ constexpr int kDec8Groups = 8;      // of 16 keys; a consumer scores two
 // (Two where a third's shared memory or registers do not fit.)
 template <bool BF16, int NT>
 constexpr int kDec8Teams = NT == 1 || (NT == 2 && BF16) ? 3 : 2;
+
+// (P' is lost below 2^-126, m is at most the largest s' less 7: a key of the tiles that take it all the same, up to 95
+// below the largest e by tcgen05, then has less than 2^-38 of the share of the sum that the key of the largest s' has.)
+constexpr int kFarScales = 80;
+// Scale bytes of values are at least kLeastExp + 127: from one below this no other is far, and nobody has to know it.
+constexpr uint32_t kLargeScale = kLeastExp + 127 + kFarScales + 1;
 
 struct Decode8Params {
   DecodeCore c;
@@ -125,6 +133,7 @@ __global__ void __launch_bounds__(kDecThreads * kDec8Teams<BF16, NT>, 1) fa_deco
   DecodeWalk* s_walk = reinterpret_cast<DecodeWalk*>(smem + SM::kMiscOff);
   int* s_len = reinterpret_cast<int*>(smem + SM::kMiscOff + 24);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + SM::kMiscOff + 28);
+  int* s_top = reinterpret_cast<int*>(smem + SM::kMiscOff + 32);             // per warp: its largest scale byte of a value
 
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&params.tm_k);
@@ -298,6 +307,7 @@ __global__ void __launch_bounds__(kDecThreads * kDec8Teams<BF16, NT>, 1) fa_deco
     const int tok_min = p.ancestors ? len - drafts - 1 : len - p.Sq;      // as in fa_decode_kernel
     const int low_max = p.pre_tokens >= 0 ? len - 1 - p.pre_tokens : 0;   // lowest key that all rows see
 
+    uint32_t far = 0;                // value scales below this byte are far from one that the references followed
     float o[NT][DC][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -344,7 +354,8 @@ __global__ void __launch_bounds__(kDecThreads * kDec8Teams<BF16, NT>, 1) fa_deco
       // (c2, c3) of each 16, rows 2 t4, 2 t4 + 1
       float over = -INFINITY;        // the most that one exceeds its row's reference by
       float back[2][2];              // 2^-e of the lane's keys' values
-      bool odd = false;              // whether one of them is not finite
+      bool odd = false;              // whether one of them is large, not finite, or far
+      const uint32_t near = min(far, kLargeScale);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int kq = meta[2 * warp + u];
@@ -360,7 +371,7 @@ __global__ void __launch_bounds__(kDecThreads * kDec8Teams<BF16, NT>, 1) fa_deco
             const int key = key0 + g + 8 * x;
             if (key >= s.hi || key < s.lo) ks = vs = 127;
           }
-          odd = odd || vs == kScaleNone;
+          odd = odd || vs - near >= kLargeScale - near;    // (unsigned: below `near`, or from kLargeScale on)
           if (vs == kScaleNone) vs = 127;
           kf[x] = scale_of(ks);
           ve[x] = (float)((int)vs - 127);
@@ -400,7 +411,19 @@ __global__ void __launch_bounds__(kDecThreads * kDec8Teams<BF16, NT>, 1) fa_deco
           }
           if (g == 0) *reinterpret_cast<float2*>(s_max + (warp * NT + n) * 8 + 2 * t4) = make_float2(mx[0], mx[1]);
         }
+        uint32_t most = 0;             // (of scales that are not large it does not matter)
+        if (__any_sync(0xffffffffu, odd)) {
+          const int r = 32 * warp + lane, first = meta[r >> 4], key = first + (r & 15);
+          const uint32_t vs = first >= 0 && key >= s.lo && key < s.hi ? scales[kDec8Tile + r] : 0;
+          most = __reduce_max_sync(0xffffffffu, vs == kScaleNone ? 0 : vs);
+        }
+        if (lane == 0) s_top[warp] = (int)most;
         sync();
+        const int4 tops = *reinterpret_cast<const int4*>(s_top);
+        if (const int top = max(max(tops.x, tops.y), max(tops.z, tops.w)) - kFarScales; top > (int)far) {
+          far = (uint32_t)top;
+          odd = true;                  // (this tile's own keys may be far from those that the references now follow)
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float top[2] = {m[n][0], m[n][1]}, f[2];
@@ -412,9 +435,11 @@ __global__ void __launch_bounds__(kDecThreads * kDec8Teams<BF16, NT>, 1) fa_deco
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            f[e] = ex2_approx(m[n][e] - top[e]);
+            const float by = m[n][e] - top[e], a = ex2_floor(by);
+            f[e] = ex2_approx(by);
             m[n][e] = top[e];
-            l[n][e] *= f[e];
+            l[n][e] *= ex2_approx(by - a);                 // (1 but where 2^by is no fp32 number)
+            l[n][e] *= ex2_approx(a);
           }
 #pragma unroll
           for (int i = 0; i < DC; ++i) {
@@ -426,21 +451,24 @@ __global__ void __launch_bounds__(kDecThreads * kDec8Teams<BF16, NT>, 1) fa_deco
         }
       }
       if (__any_sync(0xffffffffu, odd)) {
-        // Values that are not finite: the key's weight joins the sum here, and P becomes 2^100, an fp16
-        // infinity, which times the row's codes of 0 is NaN.  (What a row does not see stays -infinity.)
+        // The weights of these keys join the sum here, without their values' exponents.  Values that are not
+        // finite: P becomes 2^100, an fp16 infinity, which times the row's codes of 0 is NaN.  (What a row does
+        // not see stays -infinity.)
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (scales[kDec8Tile + 32 * warp + 16 * u + 8 * x + g] != kScaleNone) continue;
+            const uint32_t vs = scales[kDec8Tile + 32 * warp + 16 * u + 8 * x + g];
+            if (vs >= far && vs != kScaleNone) continue;
+            const float e_v = vs == kScaleNone ? 0.f : (float)((int)vs - 127);
             back[u][x] = 0.f;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 float& y = c[u][n][2 * x + e];
-                l[n][e] += ex2_approx(y - m[n][e]);
-                if (y != -INFINITY) y = m[n][e] + 100.f;
+                l[n][e] += ex2_approx(y - e_v - m[n][e]);
+                if (vs == kScaleNone && y != -INFINITY) y = m[n][e] + 100.f;
               }
           }
       }

@@ -74,7 +74,7 @@ struct alignas(16) WideTileInfo {  // of an 8-bit tile
   float k_scale;                   // 2^E_k
   float v_exp;                     // E_v
   float v_back;                    // 2^-E_v
-  int flags;                       // kWide...
+  int flags;                       // kWide..., and 256 times the largest scale byte of a value
 };
 constexpr int kWideEachV = 1;      // the values' exponents are taken key by key
 constexpr int kWideNoneV = 2;      // (with kWideEachV) some are of rows that are not finite
@@ -432,9 +432,9 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
         low_v = __reduce_min_sync(0xffffffffu, low_v);
         const bool whole = __all_sync(0xffffffffu, on == 4);               // every key is seen
         const int apart = params.e5m2 ? 8 : 15;
-        int flags = 0;
+        int flags = top_v << 8;
         if (top_v - low_v > apart || top_v == (int)kScaleNone) {
-          flags = top_v == (int)kScaleNone ? kWideEachV | kWideNoneV : kWideEachV;
+          flags |= top_v == (int)kScaleNone ? kWideEachV | kWideNoneV : kWideEachV;
           top_v = 0;                                                       // (0: the codes of V stay as they are)
         }
         int top = top_v;
@@ -593,6 +593,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
       const int low = p.pre_tokens >= 0 ? tok - p.pre_tokens : 0;
       float m = kNoScore, l = 0.f, m_gone = kNoScore;  // m_gone: the reference of what has left the accumulator
       int n = 0;                                       // tiles of the piece in this group
+      int v_high = 0;                                  // the largest scale byte of a value in them
 
 #pragma unroll 1
       for (int j = SPLIT ? t : 0; j < nt; j += SPLIT ? 2 : 1, ++n) {
@@ -653,8 +654,14 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
         auto move = [&](float top) {                   // references move up
           const float to = top - m > kMaxOver + kLiftP ? top - kLiftP : m;
           const float g = ex2_approx(m - to);
+          if constexpr (EIGHT) {                       // (as in fa_decode8_kernel)
+            const float a = ex2_floor(m - to);
+            l *= ex2_approx(m - to - a);
+            l *= ex2_approx(a);
+          } else {
+            l *= g;
+          }
           m = to;
-          l *= g;
           if (n % kWideFlush) {
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
@@ -671,7 +678,9 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
         if constexpr (EIGHT) info = s_info[tile % kWideInfo];
         // a score in log2 units with its value's exponent is s f + v
         float f = fac * info.k_scale, v = info.v_exp;
-        const bool odd = EIGHT && info.flags;
+        // taken key by key: what the converters say, and values far below others (kFarScales)
+        const bool odd = EIGHT && ((info.flags & 255) || (info.flags >> 8) + kFarScales < v_high);
+        if (EIGHT) v_high = max(v_high, info.flags >> 8);
         if (odd) {
           // Key by key, in tensor memory: the scores become what they are in log2 units, masked, the reference moves,
           // and the sum takes each without its value's exponent.  (In loops of their own: as part of the code
@@ -822,7 +831,8 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
         const float2 ml = s_ml[row];
         const float to = fmaxf(m, ml.x);
         g0 = ex2_approx(m - to), g1 = ex2_approx(ml.x - to);
-        l = fmaf(l, g0, ml.y * g1);
+        const float a0 = ex2_floor(m - to), a1 = ex2_floor(ml.x - to);
+        l = fmaf(l * ex2_approx(m - to - a0), ex2_approx(a0), ml.y * ex2_approx(ml.x - to - a1) * ex2_approx(a1));
         m_gone = m_gone - m;                           // (relative to this group's own reference)
         m = to;
         gone1 = (nt / 2) > kWideFlush;

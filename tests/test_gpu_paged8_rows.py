@@ -140,6 +140,44 @@ def test_small_keys_beside_large_ones(case):
             _compare(c, q, lens, got, none, none, None, tree, f"share {share} tree {tree is not None}")
 
 
+def _set_values(c, v):
+    """The cache's values become v [num_pages, Hkv, page, D], quantised."""
+    from tests.test_gpu_paged8 import _codes
+    c.vc, c.ve = P.quantise(v, c.fmt)
+    c.v = np.ldexp(c.vc, c.ve[..., None])
+    c.bv.copy_(_codes(c.vc, c.fmt).view(c.bv.dtype))
+    c.sv.copy_(_dev((c.ve + 127).astype(np.uint8)))
+
+
+@pytest.mark.parametrize("order", ["mixed", "small first", "large first", "one large"])
+@pytest.mark.parametrize("case", [c for c in ROWS if c[0] == "bf16"], ids=lambda c: "-".join(map(str, c)))
+def test_values_over_the_whole_range(case, order):
+    """Rows of zeros (e = -80) and values of 2^-70 beside values of 2^110: a key's share of the sum does
+    not go by its value's size, within a tile, from tile to tile and from piece to piece."""
+    import attention_forward_fa_gb300 as fa
+    dtype, fmt, Hq, Hkv, D, page, Sq = case
+    lens = [200, 3000, 130]
+    c = Cache8(44, dtype, fmt, 3, Hkv, D, page, lens)
+    q = _round(c.rng.standard_normal((3, Hq, Sq, D)), dtype)
+    size = np.full(c.v.shape[:3], -200.0)
+    for b, n in enumerate(lens):
+        for t in range(n):
+            late = t >= n // 2
+            e = {"mixed": c.rng.choice([-200, -70, 0, 60, 110]), "small first": 110 if late else -200,
+                 "large first": -200 if late else 110, "one large": 110 if t == n // 3 else -70}[order]
+            size[c.table[b, t // page], :, t % page] = e
+    _set_values(c, np.where(size[..., None] < -190, 0.0, c.rng.standard_normal(c.v.shape) * np.exp2(size)[..., None]))
+    for scale in (0.0, D ** -0.5, 2.0):
+        for tree in (None, (_trees(c.rng, 3, Sq)[0], [Sq, Sq, max(Sq - 2, 0)])):
+            tq, n = _dev(q, dtype), c.ints(lens)
+            o, l = (fa.flash_attention_decode(tq, c.obj, n, scale=scale) if tree is None else
+                    fa.flash_attention_decode_tree(tq, c.obj, n, _dev(tree[0]), new_lens=c.ints(tree[1]), scale=scale))
+            assert _status() == 0
+            a = (c.table, lens, scale)
+            ref = P.decode(q, c.k, c.v, *a, tree=tree)
+            _check8(o, l, ref, *_spread(c, q, *a, tree), dtype, f"scale {scale} tree {tree is not None}")
+
+
 @pytest.mark.parametrize("case", ROWS, ids=lambda c: "-".join(map(str, c)))
 def test_a_large_draft_reaches_no_other_branch(case):
     """One draft's key of 2^70: rows that do not see it are answered to the usual bounds."""
