@@ -158,6 +158,16 @@ __device__ __forceinline__ int decode_drafts(const DecodeCore& p, int b, int len
 __device__ __forceinline__ bool decode_ancestor(const DecodeCore& p, int b, int drafts, int i, int j) {
   return i < drafts && j < drafts && p.ancestors[b * p.anc_stride + (long long)i * p.Sq + j] != 0;
 }
+// Whether no draft sees draft j.  Such a one may hold anything, and its P = 0 times an infinity or NaN would reach every
+// row: its value is zeroed where it was copied to.  (As a rule each draft sees itself, which is looked at first.)
+__device__ __forceinline__ bool decode_blind_draft(const DecodeCore& p, int b, int drafts, int j) {
+  if (j < 0 || j >= drafts) return false;
+  const uint8_t* x = p.ancestors + b * p.anc_stride + j;
+  bool blind = x[(long long)j * p.Sq] == 0;
+#pragma unroll 1
+  for (int i = 0; blind && i < drafts; ++i) blind = x[(long long)i * p.Sq] == 0;
+  return blind;
+}
 // Lengths, and numbers of drafts, that the tables cannot hold are reported, once.
 __device__ __forceinline__ void decode_report_drafts(const DecodeCore& p) {
   if (!p.ancestors) return;
@@ -592,6 +602,14 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtasPerSm) fa_decode_kernel(c
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) c[n][e] *= p.scale_log2;
+      if (TREE && kq >= 0 && kq + 15 > tok_min && decode_blind_draft(p, b, drafts, kq + (lane & 15) - tok_min - 1)) {
+#pragma unroll 1
+        for (int i = 0; i < D / 16; ++i) {                             // (two lanes a row, half of it each)
+          const int chunk = (lane >> 4) * (D / 16) + i;
+          st_shared_v4(base + SM::kHalf + place(warp) + (chunk >> 3) * half + (lane & 15) * 128 + ((chunk & 7) << 4), make_uint4(0, 0, 0, 0));
+        }
+        fence_proxy_async_smem();                                      // (before the stage's next copy)
+      }
       if (!all) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)

@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(kWideThreads<EIGHT>, 1) fa_wide_kernel(const _
               dead = true;
               break;
             }
-            if (k < x.s.lo || k >= x.s.hi) {
+            if (k < x.s.lo || k >= x.s.hi || decode_blind_draft(p, x.b, drafts, k - base)) {
 #pragma unroll
               for (int c = 0; c < D / 64; ++c)
 #pragma unroll

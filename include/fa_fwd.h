@@ -551,7 +551,8 @@ int fa_select_pages(const void* q, const fa_paged_kv_t* kv, int32_t* page_idx, i
  * x * 2^-e, ties to even, x in fp32 as rotated.  A row that holds an infinity
  * or NaN becomes NaN (codes 0, scale byte 255) and is reported as FA_ERR_RANGE by
  * fa_check_status.  Callers that write rows themselves: scale bytes 1 to 253, of
- * values 47 to 253 (2^-80 to 2^126), codes finite.
+ * values 47 to 253 (2^-80 to 2^126), codes finite, of every token that kv_lens counts,
+ * whether a row sees it or not.
  */
 typedef struct {
   uint8_t* k_scale;
@@ -576,7 +577,8 @@ int fa_kv_append_ext(const fa_paged_kv_t* kv, const fa_kv_fp8_t* fp8, const fa_k
  * (DEVICE int32[B]; NULL: Sq); a value outside is clamped and reported as
  * FA_ERR_INDEX.  ancestors: DEVICE uint8 [Sq, Sq] per sequence, stride_b elements
  * apart (0: one tree for all); element (i, j) nonzero: draft i sees draft j.  A
- * draft sees itself only where (i, i) is set; elements past n_b are not read. */
+ * draft sees itself only where (i, i) is set; elements past n_b are not read.  A draft
+ * that no draft sees, nor itself, may hold anything in a 16-bit cache. */
 typedef struct {
   const uint8_t* ancestors;
   int64_t stride_b;

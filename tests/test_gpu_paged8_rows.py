@@ -206,3 +206,44 @@ def test_a_large_draft_reaches_no_other_branch(case):
     pick = lambda x: x[rows][None, None]
     got = [_dev(np.ascontiguousarray(pick(_host(x))).astype(np.float32)) for x in (o, l)]
     _check8(*got, [pick(x) for x in ref], pick(W), E, dtype, "clear rows")
+
+
+@pytest.mark.parametrize("dtype,fmt,Hq,Hkv,D,page,S", [
+    ("bf16", None, 4, 1, 128, 64, 8), ("fp16", None, 2, 1, 64, 16, 16), ("bf16", None, 1, 1, 128, 32, 32),          # by warps
+    ("bf16", None, 8, 1, 128, 64, 12), ("fp16", None, 8, 2, 64, 32, 60), ("bf16", None, 2, 1, 128, 16, 150),         # by tcgen05
+    ("bf16", "e4m3fn", 4, 1, 128, 64, 8), ("fp16", "e5m2", 2, 2, 64, 32, 30), ("bf16", "e5m2", 1, 1, 128, 16, 60),
+    ("bf16", "e4m3fn", 8, 1, 128, 64, 12), ("fp16", "e4m3fn", 8, 2, 64, 32, 60), ("bf16", "e4m3fn", 2, 1, 128, 16, 150),
+])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_drafts_that_no_row_sees_may_be_anything(dtype, fmt, Hq, Hkv, D, page, S, bad):
+    """Keys and values of drafts whose column of ancestors is empty, the first and the last among them, and
+    of those that only rows past a sequence's drafts name: anything in a 16-bit cache, rows that are not
+    finite in an 8-bit one."""
+    import attention_forward_fa_gb300 as fa
+    from tests.test_gpu_paged import Cache, _check
+    lens, drafts = [S + 300, S, 2 * S + 77], [S, S, S - 3]
+    c = Cache(45, dtype, 3, Hkv, D, page, lens) if fmt is None else Cache8(45, dtype, fmt, 3, Hkv, D, page, lens)
+    anc, _ = _trees(c.rng, 3, S)
+    blind = c.rng.random((3, S)) < 0.3
+    blind[0, 0] = blind[1, S - 1] = blind[2, S - 4] = True
+    for b in range(3):
+        anc[b][:, blind[b]] = False
+        anc[b, drafts[b]:] = True
+        for j in range(drafts[b]):
+            if blind[b, j]:
+                t = lens[b] - drafts[b] + j
+                p, s = int(c.table[b, t // page]), t % page
+                if fmt is None:
+                    c.tk[p, :, s], c.tv[p, :, s] = bad, -bad
+                else:
+                    c.bk[p, :, s], c.bv[p, :, s] = 0, 0
+                    c.sk[p, :, s], c.sv[p, :, s] = 255, 255
+    q = _round(c.rng.standard_normal((3, Hq, S, D)), dtype)
+    o, l = fa.flash_attention_decode_tree(_dev(q, dtype), c.obj, c.ints(lens), _dev(anc), new_lens=c.ints(drafts))
+    assert _status() == 0
+    a = (c.table, lens, D ** -0.5)
+    ref = P.decode(q, c.k, c.v, *a, tree=(anc, drafts))
+    if fmt is None:
+        _check(o, l, ref, dtype, "blind drafts")
+    else:
+        _check8(o, l, ref, *_spread(c, q, *a, (anc, drafts)), dtype, "blind drafts")
