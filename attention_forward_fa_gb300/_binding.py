@@ -746,7 +746,7 @@ def paged_kv_append(cache: PagedKV, kv_lens, k, v, *, new_lens=None, q=None, q_o
             raise ValueError("k, v, q, q_out must be of the cache's type, on its device, with a contiguous last dimension")
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
-    rot, max_pos, angles = 0, 0, (0, 0)
+    rot, max_pos, angles, tokens = 0, 0, (0, 0), _int(S)
     if cos is not None:
         table = cos.shape
         if table != sin.shape or len(table) != 2:
@@ -765,10 +765,10 @@ def paged_kv_append(cache: PagedKV, kv_lens, k, v, *, new_lens=None, q=None, q_o
                                                       rot, 1 if interleaved else 0, max_pos))
         fp8 = _fp8_of(cache)
         if fp8 is None and positions is None:
-            code = library().fa_kv_append(cache._c, x, B, Hq, Hkv, S, D, cache._flags, kv_lens.data_ptr(),
+            code = library().fa_kv_append(cache._c, x, B, Hq, Hkv, tokens, D, cache._flags, kv_lens.data_ptr(),
                                           _ptr(new_lens), raw)
         else:
-            code = library().fa_kv_append_ext(cache._c, fp8, x, B, Hq, Hkv, S, D, cache._flags, kv_lens.data_ptr(),
+            code = library().fa_kv_append_ext(cache._c, fp8, x, B, Hq, Hkv, tokens, D, cache._flags, kv_lens.data_ptr(),
                                               _ptr(new_lens), _ptr(positions), raw)
         if code:
             _raise(code)
@@ -887,7 +887,7 @@ def paged_kv_read(cache: PagedKV, lens, *, starts=None, size: Optional[int] = No
         k, v = ((torch.empty(shape, dtype=cache.dtype, device=cache.device) for _ in range(2)) if k_out is None
                 else (k_out, v_out))
         rows = fa_kv_rows_t(k.data_ptr(), v.data_ptr(), *k.stride()[:3], *v.stride()[:3])
-        _raise(library().fa_kv_read(cache._c, _fp8_of(cache), rows, cache.B, cache.Hkv, shape[2], cache.D, cache._flags,
+        _raise(library().fa_kv_read(cache._c, _fp8_of(cache), rows, cache.B, cache.Hkv, _int(shape[2]), cache.D, cache._flags,
                                     _ptr(starts), lens.data_ptr(), raw))
         return k, v
 
