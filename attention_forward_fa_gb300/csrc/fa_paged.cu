@@ -26,7 +26,7 @@ using fa_host::launch_dependent;
 constexpr long long kMostTokens = (1LL << 31) - 65536;   // of one sequence: positions are 32-bit
 constexpr long long kMostRows = (1LL << 31) - 65536;     // of a call (B * heads * tokens), counted in 32 bits
 constexpr int kMostSel = 1 << 20;                        // listed pages of one KV head
-constexpr int kWideRows = 32, kWideRows8 = 64;           // rows per KV head that decode without tcgen05
+constexpr int kWideRows = 32, kWideRows8 = 48;           // rows per KV head that decode without tcgen05
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -323,9 +323,11 @@ int decode_call(const void* q, const fa_paged_kv_t* kv, const fa_kv_fp8_t* fp8, 
   const bool fp16 = (mask_mode & FA_DTYPE_FP16) != 0;
   const int rows = Hq / Hkv * Sq;
   // Rows past which the products by tcgen05 (fa_wide.cuh) are ahead of the warp-level ones.  16 trees over up
-  // to 8192 tokens, 8 KV heads of 128, bf16: at 24, 32, 48 rows 55, 67, 96 us by warps and 65, 68, 71 by
-  // tcgen05; over an 8-bit cache, whose tiles have to be converted, at 32, 48, 64 rows 57, 79, 100 and 99, 101,
-  // 103.  (The fa_decode of a 16-bit cache without a tree keeps to its passes of 48 rows and so to its bits.)
+  // to 8192 tokens, 8 KV heads of 128, bf16: at 24, 32, 48 rows 55, 67, 93 us by warps and 65, 68, 71 by
+  // tcgen05; over an 8-bit cache, whose tiles have to be converted, at 32, 48, 64 rows 59, 82, 102 and 90, 95,
+  // 97.  With heads of 64 40, 48, 69 and 48, 48, 51; 47, 68, 86 and 58, 61, 62 (48 rows lose there).  The order
+  // is that of 128 channels for fp16, for 2 KV heads, for 2 sequences and for 16 of up to 700 tokens.
+  // (The fa_decode of a 16-bit cache without a tree keeps to its passes of 48 rows and so to its bits.)
   const bool wide = fp8 ? rows > kWideRows8 : tree && rows > kWideRows;
   const int box = std::min(kv->page_size, wide || fp8 ? 128 : fa::kDecTile);
   auto maps = [&](auto& x) {
