@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kDecThreads * kDec8Teams<BF16, NT>, 1) fa_deco
       if (__any_sync(0xffffffffu, odd)) {
         // The weights of these keys join the sum here, without their values' exponents.  Values that are not
         // finite: P becomes 2^100, an fp16 infinity, which times the row's codes of 0 is NaN.  (What a row does
-        // not see stays -infinity.)
+        // not see stays -infinity, a NaN key's score NaN; |m| 2^-22: more than a rounding of m.)
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kDecThreads * kDec8Teams<BF16, NT>, 1) fa_deco
               for (int e = 0; e < 2; ++e) {
                 float& y = c[u][n][2 * x + e];
                 l[n][e] += ex2_approx(y - e_v - m[n][e]);
-                if (vs == kScaleNone && y != -INFINITY) y = m[n][e] + 100.f;
+                if (vs == kScaleNone && y > -INFINITY) y = m[n][e] + fmaxf(100.f, fabsf(m[n][e]) * 0x1p-22f);
               }
           }
       }

@@ -105,6 +105,28 @@ def test_rows_that_are_not_finite(case, kinds):
         _compare(c, q, lens, got, bad if "k" in kinds else none, bad if "v" in kinds else none, pre, tree, f"{kinds} {form}")
 
 
+@pytest.mark.parametrize("case", ROWS, ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("kinds", ["v", "k", "kv"])
+def test_rows_that_see_nothing_finite(case, kinds):
+    """A sequence of such tokens alone, and one whose first row sees one of them and no other."""
+    import attention_forward_fa_gb300 as fa
+    dtype, fmt, Hq, Hkv, D, page, Sq = case
+    lens = [Sq, Sq + 200, Sq]
+    c = Cache8(46, dtype, fmt, 3, Hkv, D, page, lens)
+    bad = [list(range(Sq)), [], [0]]
+    for b in range(3):
+        for t in bad[b]:
+            for kind in kinds:
+                _spoil(c, kind, b, t)
+    q = _round(c.rng.standard_normal((3, Hq, Sq, D)), dtype)
+    none = [[], [], []]
+    for tree in (None, (np.broadcast_to(np.tril(np.ones((Sq, Sq), dtype=bool)), (3, Sq, Sq)).copy(), [Sq, Sq, Sq])):
+        got = (fa.flash_attention_decode(_dev(q, dtype), c.obj, c.ints(lens)) if tree is None else
+               fa.flash_attention_decode_tree(_dev(q, dtype), c.obj, c.ints(lens), _dev(tree[0])))
+        assert _status() == 0
+        _compare(c, q, lens, got, bad if "k" in kinds else none, bad if "v" in kinds else none, None, tree, f"{kinds} tree {tree is not None}")
+
+
 def _set_keys(c, k):
     """The cache's keys become k [num_pages, Hkv, page, D], quantised."""
     c.kc, c.ke = P.quantise(k, c.fmt)
