@@ -32,10 +32,12 @@
 //     of the answer over 64 sequences of up to 8192 tokens).
 //
 // Measured (32 query heads on 8 KV heads of 128, both kernels): 8 sequences of 131072
-// tokens, e4m3, bf16 313 us, 6.92 TB/s of codes and scales (the 16-bit cache: 600 us);
-// 64 of mixed lengths up to 8192, e5m2, fp16, pages of 16 95 us, 5.9 TB/s; one of 517
-// tokens 6.3 us.  Up to 16 rows bound by HBM; at 32 rows by the warp-level products (16
-// trees over up to 8192 tokens: 44 us at 24 rows, 57 at 32, of which the bytes are 21).
+// tokens, e4m3, bf16 314 us, 6.90 TB/s of codes and scales (the 16-bit cache: 600 us);
+// 64 of mixed lengths up to 8192, e5m2, fp16, pages of 16 96 us, 5.9 TB/s; one of 517
+// tokens 6.5 us; 16 of 4096, 4 and 16 rows, 30 and 35.  Up to 16 rows bound by HBM; from
+// there by the warp-level products (16 trees over up to 8192 tokens: 46 us at 24 rows, 59 at
+// 32, and, in two passes, 82 at 48, of which the bytes are 21).  ptxas reports 28 to 32 bytes
+// of spills with heads of 128 at 16 rows (bf16) and at 32, none elsewhere.
 #pragma once
 #include <type_traits>
 

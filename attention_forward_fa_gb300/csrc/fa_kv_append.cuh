@@ -19,8 +19,9 @@
 //
 // Into an 8-bit cache (kAppend8, fa_paged8.cuh) a row's D / 16 threads find its largest
 // channel with two or three shuffles and store codes; the same prompts 35.0 us, 4.99 TB/s of
-// 175 MB, half of the issue slots taken (three blocks per SM at 80 registers: 38.5 us); eight
-// drafts each of 64 sequences turned by given positions 4.7 us.
+// 175 MB, half of the issue slots taken (three blocks per SM at 80 registers: 38.5 us; at 64 each
+// of its 16 instances spills 4 to 20 bytes, where the 16-bit forms spill none); eight drafts each
+// of 64 sequences turned by given positions 4.7 us, into a 16-bit cache (kAppendPlaced) 4.6.
 #pragma once
 #include <type_traits>
 

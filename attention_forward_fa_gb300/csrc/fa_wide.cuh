@@ -26,7 +26,8 @@
 //     That is exact where the tile's scales are within 2^15, of e5m2 2^8, of each other.
 //     In other tiles (the keys', the values', or both) the codes stay and the softmax
 //     threads take each key's exponent, which is slow.  A row of zeros (e = -80) beside
-//     others makes a tile one of those, and so does a row that is not finite.
+//     others makes a tile one of those, and so does a row that is not finite (a value's
+//     also all of the piece's tiles behind it: nothing says how large its others are).
 //   * The next S of a group is issued behind its P V, so that its commit says that O is at
 //     rest: the softmax threads may then move their references and rescale O.
 //   * P is written over S, as a hi + lo pair of the operands' type (64 + 64 columns) or, over an
@@ -37,13 +38,17 @@
 //
 // Measured (32 query heads on 8 KV heads of 128, bf16, with the join): 16 trees of up to 12
 // drafts over up to 8192 tokens (48 rows) 71 us, 41 of which are the bytes', over 32768 tokens
-// each 352 us, 6.1 TB/s; 4 trees of up to 64 (256 rows) over an 8-bit cache of up to 16384
-// tokens 73 us, over 65536 each 257 us, 1068 TF/s; the same over a 16-bit cache 69 and 277 us.
+// each 348 us, 6.2 TB/s; 4 trees of up to 64 (256 rows) over an 8-bit cache of up to 16384
+// tokens 70 us, over 65536 each 260 us, 1058 TF/s; the same over a 16-bit cache 70 and 291 us.
+// A prompt's last 512 of 4096 tokens over an 8-bit cache 66 us, 521 TF/s.
 // A unit costs about 13000 cycles beside its tiles (rows in, the last P V, the groups' join, the
 // answer out); with 256 rows a group's chain (S 512 cycles, softmax 2500, P V 512) sets the step,
 // 4000 cycles a tile, half of which the tensor cores work; with up to 128 rows over an 8-bit cache
-// the conversion does (16 trees over 32768 tokens 438 us): 96 KB a tile through shared memory, which
-// the S products want too.
+// the conversion does (16 trees of 24 drafts, 96 rows, 103 us over up to 8192 tokens, 441 over 32768
+// each): 96 KB a tile through shared memory, which the S products want too.  The code of all roles
+// together is more than the instruction cache likes: what few tiles need has loops of its own.
+// With every tile taken key by key (a row of zeros in each) the 4 trees take 254 us instead of
+// 70, the 16 of 96 rows 231 instead of 103.
 #pragma once
 #include <type_traits>
 

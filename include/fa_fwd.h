@@ -552,7 +552,8 @@ int fa_select_pages(const void* q, const fa_paged_kv_t* kv, int32_t* page_idx, i
  * or NaN becomes NaN (codes 0, scale byte 255) and is reported as FA_ERR_RANGE by
  * fa_check_status.  Callers that write rows themselves: scale bytes 1 to 253, of
  * values 47 to 253 (2^-80 to 2^126), codes finite, of every token that kv_lens counts,
- * whether a row sees it or not.
+ * whether a row sees it or not.  (Caches of one scale per tensor or head hold other
+ * rows than these: they would have to be written anew.)
  */
 typedef struct {
   uint8_t* k_scale;
@@ -596,7 +597,14 @@ typedef struct {
  * pre_tokens nor page_idx (FA_ERR_UNSUPPORTED).
  * Over an 8-bit cache the products take fp16 codes, Q as fp16 of a power of
  * two times it (exact but for bf16 channels below 2^-29 of their row's largest) and P
- * as one fp16, for fp16 answers as a hi + lo pair; scores and sums are fp32.
+ * as one fp16, for fp16 answers as a hi + lo pair; scores and sums are fp32.  Past 48
+ * rows (Hq / Hkv * Sq; of trees over a 16-bit cache past 32) up to 8192 keys add up in
+ * the tensor cores' accumulators, which cut off what they add: 2^-15 of it at most.
+ * Scales of all sizes mix.  Past 48 rows, 128 keys whose scales (or their values') lie
+ * more than 2^15 apart, of e5m2 2^8, take three to four times as long; a row of zeros
+ * has the least scale.  A value row that is not finite (scale byte 255) makes the answer
+ * of each row that sees it NaN and leaves the LSE, a key row makes both NaN; rows that do
+ * not see it are answered as without it.
  */
 int fa_decode_ext(const void* q, const fa_paged_kv_t* kv, const fa_kv_fp8_t* fp8, void* o, float* lse,
                   int B, int Hq, int Hkv, int Sq, int D, float scale, int mask_mode,
