@@ -593,8 +593,9 @@ typedef struct {
  * before the drafts and those drafts that its row of ancestors names (kv_lens
  * counts the drafts; rows are a sequence's first, as fa_kv_append leaves them).
  * Rows i >= n_b are padding: whatever they hold, they are answered as rows that see
- * the tokens before the drafts, and reach no other row.  A tree goes with neither
- * pre_tokens nor page_idx (FA_ERR_UNSUPPORTED).
+ * the tokens before the drafts, and reach no other row (whose last bits may differ where
+ * padding has scores past all others).  A tree goes with neither pre_tokens nor
+ * page_idx (FA_ERR_UNSUPPORTED).
  * Over an 8-bit cache the products take fp16 codes, Q as fp16 of a power of
  * two times it (exact but for bf16 channels below 2^-29 of their row's largest) and P
  * as one fp16, for fp16 answers as a hi + lo pair; scores and sums are fp32.  Past 48
