@@ -200,13 +200,11 @@ def test_values_over_the_whole_range(case, order):
             _check8(o, l, ref, *_spread(c, q, *a, tree), dtype, f"scale {scale} tree {tree is not None}")
 
 
-@pytest.mark.parametrize("case", ROWS, ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("case", [c for c in ROWS if c[-1] >= 4], ids=lambda c: "-".join(map(str, c)))
 def test_a_large_draft_reaches_no_other_branch(case):
     """One draft's key of 2^70: rows that do not see it are answered to the usual bounds."""
     import attention_forward_fa_gb300 as fa
     dtype, fmt, Hq, Hkv, D, page, Sq = case
-    if Sq < 4:
-        pytest.skip("no branches")
     lens, drafts = [200, 3000, 130], [Sq, Sq, Sq - 1]
     c = Cache8(43, dtype, fmt, 3, Hkv, D, page, lens)
     k = c.k.copy()
